@@ -23,7 +23,10 @@ __all__ = [
     "wait_probe", "serial_forward", "serial_workspace_size", "prepare_fp8_weights",
     "fp8_workspace_size", "ptb_forward_fp8", "ptb_forward_fp8_events", "train_saved_size",
     "ptb_forward_train", "backward_workspace_size", "ptb_backward", "ptb_backward_events", "swa_attention_lse",
-    "swa_attention_backward", "set_gemm_pairs", "host_workspace_size", "ptb_forward_host", "LIB_PATH", "SYMBOLS",
+    "swa_attention_backward", "set_gemm_pairs", "host_workspace_size", "ptb_forward_host",
+    "kv_page_size", "kv_append", "kv_gather", "swa_attention_packed",
+    "swa_attention_packed_workspace_size", "swa_attention_paged",
+    "swa_attention_paged_workspace_size", "LIB_PATH", "SYMBOLS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libptb.so")
@@ -71,6 +74,18 @@ SYMBOLS = {
     "ptb_gemm_qkv_up": (_st, [_p, _p, _p, _i64, _i64, _i64, _p, _p, _sz, _p]),
     "ptb_gemm_out_down": (_st, [_p, _i64, _p, _i64, _p, _p, _p, _i64, _i64, _i64, _p, _p, _sz,
                                 _p]),
+    "ptb_kv_page_size": (_sz, [_i32] * 4),
+    "ptb_kv_append": (_st, [_p, _i64, _i64] * 3 + [_p, _p, _i64, _i32, _i32, _p, _p, _i32, _i64]
+                      + [_i32] * 3 + [_p, _i64, _i64] * 2 + [_p, _i64, _p, _i64, _i64, _i32, _i32,
+                                                             _p]),
+    "ptb_kv_gather": (_st, [_p, _i64, _p, _i64, _i64, _p, _p, _i32, _i64] + [_i32] * 4
+                      + [_p, _i64, _i64] * 2 + [_p]),
+    "swa_attention_packed_workspace_size": (_sz, [_i32, _i64, _i32, _i32]),
+    "swa_attention_packed": (_st, [_p, _i64, _i64] * 3 + [_p, _p, _i32, _i64, _i64] + [_i32] * 4
+                             + [_f32, _p, _i64, _i64, _p, _sz, _p]),
+    "swa_attention_paged_workspace_size": (_sz, [_i32] * 4),
+    "swa_attention_paged": (_st, [_p, _i64, _i64, _p, _i64, _p, _i64, _i64, _p] + [_i32] * 7
+                            + [_f32, _p, _i64, _i64, _p, _sz, _p]),
     "ptb_last_device_error": (_st, [_p]),
     "ptb_wait_probe": (_st, [ctypes.c_uint64, _p]),
 }
@@ -326,6 +341,205 @@ def swa_attention_counts(q, k, v, window: int, scale: float = 0.0, stream=None):
                                   _ptr(o), _ptr(counts), _stream(stream))
     _check(st, "swa_attention_counts")
     return o, counts
+
+
+# ---------------------------------------------------------------- serving --
+
+def kv_page_size(kv_heads: int, page_size: int, head_dim: int, bits: int) -> int:
+    """Bytes of one page of a key/value cache: `page_size` token rows of the keys and the values of
+    `kv_heads` heads in bf16 (bits 16) or 4 bits.  A cache is a uint8 CUDA tensor
+    [pages, kv_page_size(...)] of any content."""
+    n = int(load().ptb_kv_page_size(kv_heads, page_size, head_dim, bits))
+    if n == 0:
+        raise ValueError(f"no cache of {kv_heads} heads x {head_dim}, pages of {page_size} rows, "
+                         f"{bits} bits")
+    return n
+
+
+def _on_device(name: str, t, dtype) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a {str(dtype).replace('torch.', '')} CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is not on the current device")
+
+
+def _heads_view(name: str, t, shape=None) -> list:
+    """[tokens, heads, d] with a contiguous last dimension -> pointer and two strides."""
+    _on_device(name, t, torch.bfloat16)
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] with a contiguous last dimension")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    # The stride of a dimension of one entry is never used.
+    return [_ptr(t), t.stride(0) if t.shape[0] > 1 else max(8, t.stride(0) // 8 * 8),
+            t.stride(1) if t.shape[1] > 1 else max(8, t.stride(1) // 8 * 8)]
+
+
+def _int_vector(name: str, t, n: int) -> int:
+    _on_device(name, t, torch.int32)
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries")
+    return _ptr(t)
+
+
+def _offsets(name: str, t) -> int:
+    """The number of sequences that cu_seqlens speaks of."""
+    _on_device(name, t, torch.int32)
+    if t.dim() != 1 or t.shape[0] < 2:
+        raise ValueError(f"{name} must be an int32 vector of at least 2 entries")
+    return t.shape[0] - 1
+
+
+def _cache_args(cache, page_table, batch: int, kv_heads: int, head_dim: int, page_size: int,
+                bits: int) -> list:
+    _on_device("cache", cache, torch.uint8)
+    _on_device("page_table", page_table, torch.int32)
+    n = kv_page_size(kv_heads, page_size, head_dim, bits)
+    if cache.dim() != 2 or cache.shape[1] != n or not cache.is_contiguous():
+        raise ValueError(f"cache must be contiguous [pages, {n}]")
+    if (page_table.dim() != 2 or page_table.shape[0] != batch
+            or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError(f"page_table must be [{batch}, pages of a sequence], rows contiguous")
+    stride = page_table.stride(0) if batch > 1 else page_table.shape[1]
+    return [_ptr(cache), cache.shape[0], _ptr(page_table), stride, page_table.shape[1]]
+
+
+def _new(stream, *shape, dtype=torch.bfloat16):
+    """A tensor of the stream that is going to write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+def _scratch(need: int, workspace, stream):
+    """(tensor that has to outlive the launch, pointer, bytes)"""
+    if workspace is None:
+        workspace = _new(stream, max(need, 1), dtype=torch.uint8)
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def kv_append(q, k, v, cache, page_table, cu_seqlens, past, page_size: int, bits: int, cos=None,
+              sin=None, interleaved: bool = False, q_out=None, k_out=None, keep_keys: bool = True,
+              stream=None):
+    """Writes the keys and values of new tokens into the paged cache, rotated by position.
+
+    q [T, heads, d] (or None), k, v [T, kv_heads, d] bf16; sequence b has rows cu_seqlens[b] ..
+    cu_seqlens[b + 1] - 1 and its token i position past[b] + i.  cos, sin fp32
+    [positions, rot_dim / 2].  Returns (q_out, k_out), the rotated q and k: new tensors, or the
+    given ones (q and k themselves for in-place rotation); k_out is None without keep_keys."""
+    lib = load()
+    batch = _offsets("cu_seqlens", cu_seqlens)
+    kv = _heads_view("k", k)
+    tokens, kv_heads, d = k.shape
+    kv += _heads_view("v", v, k.shape)
+    heads, qa, qo, ko = 0, [None, 8, 8], [None, 8, 8], [None, 8, 8]
+    if q is not None:
+        qa = _heads_view("q", q)
+        heads = q.shape[1]
+        if q.shape[0] != tokens or q.shape[2] != d:
+            raise ValueError("q must be [tokens, heads, head_dim] of k's tokens and head_dim")
+        if q_out is None:
+            q_out = _new(stream, *q.shape)
+        qo = _heads_view("q_out", q_out, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k_out is None and keep_keys:
+        k_out = _new(stream, *k.shape)
+    if k_out is not None:
+        ko = _heads_view("k_out", k_out, k.shape)
+    rot, positions = 0, 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        for n, t in (("cos", cos), ("sin", sin)):
+            _on_device(n, t, torch.float32)
+            if t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous():
+                raise ValueError("cos and sin must be contiguous [positions, rot_dim / 2]")
+        positions, rot = cos.shape[0], 2 * cos.shape[1]
+    ca = _cache_args(cache, page_table, batch, kv_heads, d, page_size, bits)
+    st = lib.ptb_kv_append(*qa, *kv, _ptr(cos), _ptr(sin), positions, rot, int(interleaved),
+                           _int_vector("cu_seqlens", cu_seqlens, batch + 1),
+                           _int_vector("past", past, batch), batch, tokens, heads, kv_heads, d,
+                           *qo, *ko, *ca, page_size, bits, _stream(stream))
+    _check(st, "ptb_kv_append")
+    return q_out, k_out
+
+
+def kv_gather(cache, page_table, cu_seqlens, start, tokens: int, kv_heads: int, head_dim: int,
+              page_size: int, bits: int, k=None, v=None, stream=None):
+    """Reads cached rows back as bf16: row cu_seqlens[b] + i of the returned k and v
+    [tokens, kv_heads, d] is position start[b] + i of sequence b."""
+    lib = load()
+    batch = _offsets("cu_seqlens", cu_seqlens)
+    shape = (tokens, kv_heads, head_dim)
+    k = _new(stream, *shape) if k is None else k
+    v = _new(stream, *shape) if v is None else v
+    st = lib.ptb_kv_gather(*_cache_args(cache, page_table, batch, kv_heads, head_dim, page_size, bits),
+                           _int_vector("cu_seqlens", cu_seqlens, batch + 1),
+                           _int_vector("start", start, batch), batch, tokens, kv_heads, head_dim,
+                           page_size, bits, *_heads_view("k", k, shape), *_heads_view("v", v, shape),
+                           _stream(stream))
+    _check(st, "ptb_kv_gather")
+    return k, v
+
+
+def swa_attention_packed_workspace_size(batch: int, tokens_q: int, heads: int, kv_heads: int) -> int:
+    return int(load().swa_attention_packed_workspace_size(batch, tokens_q, heads, kv_heads))
+
+
+def swa_attention_packed(q, k, v, cu_seqlens, window: int, cu_seqlens_k=None, scale: float = 0.0,
+                         o=None, workspace=None, stream=None):
+    """Causal sliding-window attention over packed sequences with grouped heads.
+
+    q [Tq, heads, d], k, v [Tk, kv_heads, d] bf16 (strided, last dimension contiguous); the nq
+    queries of a sequence are the last of its nk positions (cu_seqlens_k None: nk = nq).  Returns o
+    like q; rows behind the last sequence are not written.  o may be q."""
+    lib = load()
+    batch = _offsets("cu_seqlens", cu_seqlens)
+    qa = _heads_view("q", q)
+    ka = _heads_view("k", k)
+    va = _heads_view("v", v, k.shape)
+    if q.shape[2] != k.shape[2]:
+        raise ValueError("q and k must have the same head_dim")
+    if cu_seqlens_k is None and q.shape[0] != k.shape[0]:
+        raise ValueError("q and k must have the same tokens, or cu_seqlens_k be given")
+    if o is None:
+        o = _new(stream, *q.shape)
+    oa = _heads_view("o", o, q.shape)
+    cu_k = None if cu_seqlens_k is None else _int_vector("cu_seqlens_k", cu_seqlens_k, batch + 1)
+    ws, wp, wb = _scratch(lib.swa_attention_packed_workspace_size(batch, q.shape[0], q.shape[1],
+                                                                  k.shape[1]), workspace, stream)
+    st = lib.swa_attention_packed(*qa, *ka, *va, _int_vector("cu_seqlens", cu_seqlens, batch + 1),
+                                  cu_k, batch, q.shape[0], k.shape[0], q.shape[1], k.shape[1],
+                                  q.shape[2], window, scale, *oa, wp, wb, _stream(stream))
+    _check(st, "swa_attention_packed")
+    return o
+
+
+def swa_attention_paged_workspace_size(batch: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(load().swa_attention_paged_workspace_size(batch, heads, kv_heads, head_dim))
+
+
+def swa_attention_paged(q, cache, page_table, seq_lens, kv_heads: int, page_size: int, bits: int,
+                        window: int, scale: float = 0.0, o=None, workspace=None, stream=None):
+    """Attention of one new token per sequence over the paged cache: q [B, heads, d] bf16 against
+    the last min(seq_lens[b], window) positions of sequence b.  Returns o like q; o may be q."""
+    lib = load()
+    qa = _heads_view("q", q)
+    batch, heads, d = q.shape
+    if o is None:
+        o = _new(stream, *q.shape)
+    oa = _heads_view("o", o, q.shape)
+    ws, wp, wb = _scratch(lib.swa_attention_paged_workspace_size(batch, heads, kv_heads, d),
+                          workspace, stream)
+    st = lib.swa_attention_paged(*qa, *_cache_args(cache, page_table, batch, kv_heads, d, page_size, bits),
+                                 _int_vector("seq_lens", seq_lens, batch), batch, heads, kv_heads,
+                                 d, page_size, bits, window, scale, *oa, wp, wb, _stream(stream))
+    _check(st, "swa_attention_paged")
+    return o
 
 
 def host_workspace_size(batch: int, seq: int, hidden: int, ffn: int) -> int:

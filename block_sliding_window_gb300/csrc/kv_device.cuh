@@ -1,0 +1,48 @@
+// Device-side helpers of the serving kernels: finding a token's sequence,
+// cache addresses, and the 4-bit row format (ptb.h has the layout).
+#pragma once
+
+#include "ptb_device.cuh"
+
+namespace ptb {
+
+constexpr int kKvGroup = 32;  // channels that share one (scale, centre) pair
+
+// The sequence of token t: the first b < batch with cu[b + 1] > t, or batch.
+// A whole warp searches with 32 probes a step, so up to 32 sequences take one
+// load and up to 1024 take two.  Every lane returns the same b.
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int batch, int64_t t, int lane) {
+  int lo = 0, len = batch;
+  while (len > 0) {
+    const int step = (len + 31) >> 5;
+    const int64_t at = lo + static_cast<int64_t>(lane) * step + step - 1;
+    const bool past = at >= lo + len ? true : cu[at + 1] > t;
+    const unsigned vote = __ballot_sync(0xffffffffu, past);
+    if (vote == 0) return lo + len;
+    const int f = __ffs(vote) - 1;
+    if (step == 1) return min(lo + f, batch);
+    const int64_t skip = static_cast<int64_t>(f) * step;
+    if (skip >= len) return lo + len;
+    lo += static_cast<int>(skip);
+    len = min(step, len - static_cast<int>(skip));
+  }
+  return lo;
+}
+
+// The start of position p's page of sequence b, or null when the entry is
+// outside the table or the cache.
+__device__ __forceinline__ uint8_t* kv_page(const KvCache& c, int b, int64_t p) {
+  const int64_t i = p >> c.page_shift;
+  if (i >= c.table_pages) return nullptr;
+  const int64_t page = c.table[b * c.table_stride + i];
+  if (page < 0 || page >= c.pages) return nullptr;
+  return c.base + page * c.page_bytes;
+}
+
+// Byte offsets inside a row of d / 2 code bytes (ng = d / 32 groups).
+// Key word of channels 32 w + 8 t .. + 7:
+__device__ __forceinline__ int key_word(int w, int t, int ng) { return 4 * (t * ng + w); }
+// Value half-word of channels 32 w + 4 g .. + 3:
+__device__ __forceinline__ int value_half(int w, int g, int ng) { return 2 * (g * ng + w); }
+
+}  // namespace ptb

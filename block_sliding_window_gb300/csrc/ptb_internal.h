@@ -124,6 +124,77 @@ struct SwaBwdArgs {
 bool make_tensor_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                      const uint64_t* strides_bytes, const uint32_t* box);
 
+// ------------------------------------------------------------- serving --
+
+// The paged cache of keys and values (layout: ptb.h).
+struct KvCache {
+  uint8_t* base;
+  int64_t pages, page_bytes;  // page_bytes = 2 * kv_heads * block_bytes
+  int64_t block_bytes;        // one kv head's keys or values of one page
+  const int32_t* table;       // [batch][table_stride], table_pages entries used
+  int64_t table_stride, table_pages;
+  int page_size, page_shift, kv_heads, head_dim, bits;
+};
+
+struct KvAppendArgs {
+  KvCache c;
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16 *q_out, *k_out;
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, qo_st, qo_sh, ko_st, ko_sh;
+  const float *cos, *sin;
+  int64_t positions;
+  int rot_dim, interleaved;
+  const int32_t *cu, *past;
+  int batch, heads;
+  int64_t tokens;
+  unsigned* status;
+  int sms;
+};
+
+struct KvGatherArgs {
+  KvCache c;
+  __nv_bfloat16 *k, *v;
+  int64_t k_st, k_sh, v_st, v_sh;
+  const int32_t *cu, *start;
+  int batch;
+  int64_t tokens;
+  unsigned* status;
+  int sms;
+};
+
+struct SwaPackedArgs {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16* o;
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh;
+  const int32_t *cu_q, *cu_k;
+  int batch, heads, kv_heads, head_dim, window;
+  int64_t tokens_q, tokens_k;
+  float scale_log2;
+  void* workspace;
+  unsigned* status;
+  int sms;
+};
+
+struct SwaPagedArgs {
+  KvCache c;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  int64_t q_sb, q_sh, o_sb, o_sh;
+  const int32_t* lens;
+  int batch, heads, window;
+  float scale_log2;
+  void* workspace;
+  unsigned* status;
+  int sms;
+};
+
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_gather(const KvGatherArgs& a, cudaStream_t stream);
+size_t swa_packed_workspace(int batch, int64_t tokens_q, int heads, int kv_heads);
+cudaError_t launch_swa_packed(const SwaPackedArgs& a, cudaStream_t stream);
+size_t swa_paged_workspace(int batch, int heads, int kv_heads, int head_dim, int sms);
+cudaError_t launch_swa_paged(const SwaPagedArgs& a, cudaStream_t stream);
+
 cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream);
 cudaError_t launch_layernorm(const __nv_bfloat16* x, const __nv_bfloat16* gamma,
                              const __nv_bfloat16* beta, int64_t rows, int hidden, float eps,

@@ -434,6 +434,149 @@ ptb_status ptb_gemm_out_down(const ptb_bf16* ctx, int64_t ld_ctx, const ptb_bf16
                              void* workspace, size_t workspace_bytes, ptb_stream stream);
 
 /*
+ * ------------------------------------------------------------- serving --
+ * What answering with a layer needs beside its kernels: a paged cache of
+ * keys and values, its appends and reads, and sliding-window attention over
+ * packed prompts and over that cache.  The pages define SWA on one sequence
+ * (ch.2 §2.2, SWA row); here every sequence of a batch has its own length,
+ * and query head h attends with key/value head h / (heads / kv_heads)
+ * (kv_heads divides heads; kv_heads = heads is the layer's own attention).
+ *
+ * Packed sequences: the tokens of all sequences stand one after the other;
+ * sequence b has rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 device
+ * array of batch + 1 entries, starting at 0, not decreasing, ending at most
+ * at the tensors' row count).  Rows from cu_seqlens[batch] on belong to no
+ * sequence: they are neither used nor written.  Element (t, h, c) of a tensor
+ * lives at p[t * st + h * sh + c]; strides are in elements, positive
+ * multiples of 8.
+ *
+ * Cache: pages of `page_size` token rows (16, 32, 64, 128 or 256), each of
+ * ptb_kv_page_size() bytes, 16-byte aligned, one behind the other.  A page
+ * holds the blocks of its keys, one per kv head, then those of its values:
+ *   bits 16  block [page_size][head_dim] bf16;
+ *   bits  4  block [page_size][head_dim / 2] bytes of codes, then
+ *            [page_size][head_dim / 32] pairs (scale, centre) of bf16
+ *            (head_dim a multiple of 32).  A code u in 0..15 stands for
+ *            centre + scale * (u - 8); a pair serves 32 neighbouring
+ *            channels.  Low nibble first; with NG = head_dim / 32, channel
+ *            32 w + 8 t + e (e < 8) of a key is nibble 8 (t NG + w) + e of its
+ *            row, and channel 32 w + 4 g + e (e < 4) of a value is nibble
+ *            (head_dim / 8) g + 4 w + e: the orders in which the tensor-core
+ *            fragments of swa_attention_paged take them.
+ * Position p of sequence b is row p % page_size of page
+ * page_table[b * table_stride + p / page_size] (int32, device).  Only the
+ * entries of positions that a call uses are read, so the pages that a window
+ * has left behind can be given away.
+ *
+ * The lengths, tables and positions are read on the device, so a captured
+ * call can be replayed with other values in them.  A kernel that finds an
+ * entry out of range (a length below 0 or past the tensors or the table, a
+ * page outside the cache, a position past the rotation's rows) records
+ * PTB_ERR_ARG in the status word (ptb_last_device_error), accesses nothing
+ * there and leaves that sequence, token or key out.
+ */
+
+/* Bytes of one cache page; 0 for a shape that is not supported. */
+size_t ptb_kv_page_size(int32_t kv_heads, int32_t page_size, int32_t head_dim, int32_t bits);
+
+/*
+ * ptb_kv_append: writes the keys and values of new tokens into the cache,
+ * with the position rotation applied on the way.
+ *
+ *   q [tokens, heads, d], k, v [tokens, kv_heads, d]  strided; q may be NULL
+ *   cos, sin   fp32 [positions][rot_dim / 2], or NULL with rot_dim = 0 (the
+ *              layer's own attention has no positional term)
+ *   rot_dim    rotated channels, the first of a head: a multiple of 16 up to d
+ *   interleaved  0: channel c turns against channel c + rot_dim / 2;
+ *              1: channel 2c against 2c + 1
+ *   past       int32 [batch]: tokens of each sequence that the cache already
+ *              holds; token i of sequence b gets position past[b] + i
+ *   q_out, k_out  rotated q and k; may be q and k themselves (same pointer and
+ *              strides) or NULL (q_out only with q).  They overlap nothing else
+ *
+ * Rotation of a pair (a, b) at position p: (a cos - b sin, b cos + a sin),
+ * products and sums in fp32, rounded once to bf16.  With bits = 16 the rows
+ * are stored as they are; with 4, per 32 channels of the bf16 row and in fp32:
+ *   scale = bf16((max - min) / 15), centre = bf16(min + 8 scale),
+ *   u = clamp(round((x - centre) / scale) + 8, 0, 15)   (ties to even;
+ *   scale 0: u = 8); a group with a value that is not finite, or whose range
+ *   overflows, gets scale = centre = NaN.
+ * Two tokens of one call must not share a cache row (a page that two
+ * sequences share may be read by both but not appended to).
+ */
+ptb_status ptb_kv_append(const ptb_bf16* q, int64_t q_st, int64_t q_sh, const ptb_bf16* k,
+                         int64_t k_st, int64_t k_sh, const ptb_bf16* v, int64_t v_st, int64_t v_sh,
+                         const float* cos, const float* sin, int64_t positions, int32_t rot_dim,
+                         int32_t interleaved, const int32_t* cu_seqlens, const int32_t* past,
+                         int32_t batch, int64_t tokens, int32_t heads, int32_t kv_heads,
+                         int32_t head_dim, ptb_bf16* q_out, int64_t qo_st, int64_t qo_sh,
+                         ptb_bf16* k_out, int64_t ko_st, int64_t ko_sh, void* cache, int64_t pages,
+                         const int32_t* page_table, int64_t table_stride, int64_t table_pages,
+                         int32_t page_size, int32_t bits, ptb_stream stream);
+
+/*
+ * ptb_kv_gather: reads rows of the cache back as bf16, packed: row
+ * cu_seqlens[b] + i of k and v [tokens, kv_heads, d] (strided) is position
+ * start[b] + i of sequence b.  4-bit rows give the value of each code, rounded
+ * to bf16.  With the keys of a prompt's earlier part read back, its next part
+ * is attended with swa_attention_packed.
+ */
+ptb_status ptb_kv_gather(const void* cache, int64_t pages, const int32_t* page_table,
+                         int64_t table_stride, int64_t table_pages, const int32_t* cu_seqlens,
+                         const int32_t* start, int32_t batch, int64_t tokens, int32_t kv_heads,
+                         int32_t head_dim, int32_t page_size, int32_t bits, ptb_bf16* k,
+                         int64_t k_st, int64_t k_sh, ptb_bf16* v, int64_t v_st, int64_t v_sh,
+                         ptb_stream stream);
+
+/*
+ * swa_attention_packed: causal sliding-window attention over packed
+ * sequences with grouped heads.  Sequence b has nq queries (rows of q and o
+ * by cu_seqlens_q) and nk keys (rows of k and v by cu_seqlens_k; NULL: the
+ * same as cu_seqlens_q).  Its queries are the last nq of its nk positions:
+ * query i stands at position p = nk - nq + i and attends to keys
+ * max(0, p - window + 1) .. p.  A query without keys (nk < nq) gets zeros.
+ *
+ *   q, o [tokens_q, heads, d], k, v [tokens_k, kv_heads, d]  strided bf16;
+ *        o may be q itself (same pointer and strides), and overlaps nothing else
+ *   scale  0: 1 / sqrt(d)
+ *   workspace  at least swa_attention_packed_workspace_size() bytes, 256-byte
+ *        aligned; calls that may run at the same time need one each
+ * head_dim 16, 32, 64, 96 or 128; heads / kv_heads at most 128.
+ */
+size_t swa_attention_packed_workspace_size(int32_t batch, int64_t tokens_q, int32_t heads,
+                                           int32_t kv_heads);
+ptb_status swa_attention_packed(const ptb_bf16* q, int64_t q_st, int64_t q_sh, const ptb_bf16* k,
+                                int64_t k_st, int64_t k_sh, const ptb_bf16* v, int64_t v_st,
+                                int64_t v_sh, const int32_t* cu_seqlens_q,
+                                const int32_t* cu_seqlens_k, int32_t batch, int64_t tokens_q,
+                                int64_t tokens_k, int32_t heads, int32_t kv_heads,
+                                int32_t head_dim, int32_t window, float scale, ptb_bf16* o,
+                                int64_t o_st, int64_t o_sh, void* workspace,
+                                size_t workspace_bytes, ptb_stream stream);
+
+/*
+ * swa_attention_paged: attention of one new token per sequence over the
+ * cache.  Sequence b holds seq_lens[b] positions (int32, device), the new
+ * token's own among them; its query attends to the last min(seq_lens[b],
+ * window) of them.  seq_lens[b] = 0 gives zeros.  q, o [batch, heads, d]
+ * strided bf16 (o may be q itself); keys of bits = 4 are used as the values
+ * that their codes stand for.
+ *   workspace  at least swa_attention_paged_workspace_size() bytes (depends on
+ *        the current device's SM count), 256-byte aligned; calls that may run
+ *        at the same time need one each
+ * head_dim 16 (bits 16 only), 32, 64, 96 or 128.
+ */
+size_t swa_attention_paged_workspace_size(int32_t batch, int32_t heads, int32_t kv_heads,
+                                          int32_t head_dim);
+ptb_status swa_attention_paged(const ptb_bf16* q, int64_t q_sb, int64_t q_sh, const void* cache,
+                               int64_t pages, const int32_t* page_table, int64_t table_stride,
+                               int64_t table_pages, const int32_t* seq_lens, int32_t batch,
+                               int32_t heads, int32_t kv_heads, int32_t head_dim,
+                               int32_t page_size, int32_t bits, int32_t window, float scale,
+                               ptb_bf16* o, int64_t o_sb, int64_t o_sh, void* workspace,
+                               size_t workspace_bytes, ptb_stream stream);
+
+/*
  * ptb_last_device_error: waits for the work queued on `stream` so far
  * (cudaStreamSynchronize of that stream only; other streams keep running),
  * then returns the device status word written by the kernels and clears it
