@@ -63,6 +63,10 @@ PACKED = [
     ([10, 4, 3], [6, 0, 3], 4, 4, 128, 9),       # the first queries have no keys; one sequence none
     ([64, 128], [10, 100], 2, 1, 32, 300),
     (list(range(1, 45)), None, 2, 1, 64, 20),    # more sequences than a warp has lanes
+    # more items than SMs: the sorted list
+    ([100, 1, 0, 257, 64, 300], None, 40, 40, 32, 60),
+    ([3] * 70 + [129, 31], None, 24, 12, 64, 1000),
+    ([2, 60, 1], [2, 20, 90], 96, 48, 16, 11),
 ]
 
 
