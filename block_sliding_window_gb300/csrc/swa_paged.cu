@@ -1,116 +1,884 @@
 // Sliding-window attention of one new token per sequence over the paged
-// cache (definition and cache layout: ptb.h).  One block per (sequence,
-// head); its warps take every fourth key and their running maxima, sums and
-// outputs are joined in shared memory.
+// cache (definition and cache layout: ptb.h).
+//
+// The cache is read once and bounds the kernel: 2 d bytes per key and value
+// row in bf16, d / 2 + d / 8 in 4 bits, against 4 d operations per query head.
+// The G query heads of a kv head share its rows, so the products run on the
+// tensor cores (mma.sync m16n8k16; a step has far too few rows for tcgen05's
+// 128), transposed to fill them: S^T = K Q^T with 16 keys as rows and 8 heads
+// as columns, O^T += V^T P^T with 16 channels as rows.
+//
+// Work split.  The unit is a block of 32 keys of one (sequence, kv head, up to
+// 16 query heads).  All units of the call, in order, are dealt to all warps of
+// the grid in equal contiguous shares, whatever the sequences' lengths: one
+// long sequence spreads over the whole GPU and a ragged batch stays even.  A
+// warp works alone: it streams its blocks through its own ring in shared
+// memory (bulk copies, completion on mbarriers), keeps maximum, sum and output
+// of the current segment in registers, and writes the output itself where a
+// share holds all of a segment.  The shares of a segment that was cut leave
+// (maximum, sum, output) in the workspace, and a second kernel, launched to
+// overlap this one's end, joins them in order: the same bits every time.
+//
+// 4-bit rows: codes become bf16 16 + u by placing the nibble in the mantissa,
+// exact, and
+//   q.k  = sum_w scale_w (q.(16 + u))_w + (centre_w - 24 scale_w) Q_w,
+//   sum_j p_j v_j = sum_j (p_j scale_jw)(u_j - 8) + sum_j p_j centre_jw:
+// for keys the pair is applied to the products of each 32-channel group, and
+// Q_w = sum of q over the group enters as one more product with the pairs as
+// they lie in memory (Q_w as two bf16 terms); for values the scale goes into
+// P, and the centres are one more product.  p and p * scale are rounded to
+// bf16, as P is in the other attention kernels.
+// Rows that the mask leaves out (before the window, past the length, pages out
+// of range) may hold anything: their scores are replaced and their values or
+// pairs zeroed before use.
 #include "kv_device.cuh"
 
 namespace ptb {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;        // warps of a block; they share nothing
+constexpr int kBlockKeys = 32;   // keys of a unit
+constexpr int kMinUnits = 2;     // a warp's share is at least this many units
+constexpr int kMaxWarpsPerSm = 16;
+constexpr float kRescaleLog2 = 8.0f;  // raise the reference max only past 2^8
+constexpr int kJoinThreads = 256;
 
-// Channel c of row `off` of a block of keys or values.
-template <int D>
-__device__ __forceinline__ float cached(const KvCache& k, const uint8_t* block, int off, int c,
-                                        bool key) {
-  constexpr int NG = D / kKvGroup;
-  if (k.bits == 16)
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(block)[off * D + c]);
-  if constexpr (NG > 0) {
-    const int w = c / 32, x = c % 32;
-    const int nibble = key ? 2 * key_word(w, x / 8, NG) + x % 8 : 2 * value_half(w, x / 4, NG) + x % 4;
-    const int code = (block[off * (D / 2) + nibble / 2] >> (4 * (nibble & 1))) & 15;
-    const uint32_t pair = *reinterpret_cast<const uint32_t*>(block + k.page_size * (D / 2) +
-                                                             (off * NG + w) * 4);
-    return fmaf(static_cast<float>(code - 8), bf16_lo(pair), bf16_hi(pair));
-  }
-  return 0.f;
+template <int D, int BITS>
+struct Cfg {
+  static constexpr int kAtoms = (D + 63) / 64;
+  static constexpr int NG = D / kKvGroup;
+  static constexpr int kCodeBytes = BITS == 16 ? kAtoms * kBlockKeys * 128 : kBlockKeys * (D / 2);
+  static constexpr int kPairBytes = BITS == 16 ? 0 : kBlockKeys * (D / 8);
+  static constexpr int kSideBytes = kCodeBytes + kPairBytes;  // keys or values of a unit
+  static constexpr int kStageBytes = 2 * kSideBytes;
+  static constexpr int kStages = 3;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kSmemBytes = 1024 + kWarps * (kWarpBytes + 64);
+  static constexpr int kFit = (227 * 1024) / (kSmemBytes + 1024);
+  static constexpr int kBlocksPerSm = kFit < 3 ? (kFit < 1 ? 1 : kFit) : 3;
+};
+static_assert(3 * kWarps <= kMaxWarpsPerSm, "workspace is sized by kMaxWarpsPerSm");
+
+struct PagedParams {
+  CUtensorMap map;  // bits 16: {d, rows of a page, pages}
+  SwaPagedArgs a;
+  int group, head_blocks;  // G; blocks of 8 NT query heads of a kv head
+  int warps;               // of the whole grid
+  float* part_ml;          // [2 warps][2][8 NT]
+  float* part_o;           // [2 warps][8 NT][d]
+};
+
+// The keys that sequence b's query attends to, in units.
+struct Span {
+  int n, lo;       // positions lo .. n - 1
+  int unit0, units;
+};
+
+__device__ __forceinline__ Span span_of(const SwaPagedArgs& a, int b) {
+  Span s;
+  const int64_t cap = a.c.table_pages << a.c.page_shift;
+  int n = a.lens[b];
+  if (n < 0 || n > cap) n = 0;
+  s.n = n;
+  s.lo = n > a.window ? n - a.window : 0;
+  s.unit0 = s.lo / kBlockKeys;
+  s.units = n > 0 ? (n - 1) / kBlockKeys - s.unit0 + 1 : 0;
+  return s;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) swa_paged_kernel(const SwaPagedArgs a) {
-  constexpr int E = (D + 31) / 32;
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
+// Units of all sequences together, per head block (one warp).
+__device__ __forceinline__ int64_t total_units(const SwaPagedArgs& a, int lane) {
+  int64_t sum = 0;
+  for (int b = lane; b < a.batch; b += 32) sum += span_of(a, b).units;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+__device__ __forceinline__ int64_t share_of(int64_t units, int warps) {
+  const int64_t s = (units + warps - 1) / warps;
+  return s > kMinUnits ? s : kMinUnits;
+}
+
+// A place among the units: unit i of head block hh (0 .. kv_heads *
+// head_blocks - 1) of sequence b.
+struct Place {
+  int b, hh, i;
+  Span s;
+};
+
+// The place of unit u < total (one warp).
+__device__ __forceinline__ Place place_of(const SwaPagedArgs& a, int heads, int64_t u, int lane) {
+  Place p;
+  int64_t before = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const int b = b0 + lane;
+    const int64_t mine = b < a.batch ? static_cast<int64_t>(span_of(a, b).units) * heads : 0;
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    const unsigned vote = __ballot_sync(0xffffffffu, u < before + sum);
+    if (vote || b0 + 32 >= a.batch) {
+      const int f = vote ? __ffs(vote) - 1 : 31;
+      p.b = min(b0 + f, a.batch - 1);
+      u -= before + __shfl_sync(0xffffffffu, sum - mine, f);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  p.s = span_of(a, p.b);
+  const int units = p.s.units > 0 ? p.s.units : 1;
+  p.hh = static_cast<int>(u / units);
+  p.i = static_cast<int>(u % units);
+  return p;
+}
+
+// The next unit after p; false behind the last.
+__device__ __forceinline__ void next_place(const SwaPagedArgs& a, int heads, Place& p) {
+  if (++p.i < p.s.units) return;
+  p.i = 0;
+  if (++p.hh < heads) return;
+  p.hh = 0;
+  do {
+    if (++p.b >= a.batch) return;
+    p.s = span_of(a, p.b);
+  } while (p.s.units == 0);
+}
+
+// ------------------------------------------------------------- primitives --
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Transposes an 8 x 8 matrix of 16-bit values held by a warp (lane 4 r + c:
+// row r, columns 2 c and 2 c + 1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                         int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Nibble k of both 16-bit halves of w as bf16 values 16 + u (the nibble in
+// mantissa bits 3 .. 6 of 16.0).
+template <int K>
+__device__ __forceinline__ uint32_t nibbles16(uint32_t w) {
+  const uint32_t s = K == 0 ? w << 3 : w >> (4 * K - 3);
+  return (s & 0x00780078u) | 0x41804180u;
+}
+
+// 16 + u -> u - 8 (exact).
+__device__ __forceinline__ uint32_t minus24(uint32_t x) {
+  const __nv_bfloat162 c = __floats2bfloat162_rn(-24.f, -24.f);
+  __nv_bfloat162 v = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&x), c);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y) {
+  __nv_bfloat162 v =
+      __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<__nv_bfloat162*>(&y));
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+// N consecutive words (N 1 .. 4) at 4 N-byte alignment (4-byte for N = 3).
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&r)[N], uint32_t a) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+  else
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = lds32(a + 4 * i);
+}
+
+// Row `r` (0 .. 15) of a 16-key tile of 4-bit rows stands for this key: the
+// order in which a lane's four value rows fall into different banks.
+__device__ __forceinline__ int key_of_row(int r) {
+  return ((r & 7) >> 1) + 4 * (r & 1) + (r & 8);
+}
+
+// ------------------------------------------------------------------ kernel --
+
+template <int D, int BITS, int NT>
+__global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
+    swa_paged_kernel(const __grid_constant__ PagedParams P) {
+  using C = Cfg<D, BITS>;
+  constexpr int NG = C::NG;
+  constexpr int MS = D / 16;  // 16-channel steps
+  const SwaPagedArgs& a = P.a;
+  extern __shared__ uint8_t smem_raw[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.x, h = blockIdx.y;
-  const int kvh = h / (a.heads / a.c.kv_heads);
-  int64_t n = a.lens[b];
-  if (n < 0 || n > a.c.table_pages * a.c.page_size) {
-    if (threadIdx.x == 0) record_error(a.status, PTB_ERR_ARG);
-    n = 0;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t ring = base + warp * C::kWarpBytes;
+  uint8_t* tail = smem_raw + (base - smem_addr(smem_raw)) + kWarps * C::kWarpBytes + warp * 64;
+  uint64_t* full = reinterpret_cast<uint64_t*>(tail);                     // [kStages]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(full + C::kStages);
+  volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(abort_flag + 1);  // [kStages]
+
+  if (lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) mbar_init(&full[s], 1);
+    *abort_flag = 0;
+    mbar_fence_init();
   }
-  float q[E], acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int c = lane + 32 * e;
-    q[e] = c < D ? __bfloat162float(a.q[b * a.q_sb + h * a.q_sh + c]) * a.scale_log2 : 0.f;
-    acc[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int64_t j = (n > a.window ? n - a.window : 0) + warp; j < n; j += kWarps) {
-    const uint8_t* page = kv_page(a.c, b, j);
-    if (!page) {
+  __syncwarp();
+
+  const int heads = a.c.kv_heads * P.head_blocks;
+  const int w = blockIdx.x * kWarps + warp;
+  // Sequences without keys: zeros; lengths out of range: recorded as well.
+  for (int b = w; b < a.batch; b += P.warps) {
+    const int n = a.lens[b];
+    if (n < 0 || n > (a.c.table_pages << a.c.page_shift))
       if (lane == 0) record_error(a.status, PTB_ERR_ARG);
-      continue;
-    }
-    const int off = static_cast<int>(j) & (a.c.page_size - 1);
-    const uint8_t* kb = page + kvh * a.c.block_bytes;
-    const uint8_t* vb = page + (a.c.kv_heads + kvh) * a.c.block_bytes;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = lane + 32 * e;
-      if (c < D) s = fmaf(q[e], cached<D>(a.c, kb, off, c, true), s);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float mx = fmaxf(m, s);
-    const float alpha = exp2f(m - mx), pr = exp2f(s - mx);
-    m = mx;
-    l = fmaf(l, alpha, pr);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = lane + 32 * e;
-      if (c < D) acc[e] = fmaf(acc[e], alpha, pr * cached<D>(a.c, vb, off, c, false));
-    }
+    if (span_of(a, b).units == 0)
+      for (int x = lane; x < a.heads * (D / 8); x += 32)
+        *reinterpret_cast<uint4*>(a.o + b * a.o_sb + (x / (D / 8)) * a.o_sh + x % (D / 8) * 8) =
+            make_uint4(0, 0, 0, 0);
   }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
+  const int64_t total = total_units(a, lane) * heads;
+  const int64_t share = share_of(total, P.warps);
+  const int64_t u0 = w * share, u1 = u0 + share < total ? u0 + share : total;
+  if (u0 >= u1) return;
+
+  const int page = a.c.page_size;
+  const int sub_keys = page < kBlockKeys ? page : kBlockKeys;  // keys that lie in one page
+  const int subs = kBlockKeys / sub_keys;                      // 1 or 2
+
+  // ------------------------------------------------------------ producer --
+  Place ld = place_of(a, heads, u0, lane);
+  Place at = ld;
+  int64_t loaded = u0;
+  int page_reg = -1, page_first = 0, page_left = 0;  // pages of the coming sub-blocks, one a lane
+  auto issue = [&](int stage) {
+    const int key0 = (ld.s.unit0 + ld.i) * kBlockKeys;
+    if (page_left == 0) {
+      page_first = key0;
+      const int64_t pos = static_cast<int64_t>(key0) + lane * sub_keys;
+      page_reg = -1;
+      if (pos < ld.s.n && pos + sub_keys > ld.s.lo)
+        page_reg = a.c.table[ld.b * a.c.table_stride + (pos >> a.c.page_shift)];
+      page_left = 32 / subs;
+    }
+    const int kvh = ld.hh / P.head_blocks;
+    uint32_t mask = 0;
+    int valid = 0, my_page = -1, my_sub = 0;
+    // Copies of a sub-block: bits 4: key codes, key pairs, value codes, value
+    // pairs; bits 16: the 64-channel column blocks of keys, then of values.
+    constexpr int kCopies = BITS == 4 ? 4 : 2 * C::kAtoms;
+    for (int s = 0; s < subs; ++s) {
+      const int pos = key0 + s * sub_keys;
+      const int pg = __shfl_sync(0xffffffffu, page_reg, (pos - page_first) / sub_keys);
+      const int from = max(ld.s.lo - pos, 0), to = min(ld.s.n - pos, sub_keys);
+      if (from >= to) continue;
+      if (pg < 0 || pg >= a.c.pages) {
+        if (lane == 0) record_error(a.status, PTB_ERR_ARG);
+        continue;
+      }
+      const uint32_t upto = to == 32 ? 0xffffffffu : (1u << to) - 1u;
+      mask |= (upto & ~((1u << from) - 1u)) << (s * sub_keys);
+      ++valid;
+      if (lane / kCopies == s) my_page = pg, my_sub = s;
+    }
+    const uint32_t dst = ring + stage * C::kStageBytes;
+    __syncwarp();  // the stage has been read by every lane
+    if (lane == 0) {
+      masks[stage] = mask;
+      if (valid)
+        mbar_arrive_expect_tx(&full[stage], valid * (C::kStageBytes / subs));
+      else
+        mbar_arrive(&full[stage]);
+    }
+    __syncwarp();
+    if (my_page >= 0) {
+      const int what = lane % kCopies;
+      const int off = (key0 + my_sub * sub_keys) & (page - 1);
+      if constexpr (BITS == 4) {
+        const int side = what >> 1;
+        const uint8_t* block = a.c.base + my_page * a.c.page_bytes +
+                               (side * a.c.kv_heads + kvh) * a.c.block_bytes;
+        if (what & 1)
+          bulk_load(dst + side * C::kSideBytes + C::kCodeBytes + my_sub * sub_keys * (D / 8),
+                    block + page * (D / 2) + off * (D / 8), sub_keys * (D / 8), &full[stage]);
+        else
+          bulk_load(dst + side * C::kSideBytes + my_sub * sub_keys * (D / 2),
+                    block + off * (D / 2), sub_keys * (D / 2), &full[stage]);
+      } else {
+        const int side = what / C::kAtoms, atom = what % C::kAtoms;
+        tma_rows(dst + side * C::kSideBytes + atom * kBlockKeys * 128 + my_sub * sub_keys * 128,
+                 &P.map, &full[stage], atom * 64, (side * a.c.kv_heads + kvh) * page + off, my_page);
+      }
+    }
+    --page_left;
+    ++loaded;
+    const int was_b = ld.b, was_hh = ld.hh;
+    next_place(a, heads, ld);
+    if (ld.b != was_b || ld.hh != was_hh) page_left = 0;
+  };
+
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    if (lane + 32 * e < D) so[warp][lane + 32 * e] = acc[e];
-  __syncthreads();
-  float mx = -INFINITY, total = 0.f;
-  for (int w = 0; w < kWarps; ++w)
-    if (sl[w] != 0.f) mx = fmaxf(mx, sm[w]);
-  for (int w = 0; w < kWarps; ++w)
-    if (sl[w] != 0.f) total += sl[w] * exp2f(sm[w] - mx);
-  for (int c = threadIdx.x; c < D; c += kWarps * 32) {
-    float o = 0.f;
-    for (int w = 0; w < kWarps; ++w)
-      if (sl[w] != 0.f) o += so[w][c] * exp2f(sm[w] - mx);
-    a.o[b * a.o_sb + h * a.o_sh + c] = __float2bfloat16_rn(total != 0.f ? o / total : 0.f);
+  for (int s = 0; s < C::kStages; ++s)
+    if (loaded < u1) issue(s);
+
+  // ------------------------------------------------------------ consumer --
+  int64_t u = u0;
+  int stage = 0;
+  uint32_t parity = 0;
+  bool ok = true;
+  while (u < u1 && ok) {
+    // ---- one segment: units at.i .. of (sequence, kv head, head block)
+    const int first = at.i;
+    const int kvh = at.hh / P.head_blocks;
+    const int head0 = kvh * P.group + (at.hh % P.head_blocks) * 8 * NT;  // first query head
+    const int nheads = min(8 * NT, (kvh + 1) * P.group - head0);
+    const int64_t left = u1 - u;
+    const int count = static_cast<int>(left < at.s.units - first ? left : at.s.units - first);
+
+    // Queries as B fragments (column = head g): for 16 bits channels 16 s + 2 t,
+    // + 1 and + 8, + 9; for 4 bits in the order of the codes.
+    uint32_t qf[NT][MS][2];
+    uint32_t qs[NT][2];  // Q_t: (-24 Q, Q) in two bf16 terms
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool live = nt * 8 + g < nheads;
+      const __nv_bfloat16* q = a.q + at.b * a.q_sb + (head0 + (live ? nt * 8 + g : 0)) * a.q_sh;
+      if constexpr (BITS == 16) {
+#pragma unroll
+        for (int s = 0; s < MS; ++s) {
+          qf[nt][s][0] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * t) : 0u;
+          qf[nt][s][1] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 8 + 2 * t) : 0u;
+        }
+      } else {
+        qs[nt][0] = qs[nt][1] = 0;
+#pragma unroll
+        for (int wq = 0; wq < NG; ++wq) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live) v = *reinterpret_cast<const uint4*>(q + 32 * wq + 8 * t);
+          qf[nt][2 * wq][0] = __byte_perm(v.x, v.z, 0x5410);      // channels 0, 4
+          qf[nt][2 * wq][1] = __byte_perm(v.x, v.z, 0x7632);      // 1, 5
+          qf[nt][2 * wq + 1][0] = __byte_perm(v.y, v.w, 0x5410);  // 2, 6
+          qf[nt][2 * wq + 1][1] = __byte_perm(v.y, v.w, 0x7632);  // 3, 7
+          float sum = (bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y)) +
+                      (bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w));
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          const uint32_t hi = pack_bf16x2(-24.f * sum, sum);
+          if (t == wq) {
+            qs[nt][0] = hi;
+            qs[nt][1] = pack_bf16x2(-24.f * sum - bf16_lo(hi), sum - bf16_hi(hi));
+          }
+        }
+      }
+    }
+
+    float o[NT][MS][4];
+    float oc[NT][4];  // sum_j p_j centre_j of group g (4 bits)
+    float m_ref[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int s = 0; s < MS; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][s][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) oc[nt][e] = 0.f;
+      m_ref[nt][0] = m_ref[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    for (int blk = 0; blk < count; ++blk) {
+      if (!mbar_wait_warp(&full[stage], parity, abort_flag, a.status)) {
+        ok = false;
+        break;
+      }
+      const uint32_t keys = ring + stage * C::kStageBytes;
+      const uint32_t vals = keys + C::kSideBytes;
+      const uint32_t mask = masks[stage];
+
+      // ---- scores of the unit's two 16-key tiles: s[tile][nt]: keys g (0, 1)
+      // and g + 8 (2, 3), heads 2 t (0, 2) and 2 t + 1 (1, 3)
+      float s[2][NT][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[h][nt][e] = 0.f;
+        if constexpr (BITS == 16) {
+          const int row = 16 * h + (lane & 15);
+#pragma unroll
+          for (int m = 0; m < MS; ++m) {
+            const int chunk = (m % 4) * 2 + (lane >> 4);
+            uint32_t f[4];
+            ldmatrix4(f, keys + (m / 4) * kBlockKeys * 128 + row * 128 + ((chunk ^ (row & 7)) << 4));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_bf16(s[h][nt], f[0], f[1], f[2], f[3], qf[nt][m][0], qf[nt][m][1]);
+          }
+        } else {
+          const int ka = 16 * h + key_of_row(g), kb = ka + 8;
+          const uint32_t pairs = keys + C::kCodeBytes;
+          uint32_t ca[NG], cb[NG], pa[NG], pb[NG];
+          lds_words<NG>(ca, keys + ka * (D / 2) + t * 4 * NG);
+          lds_words<NG>(cb, keys + kb * (D / 2) + t * 4 * NG);
+          lds_words<NG>(pa, pairs + ka * (D / 8));
+          lds_words<NG>(pb, pairs + kb * (D / 8));
+          const uint32_t wa = t < NG ? lds32(pairs + ka * (D / 8) + 4 * (t < NG ? t : 0)) : 0u;
+          const uint32_t wb = t < NG ? lds32(pairs + kb * (D / 8) + 4 * (t < NG ? t : 0)) : 0u;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_bf16(s[h][nt], wa, wb, wa, wb, qs[nt][0], qs[nt][1]);
+#pragma unroll
+          for (int wq = 0; wq < NG; ++wq) {
+            const uint32_t a0 = nibbles16<0>(ca[wq]), a2 = nibbles16<1>(ca[wq]);
+            const uint32_t a4 = nibbles16<2>(ca[wq]), a6 = nibbles16<3>(ca[wq]);
+            const uint32_t b0 = nibbles16<0>(cb[wq]), b2 = nibbles16<1>(cb[wq]);
+            const uint32_t b4 = nibbles16<2>(cb[wq]), b6 = nibbles16<3>(cb[wq]);
+            const float sa = bf16_lo(pa[wq]), sb = bf16_lo(pb[wq]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float acc[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_bf16(acc, a0, b0, a2, b2, qf[nt][2 * wq][0], qf[nt][2 * wq][1]);
+              mma_bf16(acc, a4, b4, a6, b6, qf[nt][2 * wq + 1][0], qf[nt][2 * wq + 1][1]);
+              s[h][nt][0] = fmaf(sa, acc[0], s[h][nt][0]);
+              s[h][nt][1] = fmaf(sa, acc[1], s[h][nt][1]);
+              s[h][nt][2] = fmaf(sb, acc[2], s[h][nt][2]);
+              s[h][nt][3] = fmaf(sb, acc[3], s[h][nt][3]);
+            }
+          }
+        }
+      }
+      if (mask != 0xffffffffu) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ra = BITS == 16 ? g : key_of_row(g);
+          const bool va = (mask >> (16 * h + ra)) & 1u, vb = (mask >> (16 * h + ra + 8)) & 1u;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            s[h][nt][0] = va ? s[h][nt][0] : -INFINITY;
+            s[h][nt][1] = va ? s[h][nt][1] : -INFINITY;
+            s[h][nt][2] = vb ? s[h][nt][2] : -INFINITY;
+            s[h][nt][3] = vb ? s[h][nt][3] : -INFINITY;
+          }
+        }
+      }
+
+      // ---- weights.  The reference max of a head is the same in all lanes
+      // and is raised only when a score passes it by more than 2^8.
+      uint32_t pf[2][NT][2];  // P^T fragments: column = head g, rows keys 2 t, 2 t + 1 / + 8
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float mx[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          mx[e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2])) *
+                  a.scale_log2;
+        if (__any_sync(0xffffffffu, mx[0] > m_ref[nt][0] + kRescaleLog2 ||
+                                        mx[1] > m_ref[nt][1] + kRescaleLog2)) {
+          float alpha[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1)
+              mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], x));
+            const float m = fmaxf(m_ref[nt][e], mx[e]);
+            alpha[e] = m == -INFINITY ? 1.f : fast_exp2(m_ref[nt][e] - m);
+            m_ref[nt][e] = m;
+            l[nt][e] *= alpha[e];
+          }
+#pragma unroll
+          for (int m = 0; m < MS; ++m) {
+            o[nt][m][0] *= alpha[0];
+            o[nt][m][1] *= alpha[1];
+            o[nt][m][2] *= alpha[0];
+            o[nt][m][3] *= alpha[1];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) oc[nt][e] *= alpha[e & 1];
+        }
+        const float m0 = m_ref[nt][0] == -INFINITY ? 0.f : m_ref[nt][0];
+        const float m1 = m_ref[nt][1] == -INFINITY ? 0.f : m_ref[nt][1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            p[e] = fast_exp2(fmaf(s[h][nt][e], a.scale_log2, (e & 1) ? -m1 : -m0));
+          l[nt][0] += p[0] + p[2];
+          l[nt][1] += p[1] + p[3];
+          pf[h][nt][0] = transpose8x8(pack_bf16x2(p[0], p[1]));
+          pf[h][nt][1] = transpose8x8(pack_bf16x2(p[2], p[3]));
+        }
+      }
+
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (BITS == 16) {
+          const int row = 16 * h + (lane & 7) + ((lane >> 4) << 3);
+          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+          if (mask != 0xffffffffu) {
+            const uint32_t bits = mask >> (16 * h + 2 * t);
+            keep0 = ((bits & 1u) ? 0xffffu : 0u) | ((bits & 2u) ? 0xffff0000u : 0u);
+            keep1 = ((bits & 256u) ? 0xffffu : 0u) | ((bits & 512u) ? 0xffff0000u : 0u);
+          }
+#pragma unroll
+          for (int m = 0; m < MS; ++m) {
+            const int chunk = (m % 4) * 2 + ((lane >> 3) & 1);
+            uint32_t f[4];
+            ldmatrix4_trans(f, vals + (m / 4) * kBlockKeys * 128 + row * 128 +
+                                   ((chunk ^ (row & 7)) << 4));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_bf16(o[nt][m], f[0] & keep0, f[1] & keep0, f[2] & keep1, f[3] & keep1,
+                       pf[h][nt][0], pf[h][nt][1]);
+          }
+        } else {
+          // Rows of this lane: keys t, t + 4 (first half), t + 8, t + 12.
+          const uint32_t pairs = vals + C::kCodeBytes;
+          uint32_t pr[4][NG], cw[4];  // pairs of the four keys; the pair of group g
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = 16 * h + t + 4 * x;
+            lds_words<NG>(pr[x], pairs + key * (D / 8));
+            cw[x] = lds32(pairs + key * (D / 8) + 4 * (g < NG ? g : 0));
+          }
+          if (mask != 0xffffffffu) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t keep = ((mask >> (16 * h + t + 4 * x)) & 1u) ? 0xffffffffu : 0u;
+#pragma unroll
+              for (int wv = 0; wv < NG; ++wv) pr[x][wv] &= keep;
+              cw[x] &= keep;
+            }
+          }
+          // Centres: row g of the product is group g (rows from NG on repeat group 0).
+          const uint32_t c0 = __byte_perm(cw[0], cw[1], 0x7632);
+          const uint32_t c1 = __byte_perm(cw[2], cw[3], 0x7632);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_bf16(oc[nt], c0, 0u, c1, 0u, pf[h][nt][0], pf[h][nt][1]);
+          // Codes: half-word w of this lane's NG holds channels 32 w + 4 g .. + 3.
+          uint32_t cv[4][(NG + 1) / 2];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t row = vals + (16 * h + t + 4 * x) * (D / 2) + g * 2 * NG;
+            if constexpr (NG % 2 == 0) {
+              lds_words<NG / 2>(cv[x], row);
+            } else {
+#pragma unroll
+              for (int wv = 0; wv < NG; ++wv) {
+                const uint32_t hw = lds16(row + 2 * wv);
+                if (wv & 1)
+                  cv[x][wv / 2] |= hw << 16;
+                else
+                  cv[x][wv / 2] = hw;
+              }
+            }
+          }
+#pragma unroll
+          for (int wv = 0; wv < NG; ++wv) {
+            const uint32_t sel = (wv & 1) ? 0x7632u : 0x5410u;
+            const uint32_t v0 = __byte_perm(cv[0][wv / 2], cv[1][wv / 2], sel);
+            const uint32_t v1 = __byte_perm(cv[2][wv / 2], cv[3][wv / 2], sel);
+            const uint32_t s0 = __byte_perm(pr[0][wv], pr[1][wv], 0x5410);
+            const uint32_t s1 = __byte_perm(pr[2][wv], pr[3][wv], 0x5410);
+            const uint32_t e0 = minus24(nibbles16<0>(v0)), e1 = minus24(nibbles16<1>(v0));
+            const uint32_t e2 = minus24(nibbles16<2>(v0)), e3 = minus24(nibbles16<3>(v0));
+            const uint32_t f0 = minus24(nibbles16<0>(v1)), f1 = minus24(nibbles16<1>(v1));
+            const uint32_t f2 = minus24(nibbles16<2>(v1)), f3 = minus24(nibbles16<3>(v1));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint32_t b0 = mul2(pf[h][nt][0], s0), b1 = mul2(pf[h][nt][1], s1);
+              mma_bf16(o[nt][2 * wv], e0, e1, f0, f1, b0, b1);
+              mma_bf16(o[nt][2 * wv + 1], e2, e3, f2, f3, b0, b1);
+            }
+          }
+        }
+      }
+
+      // ---- refill the stage
+      if (loaded < u1) issue(stage);
+      if (++stage == C::kStages) {
+        stage = 0;
+        parity ^= 1u;
+      }
+    }
+    if (!ok) break;
+
+    // ---- end of the segment
+    const bool whole = first == 0 && count == at.s.units;
+    const int64_t slot = 2ll * w + (first > 0 ? 0 : 1);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
+      if constexpr (BITS == 4) {
+        // The centres' sums of group w lie in lanes 4 w + t.
+#pragma unroll
+        for (int wv = 0; wv < NG; ++wv) {
+          const float z0 = __shfl_sync(0xffffffffu, oc[nt][0], 4 * wv + t);
+          const float z1 = __shfl_sync(0xffffffffu, oc[nt][1], 4 * wv + t);
+#pragma unroll
+          for (int m = 2 * wv; m < 2 * wv + 2; ++m) {
+            o[nt][m][0] += z0;
+            o[nt][m][1] += z1;
+            o[nt][m][2] += z0;
+            o[nt][m][3] += z1;
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int head = nt * 8 + 2 * t + e;
+        if (head >= nheads) continue;
+        if (whole) {
+          const float inv = l[nt][e] != 0.f ? 1.f / l[nt][e] : 0.f;
+          __nv_bfloat16* out = a.o + at.b * a.o_sb + (head0 + head) * a.o_sh;
+          if constexpr (BITS == 16) {
+#pragma unroll
+            for (int m = 0; m < MS; ++m) {
+              out[16 * m + g] = __float2bfloat16_rn(o[nt][m][e] * inv);
+              out[16 * m + 8 + g] = __float2bfloat16_rn(o[nt][m][e + 2] * inv);
+            }
+          } else {
+#pragma unroll
+            for (int wv = 0; wv < NG; ++wv)
+              *reinterpret_cast<uint2*>(out + 32 * wv + 4 * g) = make_uint2(
+                  pack_bf16x2(o[nt][2 * wv][e] * inv, o[nt][2 * wv][e + 2] * inv),
+                  pack_bf16x2(o[nt][2 * wv + 1][e] * inv, o[nt][2 * wv + 1][e + 2] * inv));
+          }
+        } else {
+          if (g == 0) {
+            P.part_ml[(slot * 2) * (8 * NT) + head] = m_ref[nt][e];
+            P.part_ml[(slot * 2 + 1) * (8 * NT) + head] = l[nt][e];
+          }
+          float* out = P.part_o + (slot * (8 * NT) + head) * D;
+          if constexpr (BITS == 16) {
+#pragma unroll
+            for (int m = 0; m < MS; ++m) {
+              out[16 * m + g] = o[nt][m][e];
+              out[16 * m + 8 + g] = o[nt][m][e + 2];
+            }
+          } else {
+#pragma unroll
+            for (int wv = 0; wv < NG; ++wv)
+              *reinterpret_cast<float4*>(out + 32 * wv + 4 * g) =
+                  make_float4(o[nt][2 * wv][e], o[nt][2 * wv][e + 2], o[nt][2 * wv + 1][e],
+                              o[nt][2 * wv + 1][e + 2]);
+          }
+        }
+      }
+    }
+    u += count;
+    at.i += count - 1;
+    if (u < u1) next_place(a, heads, at);
+  }
+  if (!ok) {
+    // Let this warp's copies land before the block goes away.
+    volatile int no_abort = 0;
+    const int64_t flight = loaded - u;
+    for (int64_t n = 0; n < flight && n < C::kStages; ++n) {
+      mbar_wait_warp(&full[stage], parity, &no_abort, a.status);
+      if (++stage == C::kStages) {
+        stage = 0;
+        parity ^= 1u;
+      }
+    }
   }
 }
 
-template <int D>
-cudaError_t launch_typed(const SwaPagedArgs& a, cudaStream_t stream) {
-  swa_paged_kernel<D><<<dim3(a.batch, a.heads), kWarps * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+// Joins the shares of the segments that were cut.  Block w looks at the
+// boundary between shares w - 1 and w: where it falls inside a segment of n
+// shares, the n - 1 boundary blocks split the segment's (head, 32-channel)
+// outputs among them.  Warps take every eighth share; their sums are joined
+// in shared memory in order.
+template <int NT>
+__global__ void __launch_bounds__(kJoinThreads) swa_paged_join_kernel(const PagedParams P, int d) {
+  const SwaPagedArgs& a = P.a;
+  __shared__ float so[kJoinThreads / 32][32];
+  __shared__ float sl[kJoinThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int heads = a.c.kv_heads * P.head_blocks;
+  const int64_t total = total_units(a, lane) * heads;
+  const int64_t share = share_of(total, P.warps);
+  const int64_t u = (blockIdx.x + 1) * share;
+  Place p = {};
+  if (u < total) p = place_of(a, heads, u, lane);
+  // Every block waits, so that this kernel ends after the one before it.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (u >= total || p.i == 0) return;
+  const int64_t f0 = u - p.i, f1 = f0 + p.s.units;
+  const int64_t w0 = f0 / share, w1 = (f1 - 1) / share;
+  const int n = static_cast<int>(w1 - w0 + 1);             // shares of the segment
+  const int me = static_cast<int>(blockIdx.x + 1 - w0 - 1);  // this boundary among n - 1
+  const int kvh = p.hh / P.head_blocks;
+  const int head0 = kvh * P.group + (p.hh % P.head_blocks) * 8 * NT;
+  const int nheads = min(8 * NT, (kvh + 1) * P.group - head0);
+  const int chunks = (d + 31) / 32;
+  for (int task = me; task < nheads * chunks; task += n - 1) {
+    const int head = task / chunks, c = (task % chunks) * 32 + lane;
+    float mx = -INFINITY;
+    for (int x = lane; x < n; x += 32) {
+      const int64_t slot = 2 * (w0 + x) + (x == 0 ? 1 : 0);
+      mx = fmaxf(mx, P.part_ml[(slot * 2) * (8 * NT) + head]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float acc = 0.f, l = 0.f;
+#pragma unroll 4
+    for (int x = warp; x < n; x += kJoinThreads / 32) {
+      const int64_t slot = 2 * (w0 + x) + (x == 0 ? 1 : 0);
+      const float f = exp2f(P.part_ml[(slot * 2) * (8 * NT) + head] - ref);
+      l = fmaf(f, P.part_ml[(slot * 2 + 1) * (8 * NT) + head], l);
+      if (c < d) acc = fmaf(f, P.part_o[(slot * (8 * NT) + head) * d + c], acc);
+    }
+    so[warp][lane] = acc;
+    if (lane == 0) sl[warp] = l;
+    __syncthreads();
+    if (warp == 0) {
+      float o = 0.f, sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < kJoinThreads / 32; ++x) {
+        o += so[x][lane];
+        sum += sl[x];
+      }
+      if (c < d)
+        a.o[p.b * a.o_sb + (head0 + head) * a.o_sh + c] =
+            __float2bfloat16_rn(sum != 0.f ? o / sum : 0.f);
+    }
+    __syncthreads();
+  }
+}
+
+int head_tiles(int group) { return group > 8 ? 2 : 1; }
+
+template <int D, int BITS, int NT>
+cudaError_t launch_typed(PagedParams& prm, cudaStream_t stream) {
+  using C = Cfg<D, BITS>;
+  auto kern = swa_paged_kernel<D, BITS, NT>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const int grid = prm.a.sms * C::kBlocksPerSm;
+  prm.warps = grid * kWarps;
+  kern<<<grid, kWarps * 32, C::kSmemBytes, stream>>>(prm);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(prm.warps - 1);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  // Finds its shares while the first kernel still runs, then waits for it.
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, swa_paged_join_kernel<NT>, static_cast<const PagedParams&>(prm), D);
+}
+
+template <int D, int BITS>
+cudaError_t launch_nt(PagedParams& prm, cudaStream_t stream) {
+  return head_tiles(prm.group) == 1 ? launch_typed<D, BITS, 1>(prm, stream)
+                                    : launch_typed<D, BITS, 2>(prm, stream);
+}
+
+template <int BITS>
+cudaError_t launch_d(PagedParams& prm, cudaStream_t stream) {
+  switch (prm.a.c.head_dim) {
+    case 32: return launch_nt<32, BITS>(prm, stream);
+    case 64: return launch_nt<64, BITS>(prm, stream);
+    case 96: return launch_nt<96, BITS>(prm, stream);
+    case 128: return launch_nt<128, BITS>(prm, stream);
+    default: break;
+  }
+  if constexpr (BITS == 16)
+    if (prm.a.c.head_dim == 16) return launch_nt<16, BITS>(prm, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t swa_paged_workspace(int, int, int, int, int) { return 0; }
+// Two cut segments a warp: (maximum, sum) and the output of up to 8 NT heads.
+size_t swa_paged_workspace(int, int heads, int kv_heads, int head_dim, int sms) {
+  const size_t rows = 2ull * sms * kMaxWarpsPerSm * 8 * head_tiles(heads / kv_heads);
+  return rows * (2 + head_dim) * sizeof(float);
+}
 
 cudaError_t launch_swa_paged(const SwaPagedArgs& a, cudaStream_t stream) {
-  switch (a.c.head_dim) {
-    case 16: return launch_typed<16>(a, stream);
-    case 32: return launch_typed<32>(a, stream);
-    case 64: return launch_typed<64>(a, stream);
-    case 96: return launch_typed<96>(a, stream);
-    case 128: return launch_typed<128>(a, stream);
-  }
-  return cudaErrorInvalidValue;
+  PagedParams prm;
+  prm.a = a;
+  prm.group = a.heads / a.c.kv_heads;
+  const int tile = 8 * head_tiles(prm.group);
+  prm.head_blocks = (prm.group + tile - 1) / tile;
+  const size_t slots = 2ull * a.sms * kMaxWarpsPerSm;
+  prm.part_o = static_cast<float*>(a.workspace);
+  prm.part_ml = prm.part_o + slots * tile * a.c.head_dim;
+  if (a.c.bits == 4) return launch_d<4>(prm, stream);
+  const int sub = a.c.page_size < kBlockKeys ? a.c.page_size : kBlockKeys;
+  const uint64_t row = 2ull * a.c.head_dim;
+  const uint64_t dims[3] = {static_cast<uint64_t>(a.c.head_dim), a.c.page_bytes / row,
+                            static_cast<uint64_t>(a.c.pages)};
+  const uint64_t strides[2] = {row, static_cast<uint64_t>(a.c.page_bytes)};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(sub), 1};
+  if (!make_tensor_map(&prm.map, reinterpret_cast<const __nv_bfloat16*>(a.c.base), 3, dims, strides,
+                       box))
+    return cudaErrorInvalidValue;
+  return launch_d<16>(prm, stream);
 }
 
 }  // namespace ptb
