@@ -12,6 +12,7 @@ loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -345,6 +346,7 @@ def swa_attention_counts(q, k, v, window: int, scale: float = 0.0, stream=None):
 
 # ---------------------------------------------------------------- serving --
 
+@functools.lru_cache(maxsize=None)
 def kv_page_size(kv_heads: int, page_size: int, head_dim: int, bits: int) -> int:
     """Bytes of one page of a key/value cache: `page_size` token rows of the keys and the values of
     `kv_heads` heads in bf16 (bits 16) or 4 bits.  A cache is a uint8 CUDA tensor
@@ -356,69 +358,97 @@ def kv_page_size(kv_heads: int, page_size: int, head_dim: int, bits: int) -> int
     return n
 
 
-def _on_device(name: str, t, dtype) -> None:
+def _refuse(name: str, t, dtype) -> None:
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a {str(dtype).replace('torch.', '')} CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is not on the current device")
+    raise ValueError(f"{name} is not on the current device")
 
 
-def _heads_view(name: str, t, shape=None) -> list:
+# The checks below run once per tensor of every call of the serving operators, whose kernels take a
+# few microseconds at the smallest sizes; they touch each attribute once.
+
+def _tensor(name: str, t, dtype, dev: int):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(name, t, dtype)
+    return t
+
+
+def _heads_view(name: str, t, dev: int, shape=None) -> tuple:
     """[tokens, heads, d] with a contiguous last dimension -> pointer and two strides."""
-    _on_device(name, t, torch.bfloat16)
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
-        raise ValueError(f"{name} must be [tokens, heads, head_dim] with a contiguous last dimension")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    _tensor(name, t, torch.bfloat16, dev)
+    size = t.shape
+    if len(size) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(size)}")
+    st, sh, sd = t.stride()
+    if sd != 1 and size[2] != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
     # The stride of a dimension of one entry is never used.
-    return [_ptr(t), t.stride(0) if t.shape[0] > 1 else max(8, t.stride(0) // 8 * 8),
-            t.stride(1) if t.shape[1] > 1 else max(8, t.stride(1) // 8 * 8)]
+    if size[0] <= 1:
+        st = 8
+    if size[1] <= 1:
+        sh = 8
+    return t.data_ptr(), st, sh
 
 
-def _int_vector(name: str, t, n: int) -> int:
-    _on_device(name, t, torch.int32)
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+def _int_vector(name: str, t, n: int, dev: int) -> int:
+    _tensor(name, t, torch.int32, dev)
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries")
-    return _ptr(t)
+    return t.data_ptr()
 
 
-def _offsets(name: str, t) -> int:
-    """The number of sequences that cu_seqlens speaks of."""
-    _on_device(name, t, torch.int32)
-    if t.dim() != 1 or t.shape[0] < 2:
-        raise ValueError(f"{name} must be an int32 vector of at least 2 entries")
-    return t.shape[0] - 1
+def _offsets(name: str, t, dev: int) -> tuple:
+    """The number of sequences that cu_seqlens speaks of, and its pointer."""
+    _tensor(name, t, torch.int32, dev)
+    if t.dim() != 1 or t.shape[0] < 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector of at least 2 entries")
+    return t.shape[0] - 1, t.data_ptr()
 
 
 def _cache_args(cache, page_table, batch: int, kv_heads: int, head_dim: int, page_size: int,
-                bits: int) -> list:
-    _on_device("cache", cache, torch.uint8)
-    _on_device("page_table", page_table, torch.int32)
+                bits: int, dev: int) -> tuple:
+    _tensor("cache", cache, torch.uint8, dev)
+    _tensor("page_table", page_table, torch.int32, dev)
     n = kv_page_size(kv_heads, page_size, head_dim, bits)
     if cache.dim() != 2 or cache.shape[1] != n or not cache.is_contiguous():
         raise ValueError(f"cache must be contiguous [pages, {n}]")
-    if (page_table.dim() != 2 or page_table.shape[0] != batch
-            or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+    size = page_table.shape
+    if len(size) != 2 or size[0] != batch or (size[1] > 1 and page_table.stride(1) != 1):
         raise ValueError(f"page_table must be [{batch}, pages of a sequence], rows contiguous")
-    stride = page_table.stride(0) if batch > 1 else page_table.shape[1]
-    return [_ptr(cache), cache.shape[0], _ptr(page_table), stride, page_table.shape[1]]
+    stride = page_table.stride(0) if batch > 1 else size[1]
+    return cache.data_ptr(), cache.shape[0], page_table.data_ptr(), stride, size[1]
 
 
-def _new(stream, *shape, dtype=torch.bfloat16):
-    """A tensor of the stream that is going to write it."""
+def _launch_on(stream, t) -> tuple:
+    """The current device, and the stream of the launch as an integer; t is the call's main tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("the tensors must be CUDA tensors")
+    dev = torch.cuda.current_device()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device="cuda")
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, stream.cuda_stream
+
+
+def _new(like, shape, stream, dtype=torch.bfloat16):
+    """A tensor that belongs to the stream that is going to write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device="cuda")
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _scratch(need: int, workspace, stream):
+def _scratch(need: int, workspace, like, stream) -> tuple:
     """(tensor that has to outlive the launch, pointer, bytes)"""
     if workspace is None:
-        workspace = _new(stream, max(need, 1), dtype=torch.uint8)
+        if need == 0:
+            return None, None, 0
+        workspace = _new(like, (need,), stream, torch.uint8)
+        return workspace, workspace.data_ptr(), need
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def kv_append(q, k, v, cache, page_table, cu_seqlens, past, page_size: int, bits: int, cos=None,
@@ -431,40 +461,42 @@ def kv_append(q, k, v, cache, page_table, cu_seqlens, past, page_size: int, bits
     [positions, rot_dim / 2].  Returns (q_out, k_out), the rotated q and k: new tensors, or the
     given ones (q and k themselves for in-place rotation); k_out is None without keep_keys."""
     lib = load()
-    batch = _offsets("cu_seqlens", cu_seqlens)
-    kv = _heads_view("k", k)
+    dev, raw = _launch_on(stream, k)
+    batch, cu = _offsets("cu_seqlens", cu_seqlens, dev)
+    kv = _heads_view("k", k, dev) + _heads_view("v", v, dev, k.shape)
     tokens, kv_heads, d = k.shape
-    kv += _heads_view("v", v, k.shape)
-    heads, qa, qo, ko = 0, [None, 8, 8], [None, 8, 8], [None, 8, 8]
+    heads, qa, qo, ko = 0, (None, 8, 8), (None, 8, 8), (None, 8, 8)
     if q is not None:
-        qa = _heads_view("q", q)
+        qa = _heads_view("q", q, dev)
         heads = q.shape[1]
         if q.shape[0] != tokens or q.shape[2] != d:
             raise ValueError("q must be [tokens, heads, head_dim] of k's tokens and head_dim")
         if q_out is None:
-            q_out = _new(stream, *q.shape)
-        qo = _heads_view("q_out", q_out, q.shape)
+            q_out = _new(q, q.shape, stream)
+        qo = _heads_view("q_out", q_out, dev, q.shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k_out is None and keep_keys:
-        k_out = _new(stream, *k.shape)
+        k_out = _new(k, k.shape, stream)
     if k_out is not None:
-        ko = _heads_view("k_out", k_out, k.shape)
-    rot, positions = 0, 0
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin go together")
-    if cos is not None:
-        for n, t in (("cos", cos), ("sin", sin)):
-            _on_device(n, t, torch.float32)
-            if t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous():
-                raise ValueError("cos and sin must be contiguous [positions, rot_dim / 2]")
+        ko = _heads_view("k_out", k_out, dev, k.shape)
+    rot, positions, cp, sp = 0, 0, None, None
+    if cos is not None or sin is not None:
+        if cos is None or sin is None:
+            raise ValueError("cos and sin go together")
+        _tensor("cos", cos, torch.float32, dev)
+        _tensor("sin", sin, torch.float32, dev)
+        if cos.dim() != 2 or sin.shape != cos.shape or not (cos.is_contiguous()
+                                                            and sin.is_contiguous()):
+            raise ValueError("cos and sin must be contiguous [positions, rot_dim / 2]")
         positions, rot = cos.shape[0], 2 * cos.shape[1]
-    ca = _cache_args(cache, page_table, batch, kv_heads, d, page_size, bits)
-    st = lib.ptb_kv_append(*qa, *kv, _ptr(cos), _ptr(sin), positions, rot, int(interleaved),
-                           _int_vector("cu_seqlens", cu_seqlens, batch + 1),
-                           _int_vector("past", past, batch), batch, tokens, heads, kv_heads, d,
-                           *qo, *ko, *ca, page_size, bits, _stream(stream))
-    _check(st, "ptb_kv_append")
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    st = lib.ptb_kv_append(*qa, *kv, cp, sp, positions, rot, int(interleaved), cu,
+                           _int_vector("past", past, batch, dev), batch, tokens, heads, kv_heads,
+                           d, *qo, *ko, *_cache_args(cache, page_table, batch, kv_heads, d,
+                                                     page_size, bits, dev), page_size, bits, raw)
+    if st:
+        _check(st, "ptb_kv_append")
     return q_out, k_out
 
 
@@ -473,16 +505,19 @@ def kv_gather(cache, page_table, cu_seqlens, start, tokens: int, kv_heads: int, 
     """Reads cached rows back as bf16: row cu_seqlens[b] + i of the returned k and v
     [tokens, kv_heads, d] is position start[b] + i of sequence b."""
     lib = load()
-    batch = _offsets("cu_seqlens", cu_seqlens)
-    shape = (tokens, kv_heads, head_dim)
-    k = _new(stream, *shape) if k is None else k
-    v = _new(stream, *shape) if v is None else v
-    st = lib.ptb_kv_gather(*_cache_args(cache, page_table, batch, kv_heads, head_dim, page_size, bits),
-                           _int_vector("cu_seqlens", cu_seqlens, batch + 1),
-                           _int_vector("start", start, batch), batch, tokens, kv_heads, head_dim,
-                           page_size, bits, *_heads_view("k", k, shape), *_heads_view("v", v, shape),
-                           _stream(stream))
-    _check(st, "ptb_kv_gather")
+    dev, raw = _launch_on(stream, cache)
+    batch, cu = _offsets("cu_seqlens", cu_seqlens, dev)
+    ca = _cache_args(cache, page_table, batch, kv_heads, head_dim, page_size, bits, dev)
+    shape = torch.Size((tokens, kv_heads, head_dim))
+    if k is None:
+        k = _new(cache, shape, stream, torch.bfloat16)
+    if v is None:
+        v = _new(cache, shape, stream, torch.bfloat16)
+    st = lib.ptb_kv_gather(*ca, cu, _int_vector("start", start, batch, dev), batch, tokens,
+                           kv_heads, head_dim, page_size, bits, *_heads_view("k", k, dev, shape),
+                           *_heads_view("v", v, dev, shape), raw)
+    if st:
+        _check(st, "ptb_kv_gather")
     return k, v
 
 
@@ -498,24 +533,29 @@ def swa_attention_packed(q, k, v, cu_seqlens, window: int, cu_seqlens_k=None, sc
     queries of a sequence are the last of its nk positions (cu_seqlens_k None: nk = nq).  Returns o
     like q; rows behind the last sequence are not written.  o may be q."""
     lib = load()
-    batch = _offsets("cu_seqlens", cu_seqlens)
-    qa = _heads_view("q", q)
-    ka = _heads_view("k", k)
-    va = _heads_view("v", v, k.shape)
-    if q.shape[2] != k.shape[2]:
+    dev, raw = _launch_on(stream, q)
+    batch, cu = _offsets("cu_seqlens", cu_seqlens, dev)
+    qa = _heads_view("q", q, dev)
+    ka = _heads_view("k", k, dev)
+    va = _heads_view("v", v, dev, k.shape)
+    tq, heads, d = q.shape
+    tk, kv_heads, dk = k.shape
+    if d != dk:
         raise ValueError("q and k must have the same head_dim")
-    if cu_seqlens_k is None and q.shape[0] != k.shape[0]:
+    cu_k = None
+    if cu_seqlens_k is not None:
+        cu_k = _int_vector("cu_seqlens_k", cu_seqlens_k, batch + 1, dev)
+    elif tq != tk:
         raise ValueError("q and k must have the same tokens, or cu_seqlens_k be given")
     if o is None:
-        o = _new(stream, *q.shape)
-    oa = _heads_view("o", o, q.shape)
-    cu_k = None if cu_seqlens_k is None else _int_vector("cu_seqlens_k", cu_seqlens_k, batch + 1)
-    ws, wp, wb = _scratch(lib.swa_attention_packed_workspace_size(batch, q.shape[0], q.shape[1],
-                                                                  k.shape[1]), workspace, stream)
-    st = lib.swa_attention_packed(*qa, *ka, *va, _int_vector("cu_seqlens", cu_seqlens, batch + 1),
-                                  cu_k, batch, q.shape[0], k.shape[0], q.shape[1], k.shape[1],
-                                  q.shape[2], window, scale, *oa, wp, wb, _stream(stream))
-    _check(st, "swa_attention_packed")
+        o = _new(q, q.shape, stream)
+    oa = _heads_view("o", o, dev, q.shape)
+    ws, wp, wb = _scratch(lib.swa_attention_packed_workspace_size(batch, tq, heads, kv_heads),
+                          workspace, q, stream)  # ws lives until the launch is queued
+    st = lib.swa_attention_packed(*qa, *ka, *va, cu, cu_k, batch, tq, tk, heads, kv_heads, d,
+                                  window, scale, *oa, wp, wb, raw)
+    if st:
+        _check(st, "swa_attention_packed")
     return o
 
 
@@ -528,17 +568,20 @@ def swa_attention_paged(q, cache, page_table, seq_lens, kv_heads: int, page_size
     """Attention of one new token per sequence over the paged cache: q [B, heads, d] bf16 against
     the last min(seq_lens[b], window) positions of sequence b.  Returns o like q; o may be q."""
     lib = load()
-    qa = _heads_view("q", q)
+    dev, raw = _launch_on(stream, q)
+    qa = _heads_view("q", q, dev)
     batch, heads, d = q.shape
     if o is None:
-        o = _new(stream, *q.shape)
-    oa = _heads_view("o", o, q.shape)
+        o = _new(q, q.shape, stream)
+    oa = _heads_view("o", o, dev, q.shape)
     ws, wp, wb = _scratch(lib.swa_attention_paged_workspace_size(batch, heads, kv_heads, d),
-                          workspace, stream)
-    st = lib.swa_attention_paged(*qa, *_cache_args(cache, page_table, batch, kv_heads, d, page_size, bits),
-                                 _int_vector("seq_lens", seq_lens, batch), batch, heads, kv_heads,
-                                 d, page_size, bits, window, scale, *oa, wp, wb, _stream(stream))
-    _check(st, "swa_attention_paged")
+                          workspace, q, stream)
+    st = lib.swa_attention_paged(*qa, *_cache_args(cache, page_table, batch, kv_heads, d, page_size,
+                                                   bits, dev),
+                                 _int_vector("seq_lens", seq_lens, batch, dev), batch, heads,
+                                 kv_heads, d, page_size, bits, window, scale, *oa, wp, wb, raw)
+    if st:
+        _check(st, "swa_attention_paged")
     return o
 
 

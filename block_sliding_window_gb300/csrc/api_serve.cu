@@ -163,7 +163,7 @@ size_t swa_attention_packed_workspace_size(int32_t batch, int64_t tokens_q, int3
   if (batch < 1 || tokens_q < 0 || tokens_q > kMaxTokens || kv_heads < 1 || heads < kv_heads ||
       heads % kv_heads || heads > kMaxHeads)
     return 0;
-  return round_up(swa_packed_workspace(batch, tokens_q, heads, kv_heads), kAlign);
+  return round_up(swa_packed_workspace(batch, tokens_q, heads, kv_heads, current_sms()), kAlign);
 }
 
 ptb_status swa_attention_packed(const ptb_bf16* q, int64_t q_st, int64_t q_sh, const ptb_bf16* k,

@@ -6,6 +6,20 @@
 
 namespace ptb {
 
+// Lets a kernel use `bytes` of dynamic shared memory, once per device.  Two
+// threads that set it at the same time set the same value.
+constexpr int kDeviceSlots = 64;
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, bool (&configured)[kDeviceSlots]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kDeviceSlots && configured[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < kDeviceSlots) configured[dev] = true;
+  return e;
+}
+
 constexpr int kKvGroup = 32;  // channels that share one (scale, centre) pair
 
 // The sequence of token t: the first b < batch with cu[b + 1] > t, or batch.

@@ -190,7 +190,7 @@ struct SwaPagedArgs {
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_gather(const KvGatherArgs& a, cudaStream_t stream);
-size_t swa_packed_workspace(int batch, int64_t tokens_q, int heads, int kv_heads);
+size_t swa_packed_workspace(int batch, int64_t tokens_q, int heads, int kv_heads, int sms);
 cudaError_t launch_swa_packed(const SwaPackedArgs& a, cudaStream_t stream);
 size_t swa_paged_workspace(int batch, int heads, int kv_heads, int head_dim, int sms);
 cudaError_t launch_swa_paged(const SwaPagedArgs& a, cudaStream_t stream);

@@ -693,8 +693,8 @@ template <int D>
 cudaError_t launch_typed(const PackedParams& prm, int grid, bool after_list, cudaStream_t stream) {
   using C = Cfg<D>;
   auto kern = swa_packed_kernel<D>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static bool configured[kDeviceSlots] = {};
+  cudaError_t e = allow_smem(kern, C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -728,9 +728,11 @@ int64_t most_blocks(int batch, int64_t tokens, int block) { return tokens / bloc
 
 }  // namespace
 
-// The list: its length (16 bytes), then the blocks.
-size_t swa_packed_workspace(int batch, int64_t tokens_q, int heads, int kv_heads) {
+// The list: its length (16 bytes), then the blocks; none where every SM takes
+// at most one item.
+size_t swa_packed_workspace(int batch, int64_t tokens_q, int heads, int kv_heads, int sms) {
   const int64_t n = most_blocks(batch, tokens_q, block_tokens(heads, kv_heads));
+  if (n * kv_heads <= sms) return 0;
   return static_cast<size_t>(16 + n * sizeof(int4));
 }
 

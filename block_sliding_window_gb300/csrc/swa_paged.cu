@@ -19,18 +19,27 @@
 // (maximum, sum, output) in the workspace, and a second kernel, launched to
 // overlap this one's end, joins them in order: the same bits every time.
 //
-// 4-bit rows: codes become bf16 16 + u by placing the nibble in the mantissa,
-// exact, and
-//   q.k  = sum_w scale_w (q.(16 + u))_w + (centre_w - 24 scale_w) Q_w,
-//   sum_j p_j v_j = sum_j (p_j scale_jw)(u_j - 8) + sum_j p_j centre_jw:
-// for keys the pair is applied to the products of each 32-channel group, and
-// Q_w = sum of q over the group enters as one more product with the pairs as
-// they lie in memory (Q_w as two bf16 terms); for values the scale goes into
-// P, and the centres are one more product.  p and p * scale are rounded to
-// bf16, as P is in the other attention kernels.
+// 4-bit rows:
+//   q.k = sum_w scale_w (q.u)_w + (centre_w - 8 scale_w) Q_w,  Q_w = sum of q over group w,
+//   sum_j p_j v_j = sum_j (p_j scale_jw)(u_j - 8) + sum_j p_j centre_jw.
+// Keys: the e4m3 bit pattern of a code is u / 512, so a masked word is an
+// operand as it lies; q enters as two e4m3 terms, which hold a bf16 value
+// exactly down to 2^-10 of the row's largest (below that to 2^-17 of the
+// largest).  The scale is applied to each group's product, and the rest is
+// one more product with the pairs as they lie (Q_w in two bf16 terms).
+// Values: codes become bf16 16 + u, exact, by placing the nibble in the
+// mantissa, then u - 8; the scale goes into P, and the centres are one more
+// product.  p and p * scale are rounded to bf16 once, as P is in the other
+// attention kernels.
+// The integer pipe bounds the 4-bit kernel (0.5 instructions a clock and
+// SM quarter, measured, as are 0.22 m16n8k32 e4m3 and 0.125 m16n8k16 bf16
+// products): 3 of its instructions for 8 key codes against 8 with bf16
+// operands.
 // Rows that the mask leaves out (before the window, past the length, pages out
 // of range) may hold anything: their scores are replaced and their values or
 // pairs zeroed before use.
+#include <cuda_fp16.h>
+
 #include "kv_device.cuh"
 
 namespace ptb {
@@ -43,19 +52,24 @@ constexpr int kMaxWarpsPerSm = 16;
 constexpr float kRescaleLog2 = 8.0f;  // raise the reference max only past 2^8
 constexpr int kJoinThreads = 256;
 
-template <int D, int BITS>
+template <int D, int BITS, int NT>
 struct Cfg {
   static constexpr int kAtoms = (D + 63) / 64;
   static constexpr int NG = D / kKvGroup;
-  static constexpr int kCodeBytes = BITS == 16 ? kAtoms * kBlockKeys * 128 : kBlockKeys * (D / 2);
-  static constexpr int kPairBytes = BITS == 16 ? 0 : kBlockKeys * (D / 8);
-  static constexpr int kSideBytes = kCodeBytes + kPairBytes;  // keys or values of a unit
+  // Keys or values of a unit in shared memory.  Bits 16: 64-channel column
+  // blocks of 32 rows of 128 swizzled bytes.  Bits 4: 32 rows of codes, then
+  // their pairs; with pages of 16 rows twice 16 rows and their pairs, so that
+  // such a page's block is one copy.
+  static constexpr int kSideBytes =
+      BITS == 16 ? kAtoms * kBlockKeys * 128 : kBlockKeys * (D / 2 + D / 8);
   static constexpr int kStageBytes = 2 * kSideBytes;
   static constexpr int kStages = 3;
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kSmemBytes = 1024 + kWarps * (kWarpBytes + 64);
   static constexpr int kFit = (227 * 1024) / (kSmemBytes + 1024);
-  static constexpr int kBlocksPerSm = kFit < 3 ? (kFit < 1 ? 1 : kFit) : 3;
+  // Two 8-head tiles in 4 bits need more than the 168 registers of 3 blocks.
+  static constexpr int kMost = BITS == 4 && NT == 2 ? 2 : 3;
+  static constexpr int kBlocksPerSm = kFit < kMost ? (kFit < 1 ? 1 : kFit) : kMost;
 };
 static_assert(3 * kWarps <= kMaxWarpsPerSm, "workspace is sized by kMaxWarpsPerSm");
 
@@ -159,6 +173,27 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// One 32-channel step with e4m3 operands.
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two values as e4m3 (low byte: lo), and back.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t v;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
+  return v;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -211,12 +246,6 @@ __device__ __forceinline__ uint32_t minus24(uint32_t x) {
   __nv_bfloat162 v = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&x), c);
   return *reinterpret_cast<uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y) {
-  __nv_bfloat162 v =
-      __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<__nv_bfloat162*>(&y));
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -251,9 +280,9 @@ __device__ __forceinline__ int key_of_row(int r) {
 // ------------------------------------------------------------------ kernel --
 
 template <int D, int BITS, int NT>
-__global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
+__global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
     swa_paged_kernel(const __grid_constant__ PagedParams P) {
-  using C = Cfg<D, BITS>;
+  using C = Cfg<D, BITS, NT>;
   constexpr int NG = C::NG;
   constexpr int MS = D / 16;  // 16-channel steps
   const SwaPagedArgs& a = P.a;
@@ -293,78 +322,84 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
   if (u0 >= u1) return;
 
   const int page = a.c.page_size;
-  const int sub_keys = page < kBlockKeys ? page : kBlockKeys;  // keys that lie in one page
-  const int subs = kBlockKeys / sub_keys;                      // 1 or 2
+  const int sub_shift = page < kBlockKeys ? a.c.page_shift : 5;
+  const int sub_keys = 1 << sub_shift;          // keys of a unit that lie in one page
+  const int subs = kBlockKeys >> sub_shift;     // 1 or 2
 
   // ------------------------------------------------------------ producer --
+  // A unit's copies are issued by one lane each: sub-block `lane / copies`,
+  // part `lane % copies`.  Bits 16: the 64-channel column blocks of keys,
+  // then of values.  Bits 4: the block of keys, then of values, where it is
+  // whole in the page's block; else codes and pairs of each on their own.
+  const bool split = BITS == 4 && page > kBlockKeys;
+  const int copies = BITS == 16 ? 2 * C::kAtoms : (split ? 4 : 2);
+  const int copy_sub = lane / copies, copy_part = lane % copies;
+  const bool copier = copy_sub < subs;
+  const int copy_side = copy_part >= copies / 2 ? 1 : 0;
+  const bool copy_pairs = split && (copy_part & 1);
+  const int row_bytes = BITS == 16 ? 0 : (copy_pairs ? D / 8 : (split ? D / 2 : D / 2 + D / 8));
+  const uint32_t copy_dst =
+      copy_side * C::kSideBytes +
+      (BITS == 16 ? (copy_part % C::kAtoms) * kBlockKeys * 128 + copy_sub * sub_keys * 128
+                  : copy_sub * (C::kSideBytes / 2) + (copy_pairs ? kBlockKeys * (D / 2) : 0));
+  const int64_t copy_src = copy_pairs ? page * (D / 2) : 0;
+
   Place ld = place_of(a, heads, u0, lane);
   Place at = ld;
   int64_t loaded = u0;
-  int page_reg = -1, page_first = 0, page_left = 0;  // pages of the coming sub-blocks, one a lane
+  // Pages of the coming sub-blocks, one a lane; -1: not needed, or out of range.
+  int page_reg = -1, page_next = 32;
+  int64_t lane_src = 0;  // this lane's copies: offset in a page (bits 4), or row (bits 16)
   auto issue = [&](int stage) {
     const int key0 = (ld.s.unit0 + ld.i) * kBlockKeys;
-    if (page_left == 0) {
-      page_first = key0;
-      const int64_t pos = static_cast<int64_t>(key0) + lane * sub_keys;
+    if (page_next >= 32) {
+      const int64_t pos = static_cast<int64_t>(key0) + (lane << sub_shift);
       page_reg = -1;
-      if (pos < ld.s.n && pos + sub_keys > ld.s.lo)
+      if (pos < ld.s.n && pos + sub_keys > ld.s.lo) {
         page_reg = a.c.table[ld.b * a.c.table_stride + (pos >> a.c.page_shift)];
-      page_left = 32 / subs;
-    }
-    const int kvh = ld.hh / P.head_blocks;
-    uint32_t mask = 0;
-    int valid = 0, my_page = -1, my_sub = 0;
-    // Copies of a sub-block: bits 4: key codes, key pairs, value codes, value
-    // pairs; bits 16: the 64-channel column blocks of keys, then of values.
-    constexpr int kCopies = BITS == 4 ? 4 : 2 * C::kAtoms;
-    for (int s = 0; s < subs; ++s) {
-      const int pos = key0 + s * sub_keys;
-      const int pg = __shfl_sync(0xffffffffu, page_reg, (pos - page_first) / sub_keys);
-      const int from = max(ld.s.lo - pos, 0), to = min(ld.s.n - pos, sub_keys);
-      if (from >= to) continue;
-      if (pg < 0 || pg >= a.c.pages) {
-        if (lane == 0) record_error(a.status, PTB_ERR_ARG);
-        continue;
+        if (page_reg < 0 || page_reg >= a.c.pages) {
+          page_reg = -1;
+          record_error(a.status, PTB_ERR_ARG);
+        }
       }
-      const uint32_t upto = to == 32 ? 0xffffffffu : (1u << to) - 1u;
-      mask |= (upto & ~((1u << from) - 1u)) << (s * sub_keys);
-      ++valid;
-      if (lane / kCopies == s) my_page = pg, my_sub = s;
+      page_next = 0;
+      const int block = copy_side * a.c.kv_heads + ld.hh / P.head_blocks;
+      lane_src = BITS == 16 ? block * page : block * a.c.block_bytes + copy_src;
     }
-    const uint32_t dst = ring + stage * C::kStageBytes;
-    __syncwarp();  // the stage has been read by every lane
+    const int pg = __shfl_sync(0xffffffffu, page_reg, page_next + (copier ? copy_sub : 0));
+    page_next += subs;
+    const unsigned vote = __ballot_sync(0xffffffffu, copier && copy_part == 0 && pg >= 0);
+    uint32_t mask = 0xffffffffu;
+    if (key0 < ld.s.lo || key0 + kBlockKeys > ld.s.n || __popc(vote) < subs) {
+      const int from = max(ld.s.lo - key0, 0), to = min(ld.s.n - key0, kBlockKeys);
+      mask = (to == 32 ? 0xffffffffu : (1u << to) - 1u) & ~((1u << from) - 1u);
+      if (!(vote & 1u)) mask &= subs == 1 ? 0u : 0xffff0000u;
+      if (subs == 2 && !(vote >> copies)) mask &= 0xffffu;
+    }
     if (lane == 0) {
       masks[stage] = mask;
-      if (valid)
-        mbar_arrive_expect_tx(&full[stage], valid * (C::kStageBytes / subs));
+      if (vote)
+        mbar_arrive_expect_tx(&full[stage], __popc(vote) * (C::kStageBytes >> (subs - 1)));
       else
         mbar_arrive(&full[stage]);
     }
-    __syncwarp();
-    if (my_page >= 0) {
-      const int what = lane % kCopies;
-      const int off = (key0 + my_sub * sub_keys) & (page - 1);
-      if constexpr (BITS == 4) {
-        const int side = what >> 1;
-        const uint8_t* block = a.c.base + my_page * a.c.page_bytes +
-                               (side * a.c.kv_heads + kvh) * a.c.block_bytes;
-        if (what & 1)
-          bulk_load(dst + side * C::kSideBytes + C::kCodeBytes + my_sub * sub_keys * (D / 8),
-                    block + page * (D / 2) + off * (D / 8), sub_keys * (D / 8), &full[stage]);
-        else
-          bulk_load(dst + side * C::kSideBytes + my_sub * sub_keys * (D / 2),
-                    block + off * (D / 2), sub_keys * (D / 2), &full[stage]);
-      } else {
-        const int side = what / C::kAtoms, atom = what % C::kAtoms;
-        tma_rows(dst + side * C::kSideBytes + atom * kBlockKeys * 128 + my_sub * sub_keys * 128,
-                 &P.map, &full[stage], atom * 64, (side * a.c.kv_heads + kvh) * page + off, my_page);
-      }
+    __syncwarp();  // armed, and the stage has been read by every lane
+    if (copier && pg >= 0) {
+      const uint32_t dst = ring + stage * C::kStageBytes + copy_dst;
+      const int off = (key0 + (copy_sub << sub_shift)) & (page - 1);
+      if constexpr (BITS == 4)
+        bulk_load(dst, a.c.base + pg * a.c.page_bytes + lane_src + off * row_bytes,
+                  row_bytes << sub_shift, &full[stage]);
+      else
+        tma_rows(dst, &P.map, &full[stage], (copy_part % C::kAtoms) * 64,
+                 static_cast<int>(lane_src) + off, pg);
     }
-    --page_left;
     ++loaded;
-    const int was_b = ld.b, was_hh = ld.hh;
-    next_place(a, heads, ld);
-    if (ld.b != was_b || ld.hh != was_hh) page_left = 0;
+    if (++ld.i >= ld.s.units) {
+      --ld.i;
+      next_place(a, heads, ld);
+      page_next = 32;
+    }
   };
 
 #pragma unroll
@@ -386,13 +421,17 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
     const int count = static_cast<int>(left < at.s.units - first ? left : at.s.units - first);
 
     // Queries as B fragments (column = head g): for 16 bits channels 16 s + 2 t,
-    // + 1 and + 8, + 9; for 4 bits in the order of the codes.
-    uint32_t qf[NT][MS][2];
-    uint32_t qs[NT][2];  // Q_t: (-24 Q, Q) in two bf16 terms
+    // + 1 and + 8, + 9; for 4 bits in the order of the codes and scaled, as
+    // two e4m3 terms each.
+    constexpr int QS = BITS == 16 ? MS : NG;
+    uint32_t qf[NT][QS][2], qg[BITS == 16 ? 1 : NT][QS][2];
+    uint32_t qs[NT][2];  // Q_t: (-8 Q, Q) in two bf16 terms
+    float to_log2[NT][2];  // scores of heads 2 t, 2 t + 1 to the log2 domain
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const bool live = nt * 8 + g < nheads;
       const __nv_bfloat16* q = a.q + at.b * a.q_sb + (head0 + (live ? nt * 8 + g : 0)) * a.q_sh;
+      to_log2[nt][0] = to_log2[nt][1] = a.scale_log2;
       if constexpr (BITS == 16) {
 #pragma unroll
         for (int s = 0; s < MS; ++s) {
@@ -400,25 +439,58 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
           qf[nt][s][1] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 8 + 2 * t) : 0u;
         }
       } else {
+        uint4 v[NG];
+        uint32_t mx = 0;  // largest |q|, as bits: NaN above infinity above all numbers
+#pragma unroll
+        for (int wq = 0; wq < NG; ++wq) {
+          v[wq] = make_uint4(0, 0, 0, 0);
+          if (live) v[wq] = *reinterpret_cast<const uint4*>(q + 32 * wq + 8 * t);
+          const uint32_t x[4] = {v[wq].x, v[wq].y, v[wq].z, v[wq].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = max(mx, max((x[e] << 16) & 0x7fffffffu, x[e] & 0x7fff0000u));
+        }
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // The power of two that brings the largest |q| into [128, 256); a
+        // query that is not finite gives NaN.
+        const int expo = static_cast<int>(mx >> 23);
+        const int shift = min(127 + 7 - expo, 110);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+        const float down =
+            __uint_as_float(expo == 255 ? 0x7fffffffu
+                                        : static_cast<uint32_t>(min(127 + 9 - shift, 254)) << 23);
         qs[nt][0] = qs[nt][1] = 0;
 #pragma unroll
         for (int wq = 0; wq < NG; ++wq) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (live) v = *reinterpret_cast<const uint4*>(q + 32 * wq + 8 * t);
-          qf[nt][2 * wq][0] = __byte_perm(v.x, v.z, 0x5410);      // channels 0, 4
-          qf[nt][2 * wq][1] = __byte_perm(v.x, v.z, 0x7632);      // 1, 5
-          qf[nt][2 * wq + 1][0] = __byte_perm(v.y, v.w, 0x5410);  // 2, 6
-          qf[nt][2 * wq + 1][1] = __byte_perm(v.y, v.w, 0x7632);  // 3, 7
-          float sum = (bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y)) +
-                      (bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w));
+          const uint32_t x[4] = {v[wq].x, v[wq].y, v[wq].z, v[wq].w};
+          uint32_t hi[4], lo[4];  // (2 e, 2 e + 1) of the lane's channels
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y0 = bf16_lo(x[e]) * up, y1 = bf16_hi(x[e]) * up;
+            sum += y0 + y1;
+            hi[e] = to_e4m3x2(y0, y1);
+            const float2 z = from_e4m3x2(hi[e]);
+            lo[e] = to_e4m3x2(y0 - z.x, y1 - z.y);
+          }
+          // Even channels meet the low nibbles of the code bytes, odd ones the high.
+          const uint32_t h01 = hi[0] | hi[1] << 16, h23 = hi[2] | hi[3] << 16;
+          const uint32_t l01 = lo[0] | lo[1] << 16, l23 = lo[2] | lo[3] << 16;
+          qf[nt][wq][0] = __byte_perm(h01, h23, 0x6420);
+          qf[nt][wq][1] = __byte_perm(h01, h23, 0x7531);
+          qg[nt][wq][0] = __byte_perm(l01, l23, 0x6420);
+          qg[nt][wq][1] = __byte_perm(l01, l23, 0x7531);
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          const uint32_t hi = pack_bf16x2(-24.f * sum, sum);
+          sum *= 1.f / 512;  // the codes enter as u / 512
+          const uint32_t top = pack_bf16x2(-8.f * sum, sum);
           if (t == wq) {
-            qs[nt][0] = hi;
-            qs[nt][1] = pack_bf16x2(-24.f * sum - bf16_lo(hi), sum - bf16_hi(hi));
+            qs[nt][0] = top;
+            qs[nt][1] = pack_bf16x2(-8.f * sum - bf16_lo(top), sum - bf16_hi(top));
           }
         }
+        to_log2[nt][0] *= __shfl_sync(0xffffffffu, down, 8 * t);
+        to_log2[nt][1] *= __shfl_sync(0xffffffffu, down, 8 * t + 4);
       }
     }
 
@@ -444,6 +516,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
       }
       const uint32_t keys = ring + stage * C::kStageBytes;
       const uint32_t vals = keys + C::kSideBytes;
+      // 4 bits: codes and pairs of the two 16-key tiles within a side.
+      const uint32_t code1 = subs == 1 ? 16 * (D / 2) : C::kSideBytes / 2;
+      const uint32_t pair0 = subs == 1 ? 32 * (D / 2) : 16 * (D / 2);
+      const uint32_t pair1 = pair0 + (subs == 1 ? 16 * (D / 8) : C::kSideBytes / 2);
       const uint32_t mask = masks[stage];
 
       // ---- scores of the unit's two 16-key tiles: s[tile][nt]: keys g (0, 1)
@@ -467,11 +543,11 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
               mma_bf16(s[h][nt], f[0], f[1], f[2], f[3], qf[nt][m][0], qf[nt][m][1]);
           }
         } else {
-          const int ka = 16 * h + key_of_row(g), kb = ka + 8;
-          const uint32_t pairs = keys + C::kCodeBytes;
+          const int ka = key_of_row(g), kb = ka + 8;
+          const uint32_t codes = keys + (h ? code1 : 0), pairs = keys + (h ? pair1 : pair0);
           uint32_t ca[NG], cb[NG], pa[NG], pb[NG];
-          lds_words<NG>(ca, keys + ka * (D / 2) + t * 4 * NG);
-          lds_words<NG>(cb, keys + kb * (D / 2) + t * 4 * NG);
+          lds_words<NG>(ca, codes + ka * (D / 2) + t * 4 * NG);
+          lds_words<NG>(cb, codes + kb * (D / 2) + t * 4 * NG);
           lds_words<NG>(pa, pairs + ka * (D / 8));
           lds_words<NG>(pb, pairs + kb * (D / 8));
           const uint32_t wa = t < NG ? lds32(pairs + ka * (D / 8) + 4 * (t < NG ? t : 0)) : 0u;
@@ -480,16 +556,16 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
           for (int nt = 0; nt < NT; ++nt) mma_bf16(s[h][nt], wa, wb, wa, wb, qs[nt][0], qs[nt][1]);
 #pragma unroll
           for (int wq = 0; wq < NG; ++wq) {
-            const uint32_t a0 = nibbles16<0>(ca[wq]), a2 = nibbles16<1>(ca[wq]);
-            const uint32_t a4 = nibbles16<2>(ca[wq]), a6 = nibbles16<3>(ca[wq]);
-            const uint32_t b0 = nibbles16<0>(cb[wq]), b2 = nibbles16<1>(cb[wq]);
-            const uint32_t b4 = nibbles16<2>(cb[wq]), b6 = nibbles16<3>(cb[wq]);
+            // Four codes a register, as they lie in its bytes: the e4m3 bit
+            // pattern u (0 .. 15) is the number u / 512.
+            const uint32_t a0 = ca[wq] & 0x0f0f0f0fu, a2 = (ca[wq] >> 4) & 0x0f0f0f0fu;
+            const uint32_t a1 = cb[wq] & 0x0f0f0f0fu, a3 = (cb[wq] >> 4) & 0x0f0f0f0fu;
             const float sa = bf16_lo(pa[wq]), sb = bf16_lo(pb[wq]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float acc[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_bf16(acc, a0, b0, a2, b2, qf[nt][2 * wq][0], qf[nt][2 * wq][1]);
-              mma_bf16(acc, a4, b4, a6, b6, qf[nt][2 * wq + 1][0], qf[nt][2 * wq + 1][1]);
+              mma_e4m3(acc, a0, a1, a2, a3, qf[nt][wq][0], qf[nt][wq][1]);
+              mma_e4m3(acc, a0, a1, a2, a3, qg[nt][wq][0], qg[nt][wq][1]);
               s[h][nt][0] = fmaf(sa, acc[0], s[h][nt][0]);
               s[h][nt][1] = fmaf(sa, acc[1], s[h][nt][1]);
               s[h][nt][2] = fmaf(sb, acc[2], s[h][nt][2]);
@@ -515,14 +591,33 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
 
       // ---- weights.  The reference max of a head is the same in all lanes
       // and is raised only when a score passes it by more than 2^8.
-      uint32_t pf[2][NT][2];  // P^T fragments: column = head g, rows keys 2 t, 2 t + 1 / + 8
+      // P^T fragments: column = head g, rows keys 2 t, 2 t + 1 / + 8; for bits 4
+      // pw[h][nt][w] holds P^T times the scales of group w.
+      uint32_t pf[2][NT][2], pw[2][BITS == 4 ? NT : 1][BITS == 4 ? NG : 1][2];
+      float scale_a[2][BITS == 4 ? NG : 1], scale_b[2][BITS == 4 ? NG : 1];
+      if constexpr (BITS == 4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t pairs = vals + (h ? pair1 : pair0);
+          const int ka = key_of_row(g);
+          uint32_t pa[NG], pb[NG];
+          lds_words<NG>(pa, pairs + ka * (D / 8));
+          lds_words<NG>(pb, pairs + (ka + 8) * (D / 8));
+          const bool va = (mask >> (16 * h + ka)) & 1u, vb = (mask >> (16 * h + ka + 8)) & 1u;
+#pragma unroll
+          for (int wv = 0; wv < NG; ++wv) {
+            scale_a[h][wv] = va ? bf16_lo(pa[wv]) : 0.f;
+            scale_b[h][wv] = vb ? bf16_lo(pb[wv]) : 0.f;
+          }
+        }
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float mx[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           mx[e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2])) *
-                  a.scale_log2;
+                  to_log2[nt][e];
         if (__any_sync(0xffffffffu, mx[0] > m_ref[nt][0] + kRescaleLog2 ||
                                         mx[1] > m_ref[nt][1] + kRescaleLog2)) {
           float alpha[2];
@@ -553,11 +648,19 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            p[e] = fast_exp2(fmaf(s[h][nt][e], a.scale_log2, (e & 1) ? -m1 : -m0));
+            p[e] = fast_exp2(fmaf(s[h][nt][e], to_log2[nt][e & 1], (e & 1) ? -m1 : -m0));
           l[nt][0] += p[0] + p[2];
           l[nt][1] += p[1] + p[3];
           pf[h][nt][0] = transpose8x8(pack_bf16x2(p[0], p[1]));
           pf[h][nt][1] = transpose8x8(pack_bf16x2(p[2], p[3]));
+          if constexpr (BITS == 4) {
+#pragma unroll
+            for (int wv = 0; wv < NG; ++wv) {
+              const float sa = scale_a[h][wv], sb = scale_b[h][wv];
+              pw[h][nt][wv][0] = transpose8x8(pack_bf16x2(p[0] * sa, p[1] * sa));
+              pw[h][nt][wv][1] = transpose8x8(pack_bf16x2(p[2] * sb, p[3] * sb));
+            }
+          }
         }
       }
 
@@ -585,24 +688,17 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
           }
         } else {
           // Rows of this lane: keys t, t + 4 (first half), t + 8, t + 12.
-          const uint32_t pairs = vals + C::kCodeBytes;
-          uint32_t pr[4][NG], cw[4];  // pairs of the four keys; the pair of group g
+          const uint32_t codes = vals + (h ? code1 : 0), pairs = vals + (h ? pair1 : pair0);
+          uint32_t cw[4];  // pair of group g (rows from NG on repeat group 0)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = 16 * h + t + 4 * x;
-            lds_words<NG>(pr[x], pairs + key * (D / 8));
-            cw[x] = lds32(pairs + key * (D / 8) + 4 * (g < NG ? g : 0));
-          }
+          for (int x = 0; x < 4; ++x)
+            cw[x] = lds32(pairs + (t + 4 * x) * (D / 8) + 4 * (g < NG ? g : 0));
           if (mask != 0xffffffffu) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t keep = ((mask >> (16 * h + t + 4 * x)) & 1u) ? 0xffffffffu : 0u;
-#pragma unroll
-              for (int wv = 0; wv < NG; ++wv) pr[x][wv] &= keep;
-              cw[x] &= keep;
-            }
+            for (int x = 0; x < 4; ++x)
+              cw[x] = ((mask >> (16 * h + t + 4 * x)) & 1u) ? cw[x] : 0u;
           }
-          // Centres: row g of the product is group g (rows from NG on repeat group 0).
+          // Centres: row g of the product is group g.
           const uint32_t c0 = __byte_perm(cw[0], cw[1], 0x7632);
           const uint32_t c1 = __byte_perm(cw[2], cw[3], 0x7632);
 #pragma unroll
@@ -612,7 +708,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
           uint32_t cv[4][(NG + 1) / 2];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const uint32_t row = vals + (16 * h + t + 4 * x) * (D / 2) + g * 2 * NG;
+            const uint32_t row = codes + (t + 4 * x) * (D / 2) + g * 2 * NG;
             if constexpr (NG % 2 == 0) {
               lds_words<NG / 2>(cv[x], row);
             } else {
@@ -631,17 +727,14 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS>::kBlocksPerSm)
             const uint32_t sel = (wv & 1) ? 0x7632u : 0x5410u;
             const uint32_t v0 = __byte_perm(cv[0][wv / 2], cv[1][wv / 2], sel);
             const uint32_t v1 = __byte_perm(cv[2][wv / 2], cv[3][wv / 2], sel);
-            const uint32_t s0 = __byte_perm(pr[0][wv], pr[1][wv], 0x5410);
-            const uint32_t s1 = __byte_perm(pr[2][wv], pr[3][wv], 0x5410);
             const uint32_t e0 = minus24(nibbles16<0>(v0)), e1 = minus24(nibbles16<1>(v0));
             const uint32_t e2 = minus24(nibbles16<2>(v0)), e3 = minus24(nibbles16<3>(v0));
             const uint32_t f0 = minus24(nibbles16<0>(v1)), f1 = minus24(nibbles16<1>(v1));
             const uint32_t f2 = minus24(nibbles16<2>(v1)), f3 = minus24(nibbles16<3>(v1));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t b0 = mul2(pf[h][nt][0], s0), b1 = mul2(pf[h][nt][1], s1);
-              mma_bf16(o[nt][2 * wv], e0, e1, f0, f1, b0, b1);
-              mma_bf16(o[nt][2 * wv + 1], e2, e3, f2, f3, b0, b1);
+              mma_bf16(o[nt][2 * wv], e0, e1, f0, f1, pw[h][nt][wv][0], pw[h][nt][wv][1]);
+              mma_bf16(o[nt][2 * wv + 1], e2, e3, f2, f3, pw[h][nt][wv][0], pw[h][nt][wv][1]);
             }
           }
         }
@@ -808,10 +901,10 @@ int head_tiles(int group) { return group > 8 ? 2 : 1; }
 
 template <int D, int BITS, int NT>
 cudaError_t launch_typed(PagedParams& prm, cudaStream_t stream) {
-  using C = Cfg<D, BITS>;
+  using C = Cfg<D, BITS, NT>;
   auto kern = swa_paged_kernel<D, BITS, NT>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static bool configured[kDeviceSlots] = {};
+  cudaError_t e = allow_smem(kern, C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
   const int grid = prm.a.sms * C::kBlocksPerSm;
   prm.warps = grid * kWarps;

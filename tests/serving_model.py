@@ -4,15 +4,18 @@ tests hold the kernels to.
 
 Bounds.  A rounding to bf16 is off by at most H = 2^-8 of the value (half a step).  The attention
 kernels round each softmax weight p to bf16 once before the weighted sum (the 4-bit kernel rounds
-p and then p * scale), and the result once:
+p * scale once for the codes and p once for the centres), and the result once:
     |o - o64| <= H |o| + H A + 2 E A,      A = sum_j p_j |v_j|,
-with 4 bits A counts scale |u - 8| twice and |centre| once.  E bounds the error of a score
+where with 4 bits |v| counts scale |u - 8| + |centre|.  E bounds the error of a score
 s = q.k * scale in fp32: every one of d products and sums is off by at most 2^-23 of the sum of
 magnitudes (tensor-core sums truncate), and so E = (d + 8) 2^-23 max_j sum |q||k| scale; a relative
 error E of each weight moves numerator and denominator, hence 2 E.  The 4-bit kernel forms
-q.k = sum_w scale_w (q . (16 + u))_w + (centre_w - 24 scale_w) Q_w with Q_w = sum of q over the group
-held in two bf16 terms (off by 2^-16 of it): magnitudes are counted as q (16 + u) scale and
-|Q| (24 scale + |centre|), and 2^-16 |Q| (24 scale + |centre|) is added.
+q.k = sum_w scale_w (q.u)_w + (centre_w - 8 scale_w) Q_w: magnitudes are counted as
+|q| (scale (u + 8) + |centre|).  Q_w, the sum of q over a group, is held in two bf16 terms (off by
+2^-16 of it): 2^-16 |Q| (8 scale + |centre|) is added.  q is held in two e4m3 terms after scaling
+its largest entry into [128, 256): the first leaves at most 8 units of a bf16 value's last place,
+which the second holds exactly unless they fall below half of e4m3's least step, 2^-10: an entry is
+off by at most 2^-10 / 128 of the largest, and 2^-17 max|q| sum scale u is added.
 """
 import numpy as np
 import torch
@@ -164,12 +167,13 @@ def paged(q, cache, table, lens, window, scale):
                 if u is None:
                     mk[j - lo, h] = np.abs(k[j - lo, h])
                 else:
-                    mk[j - lo, h] = s * (16 + u) + 24 * s + np.abs(z)
+                    mk[j - lo, h] = s * (8 + u) + np.abs(z)
                     for x in range(h * g, (h + 1) * g):
                         qs = np.abs(q[b, x].reshape(-1, 32).sum(-1))
-                        extra[0, x, j - lo] = 2.0 ** -16 * (qs * (24 * s + np.abs(z)).reshape(-1, 32)[:, 0]).sum()
+                        extra[0, x, j - lo] = (2.0 ** -16 * (qs * (8 * s + np.abs(z)).reshape(-1, 32)[:, 0]).sum()
+                                               + 2.0 ** -17 * np.abs(q[b, x]).max() * (s * u).sum())
                 v[j - lo, h], u, s, z = cache.get(page, off, h, 1)
-                mv[j - lo, h] = np.abs(v[j - lo, h]) if u is None else 2 * s * np.abs(u - 8) + np.abs(z)
+                mv[j - lo, h] = np.abs(v[j - lo, h]) if u is None else s * np.abs(u - 8) + np.abs(z)
         ob, bb = attend(q[b:b + 1], k, v, n - lo - 1, n, scale, mk, mv, extra)
         o[b], bound[b] = ob[0], bb[0]
     return o, bound
