@@ -72,7 +72,8 @@ size_t ptb_kv_page_size(int32_t kv_heads, int32_t page_size, int32_t head_dim, i
   if (kv_heads < 1 || kv_heads > kMaxHeads || !page_size_ok(page_size) || !head_dim_ok(head_dim))
     return 0;
   if (bits != 16 && !(bits == 4 && head_dim % 32 == 0)) return 0;
-  return static_cast<size_t>(2 * kv_heads * kv_block_bytes(page_size, head_dim, bits));
+  const int64_t bytes = 2 * kv_heads * kv_block_bytes(page_size, head_dim, bits);
+  return bytes < (1ll << 31) ? static_cast<size_t>(bytes) : 0;  // offsets in a page stay in 32 bits
 }
 
 ptb_status ptb_kv_append(const ptb_bf16* q, int64_t q_st, int64_t q_sh, const ptb_bf16* k,

@@ -20,25 +20,24 @@
 // overlap this one's end, joins them in order: the same bits every time.
 //
 // 4-bit rows:
-//   q.k = sum_w scale_w (q.u)_w + (centre_w - 8 scale_w) Q_w,  Q_w = sum of q over group w,
+//   q.k = sum_w scale_w (q.(64 + u))_w + (centre_w - 72 scale_w) Q_w,  Q_w = sum of q over group w,
 //   sum_j p_j v_j = sum_j (p_j scale_jw)(u_j - 8) + sum_j p_j centre_jw.
-// Keys: the e4m3 bit pattern of a code is u / 512, so a masked word is an
-// operand as it lies; q enters as two e4m3 terms, which hold a bf16 value
-// exactly down to 2^-10 of the row's largest (below that to 2^-17 of the
-// largest).  The scale is applied to each group's product, and the rest is
-// one more product with the pairs as they lie (Q_w in two bf16 terms).
-// Values: codes become bf16 16 + u, exact, by placing the nibble in the
-// mantissa, then u - 8; the scale goes into P, and the centres are one more
-// product.  p and p * scale are rounded to bf16 once, as P is in the other
-// attention kernels.
-// The integer pipe bounds the 4-bit kernel (0.5 instructions a clock and
-// SM quarter, measured, as are 0.22 m16n8k32 e4m3 and 0.125 m16n8k16 bf16
-// products): 3 of its instructions for 8 key codes against 8 with bf16
-// operands.
+// Keys: a nibble placed in the mantissa of the fp16 number 64 makes it 64 + u;
+// q enters as fp16, scaled by a power of two (exact down to 2^-24 of the row's
+// largest).  The scale is applied to each group's product, and the rest is one
+// more product with the pairs as they lie (Q_w in two bf16 terms).
+// Values: codes become bf16 u - 8 the same way; the scale goes into P, and the
+// centres are one more product.  p and p * scale are rounded to bf16 once, as
+// P is in the other attention kernels.
+// The integer pipe (0.5 instructions a clock and SM quarter, measured) bounds
+// the 4-bit kernel.  (e4m3 products, for which a masked word is an operand as
+// it lies, were slower: the compiler builds them from fp16 ones.)
 // Rows that the mask leaves out (before the window, past the length, pages out
 // of range) may hold anything: their scores are replaced and their values or
 // pairs zeroed before use.
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "kv_device.cuh"
 
@@ -58,8 +57,7 @@ struct Cfg {
   static constexpr int NG = D / kKvGroup;
   // Keys or values of a unit in shared memory.  Bits 16: 64-channel column
   // blocks of 32 rows of 128 swizzled bytes.  Bits 4: 32 rows of codes, then
-  // their pairs; with pages of 16 rows twice 16 rows and their pairs, so that
-  // such a page's block is one copy.
+  // their pairs.
   static constexpr int kSideBytes =
       BITS == 16 ? kAtoms * kBlockKeys * 128 : kBlockKeys * (D / 2 + D / 8);
   static constexpr int kStageBytes = 2 * kSideBytes;
@@ -67,11 +65,10 @@ struct Cfg {
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kSmemBytes = 1024 + kWarps * (kWarpBytes + 64);
   static constexpr int kFit = (227 * 1024) / (kSmemBytes + 1024);
-  // Two 8-head tiles in 4 bits need more than the 168 registers of 3 blocks.
-  static constexpr int kMost = BITS == 4 && NT == 2 ? 2 : 3;
+  static constexpr int kMost = BITS == 16 ? 3 : (NT == 1 ? 3 : 2);
   static constexpr int kBlocksPerSm = kFit < kMost ? (kFit < 1 ? 1 : kFit) : kMost;
 };
-static_assert(3 * kWarps <= kMaxWarpsPerSm, "workspace is sized by kMaxWarpsPerSm");
+static_assert(4 * kWarps <= kMaxWarpsPerSm, "workspace is sized by kMaxWarpsPerSm");
 
 struct PagedParams {
   CUtensorMap map;  // bits 16: {d, rows of a page, pages}
@@ -166,32 +163,42 @@ __device__ __forceinline__ void next_place(const SwaPagedArgs& a, int heads, Pla
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One 32-channel step with e4m3 operands.
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+// The same from a zero accumulator.
+__device__ __forceinline__ void mma_bf16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// The same with fp16 operands.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Two values as e4m3 (low byte: lo), and back.
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
-  uint16_t v;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
-  return v;
-}
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
-  return __half22float2(*reinterpret_cast<__half2*>(&h));
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -211,17 +218,18 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
 // row r, columns 2 c and 2 c + 1).
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(src), "r"(bytes), "r"(smem_addr(bar))
-      : "memory");
+// 16 bytes global -> shared, past L1; completion by groups.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0,
                                          int c1, int c2) {
@@ -232,43 +240,46 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Nibble k of both 16-bit halves of w as bf16 values 16 + u (the nibble in
-// mantissa bits 3 .. 6 of 16.0).
+// Nibble K of both 16-bit halves of w as numbers: in mantissa bits 4 .. 7 of
+// the fp16 number 64, it is 64 + u.
 template <int K>
-__device__ __forceinline__ uint32_t nibbles16(uint32_t w) {
-  const uint32_t s = K == 0 ? w << 3 : w >> (4 * K - 3);
-  return (s & 0x00780078u) | 0x41804180u;
+__device__ __forceinline__ uint32_t nibbles64(uint32_t w) {
+  const uint32_t s = K == 0 ? w << 4 : w >> (4 * K - 4);
+  return (s & 0x00f000f0u) | 0x54005400u;
 }
-
-// 16 + u -> u - 8 (exact).
-__device__ __forceinline__ uint32_t minus24(uint32_t x) {
-  const __nv_bfloat162 c = __floats2bfloat162_rn(-24.f, -24.f);
-  __nv_bfloat162 v = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&x), c);
+// As bf16: u - 8, exact.  Nibble 0 in mantissa bits 0 .. 3 of 128 and nibble 2
+// a byte further need no second shift; 1 and 3 go to bits 3 .. 6 of 16.
+__device__ __forceinline__ uint32_t add2(uint32_t x, float c) {
+  __nv_bfloat162 v = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&x), __floats2bfloat162_rn(c, c));
   return *reinterpret_cast<uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t (&v)[4]) {
+  const uint32_t r = w >> 8;
+  v[0] = add2((w & 0x000f000fu) | 0x43004300u, -136.f);
+  v[1] = add2(((w >> 1) & 0x00780078u) | 0x41804180u, -24.f);
+  v[2] = add2((r & 0x000f000fu) | 0x43004300u, -136.f);
+  v[3] = add2(((r >> 1) & 0x00780078u) | 0x41804180u, -24.f);
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-  return v;
-}
+
 // N consecutive words (N 1 .. 4) at 4 N-byte alignment (4-byte for N = 3).
 template <int N>
-__device__ __forceinline__ void lds_words(uint32_t (&r)[N], uint32_t a) {
-  if constexpr (N == 4)
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(a)
-                 : "memory");
-  else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
-  else
+__device__ __forceinline__ void lds_words(uint32_t (&r)[N], const uint8_t* p) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r[0] = v.x, r[1] = v.y;
+  } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = lds32(a + 4 * i);
+    for (int i = 0; i < N; ++i) r[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  }
+}
+__device__ __forceinline__ uint32_t lds32(const uint8_t* p) {
+  return *reinterpret_cast<const uint32_t*>(p);
+}
+__device__ __forceinline__ uint32_t lds16(const uint8_t* p) {
+  return *reinterpret_cast<const uint16_t*>(p);
 }
 
 // Row `r` (0 .. 15) of a 16-key tile of 4-bit rows stands for this key: the
@@ -292,6 +303,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
   const int g = lane >> 2, t = lane & 3;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t ring = base + warp * C::kWarpBytes;
+  const uint8_t* ring_rows = smem_raw + (ring - smem_addr(smem_raw));
   uint8_t* tail = smem_raw + (base - smem_addr(smem_raw)) + kWarps * C::kWarpBytes + warp * 64;
   uint64_t* full = reinterpret_cast<uint64_t*>(tail);                     // [kStages]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(full + C::kStages);
@@ -325,31 +337,25 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
   const int sub_shift = page < kBlockKeys ? a.c.page_shift : 5;
   const int sub_keys = 1 << sub_shift;          // keys of a unit that lie in one page
   const int subs = kBlockKeys >> sub_shift;     // 1 or 2
+  const uint32_t page_bytes = static_cast<uint32_t>(a.c.page_bytes);  // < 2^31
 
   // ------------------------------------------------------------ producer --
-  // A unit's copies are issued by one lane each: sub-block `lane / copies`,
-  // part `lane % copies`.  Bits 16: the 64-channel column blocks of keys,
-  // then of values.  Bits 4: the block of keys, then of values, where it is
-  // whole in the page's block; else codes and pairs of each on their own.
-  const bool split = BITS == 4 && page > kBlockKeys;
-  const int copies = BITS == 16 ? 2 * C::kAtoms : (split ? 4 : 2);
-  const int copy_sub = lane / copies, copy_part = lane % copies;
-  const bool copier = copy_sub < subs;
-  const int copy_side = copy_part >= copies / 2 ? 1 : 0;
-  const bool copy_pairs = split && (copy_part & 1);
-  const int row_bytes = BITS == 16 ? 0 : (copy_pairs ? D / 8 : (split ? D / 2 : D / 2 + D / 8));
-  const uint32_t copy_dst =
-      copy_side * C::kSideBytes +
-      (BITS == 16 ? (copy_part % C::kAtoms) * kBlockKeys * 128 + copy_sub * sub_keys * 128
-                  : copy_sub * (C::kSideBytes / 2) + (copy_pairs ? kBlockKeys * (D / 2) : 0));
-  const int64_t copy_src = copy_pairs ? page * (D / 2) : 0;
+  // Bits 16: tensor-map copies, issued by one lane each (sub-block `lane /
+  // copies`; the 64-channel column blocks of keys, then of values), counted
+  // on the stage's mbarrier.  Bits 4: 16-byte copies by all lanes, one commit
+  // group a unit.  (Bulk copies of 2 KB and 0.5 KB cost 60 more instructions
+  // a unit: each is issued by a loop over the lanes that carry one.)
+  constexpr int kCopies = 2 * C::kAtoms;
+  const int copy_sub = lane / kCopies, copy_part = lane % kCopies;
+  const int copy_side = copy_part / C::kAtoms, copy_atom = copy_part % C::kAtoms;
+  const int64_t value_side = static_cast<int64_t>(a.c.kv_heads) * a.c.block_bytes;
 
   Place ld = place_of(a, heads, u0, lane);
   Place at = ld;
-  int64_t loaded = u0;
+  int64_t to_load = u1 - u0;  // units whose copies are still to be issued
   // Pages of the coming sub-blocks, one a lane; -1: not needed, or out of range.
   int page_reg = -1, page_next = 32;
-  int64_t lane_src = 0;  // this lane's copies: offset in a page (bits 4), or row (bits 16)
+  int64_t head_src = 0;  // this kv head's keys in a page: bytes (bits 4) or row (bits 16)
   auto issue = [&](int stage) {
     const int key0 = (ld.s.unit0 + ld.i) * kBlockKeys;
     if (page_next >= 32) {
@@ -363,38 +369,65 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
         }
       }
       page_next = 0;
-      const int block = copy_side * a.c.kv_heads + ld.hh / P.head_blocks;
-      lane_src = BITS == 16 ? block * page : block * a.c.block_bytes + copy_src;
+      head_src = (ld.hh / P.head_blocks) * (BITS == 16 ? page : a.c.block_bytes);
     }
-    const int pg = __shfl_sync(0xffffffffu, page_reg, page_next + (copier ? copy_sub : 0));
+    const int pg0 = __shfl_sync(0xffffffffu, page_reg, page_next);
+    const int pg1 = __shfl_sync(0xffffffffu, page_reg, page_next + subs - 1);
     page_next += subs;
-    const unsigned vote = __ballot_sync(0xffffffffu, copier && copy_part == 0 && pg >= 0);
     uint32_t mask = 0xffffffffu;
-    if (key0 < ld.s.lo || key0 + kBlockKeys > ld.s.n || __popc(vote) < subs) {
+    if (key0 < ld.s.lo || key0 + kBlockKeys > ld.s.n || (pg0 | pg1) < 0) {
       const int from = max(ld.s.lo - key0, 0), to = min(ld.s.n - key0, kBlockKeys);
       mask = (to == 32 ? 0xffffffffu : (1u << to) - 1u) & ~((1u << from) - 1u);
-      if (!(vote & 1u)) mask &= subs == 1 ? 0u : 0xffff0000u;
-      if (subs == 2 && !(vote >> copies)) mask &= 0xffffu;
+      if (pg0 < 0) mask &= subs == 1 ? 0u : 0xffff0000u;
+      if (pg1 < 0) mask &= subs == 1 ? 0u : 0xffffu;
     }
-    if (lane == 0) {
-      masks[stage] = mask;
-      if (vote)
-        mbar_arrive_expect_tx(&full[stage], __popc(vote) * (C::kStageBytes >> (subs - 1)));
-      else
-        mbar_arrive(&full[stage]);
+    if constexpr (BITS == 16) {
+      const int n = pg0 < 0 ? 0 : 1, valid = n + (subs == 1 || pg1 < 0 ? 0 : 1);
+      if (lane == 0) {
+        masks[stage] = mask;
+        if (valid)
+          mbar_arrive_expect_tx(&full[stage], valid * (C::kStageBytes >> (subs - 1)));
+        else
+          mbar_arrive(&full[stage]);
+      }
+      __syncwarp();  // armed, and the stage has been read by every lane
+      const int pg = copy_sub == 0 ? pg0 : pg1;
+      if (copy_sub < subs && pg >= 0) {
+        const int off = (key0 + (copy_sub << sub_shift)) & (page - 1);
+        tma_rows(ring + stage * C::kStageBytes + copy_side * C::kSideBytes +
+                     copy_atom * kBlockKeys * 128 + copy_sub * sub_keys * 128,
+                 &P.map, &full[stage], copy_atom * 64,
+                 static_cast<int>(head_src) + copy_side * a.c.kv_heads * page + off, pg);
+      }
+    } else {
+      if (lane == 0) masks[stage] = mask;
+      __syncwarp();  // the stage has been read by every lane
+      // Rows 0 .. 15 of the unit and rows 16 .. 31.
+      const int off0 = key0 & (page - 1), off1 = (key0 + 16) & (page - 1);
+      const uint8_t* block0 =
+          a.c.base + static_cast<uint64_t>(static_cast<uint32_t>(pg0)) * page_bytes + head_src;
+      const uint8_t* block1 =
+          a.c.base + static_cast<uint64_t>(static_cast<uint32_t>(pg1)) * page_bytes + head_src;
+      const uint32_t dst = ring + stage * C::kStageBytes + lane * 16;
+      auto rows = [&](const uint8_t* lower, const uint8_t* upper, auto n, uint32_t to) {
+        constexpr int chunks = decltype(n)::value, half = chunks / 2;
+#pragma unroll
+        for (int i = 0; i < (chunks + 31) / 32; ++i) {
+          const int ch = i * 32 + lane;
+          const bool second = ch >= half;
+          if (ch < chunks && (second ? pg1 : pg0) >= 0) {
+            const uint8_t* p = (second ? upper - half * 16 : lower) + ch * 16;
+            copy16(to + i * 512, p);
+            copy16(to + i * 512 + C::kSideBytes, p + value_side);
+          }
+        }
+      };
+      rows(block0 + off0 * (D / 2), block1 + off1 * (D / 2),
+           std::integral_constant<int, kBlockKeys * (D / 2) / 16>(), dst);
+      rows(block0 + page * (D / 2) + off0 * (D / 8), block1 + page * (D / 2) + off1 * (D / 8),
+           std::integral_constant<int, kBlockKeys * (D / 8) / 16>(), dst + kBlockKeys * (D / 2));
     }
-    __syncwarp();  // armed, and the stage has been read by every lane
-    if (copier && pg >= 0) {
-      const uint32_t dst = ring + stage * C::kStageBytes + copy_dst;
-      const int off = (key0 + (copy_sub << sub_shift)) & (page - 1);
-      if constexpr (BITS == 4)
-        bulk_load(dst, a.c.base + pg * a.c.page_bytes + lane_src + off * row_bytes,
-                  row_bytes << sub_shift, &full[stage]);
-      else
-        tma_rows(dst, &P.map, &full[stage], (copy_part % C::kAtoms) * 64,
-                 static_cast<int>(lane_src) + off, pg);
-    }
-    ++loaded;
+    --to_load;
     if (++ld.i >= ld.s.units) {
       --ld.i;
       next_place(a, heads, ld);
@@ -403,8 +436,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
   };
 
 #pragma unroll
-  for (int s = 0; s < C::kStages; ++s)
-    if (loaded < u1) issue(s);
+  for (int s = 0; s < C::kStages; ++s) {
+    if (to_load > 0) issue(s);
+    if constexpr (BITS == 4) copy_commit();  // a group a stage, empty behind the last unit
+  }
 
   // ------------------------------------------------------------ consumer --
   int64_t u = u0;
@@ -421,11 +456,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
     const int count = static_cast<int>(left < at.s.units - first ? left : at.s.units - first);
 
     // Queries as B fragments (column = head g): for 16 bits channels 16 s + 2 t,
-    // + 1 and + 8, + 9; for 4 bits in the order of the codes and scaled, as
-    // two e4m3 terms each.
-    constexpr int QS = BITS == 16 ? MS : NG;
-    uint32_t qf[NT][QS][2], qg[BITS == 16 ? 1 : NT][QS][2];
-    uint32_t qs[NT][2];  // Q_t: (-8 Q, Q) in two bf16 terms
+    // + 1 and + 8, + 9; for 4 bits in the order of the codes, scaled by a
+    // power of two into fp16.
+    uint32_t qf[NT][MS][2];
+    uint32_t qs[NT][2];  // Q_t: (-72 Q, Q) in two bf16 terms
     float to_log2[NT][2];  // scores of heads 2 t, 2 t + 1 to the log2 domain
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -458,35 +492,28 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
         const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
         const float down =
             __uint_as_float(expo == 255 ? 0x7fffffffu
-                                        : static_cast<uint32_t>(min(127 + 9 - shift, 254)) << 23);
+                                        : static_cast<uint32_t>(min(127 - shift, 254)) << 23);
         qs[nt][0] = qs[nt][1] = 0;
 #pragma unroll
         for (int wq = 0; wq < NG; ++wq) {
           const uint32_t x[4] = {v[wq].x, v[wq].y, v[wq].z, v[wq].w};
-          uint32_t hi[4], lo[4];  // (2 e, 2 e + 1) of the lane's channels
-          float sum = 0.f;
+          float y[8], sum = 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float y0 = bf16_lo(x[e]) * up, y1 = bf16_hi(x[e]) * up;
-            sum += y0 + y1;
-            hi[e] = to_e4m3x2(y0, y1);
-            const float2 z = from_e4m3x2(hi[e]);
-            lo[e] = to_e4m3x2(y0 - z.x, y1 - z.y);
+            y[2 * e] = bf16_lo(x[e]) * up;
+            y[2 * e + 1] = bf16_hi(x[e]) * up;
+            sum += y[2 * e] + y[2 * e + 1];
           }
-          // Even channels meet the low nibbles of the code bytes, odd ones the high.
-          const uint32_t h01 = hi[0] | hi[1] << 16, h23 = hi[2] | hi[3] << 16;
-          const uint32_t l01 = lo[0] | lo[1] << 16, l23 = lo[2] | lo[3] << 16;
-          qf[nt][wq][0] = __byte_perm(h01, h23, 0x6420);
-          qf[nt][wq][1] = __byte_perm(h01, h23, 0x7531);
-          qg[nt][wq][0] = __byte_perm(l01, l23, 0x6420);
-          qg[nt][wq][1] = __byte_perm(l01, l23, 0x7531);
+          qf[nt][2 * wq][0] = pack_f16x2(y[0], y[4]);
+          qf[nt][2 * wq][1] = pack_f16x2(y[1], y[5]);
+          qf[nt][2 * wq + 1][0] = pack_f16x2(y[2], y[6]);
+          qf[nt][2 * wq + 1][1] = pack_f16x2(y[3], y[7]);
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          sum *= 1.f / 512;  // the codes enter as u / 512
-          const uint32_t top = pack_bf16x2(-8.f * sum, sum);
+          const uint32_t top = pack_bf16x2(-72.f * sum, sum);
           if (t == wq) {
             qs[nt][0] = top;
-            qs[nt][1] = pack_bf16x2(-8.f * sum - bf16_lo(top), sum - bf16_hi(top));
+            qs[nt][1] = pack_bf16x2(-72.f * sum - bf16_lo(top), sum - bf16_hi(top));
           }
         }
         to_log2[nt][0] *= __shfl_sync(0xffffffffu, down, 8 * t);
@@ -510,16 +537,22 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
     }
 
     for (int blk = 0; blk < count; ++blk) {
-      if (!mbar_wait_warp(&full[stage], parity, abort_flag, a.status)) {
-        ok = false;
-        break;
+      if constexpr (BITS == 16) {
+        if (!mbar_wait_warp(&full[stage], parity, abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+      } else {
+        copy_wait<C::kStages - 1>();
+        __syncwarp();
       }
       const uint32_t keys = ring + stage * C::kStageBytes;
       const uint32_t vals = keys + C::kSideBytes;
+      const uint8_t* key_rows = ring_rows + stage * C::kStageBytes;
+      const uint8_t* val_rows = key_rows + C::kSideBytes;
       // 4 bits: codes and pairs of the two 16-key tiles within a side.
-      const uint32_t code1 = subs == 1 ? 16 * (D / 2) : C::kSideBytes / 2;
-      const uint32_t pair0 = subs == 1 ? 32 * (D / 2) : 16 * (D / 2);
-      const uint32_t pair1 = pair0 + (subs == 1 ? 16 * (D / 8) : C::kSideBytes / 2);
+      constexpr uint32_t code1 = 16 * (D / 2), pair0 = kBlockKeys * (D / 2);
+      constexpr uint32_t pair1 = pair0 + 16 * (D / 8);
       const uint32_t mask = masks[stage];
 
       // ---- scores of the unit's two 16-key tiles: s[tile][nt]: keys g (0, 1)
@@ -527,10 +560,6 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
       float s[2][NT][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[h][nt][e] = 0.f;
         if constexpr (BITS == 16) {
           const int row = 16 * h + (lane & 15);
 #pragma unroll
@@ -539,12 +568,17 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
             uint32_t f[4];
             ldmatrix4(f, keys + (m / 4) * kBlockKeys * 128 + row * 128 + ((chunk ^ (row & 7)) << 4));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_bf16(s[h][nt], f[0], f[1], f[2], f[3], qf[nt][m][0], qf[nt][m][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              if (m == 0)
+                mma_bf16_zero(s[h][nt], f[0], f[1], f[2], f[3], qf[nt][m][0], qf[nt][m][1]);
+              else
+                mma_bf16(s[h][nt], f[0], f[1], f[2], f[3], qf[nt][m][0], qf[nt][m][1]);
+            }
           }
         } else {
           const int ka = key_of_row(g), kb = ka + 8;
-          const uint32_t codes = keys + (h ? code1 : 0), pairs = keys + (h ? pair1 : pair0);
+          const uint8_t* codes = key_rows + (h ? code1 : 0);
+          const uint8_t* pairs = key_rows + (h ? pair1 : pair0);
           uint32_t ca[NG], cb[NG], pa[NG], pb[NG];
           lds_words<NG>(ca, codes + ka * (D / 2) + t * 4 * NG);
           lds_words<NG>(cb, codes + kb * (D / 2) + t * 4 * NG);
@@ -553,19 +587,20 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
           const uint32_t wa = t < NG ? lds32(pairs + ka * (D / 8) + 4 * (t < NG ? t : 0)) : 0u;
           const uint32_t wb = t < NG ? lds32(pairs + kb * (D / 8) + 4 * (t < NG ? t : 0)) : 0u;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_bf16(s[h][nt], wa, wb, wa, wb, qs[nt][0], qs[nt][1]);
+          for (int nt = 0; nt < NT; ++nt)
+            mma_bf16_zero(s[h][nt], wa, wb, wa, wb, qs[nt][0], qs[nt][1]);
 #pragma unroll
           for (int wq = 0; wq < NG; ++wq) {
-            // Four codes a register, as they lie in its bytes: the e4m3 bit
-            // pattern u (0 .. 15) is the number u / 512.
-            const uint32_t a0 = ca[wq] & 0x0f0f0f0fu, a2 = (ca[wq] >> 4) & 0x0f0f0f0fu;
-            const uint32_t a1 = cb[wq] & 0x0f0f0f0fu, a3 = (cb[wq] >> 4) & 0x0f0f0f0fu;
             const float sa = bf16_lo(pa[wq]), sb = bf16_lo(pb[wq]);
+            const uint32_t a0 = nibbles64<0>(ca[wq]), a2 = nibbles64<1>(ca[wq]);
+            const uint32_t a4 = nibbles64<2>(ca[wq]), a6 = nibbles64<3>(ca[wq]);
+            const uint32_t b0 = nibbles64<0>(cb[wq]), b2 = nibbles64<1>(cb[wq]);
+            const uint32_t b4 = nibbles64<2>(cb[wq]), b6 = nibbles64<3>(cb[wq]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float acc[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_e4m3(acc, a0, a1, a2, a3, qf[nt][wq][0], qf[nt][wq][1]);
-              mma_e4m3(acc, a0, a1, a2, a3, qg[nt][wq][0], qg[nt][wq][1]);
+              float acc[4];
+              mma_f16_zero(acc, a0, b0, a2, b2, qf[nt][2 * wq][0], qf[nt][2 * wq][1]);
+              mma_f16(acc, a4, b4, a6, b6, qf[nt][2 * wq + 1][0], qf[nt][2 * wq + 1][1]);
               s[h][nt][0] = fmaf(sa, acc[0], s[h][nt][0]);
               s[h][nt][1] = fmaf(sa, acc[1], s[h][nt][1]);
               s[h][nt][2] = fmaf(sb, acc[2], s[h][nt][2]);
@@ -591,26 +626,6 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
 
       // ---- weights.  The reference max of a head is the same in all lanes
       // and is raised only when a score passes it by more than 2^8.
-      // P^T fragments: column = head g, rows keys 2 t, 2 t + 1 / + 8; for bits 4
-      // pw[h][nt][w] holds P^T times the scales of group w.
-      uint32_t pf[2][NT][2], pw[2][BITS == 4 ? NT : 1][BITS == 4 ? NG : 1][2];
-      float scale_a[2][BITS == 4 ? NG : 1], scale_b[2][BITS == 4 ? NG : 1];
-      if constexpr (BITS == 4) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t pairs = vals + (h ? pair1 : pair0);
-          const int ka = key_of_row(g);
-          uint32_t pa[NG], pb[NG];
-          lds_words<NG>(pa, pairs + ka * (D / 8));
-          lds_words<NG>(pb, pairs + (ka + 8) * (D / 8));
-          const bool va = (mask >> (16 * h + ka)) & 1u, vb = (mask >> (16 * h + ka + 8)) & 1u;
-#pragma unroll
-          for (int wv = 0; wv < NG; ++wv) {
-            scale_a[h][wv] = va ? bf16_lo(pa[wv]) : 0.f;
-            scale_b[h][wv] = vb ? bf16_lo(pb[wv]) : 0.f;
-          }
-        }
-      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float mx[2];
@@ -641,32 +656,25 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
 #pragma unroll
           for (int e = 0; e < 4; ++e) oc[nt][e] *= alpha[e & 1];
         }
-        const float m0 = m_ref[nt][0] == -INFINITY ? 0.f : m_ref[nt][0];
-        const float m1 = m_ref[nt][1] == -INFINITY ? 0.f : m_ref[nt][1];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            p[e] = fast_exp2(fmaf(s[h][nt][e], to_log2[nt][e & 1], (e & 1) ? -m1 : -m0));
-          l[nt][0] += p[0] + p[2];
-          l[nt][1] += p[1] + p[3];
-          pf[h][nt][0] = transpose8x8(pack_bf16x2(p[0], p[1]));
-          pf[h][nt][1] = transpose8x8(pack_bf16x2(p[2], p[3]));
-          if constexpr (BITS == 4) {
-#pragma unroll
-            for (int wv = 0; wv < NG; ++wv) {
-              const float sa = scale_a[h][wv], sb = scale_b[h][wv];
-              pw[h][nt][wv][0] = transpose8x8(pack_bf16x2(p[0] * sa, p[1] * sa));
-              pw[h][nt][wv][1] = transpose8x8(pack_bf16x2(p[2] * sb, p[3] * sb));
-            }
-          }
-        }
       }
 
-      // ---- O^T += V^T P^T
+      // ---- tile by tile: P, then O^T += V^T P^T
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        float p[NT][4];        // keys g, g + 8, heads 2 t, 2 t + 1, as the scores
+        uint32_t pf[NT][2];    // P^T fragments: column = head g, rows keys 2 t, 2 t + 1 / + 8
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float m0 = m_ref[nt][0] == -INFINITY ? 0.f : m_ref[nt][0];
+          const float m1 = m_ref[nt][1] == -INFINITY ? 0.f : m_ref[nt][1];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            p[nt][e] = fast_exp2(fmaf(s[h][nt][e], to_log2[nt][e & 1], (e & 1) ? -m1 : -m0));
+          l[nt][0] += p[nt][0] + p[nt][2];
+          l[nt][1] += p[nt][1] + p[nt][3];
+          pf[nt][0] = transpose8x8(pack_bf16x2(p[nt][0], p[nt][1]));
+          pf[nt][1] = transpose8x8(pack_bf16x2(p[nt][2], p[nt][3]));
+        }
         if constexpr (BITS == 16) {
           const int row = 16 * h + (lane & 7) + ((lane >> 4) << 3);
           uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
@@ -684,11 +692,16 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma_bf16(o[nt][m], f[0] & keep0, f[1] & keep0, f[2] & keep1, f[3] & keep1,
-                       pf[h][nt][0], pf[h][nt][1]);
+                       pf[nt][0], pf[nt][1]);
           }
         } else {
           // Rows of this lane: keys t, t + 4 (first half), t + 8, t + 12.
-          const uint32_t codes = vals + (h ? code1 : 0), pairs = vals + (h ? pair1 : pair0);
+          const uint8_t* codes = val_rows + (h ? code1 : 0);
+          const uint8_t* pairs = val_rows + (h ? pair1 : pair0);
+          const int ka = key_of_row(g);  // this lane's rows of p: keys ka, ka + 8
+          uint32_t pa[NG], pb[NG];
+          lds_words<NG>(pa, pairs + ka * (D / 8));
+          lds_words<NG>(pb, pairs + (ka + 8) * (D / 8));
           uint32_t cw[4];  // pair of group g (rows from NG on repeat group 0)
 #pragma unroll
           for (int x = 0; x < 4; ++x)
@@ -697,18 +710,24 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
               cw[x] = ((mask >> (16 * h + t + 4 * x)) & 1u) ? cw[x] : 0u;
+            const bool va = (mask >> (16 * h + ka)) & 1u, vb = (mask >> (16 * h + ka + 8)) & 1u;
+#pragma unroll
+            for (int wv = 0; wv < NG; ++wv) {
+              pa[wv] = va ? pa[wv] : 0u;
+              pb[wv] = vb ? pb[wv] : 0u;
+            }
           }
           // Centres: row g of the product is group g.
           const uint32_t c0 = __byte_perm(cw[0], cw[1], 0x7632);
           const uint32_t c1 = __byte_perm(cw[2], cw[3], 0x7632);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma_bf16(oc[nt], c0, 0u, c1, 0u, pf[h][nt][0], pf[h][nt][1]);
+            mma_bf16(oc[nt], c0, 0u, c1, 0u, pf[nt][0], pf[nt][1]);
           // Codes: half-word w of this lane's NG holds channels 32 w + 4 g .. + 3.
           uint32_t cv[4][(NG + 1) / 2];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const uint32_t row = codes + (t + 4 * x) * (D / 2) + g * 2 * NG;
+            const uint8_t* row = codes + (t + 4 * x) * (D / 2) + g * 2 * NG;
             if constexpr (NG % 2 == 0) {
               lds_words<NG / 2>(cv[x], row);
             } else {
@@ -727,21 +746,24 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
             const uint32_t sel = (wv & 1) ? 0x7632u : 0x5410u;
             const uint32_t v0 = __byte_perm(cv[0][wv / 2], cv[1][wv / 2], sel);
             const uint32_t v1 = __byte_perm(cv[2][wv / 2], cv[3][wv / 2], sel);
-            const uint32_t e0 = minus24(nibbles16<0>(v0)), e1 = minus24(nibbles16<1>(v0));
-            const uint32_t e2 = minus24(nibbles16<2>(v0)), e3 = minus24(nibbles16<3>(v0));
-            const uint32_t f0 = minus24(nibbles16<0>(v1)), f1 = minus24(nibbles16<1>(v1));
-            const uint32_t f2 = minus24(nibbles16<2>(v1)), f3 = minus24(nibbles16<3>(v1));
+            uint32_t e[4], f[4];
+            codes_bf16(v0, e);
+            codes_bf16(v1, f);
+            const float sa = bf16_lo(pa[wv]), sb = bf16_lo(pb[wv]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_bf16(o[nt][2 * wv], e0, e1, f0, f1, pw[h][nt][wv][0], pw[h][nt][wv][1]);
-              mma_bf16(o[nt][2 * wv + 1], e2, e3, f2, f3, pw[h][nt][wv][0], pw[h][nt][wv][1]);
+              const uint32_t w0 = transpose8x8(pack_bf16x2(p[nt][0] * sa, p[nt][1] * sa));
+              const uint32_t w1 = transpose8x8(pack_bf16x2(p[nt][2] * sb, p[nt][3] * sb));
+              mma_bf16(o[nt][2 * wv], e[0], e[1], f[0], f[1], w0, w1);
+              mma_bf16(o[nt][2 * wv + 1], e[2], e[3], f[2], f[3], w0, w1);
             }
           }
         }
       }
 
       // ---- refill the stage
-      if (loaded < u1) issue(stage);
+      if (to_load > 0) issue(stage);
+      if constexpr (BITS == 4) copy_commit();
       if (++stage == C::kStages) {
         stage = 0;
         parity ^= 1u;
@@ -819,10 +841,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
     at.i += count - 1;
     if (u < u1) next_place(a, heads, at);
   }
-  if (!ok) {
+  if (BITS == 16 && !ok) {
     // Let this warp's copies land before the block goes away.
     volatile int no_abort = 0;
-    const int64_t flight = loaded - u;
+    const int64_t flight = u1 - u - to_load;
     for (int64_t n = 0; n < flight && n < C::kStages; ++n) {
       mbar_wait_warp(&full[stage], parity, &no_abort, a.status);
       if (++stage == C::kStages) {
@@ -836,8 +858,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
 // Joins the shares of the segments that were cut.  Block w looks at the
 // boundary between shares w - 1 and w: where it falls inside a segment of n
 // shares, the n - 1 boundary blocks split the segment's (head, 32-channel)
-// outputs among them.  Warps take every eighth share; their sums are joined
-// in shared memory in order.
+// outputs among them.
 template <int NT>
 __global__ void __launch_bounds__(kJoinThreads) swa_paged_join_kernel(const PagedParams P, int d) {
   const SwaPagedArgs& a = P.a;
@@ -861,8 +882,14 @@ __global__ void __launch_bounds__(kJoinThreads) swa_paged_join_kernel(const Page
   const int head0 = kvh * P.group + (p.hh % P.head_blocks) * 8 * NT;
   const int nheads = min(8 * NT, (kvh + 1) * P.group - head0);
   const int chunks = (d + 31) / 32;
-  for (int task = me; task < nheads * chunks; task += n - 1) {
-    const int head = task / chunks, c = (task % chunks) * 32 + lane;
+  const int tasks = nheads * chunks;
+  // Few shares: a warp takes an output piece alone; many: all warps share one.
+  const bool alone = n <= kJoinThreads / 32;
+  const int step = alone ? 1 : kJoinThreads / 32;
+  for (int task0 = me; task0 < tasks; task0 += (n - 1) * (alone ? kJoinThreads / 32 : 1)) {
+    const int task = alone ? task0 + warp * (n - 1) : task0;
+    const bool live = task < tasks;
+    const int head = live ? task / chunks : 0, c = live ? (task % chunks) * 32 + lane : d;
     float mx = -INFINITY;
     for (int x = lane; x < n; x += 32) {
       const int64_t slot = 2 * (w0 + x) + (x == 0 ? 1 : 0);
@@ -872,28 +899,28 @@ __global__ void __launch_bounds__(kJoinThreads) swa_paged_join_kernel(const Page
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float ref = mx == -INFINITY ? 0.f : mx;
     float acc = 0.f, l = 0.f;
-#pragma unroll 4
-    for (int x = warp; x < n; x += kJoinThreads / 32) {
+#pragma unroll 8
+    for (int x = alone ? 0 : warp; x < n; x += step) {
       const int64_t slot = 2 * (w0 + x) + (x == 0 ? 1 : 0);
       const float f = exp2f(P.part_ml[(slot * 2) * (8 * NT) + head] - ref);
       l = fmaf(f, P.part_ml[(slot * 2 + 1) * (8 * NT) + head], l);
       if (c < d) acc = fmaf(f, P.part_o[(slot * (8 * NT) + head) * d + c], acc);
     }
-    so[warp][lane] = acc;
-    if (lane == 0) sl[warp] = l;
-    __syncthreads();
-    if (warp == 0) {
-      float o = 0.f, sum = 0.f;
+    if (!alone) {
+      so[warp][lane] = acc;
+      if (lane == 0) sl[warp] = l;
+      __syncthreads();
+      acc = l = 0.f;
 #pragma unroll
       for (int x = 0; x < kJoinThreads / 32; ++x) {
-        o += so[x][lane];
-        sum += sl[x];
+        acc += so[x][lane];
+        l += sl[x];
       }
-      if (c < d)
-        a.o[p.b * a.o_sb + (head0 + head) * a.o_sh + c] =
-            __float2bfloat16_rn(sum != 0.f ? o / sum : 0.f);
+      __syncthreads();
     }
-    __syncthreads();
+    if ((alone || warp == 0) && c < d)
+      a.o[p.b * a.o_sb + (head0 + head) * a.o_sh + c] =
+          __float2bfloat16_rn(l != 0.f ? acc / l : 0.f);
   }
 }
 

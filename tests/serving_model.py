@@ -10,12 +10,11 @@ where with 4 bits |v| counts scale |u - 8| + |centre|.  E bounds the error of a 
 s = q.k * scale in fp32: every one of d products and sums is off by at most 2^-23 of the sum of
 magnitudes (tensor-core sums truncate), and so E = (d + 8) 2^-23 max_j sum |q||k| scale; a relative
 error E of each weight moves numerator and denominator, hence 2 E.  The 4-bit kernel forms
-q.k = sum_w scale_w (q.u)_w + (centre_w - 8 scale_w) Q_w: magnitudes are counted as
-|q| (scale (u + 8) + |centre|).  Q_w, the sum of q over a group, is held in two bf16 terms (off by
-2^-16 of it): 2^-16 |Q| (8 scale + |centre|) is added.  q is held in two e4m3 terms after scaling
-its largest entry into [128, 256): the first leaves at most 8 units of a bf16 value's last place,
-which the second holds exactly unless they fall below half of e4m3's least step, 2^-10: an entry is
-off by at most 2^-10 / 128 of the largest, and 2^-17 max|q| sum scale u is added.
+q.k = sum_w scale_w (q.(64 + u))_w + (centre_w - 72 scale_w) Q_w: magnitudes are counted as
+|q| (scale (136 + u) + |centre|).  Q_w, the sum of q over a group, is held in two bf16 terms (off by
+2^-16 of it): 2^-16 |Q| (72 scale + |centre|) is added.  q is held in fp16 after scaling its largest
+entry into [128, 256): an entry is off by at most 2^-25 / 128 of the largest, which the first term
+covers.
 """
 import numpy as np
 import torch
@@ -167,11 +166,10 @@ def paged(q, cache, table, lens, window, scale):
                 if u is None:
                     mk[j - lo, h] = np.abs(k[j - lo, h])
                 else:
-                    mk[j - lo, h] = s * (8 + u) + np.abs(z)
+                    mk[j - lo, h] = s * (136 + u) + np.abs(z)
                     for x in range(h * g, (h + 1) * g):
                         qs = np.abs(q[b, x].reshape(-1, 32).sum(-1))
-                        extra[0, x, j - lo] = (2.0 ** -16 * (qs * (8 * s + np.abs(z)).reshape(-1, 32)[:, 0]).sum()
-                                               + 2.0 ** -17 * np.abs(q[b, x]).max() * (s * u).sum())
+                        extra[0, x, j - lo] = 2.0 ** -16 * (qs * (72 * s + np.abs(z)).reshape(-1, 32)[:, 0]).sum()
                 v[j - lo, h], u, s, z = cache.get(page, off, h, 1)
                 mv[j - lo, h] = np.abs(v[j - lo, h]) if u is None else s * np.abs(u - 8) + np.abs(z)
         ob, bb = attend(q[b:b + 1], k, v, n - lo - 1, n, scale, mk, mv, extra)
