@@ -37,6 +37,7 @@ constexpr int QT = 2;         // query tiles per work item
 constexpr int BKV = 64;       // keys per K/V tile (= MMA N of S, K of PV)
 constexpr int kThreads = 448;
 constexpr int kCleanWarp = 13;
+constexpr int kHeldItems = 64;  // a CTA's first items, held in shared memory
 constexpr int kBadSlots = 8;  // > items that the K/V ring can hold at once
 constexpr float kRescaleLog2 = 8.0f;  // raise the reference max only past 2^8
 
@@ -46,7 +47,8 @@ struct Cfg {
   static constexpr int kQTileBytes = kAtoms * BQ * 128;
   static constexpr int kKVBytes = kAtoms * BKV * 128;
   static constexpr int kOStageBytes = 32 * 128;
-  static constexpr int kFixed = QT * kQTileBytes + 4 * QT * kOStageBytes + 512 + 1024;
+  static constexpr int kFixed =
+      QT * kQTileBytes + 4 * QT * kOStageBytes + kHeldItems * 16 + 512 + 1024;
   static constexpr int kNSFit = (227 * 1024 - kFixed) / (2 * kKVBytes);
   static constexpr int kNS = kNSFit < 6 ? kNSFit : 6;
   static constexpr int kSmemBytes = kFixed + kNS * 2 * kKVBytes;
@@ -66,6 +68,8 @@ struct Block {
 
 struct PackedParams {
   CUtensorMap tq, tk, tv;  // {d, heads, tokens}
+  CUtensorMap to;          // the output, in boxes of 32 rows of a tile
+  int store_boxes;         // 32 rows of a tile are a box (G a power of two)
   SwaPackedArgs a;
   int group, tq_tokens;    // G, TQ
   unsigned inv_group;      // r / G = r * inv_group >> 16 for r < 128
@@ -216,6 +220,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int32_t c0,
+                                             int32_t c1, int32_t c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::
+                   "l"(reinterpret_cast<uint64_t>(map)),
+               "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
 // Bits 15 and 31: the low / high bf16 of w is not finite.
 __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
@@ -234,7 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sK = sQ + QT * C::kQTileBytes;           // [NS][kKVBytes]
   uint8_t* sV = sK + NS * C::kKVBytes;              // [NS][kKVBytes]
   uint8_t* sO = sV + NS * C::kKVBytes;              // [4 * QT][kOStageBytes]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sO + 4 * QT * C::kOStageBytes);
+  int4* held = reinterpret_cast<int4*>(sO + 4 * QT * C::kOStageBytes);  // [kHeldItems]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(held + kHeldItems);
   uint64_t* q_full = bars;
   uint64_t* q_empty = q_full + 1;
   uint64_t* kv_full = q_empty + 1;      // [NS]
@@ -244,13 +257,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = s_full + 2 * QT;   // [QT][2]: P in score buffer 0 / 1
   uint64_t* pv_done = p_full + 2 * QT;  // [QT][2]: P V of score buffer 0 / 1
   uint64_t* done_bar = pv_done + 2 * QT;  // [2 * QT]: one per issuing thread
-  int4* own_block = reinterpret_cast<int4*>(
-      (reinterpret_cast<uintptr_t>(done_bar + 2 * QT) + 15) & ~static_cast<uintptr_t>(15));
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(own_block + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 2 * QT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* own_count = abort_flag + 1;
   volatile int* bad_item = own_count + 1;  // [kBadSlots]: item k cleared values: k + 1 in k % slots
-  static_assert((2 + 3 * C::kNS + 4 * 2 * QT) * 8 + 16 + 16 + 4 * (3 + kBadSlots) <= 512, "barriers");
+  static_assert((2 + 3 * C::kNS + 4 * 2 * QT) * 8 + 4 * (3 + kBadSlots) <= 512, "barriers");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -290,17 +301,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     int4 e = make_int4(0, 0, 0, 0);
     const bool found = find_block(a, QT * TQ, blockIdx.x / a.kv_heads, lane, &e);
     if (lane == 0) {
-      *own_block = e;
+      held[0] = e;
       *own_count = found ? 1 : 0;
     }
+  }
+  // The list of this CTA's items, so that no role waits for global memory
+  // between two of them.
+  const int listed = P.count ? *P.count * a.kv_heads : 0;
+  if (P.count && threadIdx.x < kHeldItems) {
+    const int item = snake_item(threadIdx.x);
+    if (item < listed) held[threadIdx.x] = P.blocks[item / a.kv_heads];
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int num_items = P.count ? *P.count * a.kv_heads : (*own_count ? gridDim.x : 0);
-  auto item_at = [&](int item) -> Item {
-    const int4 e = P.count ? P.blocks[item / a.kv_heads] : *own_block;
+  const int num_items = P.count ? listed : (*own_count ? gridDim.x : 0);
+  auto item_at = [&](int k, int item) -> Item {
+    const int4 e = k < kHeldItems ? held[k] : P.blocks[item / a.kv_heads];
     return make_item(e, item % a.kv_heads, a.window);
   };
 
@@ -311,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t kv_count = 0, q_count = 0;
       uint32_t armed = 0, armed_parity = 0;
       for (int k = 0, item = snake_item(0); ok && item < num_items; item = snake_item(++k)) {
-        const Item it = item_at(item);
+        const Item it = item_at(k, item);
         if (it.n_tiles == 0) continue;
         if (!mbar_wait(q_empty, (q_count & 1) ^ 1u, abort_flag, a.status)) {
           ok = false;
@@ -363,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t kv_count = 0, q_count = 0, issued = 0;
       const uint32_t qx = smem_addr(sQ + x * C::kQTileBytes);
       for (int k = 0, item = snake_item(0); ok && item < num_items; item = snake_item(++k)) {
-        const Item it = item_at(item);
+        const Item it = item_at(k, item);
         if (it.n_tiles == 0) continue;
         if (!pv_role) {
           if (!mbar_wait(q_full, q_count & 1, abort_flag, a.status)) break;
@@ -448,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t kv_count = 0;
     for (int k = 0, item = snake_item(0); ok && item < num_items; item = snake_item(++k)) {
-      const Item it = item_at(item);
+      const Item it = item_at(k, item);
       for (int j = 0; j < it.n_tiles; ++j, ++kv_count) {
         const int st = kv_count % NS;
         if (!mbar_wait_warp(&kv_full[st], (kv_count / NS) & 1, abort_flag, a.status)) {
@@ -506,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     for (int k = 0, item = snake_item(0); ok && item < num_items; item = snake_item(++k)) {
-      const Item it = item_at(item);
+      const Item it = item_at(k, item);
       if (x * TQ >= it.ntok) continue;
       const int i = it.p0 + x * TQ + tok;  // position of this thread's query
       float m_ref = -INFINITY, l_run = 0.f;
@@ -618,13 +636,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool bad = any_pv && bad_item[k % kBadSlots] == k + 1;
       // One 64-column block at a time: each warp writes its 32 rows into its
       // own 4 KB of shared memory (16-byte chunk c of row r at
-      // r * 128 + ((c ^ (r % 8)) * 16)) and stores them as whole rows, 8 lanes
-      // to a 128-byte line.  A tensor-map store would write the rows of the
-      // next sequence behind a short block.
+      // r * 128 + ((c ^ (r % 8)) * 16), the layout of a 128-byte-swizzled box).
+      // Where all 32 rows belong to the item and are a box of the output
+      // (G divides 32 or 32 divides G) its lane 0 stores them with TMA, else
+      // they are stored as whole rows, 8 lanes to a 128-byte line: a box
+      // would reach into the next sequence.  175B-class heads, four prompts:
+      // 10 us of 130 more with rows alone.
+      const int row0 = quarter * 32, tok0 = static_cast<int>((row0 * P.inv_group) >> 16);
+      const int tok31 = static_cast<int>(((row0 + 31) * P.inv_group) >> 16);
+      const bool boxed = P.store_boxes && x * TQ + tok31 < it.ntok;
       uint8_t* stage = sO + (x * 4 + quarter) * C::kOStageBytes;
       constexpr int kCols = D < 32 ? D : 32;  // columns per TMEM load
 #pragma unroll
       for (int at = 0; at < C::kAtoms; ++at) {
+        // The block stored before (of this item or the last one) has left shared memory.
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
 #pragma unroll
         for (int c = at * 64; c < min(D, at * 64 + 64); c += kCols) {
           uint32_t o[32];
@@ -663,6 +690,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                            pack_bf16x2(f[e + 4], f[e + 5]), pack_bf16x2(f[e + 6], f[e + 7]));
           }
         }
+        if (boxed) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&P.to, stage, at * 64, it.kvh * G + row0 - tok0 * G,
+                         it.q_row + x * TQ + tok0);
+            bulk_commit_group();
+          }
+          continue;
+        }
         __syncwarp();
         const int chunk = lane & 7, col = at * 64 + chunk * 8;
 #pragma unroll
@@ -678,6 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
     }
+    // The output stores this warp issued complete before the CTA ends.
+    if (lane == 0) bulk_wait_all();
   }
 
   __syncwarp();
@@ -744,6 +783,12 @@ cudaError_t launch_swa_packed(const SwaPackedArgs& a, cudaStream_t stream) {
   prm.inv_group = (65536u + prm.group - 1) / prm.group;
   if (!packed_map(&prm.tq, a.q, a.head_dim, a.heads, a.tokens_q, a.q_st, a.q_sh, prm.group,
                   prm.tq_tokens))
+    return cudaErrorInvalidValue;
+  // 32 rows of a tile: 32 / G tokens of all G heads, or 32 heads of a token.
+  const int g = prm.group;
+  prm.store_boxes = (g & (g - 1)) == 0;
+  if (prm.store_boxes && !packed_map(&prm.to, a.o, a.head_dim, a.heads, a.tokens_q, a.o_st, a.o_sh,
+                                     g < 32 ? g : 32, g < 32 ? 32 / g : 1))
     return cudaErrorInvalidValue;
   // Without keys the maps are never used; they still need a valid address.
   const bool keys = a.tokens_k > 0;
