@@ -9,15 +9,17 @@
 // as columns, O^T += V^T P^T with 16 channels as rows.
 //
 // Work split.  The unit is a block of 32 keys of one (sequence, kv head, up to
-// 16 query heads).  All units of the call, in order, are dealt to all warps of
-// the grid in equal contiguous shares, whatever the sequences' lengths: one
-// long sequence spreads over the whole GPU and a ragged batch stays even.  A
-// warp works alone: it streams its blocks through its own ring in shared
-// memory (bulk copies, completion on mbarriers), keeps maximum, sum and output
-// of the current segment in registers, and writes the output itself where a
-// share holds all of a segment.  The shares of a segment that was cut leave
-// (maximum, sum, output) in the workspace, and a second kernel, launched to
-// overlap this one's end, joins them in order: the same bits every time.
+// 16 query heads).  All units of the call, in order, are dealt to the blocks,
+// one per SM, and a block's to its warps, in equal contiguous shares, whatever
+// the sequences' lengths: one long sequence spreads over the whole GPU and a
+// ragged batch stays even.  A warp works alone: it streams its units through
+// its own ring in shared memory, keeps maximum, sum and output of the current
+// segment in registers, and writes the output itself where it holds all of a
+// segment.  Partial results of cut segments are joined in shared memory at
+// the block's end, and those cut between blocks by a second kernel, launched
+// to overlap this one's end.  The order is fixed: the same bits every time.
+// (Joining all warps' parts in the second kernel cost 10 us on one long
+// sequence, of 22.)
 //
 // 4-bit rows:
 //   q.k = sum_w scale_w (q.(64 + u))_w + (centre_w - 72 scale_w) Q_w,  Q_w = sum of q over group w,
@@ -44,10 +46,8 @@
 namespace ptb {
 namespace {
 
-constexpr int kWarps = 4;        // warps of a block; they share nothing
 constexpr int kBlockKeys = 32;   // keys of a unit
-constexpr int kMinUnits = 2;     // a warp's share is at least this many units
-constexpr int kMaxWarpsPerSm = 16;
+constexpr int kMinUnits = 4;     // a block's share is at least this many units
 constexpr float kRescaleLog2 = 8.0f;  // raise the reference max only past 2^8
 constexpr int kJoinThreads = 256;
 
@@ -61,22 +61,27 @@ struct Cfg {
   static constexpr int kSideBytes =
       BITS == 16 ? kAtoms * kBlockKeys * 128 : kBlockKeys * (D / 2 + D / 8);
   static constexpr int kStageBytes = 2 * kSideBytes;
-  static constexpr int kStages = 3;
-  static constexpr int kWarpBytes = kStages * kStageBytes;
-  static constexpr int kSmemBytes = 1024 + kWarps * (kWarpBytes + 64);
-  static constexpr int kFit = (227 * 1024) / (kSmemBytes + 1024);
-  static constexpr int kMost = BITS == 16 ? 3 : (NT == 1 ? 3 : 2);
-  static constexpr int kBlocksPerSm = kFit < kMost ? (kFit < 1 ? 1 : kFit) : kMost;
+  // Bits 4: two stages a warp do as well as three (229 us each where it was
+  // measured) and leave room for the partial result.
+  static constexpr int kStages = BITS == 4 ? 2 : 3;
+  // Warps of a block, one block per SM: as many as registers (4 bits: 168 or
+  // 255 a thread) or shared memory (16 bits) allow.
+  static constexpr int kWarps =
+      BITS == 4 ? (NT == 1 ? 12 : 8) : (D > 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 8 : 7));
+  // A partial result: maxima and sums of 8 NT heads, then their outputs.
+  static constexpr int kSlotBytes = 8 * NT * (2 + D) * 4;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static_assert(kRingBytes >= kSlotBytes, "a warp's last partial result lies over its ring");
+  static constexpr int kWarpBytes = (kRingBytes + kSlotBytes + 1023) / 1024 * 1024;
+  static constexpr int kSmemBytes = 1024 + kWarps * (kWarpBytes + 128);
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
-static_assert(4 * kWarps <= kMaxWarpsPerSm, "workspace is sized by kMaxWarpsPerSm");
 
 struct PagedParams {
   CUtensorMap map;  // bits 16: {d, rows of a page, pages}
   SwaPagedArgs a;
   int group, head_blocks;  // G; blocks of 8 NT query heads of a kv head
-  int warps;               // of the whole grid
-  float* part_ml;          // [2 warps][2][8 NT]
-  float* part_o;           // [2 warps][8 NT][d]
+  float* parts;            // [2 x blocks]: partial results as in shared memory
 };
 
 // The keys that sequence b's query attends to, in units.
@@ -106,8 +111,9 @@ __device__ __forceinline__ int64_t total_units(const SwaPagedArgs& a, int lane) 
   return sum;
 }
 
-__device__ __forceinline__ int64_t share_of(int64_t units, int warps) {
-  const int64_t s = (units + warps - 1) / warps;
+// Units of a block's share.
+__device__ __forceinline__ int64_t share_of(int64_t units, int blocks) {
+  const int64_t s = (units + blocks - 1) / blocks;
   return s > kMinUnits ? s : kMinUnits;
 }
 
@@ -288,14 +294,22 @@ __device__ __forceinline__ int key_of_row(int r) {
   return ((r & 7) >> 1) + 4 * (r & 1) + (r & 8);
 }
 
+// What a warp leaves of segments that it holds in part.
+struct WarpParts {
+  int has0, end0, b0, hh0;  // a segment that began earlier; end0: it ends here
+  int has1, b1, hh1, pad;   // a segment that goes on in the next warp
+};
+static_assert(128 % sizeof(WarpParts) == 0, "stepped through in 128-byte blocks");
+
 // ------------------------------------------------------------------ kernel --
 
 template <int D, int BITS, int NT>
-__global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
+__global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
     swa_paged_kernel(const __grid_constant__ PagedParams P) {
   using C = Cfg<D, BITS, NT>;
   constexpr int NG = C::NG;
   constexpr int MS = D / 16;  // 16-channel steps
+  constexpr int kWarps = C::kWarps;
   const SwaPagedArgs& a = P.a;
   extern __shared__ uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -304,22 +318,23 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t ring = base + warp * C::kWarpBytes;
   const uint8_t* ring_rows = smem_raw + (ring - smem_addr(smem_raw));
-  uint8_t* tail = smem_raw + (base - smem_addr(smem_raw)) + kWarps * C::kWarpBytes + warp * 64;
+  uint8_t* tail = smem_raw + (base - smem_addr(smem_raw)) + kWarps * C::kWarpBytes + warp * 128;
   uint64_t* full = reinterpret_cast<uint64_t*>(tail);                     // [kStages]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(full + C::kStages);
   volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(abort_flag + 1);  // [kStages]
 
+  WarpParts* parts = reinterpret_cast<WarpParts*>(tail + 64);
   if (lane == 0) {
     for (int s = 0; s < C::kStages; ++s) mbar_init(&full[s], 1);
     *abort_flag = 0;
+    parts->has0 = parts->end0 = parts->has1 = 0;
     mbar_fence_init();
   }
   __syncwarp();
 
   const int heads = a.c.kv_heads * P.head_blocks;
-  const int w = blockIdx.x * kWarps + warp;
   // Sequences without keys: zeros; lengths out of range: recorded as well.
-  for (int b = w; b < a.batch; b += P.warps) {
+  for (int b = blockIdx.x * kWarps + warp; b < a.batch; b += gridDim.x * kWarps) {
     const int n = a.lens[b];
     if (n < 0 || n > (a.c.table_pages << a.c.page_shift))
       if (lane == 0) record_error(a.status, PTB_ERR_ARG);
@@ -328,10 +343,14 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
         *reinterpret_cast<uint4*>(a.o + b * a.o_sb + (x / (D / 8)) * a.o_sh + x % (D / 8) * 8) =
             make_uint4(0, 0, 0, 0);
   }
+  // This block's share, and this warp's part of it.
   const int64_t total = total_units(a, lane) * heads;
-  const int64_t share = share_of(total, P.warps);
-  const int64_t u0 = w * share, u1 = u0 + share < total ? u0 + share : total;
-  if (u0 >= u1) return;
+  const int64_t share = share_of(total, gridDim.x);
+  const int64_t c0 = blockIdx.x * share, c1 = c0 + share < total ? c0 + share : total;
+  if (c0 >= c1) return;  // the whole block
+  const int64_t part = (c1 - c0 + kWarps - 1) / kWarps;
+  const int64_t u0 = c0 + warp * part < c1 ? c0 + warp * part : c1;
+  const int64_t u1 = u0 + part < c1 ? u0 + part : c1;
 
   const int page = a.c.page_size;
   const int sub_shift = page < kBlockKeys ? a.c.page_shift : 5;
@@ -350,7 +369,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
   const int copy_side = copy_part / C::kAtoms, copy_atom = copy_part % C::kAtoms;
   const int64_t value_side = static_cast<int64_t>(a.c.kv_heads) * a.c.block_bytes;
 
-  Place ld = place_of(a, heads, u0, lane);
+  Place ld = place_of(a, heads, u0 < u1 ? u0 : c0, lane);
   Place at = ld;
   int64_t to_load = u1 - u0;  // units whose copies are still to be issued
   // Pages of the coming sub-blocks, one a lane; -1: not needed, or out of range.
@@ -773,7 +792,23 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
 
     // ---- end of the segment
     const bool whole = first == 0 && count == at.s.units;
-    const int64_t slot = 2ll * w + (first > 0 ? 0 : 1);
+    // A segment that began in an earlier warp leaves its partial result in the
+    // warp's slot; one that goes on in a later warp is the warp's last, and
+    // lies over the ring, which is done.
+    float* slot = reinterpret_cast<float*>(
+        smem_raw + (ring - smem_addr(smem_raw)) + (first > 0 ? C::kRingBytes : 0));
+    if (!whole && lane == 0) {
+      if (first > 0) {
+        parts->has0 = 1;
+        parts->end0 = first + count == at.s.units;
+        parts->b0 = at.b;
+        parts->hh0 = at.hh;
+      } else {
+        parts->has1 = 1;
+        parts->b1 = at.b;
+        parts->hh1 = at.hh;
+      }
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -817,10 +852,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
           }
         } else {
           if (g == 0) {
-            P.part_ml[(slot * 2) * (8 * NT) + head] = m_ref[nt][e];
-            P.part_ml[(slot * 2 + 1) * (8 * NT) + head] = l[nt][e];
+            slot[head] = m_ref[nt][e];
+            slot[8 * NT + head] = l[nt][e];
           }
-          float* out = P.part_o + (slot * (8 * NT) + head) * D;
+          float* out = slot + 16 * NT + head * D;
           if constexpr (BITS == 16) {
 #pragma unroll
             for (int m = 0; m < MS; ++m) {
@@ -853,10 +888,76 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, BITS, NT>::kBlocksPerSm)
       }
     }
   }
+  __syncthreads();
+
+  // -------------------------------------------------- join within the block --
+  // A chain is a cut segment's partial results in this block: the slot of the
+  // warp where it begins (slot 0 of warp 0: it began in an earlier block) and
+  // slots 0 of the warps that follow, up to its end.  Warps take the chains'
+  // heads in turn.  A segment with its beginning and end here is finished; of
+  // the others the block leaves one partial result each (slot 0: begun
+  // earlier; slot 1: goes on) for the join kernel.
+  int task = 0;
+  for (int c = 0; c < 2 * kWarps; ++c) {
+    const int w0 = c >> 1;
+    const bool tail_slot = c & 1;  // slot 1 of warp w0
+    const WarpParts* first = parts + (w0 - warp) * (128 / static_cast<int>(sizeof(WarpParts)));
+    if (tail_slot ? !first->has1 : (w0 > 0 || !first->has0)) continue;
+    const int b = tail_slot ? first->b1 : first->b0, hh = tail_slot ? first->hh1 : first->hh0;
+    int last = w0;
+    bool ended = !tail_slot && first->end0;
+    while (!ended && last + 1 < kWarps) {
+      const WarpParts* next = parts + (last + 1 - warp) * (128 / static_cast<int>(sizeof(WarpParts)));
+      if (!next->has0) break;
+      ++last;
+      ended = next->end0;
+    }
+    const int kvh = hh / P.head_blocks;
+    const int head0 = kvh * P.group + (hh % P.head_blocks) * 8 * NT;
+    const int nheads = min(8 * NT, (kvh + 1) * P.group - head0);
+    for (int head = 0; head < nheads; ++head, ++task) {
+      if (task % kWarps != warp) continue;
+      auto slot_of = [&](int w) {
+        return reinterpret_cast<const float*>(smem_raw + (base - smem_addr(smem_raw)) +
+                                              w * C::kWarpBytes +
+                                              (w == w0 && tail_slot ? 0 : C::kRingBytes));
+      };
+      float mx = -INFINITY;
+      for (int w = w0; w <= last; ++w) mx = fmaxf(mx, slot_of(w)[head]);
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      float sum = 0.f, acc[(D + 31) / 32];
+#pragma unroll
+      for (int i = 0; i < (D + 31) / 32; ++i) acc[i] = 0.f;
+      for (int w = w0; w <= last; ++w) {
+        const float* p = slot_of(w);
+        const float f = fast_exp2(p[head] - ref);
+        sum = fmaf(f, p[8 * NT + head], sum);
+#pragma unroll
+        for (int i = 0; i < (D + 31) / 32; ++i)
+          if (i * 32 + lane < D) acc[i] = fmaf(f, p[16 * NT + head * D + i * 32 + lane], acc[i]);
+      }
+      if (tail_slot && ended) {
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
+        __nv_bfloat16* out = a.o + b * a.o_sb + (head0 + head) * a.o_sh;
+#pragma unroll
+        for (int i = 0; i < (D + 31) / 32; ++i)
+          if (i * 32 + lane < D) out[i * 32 + lane] = __float2bfloat16_rn(acc[i] * inv);
+      } else {
+        float* out = P.parts + (2 * blockIdx.x + (tail_slot ? 1 : 0)) * (C::kSlotBytes / 4);
+        if (lane == 0) {
+          out[head] = mx;
+          out[8 * NT + head] = sum;
+        }
+#pragma unroll
+        for (int i = 0; i < (D + 31) / 32; ++i)
+          if (i * 32 + lane < D) out[16 * NT + head * D + i * 32 + lane] = acc[i];
+      }
+    }
+  }
 }
 
-// Joins the shares of the segments that were cut.  Block w looks at the
-// boundary between shares w - 1 and w: where it falls inside a segment of n
+// Joins the blocks' shares of the segments that were cut between them.  Block
+// w looks at the boundary between shares w - 1 and w: where it falls inside a segment of n
 // shares, the n - 1 boundary blocks split the segment's (head, 32-channel)
 // outputs among them.
 template <int NT>
@@ -867,7 +968,7 @@ __global__ void __launch_bounds__(kJoinThreads) swa_paged_join_kernel(const Page
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int heads = a.c.kv_heads * P.head_blocks;
   const int64_t total = total_units(a, lane) * heads;
-  const int64_t share = share_of(total, P.warps);
+  const int64_t share = share_of(total, gridDim.x + 1);
   const int64_t u = (blockIdx.x + 1) * share;
   Place p = {};
   if (u < total) p = place_of(a, heads, u, lane);
@@ -883,6 +984,9 @@ __global__ void __launch_bounds__(kJoinThreads) swa_paged_join_kernel(const Page
   const int nheads = min(8 * NT, (kvh + 1) * P.group - head0);
   const int chunks = (d + 31) / 32;
   const int tasks = nheads * chunks;
+  auto slot_of = [&](int x) {
+    return P.parts + (2 * (w0 + x) + (x == 0 ? 1 : 0)) * (8 * NT * (2 + d));
+  };
   // Few shares: a warp takes an output piece alone; many: all warps share one.
   const bool alone = n <= kJoinThreads / 32;
   const int step = alone ? 1 : kJoinThreads / 32;
@@ -892,8 +996,7 @@ __global__ void __launch_bounds__(kJoinThreads) swa_paged_join_kernel(const Page
     const int head = live ? task / chunks : 0, c = live ? (task % chunks) * 32 + lane : d;
     float mx = -INFINITY;
     for (int x = lane; x < n; x += 32) {
-      const int64_t slot = 2 * (w0 + x) + (x == 0 ? 1 : 0);
-      mx = fmaxf(mx, P.part_ml[(slot * 2) * (8 * NT) + head]);
+      mx = fmaxf(mx, slot_of(x)[head]);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -901,10 +1004,10 @@ __global__ void __launch_bounds__(kJoinThreads) swa_paged_join_kernel(const Page
     float acc = 0.f, l = 0.f;
 #pragma unroll 8
     for (int x = alone ? 0 : warp; x < n; x += step) {
-      const int64_t slot = 2 * (w0 + x) + (x == 0 ? 1 : 0);
-      const float f = exp2f(P.part_ml[(slot * 2) * (8 * NT) + head] - ref);
-      l = fmaf(f, P.part_ml[(slot * 2 + 1) * (8 * NT) + head], l);
-      if (c < d) acc = fmaf(f, P.part_o[(slot * (8 * NT) + head) * d + c], acc);
+      const float* p = slot_of(x);
+      const float f = fast_exp2(p[head] - ref);
+      l = fmaf(f, p[8 * NT + head], l);
+      if (c < d) acc = fmaf(f, p[16 * NT + head * d + c], acc);
     }
     if (!alone) {
       so[warp][lane] = acc;
@@ -933,13 +1036,12 @@ cudaError_t launch_typed(PagedParams& prm, cudaStream_t stream) {
   static bool configured[kDeviceSlots] = {};
   cudaError_t e = allow_smem(kern, C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
-  const int grid = prm.a.sms * C::kBlocksPerSm;
-  prm.warps = grid * kWarps;
-  kern<<<grid, kWarps * 32, C::kSmemBytes, stream>>>(prm);
+  const int grid = prm.a.sms;
+  kern<<<grid, C::kWarps * 32, C::kSmemBytes, stream>>>(prm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(prm.warps - 1);
+  cfg.gridDim = dim3(grid > 1 ? grid - 1 : 1);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   // Finds its shares while the first kernel still runs, then waits for it.
@@ -973,10 +1075,9 @@ cudaError_t launch_d(PagedParams& prm, cudaStream_t stream) {
 
 }  // namespace
 
-// Two cut segments a warp: (maximum, sum) and the output of up to 8 NT heads.
+// Two cut segments a block: maxima, sums and outputs of up to 8 NT heads.
 size_t swa_paged_workspace(int, int heads, int kv_heads, int head_dim, int sms) {
-  const size_t rows = 2ull * sms * kMaxWarpsPerSm * 8 * head_tiles(heads / kv_heads);
-  return rows * (2 + head_dim) * sizeof(float);
+  return 2ull * sms * 8 * head_tiles(heads / kv_heads) * (2 + head_dim) * sizeof(float);
 }
 
 cudaError_t launch_swa_paged(const SwaPagedArgs& a, cudaStream_t stream) {
@@ -985,9 +1086,7 @@ cudaError_t launch_swa_paged(const SwaPagedArgs& a, cudaStream_t stream) {
   prm.group = a.heads / a.c.kv_heads;
   const int tile = 8 * head_tiles(prm.group);
   prm.head_blocks = (prm.group + tile - 1) / tile;
-  const size_t slots = 2ull * a.sms * kMaxWarpsPerSm;
-  prm.part_o = static_cast<float*>(a.workspace);
-  prm.part_ml = prm.part_o + slots * tile * a.c.head_dim;
+  prm.parts = static_cast<float*>(a.workspace);
   if (a.c.bits == 4) return launch_d<4>(prm, stream);
   const int sub = a.c.page_size < kBlockKeys ? a.c.page_size : kBlockKeys;
   const uint64_t row = 2ull * a.c.head_dim;
