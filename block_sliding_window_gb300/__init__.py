@@ -473,13 +473,16 @@ def kv_append(q, k, v, cache, page_table, cu_seqlens, past, page_size: int, bits
             raise ValueError("q must be [tokens, heads, head_dim] of k's tokens and head_dim")
         if q_out is None:
             q_out = _new(q, q.shape, stream)
-        qo = _heads_view("q_out", q_out, dev, q.shape)
+            qo = q_out.data_ptr(), max(heads, 1) * d, d
+        else:
+            qo = _heads_view("q_out", q_out, dev, q.shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if k_out is None and keep_keys:
-        k_out = _new(k, k.shape, stream)
     if k_out is not None:
         ko = _heads_view("k_out", k_out, dev, k.shape)
+    elif keep_keys:
+        k_out = _new(k, k.shape, stream)
+        ko = k_out.data_ptr(), max(kv_heads, 1) * d, d
     rot, positions, cp, sp = 0, 0, None, None
     if cos is not None or sin is not None:
         if cos is None or sin is None:
@@ -510,12 +513,17 @@ def kv_gather(cache, page_table, cu_seqlens, start, tokens: int, kv_heads: int, 
     ca = _cache_args(cache, page_table, batch, kv_heads, head_dim, page_size, bits, dev)
     shape = torch.Size((tokens, kv_heads, head_dim))
     if k is None:
-        k = _new(cache, shape, stream, torch.bfloat16)
+        k = _new(cache, shape, stream)
+        ka = k.data_ptr(), kv_heads * head_dim, head_dim
+    else:
+        ka = _heads_view("k", k, dev, shape)
     if v is None:
-        v = _new(cache, shape, stream, torch.bfloat16)
+        v = _new(cache, shape, stream)
+        va = v.data_ptr(), kv_heads * head_dim, head_dim
+    else:
+        va = _heads_view("v", v, dev, shape)
     st = lib.ptb_kv_gather(*ca, cu, _int_vector("start", start, batch, dev), batch, tokens,
-                           kv_heads, head_dim, page_size, bits, *_heads_view("k", k, dev, shape),
-                           *_heads_view("v", v, dev, shape), raw)
+                           kv_heads, head_dim, page_size, bits, *ka, *va, raw)
     if st:
         _check(st, "ptb_kv_gather")
     return k, v
@@ -549,7 +557,9 @@ def swa_attention_packed(q, k, v, cu_seqlens, window: int, cu_seqlens_k=None, sc
         raise ValueError("q and k must have the same tokens, or cu_seqlens_k be given")
     if o is None:
         o = _new(q, q.shape, stream)
-    oa = _heads_view("o", o, dev, q.shape)
+        oa = o.data_ptr(), max(heads, 1) * d, d
+    else:
+        oa = _heads_view("o", o, dev, q.shape)
     ws, wp, wb = _scratch(lib.swa_attention_packed_workspace_size(batch, tq, heads, kv_heads),
                           workspace, q, stream)  # ws lives until the launch is queued
     st = lib.swa_attention_packed(*qa, *ka, *va, cu, cu_k, batch, tq, tk, heads, kv_heads, d,
@@ -573,7 +583,9 @@ def swa_attention_paged(q, cache, page_table, seq_lens, kv_heads: int, page_size
     batch, heads, d = q.shape
     if o is None:
         o = _new(q, q.shape, stream)
-    oa = _heads_view("o", o, dev, q.shape)
+        oa = o.data_ptr(), heads * d, d
+    else:
+        oa = _heads_view("o", o, dev, q.shape)
     ws, wp, wb = _scratch(lib.swa_attention_paged_workspace_size(batch, heads, kv_heads, d),
                           workspace, q, stream)
     st = lib.swa_attention_paged(*qa, *_cache_args(cache, page_table, batch, kv_heads, d, page_size,

@@ -2,37 +2,56 @@
 // position rotation and (bits = 4) the quantization on the way, and reading
 // rows back (layout and arithmetic: ptb.h).
 //
-// Both are single passes over memory.  A lane holds 8 neighbouring channels
-// (16 bytes) of one head row and a row lies in one warp (d / 8 lanes), so the
-// rotation's other half and a 32-channel group's minimum and maximum come
-// from shuffles, and in-place rotation is safe: a row is read in full by its
-// warp before any of it is written.
+// Both are single passes over memory and bound by it.
+//
+// Append: a warp takes a token and a batch of its head rows; a lane holds 8
+// neighbouring channels (16 bytes) of a row and a row lies in one warp (d / 8
+// lanes), so the rotation's other half and a 32-channel group's minimum and
+// maximum come from shuffles.  The batch's rows are loaded before the token's
+// sequence, position and page are looked up, which hides those dependent
+// loads.  In-place rotation is safe: a row is read in full by its warp before
+// any of it is written.
+//
+// Gather: a lane holds what lies together in a 4-bit row, 8 channels of every
+// group of a key (4 lanes a row) or 4 of every group of a value (8 lanes).
 #include "kv_device.cuh"
 
 namespace ptb {
 namespace {
 
 constexpr int kKvThreads = 128;
+constexpr int kBatch = 4;  // loads of rows that a lane has in flight
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t v) {
+  return *reinterpret_cast<__nv_bfloat162*>(&v);
+}
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) {
+  return *reinterpret_cast<uint32_t*>(&v);
+}
 
 // One (scale, centre) pair and the 8 codes of this lane, from 8 bf16 values
 // of a group that 4 neighbouring lanes share.
-__device__ __forceinline__ uint32_t quantize_group(const float (&x)[8], uint32_t& pair) {
-  float lo = x[0], hi = x[0];
-  bool finite = true;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    lo = fminf(lo, x[e]);
-    hi = fmaxf(hi, x[e]);
-    finite = finite && fabsf(x[e]) < INFINITY;
-  }
+//
+// u = round(y / s) + 8 with y = x - centre.  The quotient has to be that of an
+// IEEE division, or ties (frequent: bf16 values over a bf16 scale) would fall
+// either way; one exact remainder and one correction give it (P. Markstein,
+// IBM J. Res. Dev. 34 (1990), Theorem 7: with r the rounded reciprocal of s
+// and q within an ulp, q + r (y - q s) by two FMAs is y / s rounded).
+__device__ __forceinline__ uint32_t quantize_group(const uint4& w, uint32_t& pair) {
+  const __nv_bfloat162 v0 = as_bf162(w.x), v1 = as_bf162(w.y), v2 = as_bf162(w.z),
+                       v3 = as_bf162(w.w);
+  // NaN stays in both, an infinity makes the range infinite.
+  __nv_bfloat162 lo2 = __hmin2_nan(__hmin2_nan(v0, v1), __hmin2_nan(v2, v3));
+  __nv_bfloat162 hi2 = __hmax2_nan(__hmax2_nan(v0, v1), __hmax2_nan(v2, v3));
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    finite = __shfl_xor_sync(0xffffffffu, finite ? 1 : 0, o) && finite;
+    lo2 = __hmin2_nan(lo2, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(lo2), o)));
+    hi2 = __hmax2_nan(hi2, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(hi2), o)));
   }
+  const float lo = __bfloat162float(__hmin_nan(__low2bfloat16(lo2), __high2bfloat16(lo2)));
+  const float hi = __bfloat162float(__hmax_nan(__low2bfloat16(hi2), __high2bfloat16(hi2)));
   const float range = __fsub_rn(hi, lo);
-  if (!finite || !(range < INFINITY)) {
+  if (!(range < INFINITY)) {
     pair = 0x7fc07fc0u;  // NaN, NaN: the whole group reads as NaN
     return 0;
   }
@@ -42,12 +61,27 @@ __device__ __forceinline__ uint32_t quantize_group(const float (&x)[8], uint32_t
   const float z = __bfloat162float(centre);
   pair = static_cast<uint32_t>(__bfloat16_as_ushort(scale)) |
          (static_cast<uint32_t>(__bfloat16_as_ushort(centre)) << 16);
-  const float div = s > 0.f ? s : 1.f;
+  const uint32_t raw[4] = {w.x, w.y, w.z, w.w};
+  const float inv = __frcp_rn(s);
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
   uint32_t codes = 0;
+  if (s > 1e-30f) {  // no remainder underflows
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float u = rintf(__fdiv_rn(__fsub_rn(x[e], z), div)) + 8.f;
-    codes |= static_cast<uint32_t>(fminf(fmaxf(u, 0.f), 15.f)) << (4 * e);
+    for (int e = 7; e >= 0; --e) {
+      const float y = __fsub_rn((e & 1) ? bf16_hi(raw[e >> 1]) : bf16_lo(raw[e >> 1]), z);
+      float q = __fmul_rn(y, inv);
+      q = fmaf(fmaf(-q, s, y), inv, q);
+      codes = codes * 16u + __float_as_uint(__fadd_rn(fminf(fmaxf(q, -8.f), 7.f), kMagic));
+    }
+    codes -= (0x4b400000u - 8u) * 0x11111111u;  // kMagic's bits less 8, in each of the eight
+  } else {
+#pragma unroll 1
+    for (int e = 7; e >= 0; --e) {
+      const uint32_t word = e < 2 ? raw[0] : (e < 4 ? raw[1] : (e < 6 ? raw[2] : raw[3]));
+      const float y = __fsub_rn((e & 1) ? bf16_hi(word) : bf16_lo(word), z);
+      const float q = rintf(__fdiv_rn(y, s > 0.f ? s : 1.f));
+      codes = codes * 16u + static_cast<uint32_t>(fminf(fmaxf(q, -8.f), 7.f) + 8.f);
+    }
   }
   return codes;
 }
@@ -66,198 +100,295 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
-// Grid: x = token, y = chunk of head rows (all q heads, then k, then v).
+// A warp's number is token * batches + batch; a batch is kBatch steps of RPW
+// rows of one kind: q, then k, then v.
 template <int D>
-__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvAppendArgs a, int chunk) {
-  constexpr int L = D / 8;        // lanes a row
-  constexpr int RPW = 32 / L;     // rows a warp holds at once
+__global__ void __launch_bounds__(kKvThreads)
+    kv_append_kernel(const KvAppendArgs a, int q_batches, int kv_batches) {
+  constexpr int L = D / 8;     // lanes a row
+  constexpr int RPW = 32 / L;  // rows a warp holds at once
   constexpr int NG = D / kKvGroup;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kKvThreads / 32) + (threadIdx.x >> 5);
+  const int batches = q_batches + 2 * kv_batches;
+  const int64_t t = item / batches;
+  if (t >= a.tokens) return;
+  int batch = static_cast<int>(item - t * batches);
+  const bool is_q = batch < q_batches;
+  batch -= is_q ? 0 : q_batches;
+  const bool is_v = !is_q && batch >= kv_batches;
+  batch -= is_v ? kv_batches : 0;
+  const int rows = is_q ? a.heads : a.c.kv_heads;
+  const int sub = lane / L;  // row of this lane among the RPW
+  const int c = lane - sub * L;
+  const int h0 = batch * (kBatch * RPW) + sub;
+  const int64_t sh = is_q ? a.q_sh : (is_v ? a.v_sh : a.k_sh);
+  const __nv_bfloat16* src =
+      (is_q ? a.q + t * a.q_st : (is_v ? a.v + t * a.v_st : a.k + t * a.k_st)) + h0 * sh + 8 * c;
+
+  uint4 w[kBatch];
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i)
+    w[i] = sub < RPW && h0 + i * RPW < rows
+               ? *reinterpret_cast<const uint4*>(src + i * RPW * sh)
+               : make_uint4(0, 0, 0, 0);
+
   const int b = find_sequence(a.cu, a.batch, t, lane);
   if (b >= a.batch) return;  // a row behind the last sequence
   const int64_t first = a.cu[b], past = a.past[b];
   const int64_t pos = past + (t - first);
   if (first < 0 || first > t || past < 0 || pos >= a.positions) {
-    if (threadIdx.x == 0) record_error(a.status, PTB_ERR_ARG);
+    if (lane == 0) record_error(a.status, PTB_ERR_ARG);
     return;
   }
-  uint8_t* page = kv_page(a.c, b, pos);
-  if (!page && threadIdx.x == 0) record_error(a.status, PTB_ERR_ARG);
-  const int off = static_cast<int>(pos) & (a.c.page_size - 1);
-
-  const int sub = lane / L;       // row of this lane among the warp's RPW
-  const int c = lane - sub * L;   // its 8-channel vector
-  const bool rotated = sub < RPW && 8 * c < a.rot_dim;
-  const int half = a.rot_dim / 2;
-  // 8 (cos, sin) of this lane's channels: the same for every head.
-  float co[8], si[8];
-  if (rotated) {
-    const float* cr = a.cos + pos * half;
-    const float* sr = a.sin + pos * half;
-    if (a.interleaved) {
+  if (!is_v && a.rot_dim) {
+    const bool rotated = sub < RPW && 8 * c < a.rot_dim;
+    const int half = a.rot_dim / 2;
+    const bool lower = 8 * c < half;
+    // (cos, sin) of this lane's channels, the same for every head; the sign of
+    // the sine is its sign in the lane's outputs: x cos + other sin.
+    float co[8], si[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        co[2 * e] = co[2 * e + 1] = cr[4 * c + e];
-        si[2 * e] = si[2 * e + 1] = sr[4 * c + e];
+    for (int e = 0; e < 8; ++e) co[e] = si[e] = 0.f;
+    if (rotated) {
+      const float* cr = a.cos + pos * half;
+      const float* sr = a.sin + pos * half;
+      if (a.interleaved) {
+        const float4 x = *reinterpret_cast<const float4*>(cr + 4 * c);
+        const float4 y = *reinterpret_cast<const float4*>(sr + 4 * c);
+        co[0] = co[1] = x.x, co[2] = co[3] = x.y, co[4] = co[5] = x.z, co[6] = co[7] = x.w;
+        si[1] = y.x, si[3] = y.y, si[5] = y.z, si[7] = y.w;
+        si[0] = -y.x, si[2] = -y.y, si[4] = -y.z, si[6] = -y.w;
+      } else {
+        const int at = lower ? 8 * c : 8 * c - half;
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(cr + at + e);
+          const float4 y = *reinterpret_cast<const float4*>(sr + at + e);
+          co[e] = x.x, co[e + 1] = x.y, co[e + 2] = x.z, co[e + 3] = x.w;
+          si[e] = lower ? -y.x : y.x, si[e + 1] = lower ? -y.y : y.y;
+          si[e + 2] = lower ? -y.z : y.z, si[e + 3] = lower ? -y.w : y.w;
+        }
       }
-    } else {
-      const int at = 8 * c < half ? 8 * c : 8 * c - half;
+    }
+    // The lane whose vector this one turns against: half a rotation away.
+    const int other = (!a.interleaved && rotated) ? sub * L + (lower ? c + half / 8 : c - half / 8)
+                                                  : lane;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        co[e] = cr[at + e];
-        si[e] = sr[at + e];
+    for (int i = 0; i < kBatch; ++i) {
+      uint4 p = w[i];
+      if (!a.interleaved) {
+        p.x = __shfl_sync(0xffffffffu, w[i].x, other);
+        p.y = __shfl_sync(0xffffffffu, w[i].y, other);
+        p.z = __shfl_sync(0xffffffffu, w[i].z, other);
+        p.w = __shfl_sync(0xffffffffu, w[i].w, other);
+      }
+      if (rotated) {
+        float x[8], y[8], out[8];
+        unpack8(w[i], x);
+        unpack8(p, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          out[e] = __fadd_rn(__fmul_rn(x[e], co[e]),
+                             __fmul_rn(a.interleaved ? x[e ^ 1] : y[e], si[e]));
+        w[i] = pack8(out);
       }
     }
   }
-  const int rows = a.heads + 2 * a.c.kv_heads;
-  const int row_end = min(rows, static_cast<int>(blockIdx.y + 1) * chunk);
-  for (int r0 = blockIdx.y * chunk + warp * RPW; r0 < row_end; r0 += (kKvThreads / 32) * RPW) {
-    const int r = r0 + sub;
-    const bool live = sub < RPW && r < row_end;
-    const bool is_q = r < a.heads, is_k = !is_q && r < a.heads + a.c.kv_heads;
-    const int h = is_q ? r : (is_k ? r - a.heads : r - a.heads - a.c.kv_heads);
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (live) {
-      const __nv_bfloat16* src = is_q ? a.q + t * a.q_st + h * a.q_sh
-                                      : (is_k ? a.k + t * a.k_st + h * a.k_sh
-                                              : a.v + t * a.v_st + h * a.v_sh);
-      w = *reinterpret_cast<const uint4*>(src + 8 * c);
-    }
-    if (a.rot_dim) {
-      // The vector that this one turns against: half a rotation away.
-      const int other = sub * L + (8 * c < half ? c + half / 8 : c - half / 8);
-      const int from = (!a.interleaved && rotated) ? other : lane;
-      uint4 p;
-      p.x = __shfl_sync(0xffffffffu, w.x, from);
-      p.y = __shfl_sync(0xffffffffu, w.y, from);
-      p.z = __shfl_sync(0xffffffffu, w.z, from);
-      p.w = __shfl_sync(0xffffffffu, w.w, from);
-      if (rotated && live && (is_q || is_k)) {
-        float x[8], y[8], out[8];
-        unpack8(w, x);
-        unpack8(p, y);
+  __syncwarp();  // in place: every row has been read
+  __nv_bfloat16* out = is_q ? a.q_out : (is_v ? nullptr : a.k_out);
+  if (out) {
+    const int64_t oh = is_q ? a.qo_sh : a.ko_sh;
+    out += t * (is_q ? a.qo_st : a.ko_st) + h0 * oh + 8 * c;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float other_x = a.interleaved ? x[e ^ 1] : y[e];
-          const bool lower = a.interleaved ? (e & 1) == 0 : 8 * c < half;
-          const float u = __fmul_rn(x[e], co[e]), v = __fmul_rn(other_x, si[e]);
-          out[e] = lower ? __fsub_rn(u, v) : __fadd_rn(u, v);
-        }
-        w = pack8(out);
-      }
-    }
-    __syncwarp();  // in place: the whole row has been read
-    if (live && is_q)
-      *reinterpret_cast<uint4*>(a.q_out + t * a.qo_st + h * a.qo_sh + 8 * c) = w;
-    if (live && is_k && a.k_out)
-      *reinterpret_cast<uint4*>(a.k_out + t * a.ko_st + h * a.ko_sh + 8 * c) = w;
-    uint8_t* block = page ? page + (is_k ? h : a.c.kv_heads + h) * a.c.block_bytes : nullptr;
-    if (a.c.bits == 16) {
-      if (live && !is_q && page)
-        *reinterpret_cast<uint4*>(block + off * (2 * D) + 16 * c) = w;
-    } else if constexpr (NG > 0) {
-      float x[8];
-      unpack8(w, x);
+    for (int i = 0; i < kBatch; ++i)
+      if (sub < RPW && h0 + i * RPW < rows)
+        *reinterpret_cast<uint4*>(out + i * RPW * oh) = w[i];
+  }
+  if (is_q) return;
+
+  uint8_t* page = kv_page(a.c, b, pos);
+  if (!page) {
+    if (lane == 0) record_error(a.status, PTB_ERR_ARG);
+    return;
+  }
+  const int off = static_cast<int>(pos) & (a.c.page_size - 1);
+  uint8_t* block = page + ((is_v ? a.c.kv_heads : 0) + h0) * a.c.block_bytes;
+  const int64_t step = RPW * a.c.block_bytes;
+  if (a.c.bits == 16) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (sub < RPW && h0 + i * RPW < rows)
+        *reinterpret_cast<uint4*>(block + i * step + off * (2 * D) + 16 * c) = w[i];
+  } else if constexpr (NG > 0) {
+    const int g = c >> 2;  // group, and the vector's place in it
+    uint8_t* row = block + off * (D / 2);
+    uint8_t* pairs = block + a.c.page_size * (D / 2) + (off * NG + g) * 4;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (batch * (kBatch * RPW) + i * RPW >= rows) break;
       uint32_t pair;
-      const uint32_t codes = quantize_group(x, pair);
-      if (live && !is_q && page) {
-        uint8_t* row = block + off * (D / 2);
-        const int g = c >> 2;  // group, and the vector's place in it
-        if (is_k) {
-          *reinterpret_cast<uint32_t*>(row + key_word(g, c & 3, NG)) = codes;
+      const uint32_t codes = quantize_group(w[i], pair);
+      if (sub < RPW && h0 + i * RPW < rows) {
+        uint8_t* r = row + i * step;
+        if (!is_v) {
+          *reinterpret_cast<uint32_t*>(r + key_word(g, c & 3, NG)) = codes;
         } else {
-          *reinterpret_cast<uint16_t*>(row + value_half(g, 2 * (c & 3), NG)) =
+          *reinterpret_cast<uint16_t*>(r + value_half(g, 2 * (c & 3), NG)) =
               static_cast<uint16_t>(codes);
-          *reinterpret_cast<uint16_t*>(row + value_half(g, 2 * (c & 3) + 1, NG)) =
+          *reinterpret_cast<uint16_t*>(r + value_half(g, 2 * (c & 3) + 1, NG)) =
               static_cast<uint16_t>(codes >> 16);
         }
-        if ((c & 3) == 0)
-          *reinterpret_cast<uint32_t*>(block + a.c.page_size * (D / 2) + (off * NG + g) * 4) =
-              pair;
+        if ((c & 3) == 0) *reinterpret_cast<uint32_t*>(pairs + i * step) = pair;
       }
     }
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const KvGatherArgs a, int chunk) {
-  constexpr int L = D / 8;
-  constexpr int RPW = 32 / L;
+// N (1 .. 4) consecutive words at 4-byte alignment, 16- or 8-byte where N is 4 or 2.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&r)[N], const uint8_t* p) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r[0] = v.x, r[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  }
+}
+
+// The values of eight codes, v[k] = (nibble k of the low half, of the high
+// half) as bf16 pairs: centre + scale * (u - 8), rounded once.
+__device__ __forceinline__ void code_values(uint32_t codes, uint32_t scale2, uint32_t centre2,
+                                            uint32_t (&v)[4]) {
+  codes_bf16(codes, v);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    v[k] = as_u32(__hfma2(as_bf162(v[k]), as_bf162(scale2), as_bf162(centre2)));
+}
+
+// A warp's number is token * batches + batch of rows (k heads, then v heads).
+template <int D, int BITS>
+__global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const KvGatherArgs a, int batches,
+                                                               int batch_rows) {
   constexpr int NG = D / kKvGroup;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kKvThreads / 32) + (threadIdx.x >> 5);
+  const int64_t t = item / batches;
+  if (t >= a.tokens) return;
   const int b = find_sequence(a.cu, a.batch, t, lane);
   if (b >= a.batch) return;
   const int64_t first = a.cu[b], start = a.start[b];
   const int64_t pos = start + (t - first);
   const uint8_t* page = first < 0 || first > t || start < 0 ? nullptr : kv_page(a.c, b, pos);
   if (!page) {
-    if (threadIdx.x == 0) record_error(a.status, PTB_ERR_ARG);
+    if (lane == 0) record_error(a.status, PTB_ERR_ARG);
     return;
   }
   const int off = static_cast<int>(pos) & (a.c.page_size - 1);
-  const int sub = lane / L, c = lane - sub * L;
-  const int rows = 2 * a.c.kv_heads;
-  const int row_end = min(rows, static_cast<int>(blockIdx.y + 1) * chunk);
-  for (int r0 = blockIdx.y * chunk + warp * RPW; r0 < row_end; r0 += (kKvThreads / 32) * RPW) {
-    const int r = r0 + sub;
-    if (sub >= RPW || r >= row_end) continue;
-    const bool is_k = r < a.c.kv_heads;
-    const int h = is_k ? r : r - a.c.kv_heads;
-    const uint8_t* block = page + r * a.c.block_bytes;
-    uint4 w;
-    if (a.c.bits == 16) {
-      w = *reinterpret_cast<const uint4*>(block + off * (2 * D) + 16 * c);
-    } else {
-      const uint8_t* row = block + off * (D / 2);
-      const int g = c >> 2;
-      const uint32_t codes =
-          is_k ? *reinterpret_cast<const uint32_t*>(row + key_word(g, c & 3, NG))
-               : *reinterpret_cast<const uint16_t*>(row + value_half(g, 2 * (c & 3), NG)) |
-                     (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(
-                          row + value_half(g, 2 * (c & 3) + 1, NG)))
-                      << 16);
-      const uint32_t pair = *reinterpret_cast<const uint32_t*>(
-          block + a.c.page_size * (D / 2) + (off * NG + g) * 4);
-      float x[8];
+  const int kv = a.c.kv_heads;
+  const int row_base = static_cast<int>(item - t * batches) * batch_rows;
+  const int row_end = min(row_base + batch_rows, 2 * kv);
+  auto row_out = [&](int r) {
+    return r < kv ? a.k + t * a.k_st + r * a.k_sh : a.v + t * a.v_st + (r - kv) * a.v_sh;
+  };
+  if constexpr (BITS == 16) {
+    constexpr int L = D / 8, RPW = 32 / L;
+    const int sub = lane / L, c = lane - sub * L;
+#pragma unroll 4
+    for (int r = row_base + sub; r < row_end; r += RPW)
+      if (sub < RPW)
+        *reinterpret_cast<uint4*>(row_out(r) + 8 * c) = *reinterpret_cast<const uint4*>(
+            page + r * a.c.block_bytes + off * (2 * D) + 16 * c);
+  } else {
+    // Keys: 4 lanes a row.
+    const int t4 = lane & 3, g = lane & 7;
+#pragma unroll 2
+    for (int r = row_base + (lane >> 2); r < min(row_end, kv); r += 8) {
+      const uint8_t* block = page + r * a.c.block_bytes;
+      uint32_t codes[NG], pair[NG];
+      load_words<NG>(codes, block + off * (D / 2) + key_word(0, t4, NG));
+      load_words<NG>(pair, block + a.c.page_size * (D / 2) + off * (D / 8));
+      __nv_bfloat16* out = row_out(r) + 8 * t4;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = fmaf(static_cast<float>(static_cast<int>((codes >> (4 * e)) & 15u) - 8),
-                    bf16_lo(pair), bf16_hi(pair));
-      w = pack8(x);
+      for (int w = 0; w < NG; ++w) {
+        uint32_t v[4];
+        code_values(codes[w], __byte_perm(pair[w], pair[w], 0x1010),
+                    __byte_perm(pair[w], pair[w], 0x3232), v);
+        *reinterpret_cast<uint4*>(out + 32 * w) =
+            make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                       __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+      }
     }
-    __nv_bfloat16* dst = is_k ? a.k + t * a.k_st + h * a.k_sh : a.v + t * a.v_st + h * a.v_sh;
-    *reinterpret_cast<uint4*>(dst + 8 * c) = w;
+    // Values: 8 lanes a row.
+#pragma unroll 2
+    for (int r = max(row_base, kv) + (lane >> 3); r < row_end; r += 4) {
+      const uint8_t* block = page + r * a.c.block_bytes;
+      const uint16_t* src =
+          reinterpret_cast<const uint16_t*>(block + off * (D / 2) + value_half(0, g, NG));
+      // Two groups a word: half-words w and w + 1.
+      constexpr int NW = (NG + 1) / 2;
+      uint32_t codes[NW], pair[2 * NW];
+      if constexpr (NG % 2 == 0) {
+        load_words<NW>(codes, reinterpret_cast<const uint8_t*>(src));
+      } else {
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+          codes[w] = src[2 * w] |
+                     (2 * w + 1 < NG ? static_cast<uint32_t>(src[2 * w + 1]) << 16 : 0u);
+        pair[2 * NW - 1] = 0;
+      }
+      load_words<NG>(*reinterpret_cast<uint32_t(*)[NG]>(&pair[0]),
+                     block + a.c.page_size * (D / 2) + off * (D / 8));
+      __nv_bfloat16* out = row_out(r) + 4 * g;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        uint32_t v[4];
+        code_values(codes[w], __byte_perm(pair[2 * w], pair[2 * w + 1], 0x5410),
+                    __byte_perm(pair[2 * w], pair[2 * w + 1], 0x7632), v);
+        *reinterpret_cast<uint2*>(out + 64 * w) =
+            make_uint2(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410));
+        if (2 * w + 1 < NG)
+          *reinterpret_cast<uint2*>(out + 64 * w + 32) =
+              make_uint2(__byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+      }
+    }
   }
-}
-
-// Head rows a block takes: all of a token's, or fewer when the tokens alone
-// would leave SMs without blocks.
-int rows_per_block(int64_t tokens, int rows, int rpw, int sms) {
-  const int least = (kKvThreads / 32) * rpw;
-  int chunk = rows;
-  while (chunk > least && tokens * ((rows + chunk - 1) / chunk) < 8ll * sms)
-    chunk = (chunk + 1) / 2;
-  return chunk < least ? least : (chunk + rpw - 1) / rpw * rpw;
 }
 
 template <int D>
 cudaError_t append_typed(const KvAppendArgs& a, cudaStream_t stream) {
-  const int rows = a.heads + 2 * a.c.kv_heads;
-  const int chunk = rows_per_block(a.tokens, rows, 32 / (D / 8), a.sms);
-  const dim3 grid(static_cast<unsigned>(a.tokens), (rows + chunk - 1) / chunk);
-  kv_append_kernel<D><<<grid, kKvThreads, 0, stream>>>(a, chunk);
+  constexpr int kRows = kBatch * (32 / (D / 8));
+  const int q_batches = (a.heads + kRows - 1) / kRows;
+  const int kv_batches = (a.c.kv_heads + kRows - 1) / kRows;
+  const int batches = q_batches + 2 * kv_batches;
+  const int64_t blocks = (a.tokens * batches + kKvThreads / 32 - 1) / (kKvThreads / 32);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  kv_append_kernel<D><<<static_cast<unsigned>(blocks), kKvThreads, 0, stream>>>(a, q_batches,
+                                                                                  kv_batches);
+  return cudaGetLastError();
+}
+
+template <int D, int BITS>
+cudaError_t gather_bits(const KvGatherArgs& a, cudaStream_t stream) {
+  // 16 rows of keys or values a warp: two 8-row steps of keys, four of values.
+  const int batch_rows = 16, rows = 2 * a.c.kv_heads;
+  const int batches = (rows + batch_rows - 1) / batch_rows;
+  const int64_t blocks = (a.tokens * batches + kKvThreads / 32 - 1) / (kKvThreads / 32);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  kv_gather_kernel<D, BITS>
+      <<<static_cast<unsigned>(blocks), kKvThreads, 0, stream>>>(a, batches, batch_rows);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t gather_typed(const KvGatherArgs& a, cudaStream_t stream) {
-  const int rows = 2 * a.c.kv_heads;
-  const int chunk = rows_per_block(a.tokens, rows, 32 / (D / 8), a.sms);
-  const dim3 grid(static_cast<unsigned>(a.tokens), (rows + chunk - 1) / chunk);
-  kv_gather_kernel<D><<<grid, kKvThreads, 0, stream>>>(a, chunk);
-  return cudaGetLastError();
+  if (a.c.bits == 16) return gather_bits<D, 16>(a, stream);
+  if constexpr (D % kKvGroup == 0) return gather_bits<D, 4>(a, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace

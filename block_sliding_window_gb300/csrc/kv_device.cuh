@@ -59,4 +59,19 @@ __device__ __forceinline__ int key_word(int w, int t, int ng) { return 4 * (t * 
 // Value half-word of channels 32 w + 4 g .. + 3:
 __device__ __forceinline__ int value_half(int w, int g, int ng) { return 2 * (g * ng + w); }
 
+// The four nibbles of each 16-bit half of w as bf16 u - 8, exact: v[k] holds
+// nibble k of the low and of the high half.  A nibble in mantissa bits 0 .. 3
+// of 128 is 128 + u, in bits 3 .. 6 of 16 it is 16 + u: three shifts for four.
+__device__ __forceinline__ uint32_t bf16x2_add(uint32_t x, float c) {
+  __nv_bfloat162 v = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&x), __floats2bfloat162_rn(c, c));
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t (&v)[4]) {
+  const uint32_t r = w >> 8;
+  v[0] = bf16x2_add((w & 0x000f000fu) | 0x43004300u, -136.f);
+  v[1] = bf16x2_add(((w >> 1) & 0x00780078u) | 0x41804180u, -24.f);
+  v[2] = bf16x2_add((r & 0x000f000fu) | 0x43004300u, -136.f);
+  v[3] = bf16x2_add(((r >> 1) & 0x00780078u) | 0x41804180u, -24.f);
+}
+
 }  // namespace ptb

@@ -253,20 +253,6 @@ __device__ __forceinline__ uint32_t nibbles64(uint32_t w) {
   const uint32_t s = K == 0 ? w << 4 : w >> (4 * K - 4);
   return (s & 0x00f000f0u) | 0x54005400u;
 }
-// As bf16: u - 8, exact.  Nibble 0 in mantissa bits 0 .. 3 of 128 and nibble 2
-// a byte further need no second shift; 1 and 3 go to bits 3 .. 6 of 16.
-__device__ __forceinline__ uint32_t add2(uint32_t x, float c) {
-  __nv_bfloat162 v = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&x), __floats2bfloat162_rn(c, c));
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t (&v)[4]) {
-  const uint32_t r = w >> 8;
-  v[0] = add2((w & 0x000f000fu) | 0x43004300u, -136.f);
-  v[1] = add2(((w >> 1) & 0x00780078u) | 0x41804180u, -24.f);
-  v[2] = add2((r & 0x000f000fu) | 0x43004300u, -136.f);
-  v[3] = add2(((r >> 1) & 0x00780078u) | 0x41804180u, -24.f);
-}
-
 // N consecutive words (N 1 .. 4) at 4 N-byte alignment (4-byte for N = 3).
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t (&r)[N], const uint8_t* p) {
