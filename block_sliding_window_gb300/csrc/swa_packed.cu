@@ -18,7 +18,7 @@
 //   warps 1..4   four MMA-issuing threads: S = Q K^T and O += P V of the two
 //                query tiles (P in tensor memory)
 //   warps 5..12  softmax, one query row per thread: online maximum and sum in
-//                the log2 domain, O / l through shared memory in whole rows
+//                the log2 domain, then O / l as a row
 //   warp 13      clears what the mask leaves out: a tile that some row masks
 //                also holds rows of later positions, of the next sequence or
 //                of no sequence; their weight is 0, but 0 times a NaN or an
@@ -47,9 +47,7 @@ struct Cfg {
   static constexpr int kAtoms = (D + 63) / 64;
   static constexpr int kQTileBytes = kAtoms * BQ * 128;
   static constexpr int kKVBytes = kAtoms * BKV * 128;
-  static constexpr int kOStageBytes = 32 * 128;
-  static constexpr int kFixed =
-      QT * kQTileBytes + 4 * QT * kOStageBytes + kHeldItems * 16 + 512 + 1024;
+  static constexpr int kFixed = QT * kQTileBytes + kHeldItems * 16 + 512 + 1024;
   static constexpr int kNSFit = (227 * 1024 - kFixed) / (2 * kKVBytes);
   static constexpr int kNS = kNSFit < 6 ? kNSFit : 6;
   static constexpr int kSmemBytes = kFixed + kNS * 2 * kKVBytes;
@@ -69,8 +67,7 @@ struct Block {
 
 struct PackedParams {
   CUtensorMap tq, tk, tv;  // {d, heads, tokens}
-  CUtensorMap to;          // the output, in boxes of 32 rows of a tile
-  int store_boxes;         // 32 rows of a tile are a box (G a power of two)
+  int wide_stores;         // every output row starts on a 32-byte boundary
   SwaPackedArgs a;
   int group, tq_tokens;    // G, TQ
   unsigned inv_group;      // r / G = r * inv_group >> 16 for r < 128
@@ -221,14 +218,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int32_t c0,
-                                             int32_t c1, int32_t c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::
-                   "l"(reinterpret_cast<uint64_t>(map)),
-               "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2)
-               : "memory");
-}
-
 // Bits 15 and 31: the low / high bf16 of w is not finite.
 __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
@@ -246,8 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sQ = smem;                               // [QT][kQTileBytes]
   uint8_t* sK = sQ + QT * C::kQTileBytes;           // [NS][kKVBytes]
   uint8_t* sV = sK + NS * C::kKVBytes;              // [NS][kKVBytes]
-  uint8_t* sO = sV + NS * C::kKVBytes;              // [4 * QT][kOStageBytes]
-  int4* held = reinterpret_cast<int4*>(sO + 4 * QT * C::kOStageBytes);  // [kHeldItems]
+  int4* held = reinterpret_cast<int4*>(sV + NS * C::kKVBytes);  // [kHeldItems]
   uint64_t* bars = reinterpret_cast<uint64_t*>(held + kHeldItems);
   uint64_t* q_full = bars;
   uint64_t* q_empty = q_full + 1;
@@ -572,10 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool interior = (key0 + BKV - 1 <= i) && (key0 >= i - a.window + 1);
         if (!interior) {
+          const int hi = min(i - key0, BKV - 1), lo = max(i - a.window + 1 - key0, 0);
+          uint64_t keep = hi < lo ? 0 : (~0ull >> (BKV - 1 - hi)) & (~0ull << lo);
+          uint32_t keep0 = static_cast<uint32_t>(keep), keep1 = static_cast<uint32_t>(keep >> 32);
 #pragma unroll
-          for (int e = 0; e < BKV; ++e) {
-            const int kj = key0 + e;
-            v[e] = (kj <= i) && (kj > i - a.window) ? v[e] : -INFINITY;
+          for (int e = 0; e < 32; ++e) {
+            v[e] = (keep0 & (1u << e)) ? v[e] : -INFINITY;
+            v[32 + e] = (keep1 & (1u << e)) ? v[32 + e] : -INFINITY;
           }
         }
         // Row max as a tree of three-input maxima, then one f32x2 FMA (scale
@@ -655,89 +646,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
       const bool bad = any_pv && bad_item[k % kBadSlots] == k + 1;
-      // One 64-column block at a time: each warp writes its 32 rows into its
-      // own 4 KB of shared memory (16-byte chunk c of row r at
-      // r * 128 + ((c ^ (r % 8)) * 16), the layout of a 128-byte-swizzled box).
-      // Where all 32 rows belong to the item and are a box of the output
-      // (G divides 32 or 32 divides G) its lane 0 stores them with TMA, else
-      // they are stored as whole rows, 8 lanes to a 128-byte line: a box
-      // would reach into the next sequence.  175B-class heads, four prompts:
-      // 10 us of 130 more with rows alone.
-      const int row0 = quarter * 32, tok0 = static_cast<int>((row0 * P.inv_group) >> 16);
-      const int tok31 = static_cast<int>(((row0 + 31) * P.inv_group) >> 16);
-      const bool boxed = P.store_boxes && x * TQ + tok31 < it.ntok;
-      uint8_t* stage = sO + (x * 4 + quarter) * C::kOStageBytes;
-      constexpr int kCols = D < 32 ? D : 32;  // columns per TMEM load
+      // Rows go out of registers, 32 bytes a store where rows start on 32-byte
+      // boundaries (else 16): a store fills whole sectors, a short block needs
+      // no other path, and staging the rows for tensor-map stores was no
+      // faster (and took the shared memory of a K/V stage).
+      __nv_bfloat16* out = a.o + static_cast<int64_t>(it.q_row + x * TQ + tok) * a.o_st +
+                           static_cast<int64_t>(it.kvh * G + r - tok * G) * a.o_sh;
+      const bool live = row_used && x * TQ + tok < it.ntok;
+      constexpr int kCols = D < 32 ? D : (D % 64 == 0 ? 64 : 32);  // columns per TMEM wait
 #pragma unroll
-      for (int at = 0; at < C::kAtoms; ++at) {
-        // The block stored before (of this item or the last one) has left shared memory.
-        if (lane == 0) bulk_wait_read();
-        __syncwarp();
-#pragma unroll
-        for (int c = at * 64; c < min(D, at * 64 + 64); c += kCols) {
-          uint32_t o[32];
-          if (any_pv) {
-            if constexpr (kCols == 32)
-              tmem_ld_32x32b_x32(o_tmem + c, o);
-            else
-              tmem_ld_32x32b_x16(o_tmem + c, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-            tmem_ld_wait();
+      for (int c = 0; c < D; c += kCols) {
+        uint32_t o[kCols];
+        if (any_pv) {
+          if constexpr (kCols == 64) {
+            tmem_ld_32x32b_x32(o_tmem + c, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+            tmem_ld_32x32b_x32(o_tmem + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+          } else if constexpr (kCols == 32) {
+            tmem_ld_32x32b_x32(o_tmem + c, o);
           } else {
-#pragma unroll
-            for (int e = 0; e < kCols; ++e) o[e] = 0;
+            tmem_ld_32x32b_x16(o_tmem + c, o);
           }
-          float f[kCols];
+          tmem_ld_wait();
+        } else {
 #pragma unroll
-          for (int e = 0; e < kCols; ++e) f[e] = __uint_as_float(o[e]) * inv;
-          if (bad && row_used && x * TQ + tok < it.ntok) {
-            // Values that are not finite and that this row attends to, out of
-            // the tiles that were cleared.
-            for (int key = max(0, i - a.window + 1); key <= i; ++key) {
-              if (!tile_masked(it, key & ~(BKV - 1), a.window)) continue;
-              const __nv_bfloat16* row =
-                  a.v + static_cast<int64_t>(it.k_row + key) * a.v_st + it.kvh * a.v_sh + c;
+          for (int e = 0; e < kCols; ++e) o[e] = 0;
+        }
+        if (!live) continue;
+        float f[kCols];
 #pragma unroll
-              for (int e = 0; e < kCols; ++e) {
-                const float z = __bfloat162float(row[e]);
-                if (!(fabsf(z) < INFINITY)) f[e] += z;
-              }
+        for (int e = 0; e < kCols; ++e) f[e] = __uint_as_float(o[e]) * inv;
+        if (bad) {
+          // Values that are not finite and that this row attends to, out of
+          // the tiles that were cleared.
+          for (int key = max(0, i - a.window + 1); key <= i; ++key) {
+            if (!tile_masked(it, key & ~(BKV - 1), a.window)) continue;
+            const __nv_bfloat16* row =
+                a.v + static_cast<int64_t>(it.k_row + key) * a.v_st + it.kvh * a.v_sh + c;
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) {
+              const float z = __bfloat162float(row[e]);
+              if (!(fabsf(z) < INFINITY)) f[e] += z;
             }
           }
+        }
 #pragma unroll
-          for (int e = 0; e < kCols; e += 8) {
-            const int chunk = ((c % 64) + e) / 8;
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4)) =
-                make_uint4(pack_bf16x2(f[e], f[e + 1]), pack_bf16x2(f[e + 2], f[e + 3]),
-                           pack_bf16x2(f[e + 4], f[e + 5]), pack_bf16x2(f[e + 6], f[e + 7]));
+        for (int e = 0; e < kCols; e += 16) {
+          uint32_t w[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) w[q] = pack_bf16x2(f[e + 2 * q], f[e + 2 * q + 1]);
+          if (P.wide_stores) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + c + e),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                         "r"(w[6]), "r"(w[7])
+                         : "memory");
+          } else {
+            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(out + c + e + 8) = make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
-        if (boxed) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&P.to, stage, at * 64, it.kvh * G + row0 - tok0 * G,
-                         it.q_row + x * TQ + tok0);
-            bulk_commit_group();
-          }
-          continue;
-        }
-        __syncwarp();
-        const int chunk = lane & 7, col = at * 64 + chunk * 8;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const int row = s * 4 + (lane >> 3), rr = quarter * 32 + row;
-          const int t = static_cast<int>((rr * P.inv_group) >> 16);
-          if (rr < G * TQ && x * TQ + t < it.ntok && col < D)
-            *reinterpret_cast<uint4*>(a.o + static_cast<int64_t>(it.q_row + x * TQ + t) * a.o_st +
-                                      static_cast<int64_t>(it.kvh * G + rr - t * G) * a.o_sh + col) =
-                *reinterpret_cast<const uint4*>(stage + row * 128 + ((chunk ^ (row & 7)) << 4));
-        }
-        __syncwarp();
       }
       tc_fence_before();
     }
-    // The output stores this warp issued complete before the CTA ends.
-    if (lane == 0) bulk_wait_all();
   }
 
   __syncwarp();
@@ -805,12 +774,7 @@ cudaError_t launch_swa_packed(const SwaPackedArgs& a, cudaStream_t stream) {
   if (!packed_map(&prm.tq, a.q, a.head_dim, a.heads, a.tokens_q, a.q_st, a.q_sh, prm.group,
                   prm.tq_tokens))
     return cudaErrorInvalidValue;
-  // 32 rows of a tile: 32 / G tokens of all G heads, or 32 heads of a token.
-  const int g = prm.group;
-  prm.store_boxes = (g & (g - 1)) == 0;
-  if (prm.store_boxes && !packed_map(&prm.to, a.o, a.head_dim, a.heads, a.tokens_q, a.o_st, a.o_sh,
-                                     g < 32 ? g : 32, g < 32 ? 32 / g : 1))
-    return cudaErrorInvalidValue;
+  prm.wide_stores = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.o_st % 16 == 0 && a.o_sh % 16 == 0;
   // Without keys the maps are never used; they still need a valid address.
   const bool keys = a.tokens_k > 0;
   if (!packed_map(&prm.tk, keys ? a.k : a.q, a.head_dim, a.kv_heads, keys ? a.tokens_k : 1, a.k_st,
