@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kKvThreads)
   if (b >= a.batch) return;  // a row behind the last sequence
   const int64_t first = a.cu[b], past = a.past[b];
   const int64_t pos = past + (t - first);
-  if (first < 0 || first > t || past < 0 || pos >= a.positions) {
+  if (first < 0 || first > t || a.cu[b + 1] > a.tokens || past < 0 || pos >= a.positions) {
     if (lane == 0) record_error(a.status, PTB_ERR_ARG);
     return;
   }
@@ -300,7 +300,9 @@ __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const KvGatherArg
   if (b >= a.batch) return;
   const int64_t first = a.cu[b], start = a.start[b];
   const int64_t pos = start + (t - first);
-  const uint8_t* page = first < 0 || first > t || start < 0 ? nullptr : kv_page(a.c, b, pos);
+  const uint8_t* page = first < 0 || first > t || a.cu[b + 1] > a.tokens || start < 0
+                            ? nullptr
+                            : kv_page(a.c, b, pos);
   if (!page) {
     if (lane == 0) record_error(a.status, PTB_ERR_ARG);
     return;

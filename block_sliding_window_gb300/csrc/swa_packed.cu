@@ -136,7 +136,7 @@ constexpr int kListHeld = 1024;  // sequences whose offsets are held in shared m
 
 __global__ void __launch_bounds__(1024) packed_list_kernel(const SwaPackedArgs a, int block_tokens,
                                                            int max_tiles, int* count,
-                                                           int4* blocks) {
+                                                           int4* blocks, int capacity) {
   __shared__ int cursor[kBuckets];
   __shared__ int warp_sum[32];
   __shared__ int4 held[kListHeld];  // q0, q1, k0, k1; q1 = q0 where they are out of range
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(1024) packed_list_kernel(const SwaPackedArgs a
                                               : static_cast<int>(static_cast<float>(it.n_tiles) *
                                                                  (kBuckets - 1) / max_tiles));
         const int at = atomicAdd(&cursor[cls], 1);
-        if (pass == 1) blocks[at] = e;
+        if (pass == 1 && at < capacity) blocks[at] = e;
       }
     }
     __syncthreads();
@@ -187,7 +187,12 @@ __global__ void __launch_bounds__(1024) packed_list_kernel(const SwaPackedArgs a
 #pragma unroll
       for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
       cursor[threadIdx.x] = before + sum - mine;
-      if (threadIdx.x == kBuckets - 1) *count = before + sum;
+      if (threadIdx.x == kBuckets - 1) {
+        // Offsets that go back and forth can name more blocks than the tokens
+        // have: the list ends at its capacity.
+        *count = min(before + sum, capacity);
+        if (before + sum > capacity) record_error(a.status, PTB_ERR_ARG);
+      }
       __syncthreads();
     }
   }
@@ -697,7 +702,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Values that are not finite and that this row attends to, out of
           // the tiles that were cleared.
           for (int key = max(0, i - a.window + 1); key <= i; ++key) {
-            if (!tile_masked(it, key & ~(BKV - 1), a.window)) continue;
+            if (!tile_masked(it, key & ~(BKV - 1), a.window)) {
+              key |= BKV - 1;  // on to the next tile
+              continue;
+            }
             const __nv_bfloat16* row =
                 a.v + static_cast<int64_t>(it.k_row + key) * a.v_st + it.kvh * a.v_sh + c;
 #pragma unroll
@@ -812,7 +820,8 @@ cudaError_t launch_swa_packed(const SwaPackedArgs& a, cudaStream_t stream) {
     int4* out = reinterpret_cast<int4*>(count + 4);
     const int64_t span = a.window < a.tokens_k ? a.window : a.tokens_k;
     const int max_tiles = static_cast<int>((span + block) / BKV + 2);
-    packed_list_kernel<<<1, 1024, 0, stream>>>(a, block, max_tiles, count, out);
+    packed_list_kernel<<<1, 1024, 0, stream>>>(a, block, max_tiles, count, out,
+                                               static_cast<int>(blocks));
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     prm.count = count;

@@ -217,6 +217,65 @@ def test_packed_graph_replays_with_other_lengths(ptb_lib):
         assert (o[torch.from_numpy(~written)] == 9).all()
 
 
+@pytest.mark.parametrize("heads,kv", [(4, 2), (96, 48)])
+def test_packed_workspace_of_the_caller(ptb_lib, heads, kv):
+    """A caller's workspace with anything in it, used again and again; the small call needs none."""
+    lens, d = [90, 3, 200], 32
+    q, k, v, cu, _ = packed_inputs(lens, None, heads, kv, d, 105, tail=0)
+    n = ptb_lib.swa_attention_packed_workspace_size(3, 293, heads, kv)
+    assert (n > 0) == (kv == 48)
+    ws = torch.full((max(n, 1),), 0xA5, dtype=torch.uint8, device="cuda")
+    want, bound, _ = M.packed(M.to64(q), M.to64(k), M.to64(v), cu, cu, 50, d ** -0.5)
+    for _ in range(3):
+        held_to(ptb_lib.swa_attention_packed(q, k, v, ints(cu), 50, workspace=ws), want, bound)
+    if n:
+        with pytest.raises(ptb_lib.PTBError, match="WORKSPACE"):
+            ptb_lib.swa_attention_packed(q, k, v, ints(cu), 50, workspace=ws[:n - 16])
+
+
+def test_packed_graph_of_a_listed_call(ptb_lib):
+    """More items than SMs: the list kernel and the attention kernel in two graphs, with other
+    lengths at each replay."""
+    heads = kv = 60
+    q, k, v, _, _ = packed_inputs([300], None, heads, kv, 32, 106, tail=0)
+    cu = ints([0, 300, 300, 300])
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs = []
+    for s, o in zip(streams, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            ptb_lib.swa_attention_packed(q, k, v, cu, 40, o=o)
+        graphs.append(g)
+    for lens in ([0, 300, 300, 300], [0, 10, 11, 299], [0, 0, 150, 150]):
+        cu.copy_(ints(lens))
+        for o in outs:
+            o.fill_(9)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        want, bound, written = M.packed(M.to64(q), M.to64(k), M.to64(v), lens, lens, 40, 32 ** -0.5)
+        for o in outs:
+            held_to(o[torch.from_numpy(written)], want[written], bound[written])
+            assert (o[torch.from_numpy(~written)] == 9).all()
+
+
+def test_packed_offsets_that_go_back_stay_inside_the_list(ptb_lib):
+    """Sequences that overlap name more query blocks than the list was sized for: recorded, and
+    nothing outside o and the list is written."""
+    heads = kv = 40
+    q, k, v, _, _ = packed_inputs([512], None, heads, kv, 16, 107, tail=0)
+    cu = ints([0, 512] * 40)
+    n = ptb_lib.swa_attention_packed_workspace_size(79, 512, heads, kv)
+    ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    o = ptb_lib.swa_attention_packed(q, k, v, cu, 64, workspace=ws[:n])
+    assert ptb_lib.last_device_error() == 1
+    assert (ws[n:] == 0x5A).all() and torch.isfinite(o.float()).all()
+
+
 def test_packed_on_two_streams(ptb_lib):
     sets = [packed_inputs([400, 70, 33], None, 8, 2, 64, 110 + 5 * i, tail=0) for i in range(2)]
     want = [ptb_lib.swa_attention_packed(q, k, v, ints(cu), 128) for q, k, v, cu, _ in sets]
@@ -382,7 +441,7 @@ def test_append_4bit_special_groups(ptb_lib):
 
 def test_append_out_of_range_is_recorded(ptb_lib):
     new, past, page, d = [3, 2], [4, 9], 16, 64
-    for what in ("page", "negative page", "table", "positions", "past"):
+    for what in ("page", "negative page", "table", "positions", "past", "offsets"):
         c = append_case(ptb_lib, new, past, 2, 1, d, d, False, page, 16, 240, tail=0)
         q, k, host = model_append(c, past, 1, page, d, 16, False)
         before = c["cache"].cpu().numpy().copy()
@@ -396,8 +455,10 @@ def test_append_out_of_range_is_recorded(ptb_lib):
             c["cos"], c["sin"] = angles(p[1] + 5, d)
         elif what == "positions":
             c["cos"], c["sin"] = angles(9, d)
-        else:
+        elif what == "past":
             p[1] = -1
+        else:
+            c["cu"] = [0, 3, 6]  # past the tensors' five rows
         run_append(ptb_lib, c, p, page, 16, False)
         assert ptb_lib.last_device_error() == 1, what
         got = c["cache"].cpu().numpy()
@@ -444,6 +505,8 @@ def test_gather_out_of_range_is_recorded(ptb_lib):
         ptb_lib.kv_gather(c["cache"], table, ints([0, 3]), ints([start]), 3, 1, 64, 16, 16, k=k, v=v)
         assert ptb_lib.last_device_error() == 1
         assert (k == 7).all() and (v == 7).all()
+    ptb_lib.kv_gather(c["cache"], torch.from_numpy(c["table"]).cuda(), ints([0, 4]), ints([0]), 3, 1, 64, 16, 16, k=k, v=v)
+    assert ptb_lib.last_device_error() == 1 and (k == 7).all()
 
 
 # --------------------------------------------------------------------- paged attention --
@@ -585,6 +648,48 @@ def test_paged_graphs_and_streams(ptb_lib, bits):
         torch.cuda.synchronize()
         for out in o:
             held_to(out, want, bound)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_paged_queries_that_are_not_finite_or_zero(ptb_lib, bits):
+    """A NaN or an infinity in a query stays in its row; a query of zeros averages the values; tiny
+    and huge queries keep their weights."""
+    lens, page, d = [70, 40, 33, 90], 16, 64
+    c = filled(ptb_lib, lens, 1, d, page, bits, 365, 4)
+    q = c["q1"]
+    q[0, 1, 3], q[0, 2, 60] = float("nan"), float("inf")
+    q[1] = 0
+    q[2] *= 1e-20
+    q[3] *= 1e4
+    o = M.to64(ptb_lib.swa_attention_paged(q, c["cache"], c["table_d"], ints(lens), 1, page, bits, 1000, scale=0.01))
+    assert np.isnan(o[0, 1:3]).all()
+    q[0, 1:3] = 0
+    want, bound = M.paged(M.to64(q), c["host"], c["table"], lens, 1000, 0.01)
+    o[0, 1:3] = want[0, 1:3]
+    assert (np.abs(o - want) <= bound).all()
+
+
+def test_paged_workspace_of_the_caller(ptb_lib):
+    c = filled(ptb_lib, [500, 70], 2, 64, 32, 4, 366, 4)
+    n = ptb_lib.swa_attention_paged_workspace_size(2, 4, 2, 64)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    args = (c["q1"], c["cache"], c["table_d"], ints([500, 70]), 2, 32, 4, 300)
+    want = ptb_lib.swa_attention_paged(*args)
+    for _ in range(3):
+        assert torch.equal(ptb_lib.swa_attention_paged(*args, workspace=ws), want)
+    with pytest.raises(ptb_lib.PTBError, match="WORKSPACE"):
+        ptb_lib.swa_attention_paged(*args, workspace=ws[:n - 16])
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_paged_sequences_that_share_pages(ptb_lib, bits):
+    """Two sequences of one prefix read the same pages."""
+    page, d = 16, 64
+    c = filled(ptb_lib, [64, 100], 2, d, page, bits, 367, 4)
+    c["table"][1, :4] = c["table"][0, :4]
+    o = ptb_lib.swa_attention_paged(c["q1"], c["cache"], torch.from_numpy(c["table"]).cuda(), ints([64, 100]), 2, page, bits, 1 << 20)
+    want, bound = M.paged(M.to64(c["q1"]), c["host"], c["table"], [64, 100], 1 << 20, d ** -0.5)
+    held_to(o, want, bound)
 
 
 def test_paged_same_bits_every_time(ptb_lib):
