@@ -353,7 +353,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
   constexpr int kCopies = 2 * C::kAtoms;
   const int copy_sub = lane / kCopies, copy_part = lane % kCopies;
   const int copy_side = copy_part / C::kAtoms, copy_atom = copy_part % C::kAtoms;
-  const int64_t value_side = static_cast<int64_t>(a.c.kv_heads) * a.c.block_bytes;
+  const uint32_t value_side = static_cast<uint32_t>(a.c.kv_heads * a.c.block_bytes);
+  const uint8_t* lane_base = a.c.base + lane * 16;
 
   Place ld = place_of(a, heads, u0 < u1 ? u0 : c0, lane);
   Place at = ld;
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
       head_src = (ld.hh / P.head_blocks) * (BITS == 16 ? page : a.c.block_bytes);
     }
     const int pg0 = __shfl_sync(0xffffffffu, page_reg, page_next);
-    const int pg1 = __shfl_sync(0xffffffffu, page_reg, page_next + subs - 1);
+    const int pg1 = subs == 1 ? pg0 : __shfl_sync(0xffffffffu, page_reg, page_next + 1);
     page_next += subs;
     uint32_t mask = 0xffffffffu;
     if (key0 < ld.s.lo || key0 + kBlockKeys > ld.s.n || (pg0 | pg1) < 0) {
@@ -407,30 +408,47 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
     } else {
       if (lane == 0) masks[stage] = mask;
       __syncwarp();  // the stage has been read by every lane
-      // Rows 0 .. 15 of the unit and rows 16 .. 31.
-      const int off0 = key0 & (page - 1), off1 = (key0 + 16) & (page - 1);
-      const uint8_t* block0 =
-          a.c.base + static_cast<uint64_t>(static_cast<uint32_t>(pg0)) * page_bytes + head_src;
-      const uint8_t* block1 =
-          a.c.base + static_cast<uint64_t>(static_cast<uint32_t>(pg1)) * page_bytes + head_src;
+      constexpr int kCodes = kBlockKeys * (D / 2) / 16, kPairs = kBlockKeys * (D / 8) / 16;
       const uint32_t dst = ring + stage * C::kStageBytes + lane * 16;
-      auto rows = [&](const uint8_t* lower, const uint8_t* upper, auto n, uint32_t to) {
-        constexpr int chunks = decltype(n)::value, half = chunks / 2;
+      const uint32_t head_at = static_cast<uint32_t>(head_src);
+      if (subs == 1) {
+        // All rows in one page: every address is a lane's base plus constants.
+        if (pg0 >= 0) {
+          const uint8_t* block = lane_base + static_cast<uint64_t>(static_cast<uint32_t>(pg0)) * page_bytes;
+          const int off = key0 & (page - 1);
+          const uint8_t* k_codes = block + (head_at + off * (D / 2));
+          const uint8_t* k_pairs = block + (head_at + page * (D / 2) + off * (D / 8));
+          const uint8_t *v_codes = k_codes + value_side, *v_pairs = k_pairs + value_side;
 #pragma unroll
-        for (int i = 0; i < (chunks + 31) / 32; ++i) {
-          const int ch = i * 32 + lane;
-          const bool second = ch >= half;
-          if (ch < chunks && (second ? pg1 : pg0) >= 0) {
-            const uint8_t* p = (second ? upper - half * 16 : lower) + ch * 16;
-            copy16(to + i * 512, p);
-            copy16(to + i * 512 + C::kSideBytes, p + value_side);
+          for (int i = 0; i < (kCodes + 31) / 32; ++i)
+            if (kCodes >= i * 32 + 32 || i * 32 + lane < kCodes) {
+              copy16(dst + i * 512, k_codes + i * 512);
+              copy16(dst + i * 512 + C::kSideBytes, v_codes + i * 512);
+            }
+          if (kPairs >= 32 || lane < kPairs) {
+            copy16(dst + kBlockKeys * (D / 2), k_pairs);
+            copy16(dst + kBlockKeys * (D / 2) + C::kSideBytes, v_pairs);
           }
         }
-      };
-      rows(block0 + off0 * (D / 2), block1 + off1 * (D / 2),
-           std::integral_constant<int, kBlockKeys * (D / 2) / 16>(), dst);
-      rows(block0 + page * (D / 2) + off0 * (D / 8), block1 + page * (D / 2) + off1 * (D / 8),
-           std::integral_constant<int, kBlockKeys * (D / 8) / 16>(), dst + kBlockKeys * (D / 2));
+      } else {
+        // Pages of 16 rows: the unit is two whole blocks.
+        const uint8_t* block0 = lane_base + static_cast<uint64_t>(static_cast<uint32_t>(pg0)) * page_bytes + head_at;
+        const uint8_t* block1 = lane_base + static_cast<uint64_t>(static_cast<uint32_t>(pg1)) * page_bytes + head_at;
+        auto rows = [&](auto n, uint32_t from, uint32_t to) {
+          constexpr int chunks = decltype(n)::value, half = chunks / 2;
+#pragma unroll
+          for (int i = 0; i < (chunks + 31) / 32; ++i) {
+            const bool second = i * 32 + lane >= half;
+            if (i * 32 + lane < chunks && (second ? pg1 : pg0) >= 0) {
+              const uint8_t* p = (second ? block1 - half * 16 : block0) + (from + i * 512);
+              copy16(to + i * 512, p);
+              copy16(to + i * 512 + C::kSideBytes, p + value_side);
+            }
+          }
+        };
+        rows(std::integral_constant<int, kCodes>(), 0, dst);
+        rows(std::integral_constant<int, kPairs>(), 16 * (D / 2), dst + kBlockKeys * (D / 2));
+      }
     }
     --to_load;
     if (++ld.i >= ld.s.units) {
