@@ -82,6 +82,7 @@ struct PagedParams {
   SwaPagedArgs a;
   int group, head_blocks;  // G; blocks of 8 NT query heads of a kv head
   float* parts;            // [2 x blocks]: partial results as in shared memory
+  int4* cuts;              // [blocks]: the segment that goes on into the block
 };
 
 // The keys that sequence b's query attends to, in units.
@@ -333,7 +334,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
   const int64_t total = total_units(a, lane) * heads;
   const int64_t share = share_of(total, gridDim.x);
   const int64_t c0 = blockIdx.x * share, c1 = c0 + share < total ? c0 + share : total;
-  if (c0 >= c1) return;  // the whole block
+  if (c0 >= c1) {  // the whole block
+    if (threadIdx.x == 0) P.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
   const int64_t part = (c1 - c0 + kWarps - 1) / kWarps;
   const int64_t u0 = c0 + warp * part < c1 ? c0 + warp * part : c1;
   const int64_t u1 = u0 + part < c1 ? u0 + part : c1;
@@ -358,6 +362,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
 
   Place ld = place_of(a, heads, u0 < u1 ? u0 : c0, lane);
   Place at = ld;
+  volatile int* begin = reinterpret_cast<volatile int*>(tail + 96);  // the share's first place
+  if (threadIdx.x == 0) {
+    begin[0] = ld.b;
+    begin[1] = ld.hh;
+    begin[2] = ld.i;
+    begin[3] = ld.s.units;
+  }
   int64_t to_load = u1 - u0;  // units whose copies are still to be issued
   // Pages of the coming sub-blocks, one a lane; -1: not needed, or out of range.
   int page_reg = -1, page_next = 32;
@@ -893,6 +904,16 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
     }
   }
   __syncthreads();
+  if (threadIdx.x == 0) {
+    // For the join kernel: sequence, head block, first share and number of
+    // shares of the segment that the block's share begins inside of.
+    const int64_t f0 = c0 - begin[2];
+    const int first = static_cast<int>(f0 / share);
+    P.cuts[blockIdx.x] =
+        begin[2] > 0 ? make_int4(begin[0], begin[1], first,
+                                 static_cast<int>((f0 + begin[3] - 1) / share) - first + 1)
+                     : make_int4(0, 0, 0, 0);
+  }
 
   // -------------------------------------------------- join within the block --
   // A chain is a cut segment's partial results in this block: the slot of the
@@ -961,73 +982,73 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
 }
 
 // Joins the blocks' shares of the segments that were cut between them.  Block
-// w looks at the boundary between shares w - 1 and w: where it falls inside a segment of n
-// shares, the n - 1 boundary blocks split the segment's (head, 32-channel)
-// outputs among them.
+// w looks at the boundary between shares w and w + 1: where it falls inside a
+// segment of n shares, the n - 1 blocks of its boundaries split the segment's
+// heads among them.
 template <int NT>
 __global__ void __launch_bounds__(kJoinThreads) swa_paged_join_kernel(const PagedParams P, int d) {
   const SwaPagedArgs& a = P.a;
-  __shared__ float so[kJoinThreads / 32][32];
+  __shared__ float4 so[kJoinThreads / 32][32];
   __shared__ float sl[kJoinThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int heads = a.c.kv_heads * P.head_blocks;
-  const int64_t total = total_units(a, lane) * heads;
-  const int64_t share = share_of(total, gridDim.x + 1);
-  const int64_t u = (blockIdx.x + 1) * share;
-  Place p = {};
-  if (u < total) p = place_of(a, heads, u, lane);
   // Every block waits, so that this kernel ends after the one before it.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (u >= total || p.i == 0) return;
-  const int64_t f0 = u - p.i, f1 = f0 + p.s.units;
-  const int64_t w0 = f0 / share, w1 = (f1 - 1) / share;
-  const int n = static_cast<int>(w1 - w0 + 1);             // shares of the segment
-  const int me = static_cast<int>(blockIdx.x + 1 - w0 - 1);  // this boundary among n - 1
-  const int kvh = p.hh / P.head_blocks;
-  const int head0 = kvh * P.group + (p.hh % P.head_blocks) * 8 * NT;
+  const int4 cut = P.cuts[blockIdx.x + 1];
+  const int n = cut.w;                        // shares of the segment
+  if (n == 0) return;                         // no segment goes on here
+  const int w0 = cut.z;
+  const int me = blockIdx.x - w0;             // this boundary among n - 1
+  const int kvh = cut.y / P.head_blocks;
+  const int head0 = kvh * P.group + (cut.y % P.head_blocks) * 8 * NT;
   const int nheads = min(8 * NT, (kvh + 1) * P.group - head0);
-  const int chunks = (d + 31) / 32;
-  const int tasks = nheads * chunks;
   auto slot_of = [&](int x) {
-    return P.parts + (2 * (w0 + x) + (x == 0 ? 1 : 0)) * (8 * NT * (2 + d));
+    return P.parts + static_cast<int64_t>(2 * (w0 + x) + (x == 0 ? 1 : 0)) * (8 * NT * (2 + d));
   };
-  // Few shares: a warp takes an output piece alone; many: all warps share one.
+  // A head at a time, 4 channels a lane.  Few shares: a warp takes a head
+  // alone; many: all warps share one.
   const bool alone = n <= kJoinThreads / 32;
-  const int step = alone ? 1 : kJoinThreads / 32;
-  for (int task0 = me; task0 < tasks; task0 += (n - 1) * (alone ? kJoinThreads / 32 : 1)) {
-    const int task = alone ? task0 + warp * (n - 1) : task0;
-    const bool live = task < tasks;
-    const int head = live ? task / chunks : 0, c = live ? (task % chunks) * 32 + lane : d;
+  const bool live = lane * 4 < d;
+  for (int head = me + (alone ? warp * (n - 1) : 0); head < nheads;
+       head += (n - 1) * (alone ? kJoinThreads / 32 : 1)) {
     float mx = -INFINITY;
-    for (int x = lane; x < n; x += 32) {
-      mx = fmaxf(mx, slot_of(x)[head]);
-    }
+    for (int x = lane; x < n; x += 32) mx = fmaxf(mx, slot_of(x)[head]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float ref = mx == -INFINITY ? 0.f : mx;
-    float acc = 0.f, l = 0.f;
-#pragma unroll 8
-    for (int x = alone ? 0 : warp; x < n; x += step) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int x = alone ? 0 : warp; x < n; x += alone ? 1 : kJoinThreads / 32) {
       const float* p = slot_of(x);
       const float f = fast_exp2(p[head] - ref);
       l = fmaf(f, p[8 * NT + head], l);
-      if (c < d) acc = fmaf(f, p[16 * NT + head * d + c], acc);
+      if (live) {
+        const float4 v = *reinterpret_cast<const float4*>(p + 16 * NT + head * d + lane * 4);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
     }
     if (!alone) {
       so[warp][lane] = acc;
       if (lane == 0) sl[warp] = l;
       __syncthreads();
-      acc = l = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      l = 0.f;
 #pragma unroll
       for (int x = 0; x < kJoinThreads / 32; ++x) {
-        acc += so[x][lane];
+        const float4 v = so[x][lane];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
         l += sl[x];
       }
       __syncthreads();
     }
-    if ((alone || warp == 0) && c < d)
-      a.o[p.b * a.o_sb + (head0 + head) * a.o_sh + c] =
-          __float2bfloat16_rn(l != 0.f ? acc / l : 0.f);
+    if ((alone || warp == 0) && live) {
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      *reinterpret_cast<uint2*>(a.o + cut.x * a.o_sb + (head0 + head) * a.o_sh + lane * 4) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
   }
 }
 
@@ -1048,12 +1069,20 @@ cudaError_t launch_typed(PagedParams& prm, cudaStream_t stream) {
   cfg.gridDim = dim3(grid > 1 ? grid - 1 : 1);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
-  // Finds its shares while the first kernel still runs, then waits for it.
+  // Launched to overlap the first kernel's end where that one is long (3 us of
+  // GPU time); a call of few microseconds is bound by its launches on the
+  // host, and an overlapping one costs 3 us more there (25.5 against 22.5 us
+  // a call).  The lengths are not known here: the bound goes by the table.
+  const KvCache& c = prm.a.c;
+  const int64_t most = c.table_pages << c.page_shift;
+  const double bytes = 2.0 * prm.a.batch * c.kv_heads *
+                       static_cast<double>(most < prm.a.window ? most : prm.a.window) *
+                       (static_cast<double>(c.block_bytes) / c.page_size);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = bytes > 100e6 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, swa_paged_join_kernel<NT>, static_cast<const PagedParams&>(prm), D);
 }
 
@@ -1079,9 +1108,11 @@ cudaError_t launch_d(PagedParams& prm, cudaStream_t stream) {
 
 }  // namespace
 
-// Two cut segments a block: maxima, sums and outputs of up to 8 NT heads.
+// A block's cut, and two partial results: maxima, sums and outputs of up to
+// 8 NT heads.
 size_t swa_paged_workspace(int, int heads, int kv_heads, int head_dim, int sms) {
-  return 2ull * sms * 8 * head_tiles(heads / kv_heads) * (2 + head_dim) * sizeof(float);
+  return sms * (2ull * 8 * head_tiles(heads / kv_heads) * (2 + head_dim) * sizeof(float) +
+                sizeof(int4));
 }
 
 cudaError_t launch_swa_paged(const SwaPagedArgs& a, cudaStream_t stream) {
@@ -1090,7 +1121,8 @@ cudaError_t launch_swa_paged(const SwaPagedArgs& a, cudaStream_t stream) {
   prm.group = a.heads / a.c.kv_heads;
   const int tile = 8 * head_tiles(prm.group);
   prm.head_blocks = (prm.group + tile - 1) / tile;
-  prm.parts = static_cast<float*>(a.workspace);
+  prm.cuts = static_cast<int4*>(a.workspace);
+  prm.parts = reinterpret_cast<float*>(prm.cuts + a.sms);
   if (a.c.bits == 4) return launch_d<4>(prm, stream);
   const int sub = a.c.page_size < kBlockKeys ? a.c.page_size : kBlockKeys;
   const uint64_t row = 2ull * a.c.head_dim;
