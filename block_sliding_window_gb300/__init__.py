@@ -346,6 +346,9 @@ def swa_attention_counts(q, k, v, window: int, scale: float = 0.0, stream=None):
 
 # ---------------------------------------------------------------- serving --
 
+_INT32_MAX = 0x7fffffff  # a longer window is the same as this one; ctypes would drop its high bits
+
+
 @functools.lru_cache(maxsize=None)
 def kv_page_size(kv_heads: int, page_size: int, head_dim: int, bits: int) -> int:
     """Bytes of one page of a key/value cache: `page_size` token rows of the keys and the values of
@@ -439,16 +442,26 @@ def _new(like, shape, stream, dtype=torch.bfloat16):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _scratch(need: int, workspace, like, stream) -> tuple:
+def _scratch(need: int, workspace, like, dev: int, stream) -> tuple:
     """(tensor that has to outlive the launch, pointer, bytes)"""
     if workspace is None:
         if need == 0:
             return None, None, 0
         workspace = _new(like, (need,), stream, torch.uint8)
         return workspace, workspace.data_ptr(), need
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+@functools.lru_cache(maxsize=4096)
+def _packed_workspace(dev: int, batch: int, tokens_q: int, heads: int, kv_heads: int) -> int:
+    return swa_attention_packed_workspace_size(batch, tokens_q, heads, kv_heads)
+
+
+@functools.lru_cache(maxsize=4096)
+def _paged_workspace(dev: int, batch: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return swa_attention_paged_workspace_size(batch, heads, kv_heads, head_dim)
 
 
 def kv_append(q, k, v, cache, page_table, cu_seqlens, past, page_size: int, bits: int, cos=None,
@@ -560,10 +573,10 @@ def swa_attention_packed(q, k, v, cu_seqlens, window: int, cu_seqlens_k=None, sc
         oa = o.data_ptr(), max(heads, 1) * d, d
     else:
         oa = _heads_view("o", o, dev, q.shape)
-    ws, wp, wb = _scratch(lib.swa_attention_packed_workspace_size(batch, tq, heads, kv_heads),
-                          workspace, q, stream)  # ws lives until the launch is queued
+    ws, wp, wb = _scratch(_packed_workspace(dev, batch, tq, heads, kv_heads), workspace, q, dev,
+                          stream)  # ws lives until the launch is queued
     st = lib.swa_attention_packed(*qa, *ka, *va, cu, cu_k, batch, tq, tk, heads, kv_heads, d,
-                                  window, scale, *oa, wp, wb, raw)
+                                  min(window, _INT32_MAX), scale, *oa, wp, wb, raw)
     if st:
         _check(st, "swa_attention_packed")
     return o
@@ -586,12 +599,13 @@ def swa_attention_paged(q, cache, page_table, seq_lens, kv_heads: int, page_size
         oa = o.data_ptr(), heads * d, d
     else:
         oa = _heads_view("o", o, dev, q.shape)
-    ws, wp, wb = _scratch(lib.swa_attention_paged_workspace_size(batch, heads, kv_heads, d),
-                          workspace, q, stream)
+    ws, wp, wb = _scratch(_paged_workspace(dev, batch, heads, kv_heads, d), workspace, q, dev,
+                          stream)
     st = lib.swa_attention_paged(*qa, *_cache_args(cache, page_table, batch, kv_heads, d, page_size,
                                                    bits, dev),
                                  _int_vector("seq_lens", seq_lens, batch, dev), batch, heads,
-                                 kv_heads, d, page_size, bits, window, scale, *oa, wp, wb, raw)
+                                 kv_heads, d, page_size, bits, min(window, _INT32_MAX), scale, *oa, wp,
+                                 wb, raw)
     if st:
         _check(st, "swa_attention_paged")
     return o

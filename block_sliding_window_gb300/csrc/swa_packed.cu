@@ -57,14 +57,6 @@ struct Cfg {
 };
 static_assert(Cfg<128>::kNS + 1 < kBadSlots && Cfg<16>::kNS + 1 < kBadSlots, "bad-value slots");
 
-// One query block of a sequence, as the list holds it.
-struct Block {
-  int q_row;  // first row of q and o
-  int ntok;   // its tokens, 1 .. 2 TQ
-  int p0;     // position of the first one (negative: before the first key)
-  int k_row;  // row of the sequence's position 0 in k and v
-};
-
 struct PackedParams {
   CUtensorMap tq, tk, tv;  // {d, heads, tokens}
   int wide_stores;         // every output row starts on a 32-byte boundary
@@ -72,7 +64,7 @@ struct PackedParams {
   int group, tq_tokens;    // G, TQ
   unsigned inv_group;      // r / G = r * inv_group >> 16 for r < 128
   const int* count;        // null: the CTA finds its own item
-  const int4* blocks;
+  const int4* blocks;      // as sequence_block() makes them
 };
 
 struct Item {
@@ -117,6 +109,9 @@ __device__ __forceinline__ int sequence_blocks(const SwaPackedArgs& a, int b, in
   return (q1 - q0 + block_tokens - 1) / block_tokens;
 }
 
+// Query block i of sequence b: first row of q and o, tokens (1 .. 2 TQ),
+// position of the first one (negative: before the first key), and the row of
+// the sequence's position 0 in k and v.
 __device__ __forceinline__ int4 sequence_block(const SwaPackedArgs& a, int b, int i,
                                                int block_tokens) {
   const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];

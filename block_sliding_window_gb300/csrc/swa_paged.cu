@@ -1064,9 +1064,9 @@ cudaError_t launch_typed(PagedParams& prm, cudaStream_t stream) {
   const int grid = prm.a.sms;
   kern<<<grid, C::kWarps * 32, C::kSmemBytes, stream>>>(prm);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || grid == 1) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid > 1 ? grid - 1 : 1);
+  cfg.gridDim = dim3(grid - 1);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   // Launched to overlap the first kernel's end where that one is long (3 us of

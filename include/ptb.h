@@ -534,7 +534,8 @@ ptb_status ptb_kv_gather(const void* cache, int64_t pages, const int32_t* page_t
  * by cu_seqlens_q) and nk keys (rows of k and v by cu_seqlens_k; NULL: the
  * same as cu_seqlens_q).  Its queries are the last nq of its nk positions:
  * query i stands at position p = nk - nq + i and attends to keys
- * max(0, p - window + 1) .. p.  A query without keys (nk < nq) gets zeros.
+ * max(0, p - window + 1) .. p.  A query without keys (nk < nq) gets zeros, and
+ * so does one whose scores are all minus infinity.
  *
  *   q, o [tokens_q, heads, d], k, v [tokens_k, kv_heads, d]  strided bf16;
  *        o may be q itself (same pointer and strides), and overlaps nothing else
@@ -560,9 +561,9 @@ ptb_status swa_attention_packed(const ptb_bf16* q, int64_t q_st, int64_t q_sh, c
  * swa_attention_paged: attention of one new token per sequence over the
  * cache.  Sequence b holds seq_lens[b] positions (int32, device), the new
  * token's own among them; its query attends to the last min(seq_lens[b],
- * window) of them.  seq_lens[b] = 0 gives zeros.  q, o [batch, heads, d]
- * strided bf16 (o may be q itself); keys of bits = 4 are used as the values
- * that their codes stand for.
+ * window) of them.  seq_lens[b] = 0 gives zeros, and so do scores that are all
+ * minus infinity.  q, o [batch, heads, d] strided bf16 (o may be q itself);
+ * keys of bits = 4 are used as the values that their codes stand for.
  *   workspace  at least swa_attention_paged_workspace_size() bytes (depends on
  *        the current device's SM count), 256-byte aligned; calls that may run
  *        at the same time need one each

@@ -168,6 +168,27 @@ def test_packed_infinite_value_alone(ptb_lib):
     assert np.isfinite(o).all()
 
 
+def test_scores_of_minus_infinity(ptb_lib):
+    """A row whose scores are all minus infinity gets zeros, like one without keys; one other key
+    takes all the weight."""
+    n, heads, d, page = 70, 4, 64, 16
+    q, k, v = normal((n, heads, d), 24), normal((n, heads, d), 25), normal((n, heads, d), 26)
+    q[..., 0] = 1.0
+    k[..., 0] = float("-inf")
+    cu = ints([0, n])
+    assert (ptb_lib.swa_attention_packed(q, k, v, cu, 40) == 0).all()
+    table = ints(range(5))[None]
+    cache = new_cache(ptb_lib, 5, heads, page, d, 16)
+    ptb_lib.kv_append(None, k, v, cache, table, cu, ints([0]), page, 16)
+    assert (ptb_lib.swa_attention_paged(q[n - 1:], cache, table, ints([n]), heads, page, 16, 40) == 0).all()
+    k[50, :, 0] = 0.0
+    ptb_lib.kv_append(None, k, v, cache, table, cu, ints([0]), page, 16)
+    o = ptb_lib.swa_attention_packed(q, k, v, cu, 40)
+    assert (o[:50] == 0).all() and torch.equal(o[50:], v[50:51].expand(n - 50, heads, d))
+    o = ptb_lib.swa_attention_paged(q[n - 1:], cache, table, ints([n]), heads, page, 16, 40)
+    assert torch.equal(o[0], v[50])
+
+
 def test_packed_bad_offsets_are_recorded(ptb_lib):
     q, k, v, _, _ = packed_inputs([64, 64], None, 2, 2, 64, 90, tail=0)
     for cu in ([0, 64, 200], [0, 100, 64], [-5, 64, 128]):
@@ -679,6 +700,46 @@ def test_paged_workspace_of_the_caller(ptb_lib):
         assert torch.equal(ptb_lib.swa_attention_paged(*args, workspace=ws), want)
     with pytest.raises(ptb_lib.PTBError, match="WORKSPACE"):
         ptb_lib.swa_attention_paged(*args, workspace=ws[:n - 16])
+    with pytest.raises(ValueError, match="workspace"):
+        ptb_lib.swa_attention_paged(*args, workspace=ws.cpu())
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_paged_long_tables(ptb_lib, bits):
+    """A table with room for long sequences has the join launched early.  Calls one behind the other
+    on one stream share a workspace, eager and replayed; one writes over its own queries."""
+    lens, page, kv, d, w = [3000, 1, 700], 16, 2, 128, 1 << 20
+    c = filled(ptb_lib, lens, kv, d, page, bits, 368, 8)
+    wide = torch.full((3, 1 << 16), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c["table"].shape[1]] = c["table_d"]
+    n = ints(lens)
+    want, bound = M.paged(M.to64(c["q1"]), c["host"], c["table"], lens, w, d ** -0.5)
+    one = ptb_lib.swa_attention_paged(c["q1"], c["cache"], c["table_d"], n, kv, page, bits, w)
+    held_to(one, want, bound)
+    ws = torch.empty(ptb_lib.swa_attention_paged_workspace_size(3, 8, kv, d), dtype=torch.uint8, device="cuda")
+    qs = [c["q1"] * f for f in (1.0, -1.0, 2.0)]
+    alone = [ptb_lib.swa_attention_paged(q, c["cache"], c["table_d"], n, kv, page, bits, w) for q in qs]
+    o = [q.clone() for q in qs]
+
+    def calls():
+        for q, out in zip(qs, o):
+            ptb_lib.swa_attention_paged(q, c["cache"], wide, n, kv, page, bits, w, o=out, workspace=ws)
+
+    for _ in range(20):
+        calls()
+    for got, other in zip(o, alone):
+        assert torch.equal(got, other)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for out in o:
+        out.zero_()
+    for _ in range(5):
+        g.replay()
+    for got, other in zip(o, alone):
+        assert torch.equal(got, other)
+    q = qs[0].clone()
+    assert torch.equal(ptb_lib.swa_attention_paged(q, c["cache"], wide, n, kv, page, bits, w, o=q), alone[0])
 
 
 @pytest.mark.parametrize("bits", [16, 4])
