@@ -39,7 +39,7 @@ constexpr int BKV = 64;       // keys per K/V tile (= MMA N of S, K of PV)
 constexpr int kThreads = 448;
 constexpr int kCleanWarp = 13;
 constexpr int kHeldItems = 64;  // a CTA's first items, held in shared memory
-constexpr int kBadSlots = 8;  // > items that the K/V ring can hold at once
+constexpr int kBadSlots = 8;  // more than the items that the K/V ring can hold at once
 constexpr float kRescaleLog2 = 8.0f;  // raise the reference max only past 2^8
 
 template <int D>
@@ -236,6 +236,20 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int32_t c0, int32_t c1,
+                                                int32_t c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
+__device__ __forceinline__ void store16_past_l1(void* p, const uint4& v) {
+  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 // Bits 15 and 31: the low / high bf16 of w is not finite.
 __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
@@ -279,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_empty, QT);  // both score threads release Q
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], QT + 1);  // each query tile and the cleaning warp release a stage
+      mbar_init(&kv_empty[s], 2 * QT + 1);  // every issuing thread and the cleaning warp
       mbar_init(&v_clean[s], 1);
     }
     for (int x = 0; x < 2 * QT; ++x) {
@@ -369,6 +383,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           armed |= 1u << st;
           armed_parity = (armed_parity & ~(1u << st)) | (ph << st);
         }
+        // Behind this item's tiles, the next one's queries start on their way
+        // to L2 (64 ragged prompts: 149 us, 151 without; before the tiles they
+        // hold those up).
+        const int next = snake_item(k + 1);
+        if (next < num_items) {
+          const Item nx = item_at(k + 1, next);
+          for (int x = 0; x < (nx.ntok > TQ ? 2 : 1); ++x)
+#pragma unroll
+            for (int at = 0; at < C::kAtoms; ++at)
+              tma_prefetch_3d(&P.tq, at * 64, nx.kvh * G, nx.q_row + x * TQ);
+        }
       }
       // Let every copy this thread issued land before the CTA goes away.
       volatile int no_abort = 0;
@@ -386,82 +411,80 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc_pv = umma_idesc_bf16(BQ, D) | (1u << 16);  // B (V) MN-major
       bool ok = true;
       uint32_t kv_count = 0, q_count = 0, issued = 0;
-      const uint32_t qx = smem_addr(sQ + x * C::kQTileBytes);
+      const uint64_t qd = sw128_kmajor_desc(smem_addr(sQ + x * C::kQTileBytes));
       for (int k = 0, item = snake_item(0); ok && item < num_items; item = snake_item(++k)) {
         const Item it = item_at(k, item);
         if (it.n_tiles == 0) continue;
         if (!pv_role) {
           if (!mbar_wait(q_full, q_count & 1, abort_flag, a.status)) break;
           ++q_count;
-          tc_fence_after();
         }
         bool first_pv = true;
-        for (int j = 0; j < it.n_tiles; ++j) {
-          // Stage arrivals are parity waits, exact only within one phase: a
-          // score thread observes every stage in order and releases the
-          // tiles outside its band itself; the P V thread releases the
-          // others after their P V.
-          const uint32_t kc = kv_count + j;
-          const int st = kc % NS;
+        // What lies between a wait and the first product adds to every tile's
+        // round trip, so a role waits last for what comes last (scores: the
+        // P V of two tiles before; P V: P) and has its descriptors by then.
+        // Parity waits are exact only within one phase: both threads of a
+        // query tile observe and release every stage in order, also the tiles
+        // outside their band.
+        for (int j = 0; j < it.n_tiles; ++j, ++kv_count) {
+          const int st = kv_count % NS;
+          const uint32_t ph = (kv_count / NS) & 1;
           const bool relevant = tile_relevant(it, x, (it.kt_hi - j) * BKV, TQ, a.window);
-          if (!pv_role || relevant) {
-            if (!mbar_wait(&kv_full[st], (kc / NS) & 1, abort_flag, a.status)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
+          const uint32_t n = issued, buf = n & 1;
+          if (!mbar_wait(&kv_full[st], ph, abort_flag, a.status)) {
+            ok = false;
+            break;
           }
-          const uint32_t n = issued;
           if (!pv_role) {
             if (relevant) {
+              const uint64_t kd = sw128_kmajor_desc(smem_addr(sK + st * C::kKVBytes));
+              const uint32_t d_tmem = tmem + C::s_col(x, buf);
               // Score buffer n % 2 still holds P number n - 2 until its P V ends.
-              if (n >= 2) {
-                if (!mbar_wait(&pv_done[2 * x + (n & 1)], ((n - 2) >> 1) & 1, abort_flag,
-                               a.status)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
+              if (n >= 2 && !mbar_wait(&pv_done[2 * x + buf], ((n - 2) >> 1) & 1, abort_flag,
+                                       a.status)) {
+                ok = false;
+                break;
               }
-              const uint32_t d_tmem = tmem + C::s_col(x, n & 1);
-              const uint32_t k_addr = smem_addr(sK + st * C::kKVBytes);
+              tc_fence_after();
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t at = kk / 4, off = (kk % 4) * 32;
-                umma_bf16_ss(d_tmem, sw128_kmajor_desc(qx + at * BQ * 128 + off),
-                             sw128_kmajor_desc(k_addr + at * BKV * 128 + off), idesc_s, kk > 0);
+                umma_bf16_ss(d_tmem, qd + ((at * BQ * 128 + off) >> 4),
+                             kd + ((at * BKV * 128 + off) >> 4), idesc_s, kk > 0);
               }
-              umma_commit(&s_full[2 * x + (n & 1)]);
+              umma_commit(&s_full[2 * x + buf]);
               ++issued;
-            } else {
-              mbar_arrive(&kv_empty[st]);  // this query tile never reads the stage
             }
+            // The P V thread releases the stage after this product has ended.
+            mbar_arrive(&kv_empty[st]);
             if (j == it.n_tiles - 1) umma_commit(q_empty);  // Q_X is free once these finish
-          } else if (relevant) {
-            // P first: it says that the score thread has seen this fill of the
-            // stage, so the cleaning warp has passed the fill before (it
-            // releases a stage only then) and the parity of v_clean is exact.
-            if (!mbar_wait(&p_full[2 * x + (n & 1)], (n >> 1) & 1, abort_flag, a.status) ||
-                !mbar_wait(&v_clean[st], (kc / NS) & 1, abort_flag, a.status)) {
+          } else {
+            if (!mbar_wait(&v_clean[st], ph, abort_flag, a.status)) {
+              ok = false;
+              break;
+            }
+            if (!relevant) {
+              mbar_arrive(&kv_empty[st]);
+              continue;
+            }
+            const uint64_t vd = sw128_mnmajor_desc(smem_addr(sV + st * C::kKVBytes), BKV * 128);
+            const uint32_t p_tmem = tmem + C::s_col(x, buf);
+            const uint32_t d_tmem = tmem + C::o_col(x);
+            if (!mbar_wait(&p_full[2 * x + buf], (n >> 1) & 1, abort_flag, a.status)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t p_tmem = tmem + C::s_col(x, n & 1);
-            const uint32_t d_tmem = tmem + C::o_col(x);
-            const uint32_t v_addr = smem_addr(sV + st * C::kKVBytes);
 #pragma unroll
             for (int kk = 0; kk < BKV / 16; ++kk)  // 16 keys = 8 packed P columns
-              umma_bf16_ts(d_tmem, p_tmem + kk * 8,
-                           sw128_mnmajor_desc(v_addr + kk * 16 * 128, BKV * 128), idesc_pv,
+              umma_bf16_ts(d_tmem, p_tmem + kk * 8, vd + ((kk * 16 * 128) >> 4), idesc_pv,
                            (!first_pv || kk > 0) ? 1u : 0u);
-            umma_commit(&pv_done[2 * x + (n & 1)]);
+            umma_commit(&pv_done[2 * x + buf]);
             umma_commit(&kv_empty[st]);  // this query tile is done with the stage
             ++issued;
             first_pv = false;
           }
         }
-        kv_count += it.n_tiles;
       }
       const int me = pv_role ? QT + x : x;
       umma_commit(&done_bar[me]);
@@ -631,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           if constexpr (D % 32 == 0) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
               tmem_ld_32x32b_x32(o_tmem + c, o);
@@ -663,23 +686,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
-      const bool bad = any_pv && bad_item[k % kBadSlots] == k + 1;
+      // A later item's mark says nothing about this one: look for such values.
+      const bool bad = any_pv && bad_item[k % kBadSlots] > k;
       // Rows go out of registers, 32 bytes a store where rows start on 32-byte
-      // boundaries (else 16): a store fills whole sectors, a short block needs
-      // no other path, and staging the rows for tensor-map stores was no
-      // faster (and took the shared memory of a K/V stage).
+      // boundaries (else 16), past L1: a store fills whole sectors, and 64
+      // ragged prompts took 163 us with lines allocated in L1, 151 without.
+      // Staging rows in shared memory to store whole lines was slower (186),
+      // and so were tensor-map stores.
       __nv_bfloat16* out = a.o + static_cast<int64_t>(it.q_row + x * TQ + tok) * a.o_st +
                            static_cast<int64_t>(it.kvh * G + r - tok * G) * a.o_sh;
       const bool live = row_used && x * TQ + tok < it.ntok;
-      constexpr int kCols = D < 32 ? D : (D % 64 == 0 ? 64 : 32);  // columns per TMEM wait
-#pragma unroll
+      // The loops over columns here and in the rescaling stay loops: the code of
+      // all roles shares the instruction cache (unrolled: 177 us for 168).
+      constexpr int kCols = D < 32 ? D : 32;  // columns per TMEM wait
+#pragma unroll 1
       for (int c = 0; c < D; c += kCols) {
         uint32_t o[kCols];
         if (any_pv) {
-          if constexpr (kCols == 64) {
-            tmem_ld_32x32b_x32(o_tmem + c, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
-            tmem_ld_32x32b_x32(o_tmem + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
-          } else if constexpr (kCols == 32) {
+          if constexpr (kCols == 32) {
             tmem_ld_32x32b_x32(o_tmem + c, o);
           } else {
             tmem_ld_32x32b_x16(o_tmem + c, o);
@@ -716,13 +740,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 8; ++q) w[q] = pack_bf16x2(f[e + 2 * q], f[e + 2 * q + 1]);
           if (P.wide_stores) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + c + e),
-                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
-                         "r"(w[6]), "r"(w[7])
-                         : "memory");
+            asm volatile(
+                "st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                    out + c + e),
+                "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                "r"(w[7])
+                : "memory");
           } else {
-            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(out + c + e + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            store16_past_l1(out + c + e, make_uint4(w[0], w[1], w[2], w[3]));
+            store16_past_l1(out + c + e + 8, make_uint4(w[4], w[5], w[6], w[7]));
           }
         }
       }
