@@ -19,7 +19,10 @@
 namespace ptb {
 namespace {
 
-constexpr int kKvThreads = 128;
+// Blocks of two warps: 64 threads fill an SM up again as soon as two warps end
+// (16k tokens of 32 heads of 64, 4 bits: append and gather 129 us; 134 with 128
+// threads, 133 with 32).  Rows go past L1 (139 us with 128 threads without).
+constexpr int kKvThreads = 64;
 constexpr int kBatch = 4;  // loads of rows that a lane has in flight
 
 // Token and batch of a warp's number.  A 64-bit division costs as much as a
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(kKvThreads)
 #pragma unroll
   for (int i = 0; i < kBatch; ++i)
     w[i] = sub < RPW && h0 + i * RPW < rows
-               ? *reinterpret_cast<const uint4*>(src + i * RPW * sh)
+               ? load16_past_l1(src + i * RPW * sh)
                : make_uint4(0, 0, 0, 0);
 
   const int b = find_sequence(a.cu, a.batch, t, lane);
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kKvThreads)
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
       if (sub < RPW && h0 + i * RPW < rows)
-        *reinterpret_cast<uint4*>(out + i * RPW * oh) = w[i];
+        store16_past_l1(out + i * RPW * oh, w[i]);
   }
   if (is_q) return;
 
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(kKvThreads)
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
       if (sub < RPW && h0 + i * RPW < rows)
-        *reinterpret_cast<uint4*>(block + i * step + off * (2 * D) + 16 * c) = w[i];
+        store16_past_l1(block + i * step + off * (2 * D) + 16 * c, w[i]);
   } else if constexpr (NG > 0) {
     const int g = c >> 2;  // group, and the vector's place in it
     uint8_t* row = block + off * (D / 2);
@@ -320,8 +323,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const KvGatherArg
 #pragma unroll 4
     for (int r = row_base + sub; r < row_end; r += RPW)
       if (sub < RPW)
-        *reinterpret_cast<uint4*>(row_out(r) + 8 * c) = *reinterpret_cast<const uint4*>(
-            page + r * a.c.block_bytes + off * (2 * D) + 16 * c);
+        store16_past_l1(row_out(r) + 8 * c,
+                        load16_past_l1(page + r * a.c.block_bytes + off * (2 * D) + 16 * c));
   } else {
     // Keys: 4 lanes a row.
     const int t4 = lane & 3, g = lane & 7;
@@ -337,9 +340,10 @@ __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const KvGatherArg
         uint32_t v[4];
         code_values(codes[w], __byte_perm(pair[w], pair[w], 0x1010),
                     __byte_perm(pair[w], pair[w], 0x3232), v);
-        *reinterpret_cast<uint4*>(out + 32 * w) =
+        store16_past_l1(
+            out + 32 * w,
             make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
-                       __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+                       __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632)));
       }
     }
     // Values: 8 lanes a row.

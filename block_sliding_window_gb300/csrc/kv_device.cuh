@@ -20,6 +20,21 @@ cudaError_t allow_smem(K kern, int bytes, bool (&configured)[kDeviceSlots]) {
   return e;
 }
 
+// 16 bytes that this SM uses once, past L1.
+__device__ __forceinline__ uint4 load16_past_l1(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void store16_past_l1(void* p, const uint4& v) {
+  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 constexpr int kKvGroup = 32;  // channels that share one (scale, centre) pair
 
 // The sequence of token t: the first b < batch with cu[b + 1] > t, or batch.

@@ -244,12 +244,6 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int32_t 
                : "memory");
 }
 
-__device__ __forceinline__ void store16_past_l1(void* p, const uint4& v) {
-  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x),
-               "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-
 // Bits 15 and 31: the low / high bf16 of w is not finite.
 __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
