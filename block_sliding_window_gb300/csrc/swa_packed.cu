@@ -28,6 +28,16 @@
 //                may read it; rows that do attend to such a value get it added
 //                at the end of the item (rare path).  The scan costs 3 to 5%.
 // Every mbarrier wait is bounded; on a timeout all roles unwind.
+//
+// What bounds it.  In long prompts the tensor pipe: a 64-key tile is 2 x 384
+// cycles of scores (their operands come from shared memory, 48 cycles a K = 16
+// step where the products take 32) and 2 x 256 of P V, of 1600 measured; the
+// rest is the round trip score -> softmax -> P V -> score over two buffers
+// (waits 155, TMEM load 370, weights and their store 850 cycles).  In short
+// ones an item's end (last P V, output: 1.5 us) and, on grouped heads, memory.
+// Measured: one prompt of 16001 tokens, 16 heads of 128: 722 us, 1.45 PFLOP/s;
+// 4 prompts, 128 heads of 96, window 1024: 161 us; 64 ragged prompts, 64 heads
+// over 8, window 512: 149 us, 3.5 TB/s.
 #include "kv_device.cuh"
 
 namespace ptb {
