@@ -22,22 +22,26 @@
 // sequence, of 22.)
 //
 // 4-bit rows:
-//   q.k = sum_w scale_w (q.(64 + u))_w + (centre_w - 72 scale_w) Q_w,  Q_w = sum of q over group w,
+//   q.k = sum_w scale_w (q.u)_w + (centre_w - 8 scale_w) Q_w,  Q_w = sum of q over group w,
 //   sum_j p_j v_j = sum_j (p_j scale_jw)(u_j - 8) + sum_j p_j centre_jw.
-// Keys: a nibble placed in the mantissa of the fp16 number 64 makes it 64 + u;
-// q enters as fp16, scaled by a power of two (exact down to 2^-24 of the row's
-// largest).  The scale is applied to each group's product, and the rest is one
-// more product with the pairs as they lie (Q_w in two bf16 terms).
-// Values: codes become bf16 u - 8 the same way; the scale goes into P, and the
-// centres are one more product.  p and p * scale are rounded to bf16 once, as
-// P is in the other attention kernels.
+// Nibbles become numbers by a mask alone, as subnormals: a shift serves four.
+// Keys: fp16 u 2^-24 and u 2^-20 are operands as they are; q enters as fp16,
+// scaled by a power of two (exact down to 2^-28 of the row's largest), the
+// channels of the second kind by 2^-4 of it.  The scale is applied to each
+// group's product, and the rest is one more product with the pairs as they lie
+// (Q_w in two bf16 terms).
+// Values: bf16 u 2^-133 and u 2^-129 become multiples of u - 8 by an FMA; the
+// scale goes into P, and the centres are one more product.  p and p * scale are
+// rounded to bf16 once, as P is in the other attention kernels.
 // The integer pipe (0.5 instructions a clock and SM quarter, measured) bounds
-// the 4-bit kernel.  (e4m3 products, for which a masked word is an operand as
-// it lies, were slower: the compiler builds them from fp16 ones.)
+// the 4-bit kernel: with nibbles in the mantissas of 64 and 128, two shifts more
+// for four and an addition, 64 long sequences took 200 us, now 157.  (e4m3
+// products, for which a masked word is an operand as it lies, were slower: the
+// compiler builds them from fp16 ones.)
 // Measured on 64 sequences, 64 heads of 128 over 8: bf16 6.0 TB/s (140 us; the
-// cache alone at the rate of a copy 124); 4 bits 4.3 TB/s (200 us; 127; the
-// copies alone take 130), at 430 instructions a 16-key tile and 64% of the issue
-// slots.  One sequence of 16000 keys: 15 us, half of it the two launches' ends.
+// cache alone at the rate of a copy 124); 4 bits 5.5 TB/s (157 us; 127; the
+// copies alone take 130).  One sequence of 16000 keys: 14 us, half of it the two
+// launches' ends.
 // Rows that the mask leaves out (before the window, past the length, pages out
 // of range) may hold anything: their scores are replaced and their values or
 // pairs zeroed before use.
@@ -69,8 +73,8 @@ struct Cfg {
   // partial result.
   static constexpr int kStages = BITS == 4 ? 2 : 3;
   // Warps of a block, one block per SM: as many as registers (4 bits: 168 or
-  // 255 a thread) or shared memory (16 bits) allow.  4 bits, 64 sequences: 16
-  // warps of 128 registers took 212 us, 12 of 168 206.
+  // 255 a thread) or shared memory (16 bits) allow.  4 bits, 64 sequences, when
+  // that was chosen: 16 warps of 128 registers took 212 us, 12 of 168 206.
   static constexpr int kWarps =
       BITS == 4 ? (NT == 1 ? 12 : 8) : (D > 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 8 : 7));
   // A partial result: maxima and sums of 8 NT heads, then their outputs.
@@ -252,12 +256,30 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Nibble K of both 16-bit halves of w as numbers: in mantissa bits 4 .. 7 of
-// the fp16 number 64, it is 64 + u.
-template <int K>
-__device__ __forceinline__ uint32_t nibbles64(uint32_t w) {
-  const uint32_t s = K == 0 ? w << 4 : w >> (4 * K - 4);
-  return (s & 0x00f000f0u) | 0x54005400u;
+// Nibbles 0 .. 3 of both 16-bit halves of w as fp16 numbers: in mantissa bits
+// 0 .. 3 of a subnormal, u is u 2^-24, in bits 4 .. 7 u 2^-20.  One shift for four.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&v)[4]) {
+  const uint32_t r = w >> 8;
+  v[0] = w & 0x000f000fu;
+  v[1] = w & 0x00f000f0u;
+  v[2] = r & 0x000f000fu;
+  v[3] = r & 0x00f000f0u;
+}
+// The same as bf16 numbers around zero: in the lowest bits of a bf16 a nibble is
+// u 2^-133, four bits up u 2^-129 (subnormals and the first binade are evenly
+// spaced), and an FMA makes them (u - 8) 2^-6 and (u - 8) 2^-2, both exact.
+constexpr float kLowNibble = 64.f, kHighNibble = 4.f;  // what undoes the factors
+__device__ __forceinline__ void codes_bf16_scaled(uint32_t w, uint32_t (&v)[4]) {
+  const uint32_t r = w >> 8;
+  const uint32_t x[4] = {w & 0x000f000fu, w & 0x00f000f0u, r & 0x000f000fu, r & 0x00f000f0u};
+  const __nv_bfloat162 up = __floats2bfloat162_rn(0x1p127f, 0x1p127f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float c = -8.f / (k & 1 ? kHighNibble : kLowNibble);
+    __nv_bfloat162 y = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x[k]), up,
+                               __floats2bfloat162_rn(c, c));
+    v[k] = *reinterpret_cast<uint32_t*>(&y);
+  }
 }
 // N consecutive words (N 1 .. 4) at 4 N-byte alignment (4-byte for N = 3).
 template <int N>
@@ -498,7 +520,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
     // + 1 and + 8, + 9; for 4 bits in the order of the codes, scaled by a
     // power of two into fp16.
     uint32_t qf[NT][MS][2];
-    uint32_t qs[NT][2];  // Q_t: (-72 Q, Q) in two bf16 terms
+    uint32_t qs[NT][2];  // Q_t: (-8 Q, Q) 2^-24 in two bf16 terms
     float to_log2[NT][2];  // scores of heads 2 t, 2 t + 1 to the log2 domain
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -524,14 +546,15 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
         }
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // The power of two that brings the largest |q| into [128, 256); a
-        // query that is not finite gives NaN.
+        // The power of two that brings the largest |q| into [2^14, 2^15), the
+        // scores' unit being 2^-24 of it; a query that is not finite, or of
+        // 2^119 or more (no such power is left), gives NaN.
         const int expo = static_cast<int>(mx >> 23);
-        const int shift = min(127 + 7 - expo, 110);
+        const int shift = max(min(127 + 14 - expo, 127), 24 - 127);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
         const float down =
-            __uint_as_float(expo == 255 ? 0x7fffffffu
-                                        : static_cast<uint32_t>(min(127 - shift, 254)) << 23);
+            __uint_as_float(expo >= 127 + 119 ? 0x7fffffffu
+                                              : static_cast<uint32_t>(127 + 24 - shift) << 23);
         qs[nt][0] = qs[nt][1] = 0;
 #pragma unroll
         for (int wq = 0; wq < NG; ++wq) {
@@ -544,19 +567,24 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
             sum += y[2 * e] + y[2 * e + 1];
           }
           qf[nt][2 * wq][0] = pack_f16x2(y[0], y[4]);
-          qf[nt][2 * wq][1] = pack_f16x2(y[1], y[5]);
+          qf[nt][2 * wq][1] = pack_f16x2(y[1] * 0.0625f, y[5] * 0.0625f);
           qf[nt][2 * wq + 1][0] = pack_f16x2(y[2], y[6]);
-          qf[nt][2 * wq + 1][1] = pack_f16x2(y[3], y[7]);
+          qf[nt][2 * wq + 1][1] = pack_f16x2(y[3] * 0.0625f, y[7] * 0.0625f);
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          const uint32_t top = pack_bf16x2(-72.f * sum, sum);
+          sum *= 0x1p-24f;
+          const uint32_t top = pack_bf16x2(-8.f * sum, sum);
           if (t == wq) {
             qs[nt][0] = top;
-            qs[nt][1] = pack_bf16x2(-72.f * sum - bf16_lo(top), sum - bf16_hi(top));
+            qs[nt][1] = pack_bf16x2(-8.f * sum - bf16_lo(top), sum - bf16_hi(top));
           }
         }
-        to_log2[nt][0] *= __shfl_sync(0xffffffffu, down, 8 * t);
-        to_log2[nt][1] *= __shfl_sync(0xffffffffu, down, 8 * t + 4);
+        // Never 0: a masked score times it has to stay minus infinity.
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          to_log2[nt][e] *= __shfl_sync(0xffffffffu, down, 8 * t + 4 * e);
+          if (to_log2[nt][e] == 0.f) to_log2[nt][e] = 0x1p-126f;
+        }
       }
     }
 
@@ -631,15 +659,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
 #pragma unroll
           for (int wq = 0; wq < NG; ++wq) {
             const float sa = bf16_lo(pa[wq]), sb = bf16_lo(pb[wq]);
-            const uint32_t a0 = nibbles64<0>(ca[wq]), a2 = nibbles64<1>(ca[wq]);
-            const uint32_t a4 = nibbles64<2>(ca[wq]), a6 = nibbles64<3>(ca[wq]);
-            const uint32_t b0 = nibbles64<0>(cb[wq]), b2 = nibbles64<1>(cb[wq]);
-            const uint32_t b4 = nibbles64<2>(cb[wq]), b6 = nibbles64<3>(cb[wq]);
+            uint32_t na[4], nb[4];
+            codes_f16(ca[wq], na);
+            codes_f16(cb[wq], nb);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float acc[4];
-              mma_f16_zero(acc, a0, b0, a2, b2, qf[nt][2 * wq][0], qf[nt][2 * wq][1]);
-              mma_f16(acc, a4, b4, a6, b6, qf[nt][2 * wq + 1][0], qf[nt][2 * wq + 1][1]);
+              mma_f16_zero(acc, na[0], nb[0], na[1], nb[1], qf[nt][2 * wq][0], qf[nt][2 * wq][1]);
+              mma_f16(acc, na[2], nb[2], na[3], nb[3], qf[nt][2 * wq + 1][0], qf[nt][2 * wq + 1][1]);
               s[h][nt][0] = fmaf(sa, acc[0], s[h][nt][0]);
               s[h][nt][1] = fmaf(sa, acc[1], s[h][nt][1]);
               s[h][nt][2] = fmaf(sb, acc[2], s[h][nt][2]);
@@ -786,8 +813,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
             const uint32_t v0 = __byte_perm(cv[0][wv / 2], cv[1][wv / 2], sel);
             const uint32_t v1 = __byte_perm(cv[2][wv / 2], cv[3][wv / 2], sel);
             uint32_t e[4], f[4];
-            codes_bf16(v0, e);
-            codes_bf16(v1, f);
+            codes_bf16_scaled(v0, e);
+            codes_bf16_scaled(v1, f);
             const float sa = bf16_lo(pa[wv]), sb = bf16_lo(pb[wv]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -843,10 +870,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
           const float z1 = __shfl_sync(0xffffffffu, oc[nt][1], 4 * wv + t);
 #pragma unroll
           for (int m = 2 * wv; m < 2 * wv + 2; ++m) {
-            o[nt][m][0] += z0;
-            o[nt][m][1] += z1;
-            o[nt][m][2] += z0;
-            o[nt][m][3] += z1;
+            o[nt][m][0] = fmaf(o[nt][m][0], kLowNibble, z0);
+            o[nt][m][1] = fmaf(o[nt][m][1], kLowNibble, z1);
+            o[nt][m][2] = fmaf(o[nt][m][2], kHighNibble, z0);
+            o[nt][m][3] = fmaf(o[nt][m][3], kHighNibble, z1);
           }
         }
       }

@@ -690,6 +690,23 @@ def test_paged_queries_that_are_not_finite_or_zero(ptb_lib, bits):
     assert (np.abs(o - want) <= bound).all()
 
 
+@pytest.mark.parametrize("power", [-126, -100, -40, 0, 40, 100, 116])
+def test_paged_4bit_query_range(ptb_lib, power):
+    """Queries of any magnitude with a scale that makes up for it; beyond 2^119 they give NaN."""
+    lens, page, d = [70, 40], 16, 64
+    c = filled(ptb_lib, lens, 2, d, page, 4, 369, 4)
+    q = c["q1"].clamp(-3.9, 3.9)
+    q[1, 1] = 0
+    scale = 2.0 ** max(-3 - power, -126)
+    q = (q.double() * 2.0 ** power).to(torch.bfloat16)
+    o = ptb_lib.swa_attention_paged(q, c["cache"], c["table_d"], ints(lens), 2, page, 4, 1000, scale=scale)
+    want, bound = M.paged(M.to64(q), c["host"], c["table"], lens, 1000, scale)
+    held_to(o, want, bound)
+    q[0, 2, 7] = 2.0 ** 119
+    o = ptb_lib.swa_attention_paged(q, c["cache"], c["table_d"], ints(lens), 2, page, 4, 1000, scale=scale)
+    assert torch.isnan(o[0, 2]).all() and torch.isfinite(o[0, :2]).all() and torch.isfinite(o[1]).all()
+
+
 def test_paged_workspace_of_the_caller(ptb_lib):
     c = filled(ptb_lib, [500, 70], 2, 64, 32, 4, 366, 4)
     n = ptb_lib.swa_attention_paged_workspace_size(2, 4, 2, 64)
