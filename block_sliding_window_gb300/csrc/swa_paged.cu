@@ -73,8 +73,8 @@ struct Cfg {
   // partial result.
   static constexpr int kStages = BITS == 4 ? 2 : 3;
   // Warps of a block, one block per SM: as many as registers (4 bits: 168 or
-  // 255 a thread) or shared memory (16 bits) allow.  4 bits, 64 sequences, when
-  // that was chosen: 16 warps of 128 registers took 212 us, 12 of 168 206.
+  // 255 a thread) or shared memory (16 bits) allow.  4 bits, 64 sequences:
+  // 14 warps of 128 registers take 174 us, 12 of 164 159.
   static constexpr int kWarps =
       BITS == 4 ? (NT == 1 ? 12 : 8) : (D > 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 8 : 7));
   // A partial result: maxima and sums of 8 NT heads, then their outputs.
