@@ -40,7 +40,7 @@
 // compiler builds them from fp16 ones.)
 // Measured on 64 sequences, 64 heads of 128 over 8: bf16 6.0 TB/s (140 us; the
 // cache alone at the rate of a copy 124); 4 bits 5.5 TB/s (157 us; 127; the
-// copies alone take 130).  One sequence of 16000 keys: 14 us, half of it the two
+// copies alone take 130).  One sequence of 16000 keys: 12 us, half of it the two
 // launches' ends.
 // Rows that the mask leaves out (before the window, past the length, pages out
 // of range) may hold anything: their scores are replaced and their values or
@@ -951,65 +951,74 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
   // A chain is a cut segment's partial results in this block: the slot of the
   // warp where it begins (slot 0 of warp 0: it began in an earlier block) and
   // slots 0 of the warps that follow, up to its end.  Warps take the chains'
-  // heads in turn.  A segment with its beginning and end here is finished; of
-  // the others the block leaves one partial result each (slot 0: begun
-  // earlier; slot 1: goes on) for the join kernel.
-  int task = 0;
-  for (int c = 0; c < 2 * kWarps; ++c) {
-    const int w0 = c >> 1;
-    const bool tail_slot = c & 1;  // slot 1 of warp w0
-    const WarpParts* first = parts + (w0 - warp) * (128 / static_cast<int>(sizeof(WarpParts)));
-    if (tail_slot ? !first->has1 : (w0 > 0 || !first->has0)) continue;
-    const int b = tail_slot ? first->b1 : first->b0, hh = tail_slot ? first->hh1 : first->hh0;
-    int last = w0;
-    bool ended = !tail_slot && first->end0;
-    while (!ended && last + 1 < kWarps) {
-      const WarpParts* next = parts + (last + 1 - warp) * (128 / static_cast<int>(sizeof(WarpParts)));
-      if (!next->has0) break;
-      ++last;
-      ended = next->end0;
-    }
+  // heads in turn, a lane a part (statistics) or 4 channels (outputs); 96
+  // windows of 1024 took 60 us with look-ups part by part, 55 so.  A segment
+  // with its beginning and end here is finished; of the others the block
+  // leaves one partial result each (slot 0: begun earlier; slot 1: goes on)
+  // for the join kernel.
+  auto parts_of = [&](int w) {
+    return parts + (w - warp) * (128 / static_cast<int>(sizeof(WarpParts)));
+  };
+  auto slot_of = [&](int w, bool begins) {
+    return reinterpret_cast<const float*>(smem_raw + (base - smem_addr(smem_raw)) +
+                                          w * C::kWarpBytes + (begins ? 0 : C::kRingBytes));
+  };
+  const WarpParts* its = parts_of(lane < kWarps ? lane : 0);
+  const unsigned has0 = __ballot_sync(0xffffffffu, lane < kWarps && its->has0);
+  const unsigned ends = __ballot_sync(0xffffffffu, lane < kWarps && its->end0);
+  const unsigned has1 = __ballot_sync(0xffffffffu, lane < kWarps && its->has1);
+  int turn = warp;  // heads that other warps take before this one's next
+  for (unsigned left = has1 << 1 | (has0 & 1u); left; left &= left - 1) {
+    const int c = __ffs(left) - 1;
+    const bool begins = c > 0;  // in warp c - 1 of this block
+    const int w0 = begins ? c - 1 : 0, from = begins ? c : 0;
+    const int run = __ffs(~(has0 >> from)) - 1, end = __ffs(ends >> from);
+    const bool ended = end > 0 && end <= run;
+    const int n = (ended ? end : run) + (begins ? 1 : 0);  // parts, in warps w0 ..
+    const int b = begins ? parts_of(w0)->b1 : parts_of(0)->b0;
+    const int hh = begins ? parts_of(w0)->hh1 : parts_of(0)->hh0;
     const int kvh = hh / P.head_blocks;
     const int head0 = kvh * P.group + (hh % P.head_blocks) * 8 * NT;
     const int nheads = min(8 * NT, (kvh + 1) * P.group - head0);
-    for (int head = 0; head < nheads; ++head, ++task) {
-      if (task % kWarps != warp) continue;
-      auto slot_of = [&](int w) {
-        return reinterpret_cast<const float*>(smem_raw + (base - smem_addr(smem_raw)) +
-                                              w * C::kWarpBytes +
-                                              (w == w0 && tail_slot ? 0 : C::kRingBytes));
-      };
-      float mx = -INFINITY;
-      for (int w = w0; w <= last; ++w) mx = fmaxf(mx, slot_of(w)[head]);
-      const float ref = mx == -INFINITY ? 0.f : mx;
-      float sum = 0.f, acc[(D + 31) / 32];
+    for (; turn < nheads; turn += kWarps) {
+      const int head = turn;
+      const bool part = lane < n;
+      const float* p = slot_of(w0 + (part ? lane : 0), begins && (lane == 0 || !part));
+      const float m = part ? p[head] : -INFINITY;
+      float mx = m, sum = part ? p[8 * NT + head] : 0.f;
 #pragma unroll
-      for (int i = 0; i < (D + 31) / 32; ++i) acc[i] = 0.f;
-      for (int w = w0; w <= last; ++w) {
-        const float* p = slot_of(w);
-        const float f = fast_exp2(p[head] - ref);
-        sum = fmaf(f, p[8 * NT + head], sum);
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float f = fast_exp2(m - (mx == -INFINITY ? 0.f : mx));
+      sum *= f;
 #pragma unroll
-        for (int i = 0; i < (D + 31) / 32; ++i)
-          if (i * 32 + lane < D) acc[i] = fmaf(f, p[16 * NT + head * D + i * 32 + lane], acc[i]);
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const bool live = lane * 4 < D;
+#pragma unroll 2
+      for (int i = 0; i < n; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float4 v = *reinterpret_cast<const float4*>(slot_of(w0 + i, begins && i == 0) +
+                                                          16 * NT + head * D + (live ? lane * 4 : 0));
+        acc.x = fmaf(fi, v.x, acc.x);
+        acc.y = fmaf(fi, v.y, acc.y);
+        acc.z = fmaf(fi, v.z, acc.z);
+        acc.w = fmaf(fi, v.w, acc.w);
       }
-      if (tail_slot && ended) {
+      if (begins && ended) {
         const float inv = sum != 0.f ? 1.f / sum : 0.f;
-        __nv_bfloat16* out = a.o + b * a.o_sb + (head0 + head) * a.o_sh;
-#pragma unroll
-        for (int i = 0; i < (D + 31) / 32; ++i)
-          if (i * 32 + lane < D) out[i * 32 + lane] = __float2bfloat16_rn(acc[i] * inv);
+        if (live)
+          *reinterpret_cast<uint2*>(a.o + b * a.o_sb + (head0 + head) * a.o_sh + lane * 4) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       } else {
-        float* out = P.parts + (2 * blockIdx.x + (tail_slot ? 1 : 0)) * (C::kSlotBytes / 4);
+        float* out = P.parts + (2 * blockIdx.x + (begins ? 1 : 0)) * (C::kSlotBytes / 4);
         if (lane == 0) {
           out[head] = mx;
           out[8 * NT + head] = sum;
         }
-#pragma unroll
-        for (int i = 0; i < (D + 31) / 32; ++i)
-          if (i * 32 + lane < D) out[16 * NT + head * D + i * 32 + lane] = acc[i];
+        if (live) *reinterpret_cast<float4*>(out + 16 * NT + head * D + lane * 4) = acc;
       }
     }
+    turn -= nheads;
   }
 }
 
