@@ -15,6 +15,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = 1ll << 30;  // token rows and positions stay in int
 constexpr int32_t kMaxHeads = 65535;
+constexpr int32_t kMaxPackedGroup = 128;  // a query tile holds at least one token of all its heads
 
 bool page_size_ok(int32_t p) { return p >= 16 && p <= 256 && (p & (p - 1)) == 0; }
 
@@ -162,7 +163,7 @@ ptb_status ptb_kv_gather(const void* cache, int64_t pages, const int32_t* page_t
 size_t swa_attention_packed_workspace_size(int32_t batch, int64_t tokens_q, int32_t heads,
                                            int32_t kv_heads) {
   if (batch < 1 || tokens_q < 0 || tokens_q > kMaxTokens || kv_heads < 1 || heads < kv_heads ||
-      heads % kv_heads || heads > kMaxHeads)
+      heads % kv_heads || heads / kv_heads > kMaxPackedGroup || heads > kMaxHeads)
     return 0;
   return round_up(swa_packed_workspace(batch, tokens_q, heads, kv_heads, current_sms()), kAlign);
 }
@@ -179,8 +180,8 @@ ptb_status swa_attention_packed(const ptb_bf16* q, int64_t q_st, int64_t q_sh, c
       window < 1)
     return PTB_ERR_ARG;
   if (scale < 0.f || !std::isfinite(scale)) return PTB_ERR_ARG;
-  if (!head_dim_ok(head_dim) || heads % kv_heads || heads / kv_heads > 128 || heads > kMaxHeads ||
-      batch > 65535 || tokens_q > kMaxTokens || tokens_k > kMaxTokens)
+  if (!head_dim_ok(head_dim) || heads % kv_heads || heads / kv_heads > kMaxPackedGroup ||
+      heads > kMaxHeads || batch > 65535 || tokens_q > kMaxTokens || tokens_k > kMaxTokens)
     return PTB_ERR_SHAPE;
   PTB_TRY(check_view(q, q_st, q_sh, tokens_q));
   PTB_TRY(check_view(k, k_st, k_sh, tokens_k));

@@ -543,7 +543,8 @@ ptb_status ptb_kv_gather(const void* cache, int64_t pages, const int32_t* page_t
  *   workspace  at least swa_attention_packed_workspace_size() bytes, 256-byte
  *        aligned; calls that may run at the same time need one each.  The size
  *        depends on the current device's SM count and is 0 for calls so
- *        small that they need none (workspace may then be NULL)
+ *        small that they need none (workspace may then be NULL), and for shapes
+ *        that are refused
  * head_dim 16, 32, 64, 96 or 128; heads / kv_heads at most 128.
  */
 size_t swa_attention_packed_workspace_size(int32_t batch, int64_t tokens_q, int32_t heads,

@@ -1,0 +1,40 @@
+"""Limits of the serving entry points, on the host: sizes asked for shapes that are refused.  Nothing
+here touches a device."""
+
+import subprocess
+import sys
+
+import pytest
+
+SHAPE = 2
+
+SIZES = """
+import block_sliding_window_gb300 as bsw
+lib = bsw.load()
+for a in {cases!r}:
+    print(lib.swa_attention_packed_workspace_size(*a), flush=True)
+"""
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__.build()
+    import block_sliding_window_gb300 as bsw
+    return bsw.load()
+
+
+def test_packed_workspace_of_groups_beyond_a_tile(lib):
+    """More than 128 query heads of one kv head: size 0, like every refused shape.  In a process of
+    its own: dividing by a tile of no tokens would end it."""
+    cases = [(2, 100, 256, 1), (1, 0, 129, 1), (3, 5000, 65535, 1), (2, 100, 1290, 10)]
+    r = subprocess.run([sys.executable, "-c", SIZES.format(cases=cases)], capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stderr)
+    assert r.stdout.split() == ["0"] * len(cases)
+    # 128 is served; a call of any length is refused beyond it
+    assert lib.swa_attention_packed_workspace_size(2, 10 ** 6, 128, 1) > 0
+    p = 1 << 20
+    for heads in (129, 256):
+        st = lib.swa_attention_packed(p, heads * 64, 64, 2 * p, 64, 64, 3 * p, 64, 64, p, None, 2, 100, 100, heads, 1, 64,
+                                      8, 0.0, 4 * p, heads * 64, 64, p, 1 << 40, None)
+        assert st == SHAPE
