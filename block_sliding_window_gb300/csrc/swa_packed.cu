@@ -648,7 +648,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float s0, s1;
         f2_split(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), s0, s1);
         l_run += s0 + s1;
-        // P (bf16 pairs) over the first 32 columns of the scores just read.
+        // P (bf16 pairs) over the first 32 columns of the scores just read; lanes
+        // that raised their maximum are back with the others.
+        __syncwarp();
         tmem_st_32x32b_x32(tmem + lane_base + C::s_col(x, buf), pk);
         if (any_pv && __any_sync(0xffffffffu, raise)) {
           // O must hold every earlier P V of this item before it is rescaled.
@@ -717,44 +719,46 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < kCols; ++e) o[e] = 0;
         }
-        if (!live) continue;
-        float f[kCols];
+        if (live) {
+          float f[kCols];
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) f[e] = __uint_as_float(o[e]) * inv;
-        if (bad) {
-          // Values that are not finite and that this row attends to, out of
-          // the tiles that were cleared.
-          for (int key = max(0, i - a.window + 1); key <= i; ++key) {
-            if (!tile_masked(it, key & ~(BKV - 1), a.window)) {
-              key |= BKV - 1;  // on to the next tile
-              continue;
+          for (int e = 0; e < kCols; ++e) f[e] = __uint_as_float(o[e]) * inv;
+          if (bad) {
+            // Values that are not finite and that this row attends to, out of
+            // the tiles that were cleared.
+            for (int key = max(0, i - a.window + 1); key <= i; ++key) {
+              if (!tile_masked(it, key & ~(BKV - 1), a.window)) {
+                key |= BKV - 1;  // on to the next tile
+                continue;
+              }
+              const __nv_bfloat16* row =
+                  a.v + static_cast<int64_t>(it.k_row + key) * a.v_st + it.kvh * a.v_sh + c;
+#pragma unroll
+              for (int e = 0; e < kCols; ++e) {
+                const float z = __bfloat162float(row[e]);
+                if (!(fabsf(z) < INFINITY)) f[e] += z;
+              }
             }
-            const __nv_bfloat16* row =
-                a.v + static_cast<int64_t>(it.k_row + key) * a.v_st + it.kvh * a.v_sh + c;
+          }
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) {
-              const float z = __bfloat162float(row[e]);
-              if (!(fabsf(z) < INFINITY)) f[e] += z;
+          for (int e = 0; e < kCols; e += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) w[q] = pack_bf16x2(f[e + 2 * q], f[e + 2 * q + 1]);
+            if (P.wide_stores) {
+              asm volatile(
+                  "st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                      out + c + e),
+                  "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                  "r"(w[7])
+                  : "memory");
+            } else {
+              store16_past_l1(out + c + e, make_uint4(w[0], w[1], w[2], w[3]));
+              store16_past_l1(out + c + e + 8, make_uint4(w[4], w[5], w[6], w[7]));
             }
           }
         }
-#pragma unroll
-        for (int e = 0; e < kCols; e += 16) {
-          uint32_t w[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) w[q] = pack_bf16x2(f[e + 2 * q], f[e + 2 * q + 1]);
-          if (P.wide_stores) {
-            asm volatile(
-                "st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                    out + c + e),
-                "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
-                "r"(w[7])
-                : "memory");
-          } else {
-            store16_past_l1(out + c + e, make_uint4(w[0], w[1], w[2], w[3]));
-            store16_past_l1(out + c + e + 8, make_uint4(w[4], w[5], w[6], w[7]));
-          }
-        }
+        __syncwarp();  // the next columns' load is the whole warp's
       }
       tc_fence_before();
     }
