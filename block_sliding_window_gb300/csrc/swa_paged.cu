@@ -651,8 +651,15 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
           lds_words<NG>(cb, codes + kb * (D / 2) + t * 4 * NG);
           lds_words<NG>(pa, pairs + ka * (D / 8));
           lds_words<NG>(pb, pairs + kb * (D / 8));
-          const uint32_t wa = t < NG ? lds32(pairs + ka * (D / 8) + 4 * (t < NG ? t : 0)) : 0u;
-          const uint32_t wb = t < NG ? lds32(pairs + kb * (D / 8) + 4 * (t < NG ? t : 0)) : 0u;
+          // All lanes load (beyond the last group: group 0), so that none is away
+          // when the products begin; the queries' terms of such lanes are zero.
+          const int group = t < NG ? t : 0;
+          uint32_t wa = lds32(pairs + ka * (D / 8) + 4 * group);
+          uint32_t wb = lds32(pairs + kb * (D / 8) + 4 * group);
+          if constexpr (NG < 4) {
+            wa = t < NG ? wa : 0u;
+            wb = t < NG ? wb : 0u;
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             mma_bf16_zero(s[h][nt], wa, wb, wa, wb, qs[nt][0], qs[nt][1]);

@@ -71,3 +71,36 @@ def test_packed_partly_filled_tiles_with_infinite_values(ptb_lib, heads, kv, d):
     for rows, columns in ((written & ~sees, list(range(d))), (sees, plain)):
         over = np.abs(got - want)[rows][..., columns] - bound[rows][..., columns]
         assert (over <= 0).all(), over.max()
+
+
+@pytest.mark.parametrize("heads", [3, 11])
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+def test_paged_4bit_rows_that_hold_nan_in_one_group(ptb_lib, heads, d):
+    """Every number of groups a row: NaN in one group of keys or values that the window has left
+    reaches nothing, and in a key inside the window it reaches its sequence alone."""
+    lens, window, page = [75, 64, 33], 30, 16
+    pages = sum(-(-n // page) for n in lens)
+    table = np.full((3, 5), -1, dtype=np.int32)
+    at = 0
+    for b, n in enumerate(lens):
+        need = -(-n // page)
+        table[b, :need] = range(at, at + need)
+        at += need
+    cache = torch.full((pages, ptb_lib.kv_page_size(1, page, d, 4)), 0xFF, dtype=torch.uint8, device="cuda")
+    cu = cumulated(lens)
+    k, v, q = normal((cu[-1], 1, d), 21), normal((cu[-1], 1, d), 22), normal((3, heads, d), 23)
+    first, last = 0, d // 32 - 1
+    for b, n in enumerate(lens):
+        for p in range(n - window):
+            k[cu[b] + p, 0, 32 * (first if p % 2 else last)] = float("nan")
+            v[cu[b] + p, 0, 32 * (last if p % 2 else first)] = float("nan")
+    dev = torch.from_numpy(table).cuda()
+    ptb_lib.kv_append(None, k, v, cache, dev, ints(cu), ints([0] * 3), page, 4, keep_keys=False)
+    host = M.Cache(cache.cpu().numpy(), 1, page, d, 4)
+    o = M.to64(ptb_lib.swa_attention_paged(q, cache, dev, ints(lens), 1, page, 4, window))
+    want, bound = M.paged(M.to64(q), host, table, lens, window, d ** -0.5)
+    assert (np.abs(o - want) <= bound).all()
+    k[cu[1] + 50, 0, 32 * last] = float("nan")
+    ptb_lib.kv_append(None, k, v, cache, dev, ints(cu), ints([0] * 3), page, 4, keep_keys=False)
+    o = M.to64(ptb_lib.swa_attention_paged(q, cache, dev, ints(lens), 1, page, 4, window))
+    assert np.isnan(o[1]).all() and (np.abs(o - want)[[0, 2]] <= bound[[0, 2]]).all()
