@@ -35,6 +35,20 @@ __device__ __forceinline__ void store16_past_l1(void* p, const uint4& v) {
                : "memory");
 }
 
+// Scores beyond fp32's grain.  exp2(s f - m), with m = s f of the row's largest
+// score rounded to fp32, takes the exact product in its FMA: the largest weight
+// comes out as 2^r, r up to half a step of m.  That cancels in O / l until r is
+// tens (m of 2^31: 128, and the weight infinite or 0).  From kLargeScore on a row
+// therefore goes on with f rounded up to a power of two, which makes products
+// exact and r zero.  It changes no weight that counts: fp32 scores that differ
+// do so by at least 2^-24 of themselves, here 32, so every weight is that of the
+// largest score or below 2^-32 of it, with either factor; and as f only grows,
+// maxima of parts of a row that went either way keep their order.
+constexpr float kLargeScore = 536870912.f;  // 2^29, in the log2 domain
+__device__ __forceinline__ float power_of_two_above(float f) {  // f > 0
+  return __uint_as_float((__float_as_uint(f) + 0x007fffffu) & 0xff800000u);
+}
+
 constexpr int kKvGroup = 32;  // channels that share one (scale, centre) pair
 
 // The sequence of token t: the first b < batch with cu[b + 1] > t, or batch.

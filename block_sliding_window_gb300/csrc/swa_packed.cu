@@ -582,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (x * TQ >= it.ntok) continue;
       const int i = it.p0 + x * TQ + tok;  // position of this thread's query
       float m_ref = -INFINITY, l_run = 0.f;
+      float scale = a.scale_log2;  // of this row (kLargeScore)
       bool any_pv = false;
       for (int j = 0; j < it.n_tiles; ++j) {
         const int key0 = (it.kt_hi - j) * BKV;
@@ -624,7 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 7; ++t) m2[t] = fmax3(m1[3 * t], m1[3 * t + 1], m1[3 * t + 2]);
         m2[7] = m1[21];
         float mx = fmax3(fmax3(m2[0], m2[1], m2[2]), fmax3(m2[3], m2[4], m2[5]), fmaxf(m2[6], m2[7]));
-        mx *= a.scale_log2;  // row max in the log2 domain
+        const float raw_max = mx;
+        mx = __fmul_rn(mx, scale);  // row max in the log2 domain, rounded for every use
         // Raise the reference max only when the row max passes it by 2^8.
         float alpha = 1.f;
         const bool raise = mx > m_ref + kRescaleLog2;
@@ -632,9 +634,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           alpha = fast_exp2(m_ref - mx);  // 0 while m_ref is -inf
           l_run *= alpha;
           m_ref = mx;
+          if (fabsf(mx) >= kLargeScore) {
+            scale = power_of_two_above(scale);
+            m_ref = __fmul_rn(raw_max, scale);
+          }
         }
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        const uint64_t scale2 = f2(a.scale_log2, a.scale_log2), shift2 = f2(-m_use, -m_use);
+        const uint64_t scale2 = f2(scale, scale), shift2 = f2(-m_use, -m_use);
         uint64_t sum2[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
         uint32_t pk[BKV / 2];
 #pragma unroll

@@ -701,11 +701,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
       // and is raised only when a score passes it by more than 2^8.
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float mx[2];
+        float raw[2], mx[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          mx[e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2])) *
-                  to_log2[nt][e];
+        for (int e = 0; e < 2; ++e) {
+          raw[e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+          mx[e] = __fmul_rn(raw[e], to_log2[nt][e]);
+        }
         if (__any_sync(0xffffffffu, mx[0] > m_ref[nt][0] + kRescaleLog2 ||
                                         mx[1] > m_ref[nt][1] + kRescaleLog2)) {
           float alpha[2];
@@ -713,9 +714,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1)
-              mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], x));
-            const float m = fmaxf(m_ref[nt][e], mx[e]);
+              raw[e] = fmaxf(raw[e], __shfl_xor_sync(0xffffffffu, raw[e], x));
+            mx[e] = __fmul_rn(raw[e], to_log2[nt][e]);
+            float m = fmaxf(m_ref[nt][e], mx[e]);
             alpha[e] = m == -INFINITY ? 1.f : fast_exp2(m_ref[nt][e] - m);
+            if (mx[e] > m_ref[nt][e] && fabsf(mx[e]) >= kLargeScore) {
+              to_log2[nt][e] = power_of_two_above(to_log2[nt][e]);
+              m = __fmul_rn(raw[e], to_log2[nt][e]);
+            }
             m_ref[nt][e] = m;
             l[nt][e] *= alpha[e];
           }

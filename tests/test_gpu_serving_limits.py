@@ -104,3 +104,84 @@ def test_paged_4bit_rows_that_hold_nan_in_one_group(ptb_lib, heads, d):
     ptb_lib.kv_append(None, k, v, cache, dev, ints(cu), ints([0] * 3), page, 4, keep_keys=False)
     o = M.to64(ptb_lib.swa_attention_paged(q, cache, dev, ints(lens), 1, page, 4, window))
     assert np.isnan(o[1]).all() and (np.abs(o - want)[[0, 2]] <= bound[[0, 2]]).all()
+
+
+# ------------------------------------------------------------------------- scores of any size --
+#
+# One channel of q and k is not zero, so a score is one product of two bf16 values, exact in fp32,
+# and the scores of two keys are equal or differ by 2^-8 of their size: 2^10 and more here.  The
+# weights are then 0 or equal, whatever the last bits of a score.
+#
+# From 2^29 in the log2 domain on (power 15: at least 2^30 * 0.7 * 1.44) the largest score's weight
+# is exactly 1.  At powers 10 and 13 scores are at most 2^26 * 1.5 * 2 * 0.7 * 1.45 < 2^29: the exact
+# product and the maximum, rounded to fp32, differ by r, |r| <= 2^4, and the weight is 2^r.  It
+# cancels against the sum of weights, but is rounded to bf16 before the weighted sum (H of it),
+# which the sum is not: H times the sum of the weighted magnitudes is added there.
+
+def weight_error(power):
+    return M.H if power < 15 else 0.0
+
+
+def one_channel(t, heads, kv, d, power, seed, rising=False):
+    rng = np.random.RandomState(seed)
+    q, k = torch.zeros(t, heads, d), torch.zeros(t, kv, d)
+    q[:, :, 0] = torch.from_numpy(rng.choice([-1.5, -1.0, 1.0, 1.25], (t, heads))) * 2.0 ** power
+    m = 1 + (np.arange(t) % 128) / 128 if rising else 1 + rng.permutation(128 * (1 + t // 128))[:t] % 128 / 128
+    k[:, :, 0] = torch.from_numpy(m)[:, None] * 2.0 ** power
+    return q.to(torch.bfloat16).cuda(), k.to(torch.bfloat16).cuda(), normal((t, kv, d), seed)
+
+
+def weights64(q, k, first, window, scale):
+    """[m, h, n] softmax weights of rows at positions first.., float64."""
+    g = q.shape[1] // k.shape[1]
+    s = np.einsum("mhd,nhd->mhn", q, np.repeat(k, g, 1)) * scale
+    p, j = first + np.arange(q.shape[0])[:, None], np.arange(k.shape[0])[None]
+    s = np.where(((j <= p) & (p - j < window))[:, None], s, -np.inf)
+    w = np.exp(s - s.max(-1, keepdims=True))
+    return w / w.sum(-1, keepdims=True)
+
+
+@pytest.mark.parametrize("rising", [False, True])
+@pytest.mark.parametrize("power", [10, 13, 15, 16, 17, 20, 33, 60])
+def test_packed_scores_of_any_size(ptb_lib, power, rising):
+    t, heads, kv, d, window = 300, 4, 2, 64, 100
+    q, k, v = one_channel(t, heads, kv, d, power, 31, rising)
+    q[150:] = 0  # rows whose scores are all equal, in tiles of the others
+    cu = [0, 200, t]
+    o = M.to64(ptb_lib.swa_attention_packed(q, k, v, ints(cu), window, scale=0.7))
+    for a, b in zip(cu, cu[1:]):
+        w = weights64(M.to64(q)[a:b], M.to64(k)[a:b], 0, window, 0.7)
+        v64 = np.repeat(M.to64(v)[a:b], heads // kv, 1)
+        want, mag = np.einsum("mhn,nhd->mhd", w, v64), np.einsum("mhn,nhd->mhd", w, np.abs(v64))
+        # fp32 sums of at most 100 values
+        assert (np.abs(o[a:b] - want) <= M.H * np.abs(want) + 1.01 * (2.0 ** -16 + weight_error(power)) * mag).all()
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("heads,rising", [(2, False), (2, True), (24, False)])
+@pytest.mark.parametrize("power", [10, 15, 16, 17, 20, 33, 58])
+def test_paged_scores_of_any_size(ptb_lib, bits, power, heads, rising):
+    n, kv, d, page, window = 300, 2, 64, 16, 250
+    q, k, v = one_channel(n, heads, kv, d, power, 41, rising)
+    q = torch.cat([q[:2], torch.zeros_like(q[:1])])
+    pages = -(-n // page)
+    table = ints(range(pages))[None].repeat(3, 1)
+    cache = torch.zeros(pages, ptb_lib.kv_page_size(kv, page, d, bits), dtype=torch.uint8, device="cuda")
+    ptb_lib.kv_append(None, k, v, cache, table[:1], ints([0, n]), ints([0]), page, bits, keep_keys=False)
+    lens = [n, 130, n]
+    o = M.to64(ptb_lib.swa_attention_paged(q, cache, table, ints(lens), kv, page, bits, window, scale=0.7))
+    host = M.Cache(cache.cpu().numpy(), kv, page, d, bits)
+    k64, v64, mag = np.zeros((n, kv, d)), np.zeros((n, kv, d)), np.zeros((n, kv, d))
+    for p in range(n):
+        for h in range(kv):
+            k64[p, h] = host.get(p // page, p % page, h, 0)[0]
+            v64[p, h], u, s, z = host.get(p // page, p % page, h, 1)
+            # 4 bits: p * scale is rounded before the sum whatever p is, p for the centres as above
+            mag[p, h] = (weight_error(power) * np.abs(v64[p, h]) if u is None else
+                         M.H * s * np.abs(u - 8) + weight_error(power) * np.abs(z))
+    g = heads // kv
+    for b, m in enumerate(lens):
+        w = weights64(M.to64(q[b:b + 1]), k64[:m], m - 1, window, 0.7)[0]
+        want = np.einsum("hn,nhd->hd", w, np.repeat(v64[:m], g, 1))
+        err = np.einsum("hn,nhd->hd", w, np.repeat(mag[:m] + 2.0 ** -16 * np.abs(v64[:m]), g, 1))
+        assert (np.abs(o[b] - want) <= M.H * np.abs(want) + 1.01 * err).all(), (b, np.abs(o[b] - want).max())
