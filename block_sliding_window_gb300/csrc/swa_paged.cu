@@ -579,11 +579,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
             qs[nt][1] = pack_bf16x2(-8.f * sum - bf16_lo(top), sum - bf16_hi(top));
           }
         }
-        // Never 0: a masked score times it has to stay minus infinity.
+        // Never 0 or infinite: a masked score times 0 would not stay minus infinity, and
+        // times infinity a finite score below zero would become a masked one.  Beyond
+        // the last power of two the row is NaN (scale |q| of 2^116.4 and more).
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           to_log2[nt][e] *= __shfl_sync(0xffffffffu, down, 8 * t + 4 * e);
           if (to_log2[nt][e] == 0.f) to_log2[nt][e] = 0x1p-126f;
+          if (to_log2[nt][e] > 0x1p127f) to_log2[nt][e] = __uint_as_float(0x7fffffffu);
         }
       }
     }

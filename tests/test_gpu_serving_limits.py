@@ -185,3 +185,36 @@ def test_paged_scores_of_any_size(ptb_lib, bits, power, heads, rising):
         want = np.einsum("hn,nhd->hd", w, np.repeat(v64[:m], g, 1))
         err = np.einsum("hn,nhd->hd", w, np.repeat(mag[:m] + 2.0 ** -16 * np.abs(v64[:m]), g, 1))
         assert (np.abs(o[b] - want) <= M.H * np.abs(want) + 1.01 * err).all(), (b, np.abs(o[b] - want).max())
+
+
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("heads", [2, 12])
+def test_paged_4bit_queries_that_the_scale_takes_out_of_range(ptb_lib, heads, sign):
+    """Scale times a query of 2^118 and more: NaN in its row, for scores of either sign (and not the
+    zeros of a row without keys); up to 2^116 the row that its neighbours get."""
+    n, d, page = 70, 64, 16
+    pages = -(-n // page)
+    k, v = normal((n, 1, d), 51).abs() + 0.5, normal((n, 1, d), 52)
+    table = ints(range(pages))[None].repeat(2, 1)
+    cache = torch.zeros(pages, ptb_lib.kv_page_size(1, page, d, 4), dtype=torch.uint8, device="cuda")
+    ptb_lib.kv_append(None, k, v, cache, table[:1], ints([0, n]), ints([0]), page, 4, keep_keys=False)
+    host = M.Cache(cache.cpu().numpy(), 1, page, d, 4)
+    for power, scale in ((118, 1.0), (100, 2.0 ** 18), (0, 2.0 ** 118), (117, 4.0)):
+        q = torch.zeros(2, heads, d, dtype=torch.bfloat16, device="cuda")
+        q[:, :, 3] = 2.0 ** (power - 130)  # the other heads: scores of 2^-12 and less
+        q[0, 1, 3] = sign * 2.0 ** power
+        o = M.to64(ptb_lib.swa_attention_paged(q, cache, table, ints([n, n]), 1, page, 4, 1000, scale=scale))
+        assert np.isnan(o[0, 1]).all(), (power, scale)
+        q[0, 1, 3] = sign * 2.0 ** (power - 130)
+        want, bound = M.paged(M.to64(q), host, table.cpu().numpy(), [n, n], 1000, scale)
+        o[0, 1] = want[0, 1]
+        assert (np.abs(o - want) <= bound).all()
+    # scores of 2^115 and more: all the weight on the largest
+    q[:, :, 3] = sign * 2.0 ** 115
+    o = M.to64(ptb_lib.swa_attention_paged(q, cache, table, ints([n, n]), 1, page, 4, 1000, scale=1.0))
+    key = np.array([host.get(p // page, p % page, 0, 0)[0][3] for p in range(n)]) * sign
+    w = (key == key.max()) / (key == key.max()).sum()
+    got = [host.get(p // page, p % page, 0, 1) for p in range(n)]
+    want = w @ np.stack([x[0] for x in got])
+    err = w @ np.stack([M.H * x[2] * np.abs(x[1] - 8) + 2.0 ** -16 * np.abs(x[0]) for x in got])
+    assert (np.abs(o - want) <= M.H * np.abs(want) + 1.01 * err).all()
