@@ -26,6 +26,11 @@ int64_t kv_block_bytes(int32_t page_size, int32_t head_dim, int32_t bits) {
 
 bool stride_ok(int64_t s) { return s > 0 && s % 8 == 0 && s < (1ll << 39); }
 
+// 0 stands for the default.  Times log2(e) the scale has to stay below 2^127: an
+// infinite factor makes NaN of a score of zero, and the kernels round it up to a
+// power of two for large scores.
+bool scale_ok(float s) { return s >= 0.f && s <= 0x1p126f; }
+
 // Shape, alignment and table of a cache; the device is not touched.
 ptb_status fill_cache(KvCache* c, const void* base, int64_t pages, const int32_t* table,
                       int64_t table_stride, int64_t table_pages, int32_t kv_heads,
@@ -179,7 +184,7 @@ ptb_status swa_attention_packed(const ptb_bf16* q, int64_t q_st, int64_t q_sh, c
   if (!cu_seqlens_q || batch < 1 || tokens_q < 0 || tokens_k < 0 || heads < 1 || kv_heads < 1 ||
       window < 1)
     return PTB_ERR_ARG;
-  if (scale < 0.f || !std::isfinite(scale)) return PTB_ERR_ARG;
+  if (!scale_ok(scale)) return PTB_ERR_ARG;
   if (!head_dim_ok(head_dim) || heads % kv_heads || heads / kv_heads > kMaxPackedGroup ||
       heads > kMaxHeads || batch > 65535 || tokens_q > kMaxTokens || tokens_k > kMaxTokens)
     return PTB_ERR_SHAPE;
@@ -241,7 +246,7 @@ ptb_status swa_attention_paged(const ptb_bf16* q, int64_t q_sb, int64_t q_sh, co
   SwaPagedArgs a;
   std::memset(&a, 0, sizeof(a));
   if (!seq_lens || batch < 1 || heads < 1 || kv_heads < 1 || window < 1) return PTB_ERR_ARG;
-  if (scale < 0.f || !std::isfinite(scale)) return PTB_ERR_ARG;
+  if (!scale_ok(scale)) return PTB_ERR_ARG;
   if (batch > 65535 || heads > kMaxHeads || heads % kv_heads) return PTB_ERR_SHAPE;
   PTB_TRY(fill_cache(&a.c, cache, pages, page_table, table_stride, table_pages, kv_heads, head_dim,
                      page_size, bits));

@@ -539,7 +539,7 @@ ptb_status ptb_kv_gather(const void* cache, int64_t pages, const int32_t* page_t
  *
  *   q, o [tokens_q, heads, d], k, v [tokens_k, kv_heads, d]  strided bf16;
  *        o may be q itself (same pointer and strides), and overlaps nothing else
- *   scale  0: 1 / sqrt(d)
+ *   scale  0: 1 / sqrt(d); 0 to 2^126
  *   workspace  at least swa_attention_packed_workspace_size() bytes, 256-byte
  *        aligned; calls that may run at the same time need one each.  The size
  *        depends on the current device's SM count and is 0 for calls so
@@ -564,10 +564,10 @@ ptb_status swa_attention_packed(const ptb_bf16* q, int64_t q_st, int64_t q_sh, c
  * token's own among them; its query attends to the last min(seq_lens[b],
  * window) of them.  seq_lens[b] = 0 gives zeros, and so do scores that are all
  * minus infinity.  q, o [batch, heads, d] strided bf16 (o may be q itself);
- * keys of bits = 4 are used as the values that their codes stand for.  With
- * them a query row whose largest magnitude is m gives NaN from m = 2^119 on,
- * and from scale * m = 2^118 on; below 2^116 the latter is always computed, in
- * between it depends on m.
+ * scale as above; keys of bits = 4 are used as the values that their codes
+ * stand for.  With them a query row whose largest magnitude is m gives NaN from
+ * m = 2^119 on, and from scale * m = 2^118 on; below 2^116 the latter is always
+ * computed, in between it depends on m.
  *   workspace  at least swa_attention_paged_workspace_size() bytes (depends on
  *        the current device's SM count), 256-byte aligned; calls that may run
  *        at the same time need one each

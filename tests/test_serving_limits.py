@@ -38,3 +38,17 @@ def test_packed_workspace_of_groups_beyond_a_tile(lib):
         st = lib.swa_attention_packed(p, heads * 64, 64, 2 * p, 64, 64, 3 * p, 64, 64, p, None, 2, 100, 100, heads, 1, 64,
                                       8, 0.0, 4 * p, heads * 64, 64, p, 1 << 40, None)
         assert st == SHAPE
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 126 * 1.0001, 3e38, -1e-30, float("nan"), float("inf")])
+def test_attention_refuses_scales_whose_factor_overflows(lib, scale):
+    """scale * log2(e) has to be a number below 2^127 (2^126 is the last power of two that is)."""
+    p, arg, align = 1 << 20, 1, 3
+    # lens and cu_seqlens are misaligned, so that no scale gets as far as a launch
+    packed = lambda s: lib.swa_attention_packed(p, 256, 64, 2 * p, 128, 64, 3 * p, 128, 64, p + 1, None, 2, 100, 100, 4, 2,  # noqa: E731
+                                                64, 8, s, 4 * p, 256, 64, p, 1 << 40, None)
+    paged = lambda s: lib.swa_attention_paged(p, 256, 64, 2 * p, 10, p, 5, 5, p + 1, 2, 4, 2, 64, 16, 4, 8, s, 4 * p, 256, 64,  # noqa: E731
+                                              p, 1 << 40, None)
+    for call in (packed, paged):
+        assert call(scale) == arg
+        assert call(2.0 ** 126) == align and call(0.0) == align
