@@ -346,7 +346,19 @@ def swa_attention_counts(q, k, v, window: int, scale: float = 0.0, stream=None):
 
 # ---------------------------------------------------------------- serving --
 
-_INT32_MAX = 0x7fffffff  # a longer window is the same as this one; ctypes would drop its high bits
+_INT32_MAX = 0x7fffffff
+
+
+def _window(window: int) -> int:
+    """A window longer than this is the same as this one, and one below 0 refused like 0: ctypes would
+    drop the high bits of either."""
+    return min(max(window, 0), _INT32_MAX)
+
+
+def _fits32(*numbers: int) -> None:
+    for n in numbers:
+        if not -_INT32_MAX <= n <= _INT32_MAX:
+            raise ValueError(f"{n} does not fit in 32 bits")
 
 
 @functools.lru_cache(maxsize=None)
@@ -354,6 +366,7 @@ def kv_page_size(kv_heads: int, page_size: int, head_dim: int, bits: int) -> int
     """Bytes of one page of a key/value cache: `page_size` token rows of the keys and the values of
     `kv_heads` heads in bf16 (bits 16) or 4 bits.  A cache is a uint8 CUDA tensor
     [pages, kv_page_size(...)] of any content."""
+    _fits32(kv_heads, page_size, head_dim, bits)
     n = int(load().ptb_kv_page_size(kv_heads, page_size, head_dim, bits))
     if n == 0:
         raise ValueError(f"no cache of {kv_heads} heads x {head_dim}, pages of {page_size} rows, "
@@ -543,6 +556,7 @@ def kv_gather(cache, page_table, cu_seqlens, start, tokens: int, kv_heads: int, 
 
 
 def swa_attention_packed_workspace_size(batch: int, tokens_q: int, heads: int, kv_heads: int) -> int:
+    _fits32(batch, heads, kv_heads)
     return int(load().swa_attention_packed_workspace_size(batch, tokens_q, heads, kv_heads))
 
 
@@ -576,13 +590,14 @@ def swa_attention_packed(q, k, v, cu_seqlens, window: int, cu_seqlens_k=None, sc
     ws, wp, wb = _scratch(_packed_workspace(dev, batch, tq, heads, kv_heads), workspace, q, dev,
                           stream)  # ws lives until the launch is queued
     st = lib.swa_attention_packed(*qa, *ka, *va, cu, cu_k, batch, tq, tk, heads, kv_heads, d,
-                                  min(window, _INT32_MAX), scale, *oa, wp, wb, raw)
+                                  _window(window), scale, *oa, wp, wb, raw)
     if st:
         _check(st, "swa_attention_packed")
     return o
 
 
 def swa_attention_paged_workspace_size(batch: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    _fits32(batch, heads, kv_heads, head_dim)
     return int(load().swa_attention_paged_workspace_size(batch, heads, kv_heads, head_dim))
 
 
@@ -604,7 +619,7 @@ def swa_attention_paged(q, cache, page_table, seq_lens, kv_heads: int, page_size
     st = lib.swa_attention_paged(*qa, *_cache_args(cache, page_table, batch, kv_heads, d, page_size,
                                                    bits, dev),
                                  _int_vector("seq_lens", seq_lens, batch, dev), batch, heads,
-                                 kv_heads, d, page_size, bits, min(window, _INT32_MAX), scale, *oa, wp,
+                                 kv_heads, d, page_size, bits, _window(window), scale, *oa, wp,
                                  wb, raw)
     if st:
         _check(st, "swa_attention_paged")

@@ -34,6 +34,17 @@ def test_packed_refuses_groups_beyond_a_tile(ptb_lib, heads):
         ptb_lib.swa_attention_packed(q, k, v, ints([0, 10]), 4)
 
 
+@pytest.mark.parametrize("window", [0, -1, -(1 << 31) - 5, -(1 << 32) + 5, -(1 << 40) + 1])
+def test_attention_refuses_windows_below_one(ptb_lib, window):
+    """Also those whose low 32 bits are a positive number."""
+    q, kv, page = normal((10, 2, 16), 1), normal((10, 1, 16), 2), 16
+    cache = torch.zeros(1, ptb_lib.kv_page_size(1, page, 16, 16), dtype=torch.uint8, device="cuda")
+    with pytest.raises(ptb_lib.PTBError, match="ARG"):
+        ptb_lib.swa_attention_packed(q, kv, kv.clone(), ints([0, 10]), window)
+    with pytest.raises(ptb_lib.PTBError, match="ARG"):
+        ptb_lib.swa_attention_paged(q[:1], cache, ints([0])[None], ints([5]), 1, page, 16, window)
+
+
 # ----------------------------------------------------------------------- partly filled tiles --
 
 def cumulated(ls):

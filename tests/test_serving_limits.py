@@ -52,3 +52,17 @@ def test_attention_refuses_scales_whose_factor_overflows(lib, scale):
     for call in (packed, paged):
         assert call(scale) == arg
         assert call(2.0 ** 126) == align and call(0.0) == align
+
+
+@pytest.mark.parametrize("high", [1 << 32, -(1 << 32), 1 << 40])
+def test_sizes_refuse_numbers_beyond_32_bits(lib, high):
+    """Not the answer for their low 32 bits."""
+    import block_sliding_window_gb300 as bsw
+    for f, args in ((bsw.kv_page_size, (8, 64, 128, 16)), (bsw.swa_attention_paged_workspace_size, (2, 4, 2, 64)),
+                    (bsw.swa_attention_packed_workspace_size, (2, 10 ** 6, 4, 2))):
+        assert f(*args) > 0
+        for i in range(4):
+            if args[i] == 10 ** 6:  # tokens: 64 bits
+                continue
+            with pytest.raises(ValueError, match="32 bits"):
+                f(*(a + high if i == j else a for j, a in enumerate(args)))
