@@ -5,6 +5,9 @@ import subprocess
 import sys
 
 import pytest
+import torch
+
+from tests import serving_exact as X
 
 SHAPE = 2
 
@@ -66,3 +69,35 @@ def test_sizes_refuse_numbers_beyond_32_bits(lib, high):
                 continue
             with pytest.raises(ValueError, match="32 bits"):
                 f(*(a + high if i == j else a for j, a in enumerate(args)))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_limits_of_long_rows_show_a_lost_key(bits):
+    """Mistakes planted in the 64-bit model pass the limits that GPU rows are held to: a block of 32
+    keys left out, one key left out, a page taken twice, a row of codes that reads another's pair."""
+    n, heads, kv, d, page = 1500, 4, 2, 64, 16
+    gen = torch.Generator().manual_seed(5)
+    pages = -(-n // page)
+    cache = torch.zeros(pages, 2, kv, page * (2 * d if bits == 16 else d // 2 + d // 8), dtype=torch.uint8)
+    x = torch.randn(pages, 2, kv, page, d, generator=gen)
+    if bits == 16:
+        cache[:] = x.to(torch.bfloat16).flatten(-2).view(torch.uint8)
+    else:
+        cache[..., :page * d // 2] = torch.randint(0, 256, (pages, 2, kv, page * d // 2), generator=gen, dtype=torch.uint8)
+        pair = torch.rand(pages, 2, kv, page * d // 32, 2, generator=gen) * torch.tensor([0.2, 0.1]) + torch.tensor([0.1, -0.05])
+        cache[..., page * d // 2:] = pair.to(torch.bfloat16).flatten(-2).view(torch.uint8)
+    cache = cache.flatten(1)
+    q = torch.randn(1, heads, d, generator=gen).to(torch.bfloat16)
+    table = torch.arange(pages, dtype=torch.int32)[None]
+    args = (kv, page, bits)
+    want, bound = X.paged(q, cache, table, [n], *args, 1 << 20, d ** -0.5)
+    assert X.row_error(want.bfloat16().double(), want) <= X.ROW_LIMIT / 3  # the output's rounding alone
+    assert torch.isfinite(want).all() and (bound > 0).all()
+    twice = table.clone()
+    twice[0, 10] = 11
+    moved = cache.clone()
+    at = page * d // 2 if bits == 4 else 0
+    moved.view(pages, 2, kv, -1)[3, 1, :, at:] = moved.view(pages, 2, kv, -1)[3, 1, :, at:].roll(d // 8 if bits == 4 else 2 * d, -1)
+    for c, t, m, w in ((cache, table, n, n - 32), (cache, table, n, n - 1), (cache, twice, n, n), (moved, table, n, n)):
+        other, _ = X.paged(q, c, t, [m], *args, w, d ** -0.5)
+        assert X.row_error(other, want) > X.ROW_LIMIT, (w, X.row_error(other, want))
