@@ -1126,10 +1126,12 @@ cudaError_t launch_typed(PagedParams& prm, cudaStream_t stream) {
   cfg.gridDim = dim3(grid - 1);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
-  // Launched to overlap the first kernel's end where that one is long (3 us of
-  // GPU time); a call of few microseconds is bound by its launches on the
-  // host, and an overlapping one costs 3 us more there (25.5 against 22.5 us
-  // a call).  The lengths are not known here: the bound goes by the table.
+  // Launched to overlap the first kernel's end where that one is long: with 64
+  // heads over 8, calls of 100 to 400 MB take 2 us less so (4 bits, 100 MB: 30.9
+  // us a call for 32.9).  Shorter ones are bound by the host, 20 us either way,
+  // and replayed from a graph they lose by it in 4 bits (8 to 100 MB: 0.6 to 0.9
+  // us; bf16 no difference).  The lengths are not known here, so the bound goes
+  // by the table: a short call under a wide one loses that much.
   const KvCache& c = prm.a.c;
   const int64_t most = c.table_pages << c.page_shift;
   const double bytes = 2.0 * prm.a.batch * c.kv_heads *
