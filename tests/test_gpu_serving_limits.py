@@ -229,3 +229,79 @@ def test_paged_4bit_queries_that_the_scale_takes_out_of_range(ptb_lib, heads, si
     want = w @ np.stack([x[0] for x in got])
     err = w @ np.stack([M.H * x[2] * np.abs(x[1] - 8) + 2.0 ** -16 * np.abs(x[0]) for x in got])
     assert (np.abs(o - want) <= M.H * np.abs(want) + 1.01 * err).all()
+
+
+# ------------------------------------------------------------------- graphs and other streams --
+
+@pytest.mark.parametrize("bits,inter", [(16, False), (4, True)])
+def test_decode_steps_captured_once(ptb_lib, bits, inter):
+    """Append, read back and attend in one graph whose lengths move on the device: each replay is the
+    next step, bit for bit what the eager calls give; a second graph runs on another stream."""
+    prompts, steps, heads, kv, d, page, window = [5, 31, 16, 1], 20, 6, 2, 64, 16, 24
+    batch = len(prompts)
+    need = [-(-(n + steps) // page) for n in prompts]
+    cos = torch.cos(torch.arange(64.0)[:, None] * torch.arange(1, d // 2 + 1) / 50).cuda()
+    sin = torch.sin(torch.arange(64.0)[:, None] * torch.arange(1, d // 2 + 1) / 50).cuda()
+    cu, one = cumulated(prompts), ints(range(batch + 1))
+    q0, k0, v0 = (normal((cu[-1], n, d), 60 + i) for i, n in enumerate((heads, kv, kv)))
+    new = [[normal((batch, n, d), 70 + 3 * s + i) for i, n in enumerate((heads, kv, kv))] for s in range(steps)]
+
+    def start():
+        order = np.random.RandomState(3).permutation(sum(need))
+        table = np.full((batch, max(need)), -1, dtype=np.int32)
+        for b, n in enumerate(need):
+            table[b, :n], order = order[:n], order[n:]
+        cache = torch.full((sum(need), ptb_lib.kv_page_size(kv, page, d, bits)), 0xFF, dtype=torch.uint8, device="cuda")
+        s = dict(cache=cache, table=torch.from_numpy(table).cuda(), past=ints([0] * batch), lens=ints(prompts))
+        ptb_lib.kv_append(q0, k0, v0, cache, s["table"], ints(cu), s["past"], page, bits, cos=cos, sin=sin, interleaved=inter)
+        s["past"].copy_(ints(prompts))
+        s["in"] = [t.clone() for t in new[0]]
+        return s
+
+    def step(s, stream=None):
+        q, k, v = s["in"]
+        s["q"], s["k"] = ptb_lib.kv_append(q, k, v, s["cache"], s["table"], one, s["past"], page, bits, cos=cos, sin=sin,
+                                           interleaved=inter, stream=stream)
+        s["kr"], s["vr"] = ptb_lib.kv_gather(s["cache"], s["table"], one, s["past"], batch, kv, d, page, bits, stream=stream)
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            s["lens"].copy_(s["past"] + 1)
+        s["o"] = ptb_lib.swa_attention_paged(s["q"], s["cache"], s["table"], s["lens"], kv, page, bits, window, stream=stream)
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            s["past"].add_(1)
+
+    want = []
+    s = start()
+    for x in new:
+        for a, b in zip(s["in"], x):
+            a.copy_(b)
+        step(s)
+        want.append([s[n].clone() for n in ("q", "k", "kr", "vr", "o")])
+    torch.cuda.synchronize()
+    runs = []
+    for _ in range(2):
+        s, stream = start(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            step(s)
+        runs.append((s, stream, g))
+    for x, w in zip(new, want):
+        for s, stream, g in runs:
+            with torch.cuda.stream(stream):
+                for a, b in zip(s["in"], x):
+                    a.copy_(b)
+                g.replay()
+        torch.cuda.synchronize()
+        for s, _, _ in runs:
+            for n, t in zip(("q", "k", "kr", "vr", "o"), w):
+                assert torch.equal(s[n], t), n
+    s, stream = start(), torch.cuda.Stream()  # eager, the stream given to each call
+    torch.cuda.synchronize()
+    for x, w in zip(new, want):
+        with torch.cuda.stream(stream):
+            for a, b in zip(s["in"], x):
+                a.copy_(b)
+        step(s, stream)
+        stream.synchronize()
+        for n, t in zip(("q", "k", "kr", "vr", "o"), w):
+            assert torch.equal(s[n], t), n
