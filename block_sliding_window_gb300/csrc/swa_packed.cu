@@ -35,9 +35,10 @@
 // rest is the round trip score -> softmax -> P V -> score over two buffers
 // (waits 155, TMEM load 370, weights and their store 850 cycles).  In short
 // ones an item's end (last P V, output: 1.5 us) and, on grouped heads, memory.
-// Measured: one prompt of 16001 tokens, 16 heads of 128: 722 us, 1.45 PFLOP/s;
-// 4 prompts, 128 heads of 96, window 1024: 161 us; 64 ragged prompts, 64 heads
-// over 8, window 512: 149 us, 3.5 TB/s.
+// Measured: one prompt of 16001 tokens, 16 heads of 128: 727 us, 1.44 PFLOP/s;
+// 4 prompts, 128 heads of 96, window 1024: 163 us; 64 ragged prompts, 64 heads
+// over 8, window 512: 151 us, 3.5 TB/s.  (A row's own factor for large scores is
+// 1% of that: 149 and 161 us with one factor for all.)
 #include "kv_device.cuh"
 
 namespace ptb {
