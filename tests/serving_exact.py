@@ -13,8 +13,11 @@ mag_k = scale (u + 8) + |centre|, and x counts, per key and times the score's sc
 exp2 and the factor log2(e) scale add 2^-21.  Weights off by a relative e move numerator and
 denominator: 2 e A, A = sum_j p_j |v_j|.  Weights are rounded once before the weighted sum (4 bits:
 p scale once for the codes, p once for the centres, |v| counts as scale |u - 8| + |centre|) but not
-in their own sum: H A.  Both sums run over n keys in fp32: (n + d) 2^-22 A.  The output is rounded:
-    |o - o64| <= H |o64| + 1.01 (H + 2 e + (n + d) 2^-22) A.
+in their own sum: H B, where B = A less the term of the key with the largest score in the paged
+kernel (it is the reference of its part of the row: its weight there is 1, and 1 and a scale are bf16
+numbers), B = A in the packed one.  Both sums run over n keys in fp32: (n + d) 2^-22 A.  The output is
+rounded:
+    |o - o64| <= H |o64| + 1.01 (H B + (2 e + (n + d) 2^-22) A).
 
 Over thousands of keys that bound is far above a row's real error, and above what a lost block of
 keys changes.  For values that are independent and centred at zero the length of a row says more:
@@ -90,7 +93,10 @@ def paged(q, cache, table, lens, kv, page, bits, window, scale):
         p = torch.softmax(s, -1)
         o[b] = torch.einsum("hgn,nhd->hgd", p, v).reshape(heads, d)
         a = torch.einsum("hgn,nhd->hgd", p, mag_v).reshape(heads, d)
-        bound[b] = H * o[b].abs() + 1.01 * (H + 2 * e.reshape(heads, 1) + (n - lo + d) * 2.0 ** -22) * a + 1e-30
+        top = p.argmax(-1, keepdim=True)  # [kv, g, 1]
+        of_top = torch.gather(mag_v.transpose(0, 1), 1, top.expand(-1, -1, d)) * p.gather(-1, top)
+        rest = (a - of_top.reshape(heads, d)).clamp(min=0)
+        bound[b] = H * o[b].abs() + 1.01 * (H * rest + (2 * e.reshape(heads, 1) + (n - lo + d) * 2.0 ** -22) * a) + 1e-30
     return o, bound
 
 

@@ -129,6 +129,28 @@ def test_paged_many_units_of_one_sequence(ptb_lib, bits):
     held_to(o, *X.paged(q, cache, table, lens, kv, page, bits, 1 << 20, d ** -0.5))
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("heads,kv,d", [(16, 8, 64), (96, 8, 128), (8, 8, 32), (24, 8, 96)])
+def test_paged_one_heavy_key(ptb_lib, heads, kv, d, bits):
+    """A key with most of the weight that comes after the reference of its part was set, by less than 2^8
+    over it, is not rounded on its way into the output: within the bound, which leaves its weight out,
+    and on the average no further from 64 bits than the output's own rounding and a tenth.  So many
+    sequences that a warp holds whole ones."""
+    page, sms = 16, torch.cuda.get_device_properties(0).multi_processor_count
+    lens = [33 + b % 17 for b in range(6 * 12 * sms // (2 * kv))]
+    q, cache, table = filled(ptb_lib, lens, heads, kv, d, page, bits, 700, False)
+    k, v, cu = normal((sum(lens), kv, d), 701, std=0.02), normal((sum(lens), kv, d), 702), cumulated(lens)
+    q[:, :, 0], k[:, :, 0] = 4.0, 0.0
+    for b, n in enumerate(lens):
+        k[cu[b] + 32 + b % (n - 32), :, 0] = (7 + b % 31 / 32) * np.log(2) / (4 * d ** -0.5)
+    ptb_lib.kv_append(None, k, v, cache, table, ints(cu), ints([0] * len(lens)), page, bits, keep_keys=False)
+    o = ptb_lib.swa_attention_paged(q, cache, table, ints(lens), kv, page, bits, 1 << 20)
+    want, bound = X.paged(q, cache, table, lens, kv, page, bits, 1 << 20, d ** -0.5)
+    assert ((o.double() - want).abs() <= bound).all()
+    err, own = (o.double() - want).norm(), (want.bfloat16().double() - want).norm()
+    assert err <= 1.1 * own, err / own
+
+
 @pytest.mark.parametrize("heads,kv,d,page,window", [(8, 2, 128, 16, 1 << 20), (24, 2, 64, 32, 40), (6, 2, 96, 16, 1 << 20),
                                                     (40, 2, 96, 32, 48), (3, 3, 32, 64, 100)])
 def test_paged_4bit_short_sequences(ptb_lib, heads, kv, d, page, window):
