@@ -43,10 +43,17 @@ __device__ __forceinline__ void store16_past_l1(void* p, const uint4& v) {
 // exact and r zero.  It changes no weight that counts: fp32 scores that differ
 // do so by at least 2^-24 of themselves, here 32, so every weight is that of the
 // largest score or below 2^-32 of it, with either factor; and as f only grows,
-// maxima of parts of a row that went either way keep their order.
+// maxima of parts of a row that went either way keep their order.  A row whose
+// scores so far were all below -2^29 takes f itself again where one is not.
 constexpr float kLargeScore = 536870912.f;  // 2^29, in the log2 domain
-__device__ __forceinline__ float power_of_two_above(float f) {  // f > 0
-  return __uint_as_float((__float_as_uint(f) + 0x007fffffu) & 0xff800000u);
+// The reference max of a row whose largest score is `largest`, and the factor
+// that goes with it, from the row's own factor f > 0.
+__device__ __forceinline__ float reference_max(float largest, float f, float& factor) {
+  factor = f;
+  const float m = __fmul_rn(largest, f);
+  if (fabsf(m) < kLargeScore) return m;
+  factor = __uint_as_float((__float_as_uint(f) + 0x007fffffu) & 0xff800000u);
+  return __fmul_rn(largest, factor);
 }
 
 constexpr int kKvGroup = 32;  // channels that share one (scale, centre) pair

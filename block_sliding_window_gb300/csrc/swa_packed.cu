@@ -632,13 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         const bool raise = mx > m_ref + kRescaleLog2;
         if (raise) {
-          alpha = fast_exp2(m_ref - mx);  // 0 while m_ref is -inf
+          const float m = reference_max(raw_max, a.scale_log2, scale);
+          alpha = fast_exp2(m_ref - m);  // 0 while m_ref is -inf
           l_run *= alpha;
-          m_ref = mx;
-          if (fabsf(mx) >= kLargeScore) {
-            scale = power_of_two_above(scale);
-            m_ref = __fmul_rn(raw_max, scale);
-          }
+          m_ref = m;
         }
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
         const uint64_t scale2 = f2(scale, scale), shift2 = f2(-m_use, -m_use);

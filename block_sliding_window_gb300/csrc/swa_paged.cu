@@ -520,7 +520,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
     // power of two into fp16.
     uint32_t qf[NT][MS][2];
     uint32_t qs[NT][2];  // Q_t: (-8 Q, Q) 2^-24 in two bf16 terms
-    float to_log2[NT][2];  // scores of heads 2 t, 2 t + 1 to the log2 domain
+    float to_log2[NT][2];  // scores of heads 2 t, 2 t + 1 to the log2 domain, now
+    [[maybe_unused]] float own_log2[NT][2];  // and as their queries have it (4 bits)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const bool live = nt * 8 + g < nheads;
@@ -586,6 +587,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
           to_log2[nt][e] *= __shfl_sync(0xffffffffu, down, 8 * t + 4 * e);
           if (to_log2[nt][e] == 0.f) to_log2[nt][e] = 0x1p-126f;
           if (to_log2[nt][e] > 0x1p127f) to_log2[nt][e] = __uint_as_float(0x7fffffffu);
+          own_log2[nt][e] = to_log2[nt][e];
         }
       }
     }
@@ -593,6 +595,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
     float o[NT][MS][4];
     float oc[NT][4];  // sum_j p_j centre_j of group g (4 bits)
     float m_ref[NT][2], l[NT][2];
+    bool large = false;  // some score was large (kLargeScore); the same in all lanes
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -715,20 +718,26 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NT>::kWarps * 32, 1)
           mx[e] = __fmul_rn(raw[e], to_log2[nt][e]);
         }
         if (__any_sync(0xffffffffu, mx[0] > m_ref[nt][0] || mx[1] > m_ref[nt][1])) {
-          float alpha[2];
+          float alpha[2], m[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1)
               raw[e] = fmaxf(raw[e], __shfl_xor_sync(0xffffffffu, raw[e], x));
-            mx[e] = __fmul_rn(raw[e], to_log2[nt][e]);
-            float m = fmaxf(m_ref[nt][e], mx[e]);
-            alpha[e] = m == -INFINITY ? 1.f : fast_exp2(m_ref[nt][e] - m);
-            if (mx[e] > m_ref[nt][e] && fabsf(mx[e]) >= kLargeScore) {
-              to_log2[nt][e] = power_of_two_above(to_log2[nt][e]);
-              m = __fmul_rn(raw[e], to_log2[nt][e]);
-            }
-            m_ref[nt][e] = m;
+            m[e] = fmaxf(m_ref[nt][e], __fmul_rn(raw[e], to_log2[nt][e]));
+          }
+          if (large || __any_sync(0xffffffffu, fmaxf(fabsf(m[0]), fabsf(m[1])) >= kLargeScore)) {
+            large = true;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (m[e] > m_ref[nt][e])
+                m[e] = reference_max(raw[e], BITS == 16 ? a.scale_log2 : own_log2[nt][e], to_log2[nt][e]);
+            __syncwarp();
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            alpha[e] = m[e] == -INFINITY ? 1.f : fast_exp2(m_ref[nt][e] - m[e]);
+            m_ref[nt][e] = m[e];
             l[nt][e] *= alpha[e];
           }
 #pragma unroll

@@ -305,3 +305,65 @@ def test_decode_steps_captured_once(ptb_lib, bits, inter):
         stream.synchronize()
         for n, t in zip(("q", "k", "kr", "vr", "o"), w):
             assert torch.equal(s[n], t), n
+
+
+# A row whose scores are large in one part and ordinary in another: the ordinary part's weights go by
+# the ordinary factor, whichever part comes first.
+
+def two_sizes(t, heads, kv, d, order, seed):
+    """Scores of -2^30 and less (times 0.7) for some keys and of -3 to 3 for the others, in runs of
+    keys as `order` says (0: ordinary), of 2^30 and more for those of order 2; one channel each, in
+    groups of their own, so that no score of a kind holds a rounding of the other's size."""
+    rng = np.random.RandomState(seed)
+    q, k = torch.zeros(t, heads, d), torch.zeros(t, kv, d)
+    q[:, :, 0], q[:, :, 32] = 2.0 ** 15, 1.0
+    for at, n, kind in order:
+        if kind:
+            k[at:at + n, :, 0] = torch.from_numpy(rng.randint(128, 256, n) / 128.0)[:, None] * (2.0 ** 15 * (1 if kind == 2 else -1))
+        else:
+            k[at:at + n, :, 32] = torch.from_numpy(rng.randint(-24, 25, n) / 8.0)[:, None]
+    return q.to(torch.bfloat16).cuda(), k.to(torch.bfloat16).cuda(), normal((t, kv, d), seed)
+
+
+ORDERS = [
+    [(0, 150, 1), (150, 150, 0)], [(0, 150, 0), (150, 150, 1)], [(0, 300, 1)], [(0, 40, 1), (40, 3, 0), (43, 257, 1)],
+    [(0, 200, 1), (200, 60, 0), (260, 1, 2), (261, 39, 0)], [(0, 64, 0), (64, 64, 1), (128, 64, 0), (192, 108, 1)],
+]
+
+
+@pytest.mark.parametrize("order", range(len(ORDERS)))
+@pytest.mark.parametrize("scale", [0.7, 1.2])
+def test_packed_scores_large_in_one_part_of_a_row(ptb_lib, order, scale):
+    t, heads, kv, d = 300, 2, 1, 64
+    q, k, v = two_sizes(t, heads, kv, d, ORDERS[order], 81)
+    for window in (1 << 20, 180):
+        o = M.to64(ptb_lib.swa_attention_packed(q, k, v, ints([0, t]), window, scale=scale))
+        w = weights64(M.to64(q), M.to64(k), 0, window, scale)
+        v64 = np.repeat(M.to64(v), heads // kv, 1)
+        want, mag = np.einsum("mhn,nhd->mhd", w, v64), np.einsum("mhn,nhd->mhd", w, np.abs(v64))
+        # ordinary scores are exact; weights rounded to bf16 once, sums of at most 300 in fp32
+        assert (np.abs(o - want) <= M.H * np.abs(want) + 1.01 * (M.H + 2.0 ** -14) * mag).all(), window
+
+
+@pytest.mark.parametrize("order", range(len(ORDERS)))
+@pytest.mark.parametrize("bits,heads", [(16, 2), (4, 2), (16, 12), (4, 12)])
+def test_paged_scores_large_in_one_part_of_a_row(ptb_lib, order, bits, heads):
+    """Many copies of the sequence, so that a warp takes its parts one after the other."""
+    n, kv, d, page, scale = 300, 1, 64, 64, 0.7
+    q, k, v = two_sizes(n, heads, kv, d, ORDERS[order], 91)
+    batch = 12 * torch.cuda.get_device_properties(0).multi_processor_count
+    pages = -(-n // page)
+    cache = torch.zeros(pages, ptb_lib.kv_page_size(kv, page, d, bits), dtype=torch.uint8, device="cuda")
+    table = ints(range(pages))[None]
+    ptb_lib.kv_append(None, k, v, cache, table, ints([0, n]), ints([0]), page, bits, keep_keys=False)
+    host = M.Cache(cache.cpu().numpy(), kv, page, d, bits)
+    rows = [[host.get(p // page, p % page, 0, i) for p in range(n)] for i in (0, 1)]
+    k64, v64 = (np.stack([x[0] for x in r]) for r in rows)
+    mag = np.abs(v64) if bits == 16 else np.stack([s * np.abs(u - 8) + np.abs(z) for _, u, s, z in rows[1]])
+    for window in (1 << 20, 180):
+        o = ptb_lib.swa_attention_paged(q[:1].repeat(batch, 1, 1), cache, table.repeat(batch, 1), ints([n] * batch), kv, page,
+                                        bits, window, scale=scale)
+        w = weights64(M.to64(q[:1]), k64[:, None], n - 1, window, scale)[0]
+        want, a = w @ v64, w @ mag
+        # ordinary scores are off by a few units of 2^-22, sums of at most 300 weights in fp32
+        assert (np.abs(M.to64(o) - want) <= M.H * np.abs(want) + 1.01 * (M.H + 2.0 ** -14) * a).all(), window
