@@ -35,11 +35,11 @@
 // rounded to bf16 once, as P is in the other attention kernels.
 // The integer pipe (0.5 instructions a clock and SM quarter, measured) bounds
 // the 4-bit kernel: with nibbles in the mantissas of 64 and 128, two shifts more
-// for four and an addition, 64 long sequences took 200 us, now 158.  (e4m3
+// for four and an addition, 64 long sequences took 200 us, now 159.  (e4m3
 // products, for which a masked word is an operand as it lies, were slower: the
 // compiler builds them from fp16 ones.)
 // Measured on 64 sequences, 64 heads of 128 over 8: bf16 6.0 TB/s (140 us; the
-// cache alone at the rate of a copy 124); 4 bits 5.4 TB/s (158 us; 127; the
+// cache alone at the rate of a copy 124); 4 bits 5.4 TB/s (159 us; 127; the
 // copies alone take 130).  One sequence of 16000 keys: 12 us, half of it the two
 // launches' ends.
 // Rows that the mask leaves out (before the window, past the length, pages out
