@@ -27,7 +27,10 @@ __all__ = [
     "swa_attention_backward", "set_gemm_pairs", "host_workspace_size", "ptb_forward_host",
     "kv_page_size", "kv_append", "kv_gather", "swa_attention_packed",
     "swa_attention_packed_workspace_size", "swa_attention_paged",
-    "swa_attention_paged_workspace_size", "LIB_PATH", "SYMBOLS",
+    "swa_attention_paged_workspace_size", "checkpoint_pack", "checkpoint_unpack", "gated_ffn",
+    "gated_ffn_train", "gated_ffn_workspace_size", "gated_ffn_backward",
+    "gated_ffn_backward_workspace_size", "norm_residual", "norm_residual_train",
+    "norm_residual_backward", "norm_residual_backward_workspace_size", "LIB_PATH", "SYMBOLS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libptb.so")
@@ -87,6 +90,20 @@ SYMBOLS = {
     "swa_attention_paged_workspace_size": (_sz, [_i32] * 4),
     "swa_attention_paged": (_st, [_p, _i64, _i64, _p, _i64, _p, _i64, _i64, _p] + [_i32] * 7
                             + [_f32, _p, _i64, _i64, _p, _sz, _p]),
+    "ptb_checkpoint_pack": (_st, [_p] + [_i64] * 3 + [_p, _i64] * 2 + [_p]),
+    "ptb_checkpoint_unpack": (_st, [_p, _i64] * 2 + [_i64] * 2 + [_p, _i64, _p]),
+    "ptb_gated_ffn_workspace_size": (_sz, [_i64] * 3),
+    "ptb_gated_ffn": (_st, [_p, _i64] + [_p] * 4 + [_i64] * 4 + [_i32, _p, _i64, _p, _p, _p, _sz,
+                                                                _p]),
+    "ptb_gated_ffn_backward_workspace_size": (_sz, [_i64] * 3 + [_i32]),
+    "ptb_gated_ffn_backward": (_st, [_p, _i64] * 3 + [_p] * 5 + [_i64] * 3 + [_i32, _p, _i64]
+                               + [_p] * 3 + [_i32, _p, _sz, _p]),
+    "ptb_norm_residual": (_st, [_p, _i64] * 2 + [_p] * 3 + [_i64, _f32, _p, _p, _i32, _f32, _i64,
+                                                            _i64] + [_p, _i64] * 2 + [_p, _p]),
+    "ptb_norm_residual_backward_workspace_size": (_sz, [_i64] * 3),
+    "ptb_norm_residual_backward": (_st, [_p, _i64] * 5 + [_p] * 4 + [_i64, _f32, _p, _i32, _i64,
+                                                                     _i64] + [_p, _i64] * 2
+                                   + [_p] * 6 + [_sz, _p]),
     "ptb_last_device_error": (_st, [_p]),
     "ptb_wait_probe": (_st, [ctypes.c_uint64, _p]),
 }
@@ -624,6 +641,364 @@ def swa_attention_paged(q, cache, page_table, seq_lens, kv_heads: int, page_size
     if st:
         _check(st, "swa_attention_paged")
     return o
+
+
+# ----------------------------- gated feed-forward, norms, 8-bit checkpoints --
+# A checkpoint is a pair (codes int8 [rows, cols], exps uint8 [rows, cols / 32]); wherever one may
+# stand for a bf16 tensor, the pair is given in the tensor's place.
+
+def _matrix(name: str, t, dev: int, cols=None, rows=None, dtype=torch.bfloat16) -> tuple:
+    """[..., cols] with contiguous rows at one stride -> (pointer, row stride, rows, cols)."""
+    _tensor(name, t, dtype, dev)
+    size = t.shape
+    if len(size) < 2:
+        raise ValueError(f"{name} must have at least 2 dimensions")
+    c = size[-1]
+    if (cols is not None and c != cols) or c < 1:
+        raise ValueError(f"{name} must have {cols} columns, not {c}")
+    st = t.stride()
+    if st[-1] != 1 and c != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    n, ld = size[-2], st[-2]
+    if len(size) > 2:
+        # The leading dimensions have to run on at the rows' stride.
+        for d in range(len(size) - 3, -1, -1):
+            if size[d] != 1:
+                if n > 1 and st[d] != n * ld:
+                    raise ValueError(f"{name} must have its rows at one stride")
+                if n == 1:
+                    ld = st[d]
+                n *= size[d]
+    if rows is not None and n != rows:
+        raise ValueError(f"{name} must have {rows} rows, not {n}")
+    # The stride of a single row is never used.
+    return t.data_ptr(), ld if n > 1 else c, n, c
+
+
+def _vector(name: str, t, n: int, dev: int, dtype=torch.bfloat16):
+    if t is None:
+        return None
+    _tensor(name, t, dtype, dev)
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} entries")
+    return t.data_ptr()
+
+
+def _whole(name: str, t, shape: tuple, dev: int, dtype=torch.bfloat16) -> int:
+    _tensor(name, t, dtype, dev)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape {shape}, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _checkpoint(name: str, pair, dev: int, cols=None, rows=None) -> tuple:
+    """A checkpoint -> (pointer, stride, rows, cols) of its codes, (pointer, stride) of its exps."""
+    if not isinstance(pair, tuple) or len(pair) != 2:
+        raise TypeError(f"{name} must be a pair (codes, exps)")
+    c = _matrix(f"{name}'s codes", pair[0], dev, cols, rows, torch.int8)
+    if c[3] % 32:
+        raise ValueError(f"{name} must have a multiple of 32 columns")
+    e = _matrix(f"{name}'s exps", pair[1], dev, c[3] // 32, c[2], torch.uint8)
+    return c + e[:2]
+
+
+def _either(name: str, t, dev: int, cols=None, rows=None) -> tuple:
+    """A bf16 matrix or a checkpoint -> (pointer, stride, exps or None, exps' stride, rows, cols)."""
+    if isinstance(t, tuple):
+        p, ld, n, c, ep, eld = _checkpoint(name, t, dev, cols, rows)
+        return p, ld, ep, eld, n, c
+    p, ld, n, c = _matrix(name, t, dev, cols, rows)
+    return p, ld, None, 0, n, c
+
+
+def checkpoint_pack(x, codes=None, exps=None, stream=None) -> tuple:
+    """x [..., cols] bf16 (cols a multiple of 32) as 8-bit codes with one power-of-two scale for 32
+    neighbouring channels: the pair (codes int8 [..., cols], exps uint8 [..., cols / 32])."""
+    lib = load()
+    dev, raw = _launch_on(stream, x)
+    p, ld, rows, cols = _matrix("x", x, dev)
+    if cols % 32:
+        raise ValueError("x must have a multiple of 32 columns")
+    if codes is None:
+        codes = _new(x, x.shape, stream, torch.int8)
+    if exps is None:
+        exps = _new(x, x.shape[:-1] + (cols // 32,), stream, torch.uint8)
+    c = _checkpoint("the checkpoint", (codes, exps), dev, cols, rows)
+    st = lib.ptb_checkpoint_pack(p, ld, rows, cols, c[0], c[1], c[4], c[5], raw)
+    if st:
+        _check(st, "ptb_checkpoint_pack")
+    return codes, exps
+
+
+def checkpoint_unpack(codes, exps, x=None, stream=None) -> torch.Tensor:
+    """The bf16 values that a checkpoint's codes stand for."""
+    lib = load()
+    dev, raw = _launch_on(stream, codes)
+    p, ld, rows, cols, ep, eld = _checkpoint("the checkpoint", (codes, exps), dev)
+    if x is None:
+        x = _new(codes, codes.shape, stream)
+    xp, xld, _, _ = _matrix("x", x, dev, cols, rows)
+    st = lib.ptb_checkpoint_unpack(p, ld, ep, eld, rows, cols, xp, xld, raw)
+    if st:
+        _check(st, "ptb_checkpoint_unpack")
+    return x
+
+
+_ACTIVATIONS = {"silu": 0, "gelu": 1}
+
+
+def _activation(name: str) -> int:
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
+    return _ACTIVATIONS[name]
+
+
+def gated_ffn_workspace_size(tokens: int, hidden: int, ffn: int) -> int:
+    return int(load().ptb_gated_ffn_workspace_size(tokens, hidden, ffn))
+
+
+def gated_ffn_backward_workspace_size(tokens: int, hidden: int, ffn: int, x_bits: int = 16) -> int:
+    _fits32(x_bits)
+    return int(load().ptb_gated_ffn_backward_workspace_size(tokens, hidden, ffn, x_bits))
+
+
+@functools.lru_cache(maxsize=4096)
+def _gated_workspace(dev: int, tokens: int, hidden: int, ffn: int) -> int:
+    return gated_ffn_workspace_size(tokens, hidden, ffn)
+
+
+@functools.lru_cache(maxsize=4096)
+def _gated_backward_workspace(dev: int, tokens: int, hidden: int, ffn: int, x_bits: int) -> int:
+    return gated_ffn_backward_workspace_size(tokens, hidden, ffn, x_bits)
+
+
+def _gated_weights(w_gate, w_up, w_down, hidden: int, dev: int) -> tuple:
+    _tensor("w_gate", w_gate, torch.bfloat16, dev)
+    if w_gate.dim() != 2:
+        raise ValueError("w_gate must be [ffn, hidden]")
+    ffn = w_gate.shape[0]
+    return ffn, (_whole("w_gate", w_gate, (ffn, hidden), dev), _whole("w_up", w_up, (ffn, hidden), dev),
+                 _whole("w_down", w_down, (hidden, ffn), dev))
+
+
+def _gated_forward(x, w_gate, w_up, w_down, activation, residual, kept, bits, y, workspace, stream):
+    lib = load()
+    dev, raw = _launch_on(stream, x)
+    xp, ldx, tokens, hidden = _matrix("x", x, dev)
+    ffn, wp = _gated_weights(w_gate, w_up, w_down, hidden, dev)
+    act = _activation(activation)
+    rp, ldr = None, 0
+    if residual is not None:
+        rp, ldr, _, _ = _matrix("residual", residual, dev, hidden, tokens)
+    if y is None:
+        y = _new(x, x.shape, stream)
+    yp, ldy, _, _ = _matrix("y", y, dev, hidden, tokens)
+    kp = ke = None
+    if bits == 16:
+        if kept is None:
+            kept = _new(x, (tokens, 2 * ffn), stream)
+        kp = _whole("kept", kept, (tokens, 2 * ffn), dev)
+    elif bits == 8:
+        if kept is None:
+            kept = (_new(x, (tokens, 2 * ffn), stream, torch.int8),
+                    _new(x, (tokens, ffn // 16), stream, torch.uint8))
+        kp, ke = _kept_pair(kept, tokens, ffn, dev)
+    ws, wsp, wsb = _scratch(_gated_workspace(dev, tokens, hidden, ffn), workspace, x, dev, stream)
+    st = lib.ptb_gated_ffn(xp, ldx, *wp, rp, ldr, tokens, hidden, ffn, act, yp, ldy, kp, ke, wsp,
+                           wsb, raw)
+    if st:
+        _check(st, "ptb_gated_ffn")
+    return y, kept
+
+
+def _kept_pair(kept, tokens: int, ffn: int, dev: int) -> tuple:
+    if not isinstance(kept, tuple) or len(kept) != 2:
+        raise TypeError("kept must be a pair (codes, exps)")
+    return (_whole("kept's codes", kept[0], (tokens, 2 * ffn), dev, torch.int8),
+            _whole("kept's exps", kept[1], (tokens, ffn // 16), dev, torch.uint8))
+
+
+def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", residual=None, y=None,
+              workspace=None, stream=None) -> torch.Tensor:
+    """y = [residual +] (act(x w_gate^T) * (x w_up^T)) w_down^T for x [..., hidden] bf16,
+    w_gate, w_up [ffn, hidden], w_down [hidden, ffn]; activation "silu" or "gelu" (tanh).  y may be
+    x or residual."""
+    return _gated_forward(x, w_gate, w_up, w_down, activation, residual, None, 0, y, workspace,
+                          stream)[0]
+
+
+def gated_ffn_train(x, w_gate, w_up, w_down, activation: str = "silu", bits: int = 16,
+                    residual=None, y=None, kept=None, workspace=None, stream=None) -> tuple:
+    """gated_ffn that also keeps what gated_ffn_backward reads; returns (y, kept).  kept: gate and up
+    [tokens, 2 ffn], bf16 with bits = 16, a checkpoint (codes, exps) with bits = 8."""
+    if bits not in (8, 16):
+        raise ValueError("bits must be 8 or 16")
+    return _gated_forward(x, w_gate, w_up, w_down, activation, residual, kept, bits, y, workspace,
+                          stream)
+
+
+def gated_ffn_backward(dy, x, w_gate, w_up, w_down, kept, activation: str = "silu",
+                       grad_dtype=torch.bfloat16, grads=None, workspace=None, stream=None) -> dict:
+    """Gradients of gated_ffn for the upstream dy: dx (bf16), dw_gate, dw_up, dw_down (grad_dtype
+    bfloat16 or float32), as a dict, or written into `grads`, a dict of tensors with those keys.
+    kept from gated_ffn_train; x bf16 or a checkpoint of it.  dx may be dy or x."""
+    lib = load()
+    dev, raw = _launch_on(stream, dy)
+    dyp, lddy, tokens, hidden = _matrix("dy", dy, dev)
+    xp, ldx, xe, ldxe, _, _ = _either("x", x, dev, hidden, tokens)
+    ffn, wp = _gated_weights(w_gate, w_up, w_down, hidden, dev)
+    act = _activation(activation)
+    if isinstance(kept, tuple):
+        kp, ke = _kept_pair(kept, tokens, ffn, dev)
+    else:
+        kp, ke = _whole("kept", kept, (tokens, 2 * ffn), dev), None
+    if grads is None:
+        grads = dict(dx=_new(dy, dy.shape, stream), dw_gate=_new(dy, (ffn, hidden), stream, grad_dtype),
+                     dw_up=_new(dy, (ffn, hidden), stream, grad_dtype),
+                     dw_down=_new(dy, (hidden, ffn), stream, grad_dtype))
+    else:
+        grad_dtype = grads["dw_gate"].dtype
+    if grad_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("weight gradients are bfloat16 or float32")
+    dxp, lddx, _, _ = _matrix("dx", grads["dx"], dev, hidden, tokens)
+    gp = (_whole("dw_gate", grads["dw_gate"], (ffn, hidden), dev, grad_dtype),
+          _whole("dw_up", grads["dw_up"], (ffn, hidden), dev, grad_dtype),
+          _whole("dw_down", grads["dw_down"], (hidden, ffn), dev, grad_dtype))
+    ws, wsp, wsb = _scratch(_gated_backward_workspace(dev, tokens, hidden, ffn, 16 if xe is None else 8),
+                            workspace, dy, dev, stream)
+    st = lib.ptb_gated_ffn_backward(dyp, lddy, xp, ldx, xe, ldxe, *wp, kp, ke, tokens, hidden, ffn,
+                                    act, dxp, lddx, *gp, 16 if grad_dtype is torch.bfloat16 else 32,
+                                    wsp, wsb, raw)
+    if st:
+        _check(st, "ptb_gated_ffn_backward")
+    return grads
+
+
+def _gate(gate, rows: int, hidden: int, dev: int) -> tuple:
+    """(pointer, gates) of a gate [hidden] or [gates, hidden]."""
+    if gate is None:
+        return None, 1
+    _tensor("gate", gate, torch.bfloat16, dev)
+    size = gate.shape
+    if len(size) not in (1, 2) or size[-1] != hidden or not gate.is_contiguous():
+        raise ValueError(f"gate must be contiguous [{hidden}] or [gates, {hidden}]")
+    gates = size[0] if len(size) == 2 else 1
+    if gates < 1 or rows % gates:
+        raise ValueError(f"{gates} gates do not divide {rows} rows")
+    return gate.data_ptr(), gates
+
+
+def norm_residual_backward_workspace_size(rows: int, hidden: int, gates: int = 1) -> int:
+    return int(load().ptb_norm_residual_backward_workspace_size(rows, hidden, gates))
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_workspace(dev: int, rows: int, hidden: int, gates: int) -> int:
+    return norm_residual_backward_workspace_size(rows, hidden, gates)
+
+
+def _norm_forward(x, o, post_gamma, post_beta, gate, alpha, pre_gamma, pre_beta, rms, eps, y, h,
+                  stats, keep, stream):
+    lib = load()
+    dev, raw = _launch_on(stream, x)
+    xp, ldx, rows, hidden = _matrix("x", x, dev)
+    op, ldo, _, _ = _matrix("o", o, dev, hidden, rows)
+    gp, gates = _gate(gate, rows, hidden, dev)
+    if y is None:
+        y = _new(x, x.shape, stream)
+    yp, ldy, _, _ = _matrix("y", y, dev, hidden, rows)
+    hp, ldh = None, 0
+    if pre_gamma is not None:
+        if h is None:
+            h = _new(x, x.shape, stream)
+        hp, ldh, _, _ = _matrix("h", h, dev, hidden, rows)
+    elif h is not None:
+        raise ValueError("h without pre_gamma")
+    sp = None
+    if keep:
+        if stats is None:
+            stats = _new(x, (rows, 4), stream, torch.float32)
+        sp = _whole("stats", stats, (rows, 4), dev, torch.float32)
+    st = lib.ptb_norm_residual(xp, ldx, op, ldo, _vector("post_gamma", post_gamma, hidden, dev),
+                               _vector("post_beta", post_beta, hidden, dev), gp, gates, alpha,
+                               _vector("pre_gamma", pre_gamma, hidden, dev),
+                               _vector("pre_beta", pre_beta, hidden, dev), int(rms), eps, rows,
+                               hidden, yp, ldy, hp, ldh, sp, raw)
+    if st:
+        _check(st, "ptb_norm_residual")
+    return y, h, stats
+
+
+def norm_residual(x, o, post_gamma=None, post_beta=None, gate=None, alpha: float = 1.0,
+                  pre_gamma=None, pre_beta=None, rms: bool = False, eps: float = 1e-5, y=None,
+                  h=None, stream=None) -> tuple:
+    """The residual stream x after a block with output o, and the next block's input:
+    y = alpha x + gate * (N(o) post_gamma + post_beta), h = N(y) pre_gamma + pre_beta, N the layer
+    norm or the rms norm.  Without post_gamma o itself is added, without gate it is 1, without
+    pre_gamma h is None.  gate [hidden], or [gates, hidden] for rows / gates rows in a row each.
+    Returns (y, h); both may be x or o."""
+    return _norm_forward(x, o, post_gamma, post_beta, gate, alpha, pre_gamma, pre_beta, rms, eps, y,
+                         h, None, False, stream)[:2]
+
+
+def norm_residual_train(x, o, post_gamma=None, post_beta=None, gate=None, alpha: float = 1.0,
+                        pre_gamma=None, pre_beta=None, rms: bool = False, eps: float = 1e-5, y=None,
+                        h=None, stats=None, stream=None) -> tuple:
+    """norm_residual that also keeps its rows' statistics for norm_residual_backward; returns
+    (y, h, stats [rows, 4] fp32)."""
+    return _norm_forward(x, o, post_gamma, post_beta, gate, alpha, pre_gamma, pre_beta, rms, eps, y,
+                         h, stats, True, stream)
+
+
+def norm_residual_backward(dy, dh, y, o, stats, post_gamma=None, post_beta=None, gate=None,
+                           alpha: float = 1.0, pre_gamma=None, pre_beta=None, rms: bool = False,
+                           grads=None, workspace=None, stream=None) -> dict:
+    """Gradients of norm_residual for those of y (dy; None: zero) and h (dh; with pre_gamma): dx and
+    do (bf16) and, for the parameters that are given, dpost_gamma, dpost_beta, dgate, dpre_gamma,
+    dpre_beta (fp32), as a dict, or written into the tensors of `grads`, a dict with those keys.
+    y and stats as norm_residual_train left them, o bf16 or a checkpoint of it."""
+    lib = load()
+    main = dh if dy is None else dy
+    dev, raw = _launch_on(stream, main)
+    _, _, rows, hidden = _matrix("dy" if dy is not None else "dh", main, dev)
+    dyp, lddy = (None, 0) if dy is None else _matrix("dy", dy, dev)[:2]
+    dhp = yp = None
+    lddh = ldy = 0
+    if pre_gamma is not None:
+        dhp, lddh, _, _ = _matrix("dh", dh, dev, hidden, rows)
+        yp, ldy, _, _ = _matrix("y", y, dev, hidden, rows)
+    elif dh is not None:
+        raise ValueError("dh without pre_gamma")
+    op, ldo, oe, ldoe, _, _ = _either("o", o, dev, hidden, rows)
+    gp, gates = _gate(gate, rows, hidden, dev)
+    sp = _whole("stats", stats, (rows, 4), dev, torch.float32)
+    own = grads is None
+    if own:
+        grads = dict(dx=_new(main, main.shape, stream), do=_new(main, main.shape, stream))
+    out = []
+    for name, t in (("post_gamma", post_gamma), ("post_beta", post_beta), ("gate", gate),
+                    ("pre_gamma", pre_gamma), ("pre_beta", pre_beta)):
+        key = "d" + name
+        if t is None:
+            out.append(None)
+            continue
+        if name != "gate":
+            _vector(name, t, hidden, dev)
+        if own:
+            grads[key] = _new(main, t.shape, stream, torch.float32)
+        g = grads.get(key)
+        out.append(None if g is None else _whole(key, g, tuple(t.shape), dev, torch.float32))
+    dxp, lddx, _, _ = _matrix("dx", grads["dx"], dev, hidden, rows)
+    dop, lddo, _, _ = _matrix("do", grads["do"], dev, hidden, rows)
+    ws, wsp, wsb = _scratch(_norm_workspace(dev, rows, hidden, gates), workspace, main, dev, stream)
+    st = lib.ptb_norm_residual_backward(
+        dyp, lddy, dhp, lddh, yp, ldy, op, ldo, oe, ldoe, sp,
+        _vector("post_gamma", post_gamma, hidden, dev), _vector("post_beta", post_beta, hidden, dev),
+        gp, gates, alpha, _vector("pre_gamma", pre_gamma, hidden, dev), int(rms), rows, hidden, dxp,
+        lddx, dop, lddo, *out, wsp, wsb, raw)
+    if st:
+        _check(st, "ptb_norm_residual_backward")
+    return grads
 
 
 def host_workspace_size(batch: int, seq: int, hidden: int, ffn: int) -> int:

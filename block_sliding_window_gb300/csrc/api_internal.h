@@ -113,6 +113,11 @@ struct GemmCall {
   ptb_bf16* aux = nullptr;
   int64_t ld_aux = 0;
   int64_t gelu_col = 0;
+  // kEpiGated (K-major; b0, b1 are the weights [N / 2, K] of gate and up) and kEpiDgated.
+  int act = 0;
+  int64_t ffn = 0;
+  void* kept = nullptr;
+  uint8_t* kept_exps = nullptr;
   int block_n() const {
     return n_split ? pick_block_n(n_split, N - n_split) : pick_block_n(N, N);
   }
@@ -123,6 +128,10 @@ struct GemmCall {
 size_t call_scratch(const GemmCall& c, int sms);
 ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t scratch_bytes,
                      cudaStream_t stream);
+
+// Split-wave scratch of a forward GEMM.
+size_t spec_scratch(const GemmSpec& g, int64_t tokens, int sms);
+ptb_status check_gemm_shape(int64_t tokens, int64_t hidden, int64_t ffn);
 
 // Split-wave scratch of the layer's GEMMs (the largest of them).
 size_t layer_gemm_scratch(int64_t tokens, int64_t hidden, int64_t ffn, int sms);

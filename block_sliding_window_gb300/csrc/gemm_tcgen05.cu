@@ -37,6 +37,8 @@
 //
 // Every mbarrier wait is bounded (see mbar_wait); on a timeout all roles
 // unwind, wait for their own copies and MMAs, free TMEM and return.
+#include "checkpoint_device.cuh"
+#include "gated_device.cuh"
 #include "ptb_device.cuh"
 
 namespace ptb {
@@ -79,12 +81,6 @@ struct Cfg {
   static constexpr int kSmemBytes =
       kStages * kStageBytes + kBarBytes + (STAGE ? kF32StageBytes : 0) + 1024;
 };
-
-__device__ __forceinline__ float gelu_tanh(float z) {
-  const float k0 = 0.7978845608028654f;  // sqrt(2 / pi)
-  const float k1 = 0.044715f;
-  return 0.5f * z * (1.0f + tanhf(k0 * (z + k1 * z * z * z)));
-}
 
 // One unit of work: k-blocks [kb0, kb1) of one output tile.  slot >= 0 marks
 // a K piece of a remainder tile (its index in the partial-tile buffer).
@@ -141,15 +137,6 @@ __device__ __forceinline__ void dequantize(const GemmArgs& p, int row, int col, 
   }
 }
 
-// d/dz gelu_tanh(z) = 0.5 (1 + t) + 0.5 z (1 - t^2) c (1 + 3 a z^2),
-// t = tanh(c (z + a z^3)), c = sqrt(2 / pi), a = 0.044715.
-__device__ __forceinline__ float gelu_tanh_grad(float z) {
-  const float k0 = 0.7978845608028654f;
-  const float k1 = 0.044715f;
-  const float t = tanhf(k0 * (z + k1 * z * z * z));
-  return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * k0 * (1.0f + 3.0f * k1 * z * z);
-}
-
 __device__ __forceinline__ void store_bf16x32(__nv_bfloat16* dst_row, const uint32_t (&packed)[16]) {
   uint4* dst = reinterpret_cast<uint4*>(dst_row);
 #pragma unroll
@@ -182,7 +169,10 @@ __device__ __forceinline__ void store_chunk(const GemmArgs& p, int row, int col,
     return;
   }
   uint32_t packed[16];
-  if constexpr (EPI == kEpiQkvGelu) {
+  if constexpr (EPI == kEpiBf16) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(acc[2 * j], acc[2 * j + 1]);
+  } else if constexpr (EPI == kEpiQkvGelu) {
     if (col >= p.gelu_col) {
       if (p.aux) {  // keep the pre-activation for the backward pass
 #pragma unroll
@@ -228,6 +218,82 @@ __device__ __forceinline__ void store_chunk(const GemmArgs& p, int row, int col,
     }
   }
   store_bf16x32(static_cast<__nv_bfloat16*>(base) + r * ld + c, packed);
+}
+
+__device__ __forceinline__ void pack_row(const float (&v)[32], uint32_t (&packed)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+}
+
+// Forward of a gated feed-forward, 32 columns of one row: gate g and up u (fp32 accumulators) ->
+// act(g) * u, rounded once; what the backward pass keeps is rounded from the accumulators, too.
+__device__ __forceinline__ void store_gated(const GemmArgs& p, int row, int col,
+                                            const float (&g)[32], const float (&u)[32]) {
+  uint32_t packed[16];
+  if (p.kept) {
+    const int64_t at = static_cast<int64_t>(row) * 2 * p.ffn + col;
+    if (p.kept_exps) {
+      uint8_t* codes = static_cast<uint8_t*>(p.kept);
+      ckpt_store_group(g, codes + at, p.kept_exps + at / kCkptGroup);
+      ckpt_store_group(u, codes + at + p.ffn, p.kept_exps + (at + p.ffn) / kCkptGroup);
+    } else {
+      __nv_bfloat16* kept = static_cast<__nv_bfloat16*>(p.kept);
+      pack_row(g, packed);
+      store_bf16x32(kept + at, packed);
+      pack_row(u, packed);
+      store_bf16x32(kept + at + p.ffn, packed);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    packed[j] = pack_bf16x2(gated_act(g[2 * j], p.act) * u[2 * j],
+                            gated_act(g[2 * j + 1], p.act) * u[2 * j + 1]);
+  store_bf16x32(static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + col, packed);
+}
+
+__device__ __forceinline__ void load_bf16x32(const __nv_bfloat16* src_row, float (&v)[32]) {
+  const uint4* src = reinterpret_cast<const uint4*>(src_row);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint4 q = __ldg(src + k);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[8 * k + 2 * j] = bf16_lo(w[j]);
+      v[8 * k + 2 * j + 1] = bf16_hi(w[j]);
+    }
+  }
+}
+
+// Backward of act(g) * u for its gradient d, 32 columns of one row, g and u as they were kept:
+// act(g) * u once more for the weight gradient of the down projection, d u act'(g) and d act(g).
+__device__ __forceinline__ void store_dgated(const GemmArgs& p, int row, int col,
+                                             const float (&d)[32]) {
+  float g[32], u[32];
+  const int64_t at = static_cast<int64_t>(row) * 2 * p.ffn + col;
+  if (p.kept_exps) {
+    const uint8_t* codes = static_cast<const uint8_t*>(p.kept);
+    ckpt_load_group(codes + at, p.kept_exps + at / kCkptGroup, g);
+    ckpt_load_group(codes + at + p.ffn, p.kept_exps + (at + p.ffn) / kCkptGroup, u);
+  } else {
+    const __nv_bfloat16* kept = static_cast<const __nv_bfloat16*>(p.kept);
+    load_bf16x32(kept + at, g);
+    load_bf16x32(kept + at + p.ffn, u);
+  }
+  uint32_t pa[16], pg[16], pu[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float a0, s0, a1, s1;
+    gated_act_grad(g[2 * j], p.act, a0, s0);
+    gated_act_grad(g[2 * j + 1], p.act, a1, s1);
+    pa[j] = pack_bf16x2(a0 * u[2 * j], a1 * u[2 * j + 1]);
+    pg[j] = pack_bf16x2(d[2 * j] * u[2 * j] * s0, d[2 * j + 1] * u[2 * j + 1] * s1);
+    pu[j] = pack_bf16x2(d[2 * j] * a0, d[2 * j + 1] * a1);
+  }
+  store_bf16x32(static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + col, pa);
+  __nv_bfloat16* out1 = static_cast<__nv_bfloat16*>(p.out1) + row * p.ld_out1 + col;
+  store_bf16x32(out1, pg);
+  store_bf16x32(out1 + p.ffn, pu);
 }
 
 // Output tile origin of tile index t (M index fastest, or N index fastest).
@@ -280,6 +346,26 @@ __device__ __forceinline__ void store_chunk_f32_warp(const GemmArgs& p, int row,
   __syncwarp();
 }
 
+// Sum of the K pieces' partials of 32 columns of a row, in piece order.
+template <int BN, int ROWS>
+__device__ __forceinline__ void sum_pieces(const GemmArgs& p, int group0, int prow, int c,
+                                           float (&acc)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) acc[j] = 0.f;
+  for (int s = 0; s < p.split_s; ++s) {
+    const float4* src = reinterpret_cast<const float4*>(
+        p.partials + (static_cast<int64_t>(group0 + s) * ROWS + prow) * BN + c);
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const float4 q = __ldcg(src + v);
+      acc[4 * v] += q.x;
+      acc[4 * v + 1] += q.y;
+      acc[4 * v + 2] += q.z;
+      acc[4 * v + 3] += q.w;
+    }
+  }
+}
+
 // The epilogue of one unit for one thread's output row `row`: a whole tile
 // goes straight from TMEM through store_chunk; a K piece of a split tile
 // publishes its fp32 partial (row `prow` of the ROWS-row partial tile) and
@@ -316,6 +402,31 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
     finish = prev == static_cast<unsigned>(p.split_s - 1);
     if (finish) __threadfence();
   }
+  if constexpr (EPI == kEpiGated) {
+    // Columns c and BN / 2 + c of the tile are gate and up of output column n0 / 2 + c.
+    if (finish) {
+      const int group0 = u.slot < 0 ? 0 : (u.slot / p.split_s) * p.split_s;
+#pragma unroll 1
+      for (int c = 0; c < BN / 2; c += 32) {
+        float v[2][32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int at = h * (BN / 2) + c;
+          if (u.slot < 0) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(t_row + at, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[h][j] = __uint_as_float(r[j]);
+          } else {
+            sum_pieces<BN, ROWS>(p, group0, prow, at, v[h]);
+          }
+        }
+        if (row < p.M) store_gated(p, row, n0 / 2 + c, v[0], v[1]);
+      }
+    }
+    return;
+  }
   if (finish && u.slot < 0) {
 #pragma unroll 1
     for (int c = 0; c < BN; c += 32) {
@@ -328,8 +439,12 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
       if constexpr (FP8) dequantize(p, row, n0 + c, acc);
       if constexpr (STAGE)
         store_chunk_f32_warp(p, row, n0 + c, acc, lane, f32_stage);
-      else if (row < p.M)
-        store_chunk<EPI>(p, row, n0 + c, acc);
+      else if (row < p.M) {
+        if constexpr (EPI == kEpiDgated)
+          store_dgated(p, row, n0 + c, acc);
+        else
+          store_chunk<EPI>(p, row, n0 + c, acc);
+      }
     }
   } else if (finish) {
     // Sum every piece's partial (this warp's own included) in piece order,
@@ -338,25 +453,16 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
 #pragma unroll 1
     for (int c = 0; c < BN; c += 32) {
       float acc[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) acc[j] = 0.f;
-      for (int s = 0; s < p.split_s; ++s) {
-        const float4* src = reinterpret_cast<const float4*>(
-            p.partials + (static_cast<int64_t>(group0 + s) * ROWS + prow) * BN + c);
-#pragma unroll
-        for (int v = 0; v < 8; ++v) {
-          const float4 q = __ldcg(src + v);
-          acc[4 * v] += q.x;
-          acc[4 * v + 1] += q.y;
-          acc[4 * v + 2] += q.z;
-          acc[4 * v + 3] += q.w;
-        }
-      }
+      sum_pieces<BN, ROWS>(p, group0, prow, c, acc);
       if constexpr (FP8) dequantize(p, row, n0 + c, acc);
       if constexpr (STAGE)
         store_chunk_f32_warp(p, row, n0 + c, acc, lane, f32_stage);
-      else if (row < p.M)
-        store_chunk<EPI>(p, row, n0 + c, acc);
+      else if (row < p.M) {
+        if constexpr (EPI == kEpiDgated)
+          store_dgated(p, row, n0 + c, acc);
+        else
+          store_chunk<EPI>(p, row, n0 + c, acc);
+      }
     }
   }
 }
@@ -466,6 +572,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             for (int h = 0; h < BN / 64; ++h)
               tma_load_2d(stage_b(stage) + h * kMnBlock, bmap, &full_bar[stage], by + 64 * h, kx,
                           pol_b);
+          } else if constexpr (EPI == kEpiGated) {
+            // Rows n0 / 2 .. of the gate's weights, then the same rows of up's.
+            tma_load_2d(stage_b(stage), &p.b0, &full_bar[stage], kx, n0 / 2, pol_b);
+            tma_load_2d(stage_b(stage) + BN / 2 * 128, &p.b1, &full_bar[stage], kx, n0 / 2, pol_b);
           } else {
             tma_load_2d(stage_b(stage), bmap, &full_bar[stage], kx, by, pol_b);
           }
@@ -723,6 +833,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int h = 0; h < BN / 128; ++h)
               tma_load_2d_pair(stage_b(stage) + h * kMnBlock, bmap, leader_full, by + 64 * h, kx,
                                pol_b);
+          } else if constexpr (EPI == kEpiGated) {
+            // Rank 0 brings the gate's rows, rank 1 the same rows of up.
+            tma_load_2d_pair(stage_b(stage), rank == 0 ? &p.b0 : &p.b1, leader_full, kx, n0 / 2,
+                             pol_b);
           } else {
             tma_load_2d_pair(stage_b(stage), bmap, leader_full, kx, by, pol_b);
           }
@@ -932,8 +1046,16 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
       return launch_pair<kEpiQkvGelu, kLayoutKK>(a, stream);
     if (a.layout == kLayoutKK && a.epilogue == kEpiResidual)
       return launch_pair<kEpiResidual, kLayoutKK>(a, stream);
+    if (a.layout == kLayoutKK && a.epilogue == kEpiGated)
+      return launch_pair<kEpiGated, kLayoutKK>(a, stream);
     if (a.layout == kLayoutKN && a.epilogue == kEpiDgelu)
       return launch_pair<kEpiDgelu, kLayoutKN>(a, stream);
+    if (a.layout == kLayoutKN && a.epilogue == kEpiDgated)
+      return launch_pair<kEpiDgated, kLayoutKN>(a, stream);
+    if (a.layout == kLayoutKN && a.epilogue == kEpiBf16)
+      return launch_pair<kEpiBf16, kLayoutKN>(a, stream);
+    if (a.layout == kLayoutNN && a.epilogue == kEpiBf16)
+      return launch_pair<kEpiBf16, kLayoutNN>(a, stream);
     if (a.layout == kLayoutKN && a.epilogue == kEpiF32)
       return launch_pair<kEpiF32, kLayoutKN>(a, stream);
     if (a.layout == kLayoutNN && a.epilogue == kEpiF32)
@@ -949,16 +1071,25 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
     if (a.epilogue == kEpiResidual)
       return a.fp8 ? launch_bn<kEpiResidual, true, kLayoutKK>(a, stream)
                    : launch_bn<kEpiResidual, false, kLayoutKK>(a, stream);
+    if (a.epilogue == kEpiGated && !a.fp8) {
+      // Half of a tile's columns are the gate's: tiles of 64 would leave 32 rows of weights a box.
+      if (a.block_n == 256) return launch_typed<256, kEpiGated, false, kLayoutKK>(a, stream);
+      if (a.block_n == 128) return launch_typed<128, kEpiGated, false, kLayoutKK>(a, stream);
+    }
     return cudaErrorInvalidValue;
   }
   if (a.fp8) return cudaErrorInvalidValue;
   if (a.layout == kLayoutKN) {
     if (a.epilogue == kEpiDgelu) return launch_bn<kEpiDgelu, false, kLayoutKN>(a, stream);
+    if (a.epilogue == kEpiDgated) return launch_bn<kEpiDgated, false, kLayoutKN>(a, stream);
+    if (a.epilogue == kEpiBf16) return launch_bn<kEpiBf16, false, kLayoutKN>(a, stream);
     if (a.epilogue == kEpiF32) return launch_bn<kEpiF32, false, kLayoutKN>(a, stream);
     return cudaErrorInvalidValue;
   }
   if (a.layout == kLayoutNN && a.epilogue == kEpiF32)
     return launch_bn<kEpiF32, false, kLayoutNN>(a, stream);
+  if (a.layout == kLayoutNN && a.epilogue == kEpiBf16)
+    return launch_bn<kEpiBf16, false, kLayoutNN>(a, stream);
   return cudaErrorInvalidValue;
 }
 

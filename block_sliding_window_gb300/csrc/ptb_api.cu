@@ -316,7 +316,10 @@ ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t s
   // N extent is its N part under an N split, else N.
   const int64_t bk0 = c.k_split ? k0 : c.K, bk1 = c.k_split ? k1 : c.K;
   const int64_t bn0 = c.n_split ? n0 : c.N, bn1 = c.n_split ? n1 : c.N;
-  if (bmn)
+  if (c.epilogue == kEpiGated)  // half of a tile's rows from each; a pair's CTAs load one half each
+    ok = ok && make_map(&a.b0, c.b0, c.K, c.N / 2, c.ldb0, a.block_n / 2) &&
+         make_map(&a.b1, c.b1, c.K, c.N / 2, c.ldb0, a.block_n / 2);
+  else if (bmn)
     ok = ok && make_map_mn(&a.b0, c.b0, bn0, bk0, c.ldb0) && make_map_mn(&a.b1, b1, bn1, bk1, ldb1);
   else
     ok = ok && make_map(&a.b0, c.b0, bk0, bn0, c.ldb0, box_b) &&
@@ -346,6 +349,10 @@ ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t s
   a.aux = c.aux ? bf(c.aux) : nullptr;
   a.ld_aux = c.ld_aux;
   a.gelu_col = static_cast<int>(c.gelu_col ? c.gelu_col : c.N);
+  a.act = c.act;
+  a.ffn = static_cast<int>(c.ffn);
+  a.kept = c.kept;
+  a.kept_exps = c.kept_exps;
   apply_plan(a, c.kb(), ds->sms, scratch, scratch_bytes);
   a.status = ds->status;
   return launch_status(launch_gemm(a, stream));

@@ -19,7 +19,15 @@ enum GemmEpilogue : int {
   kEpiDgelu = 2,     // columns >= gelu_col store bf16(acc * gelu_tanh'(aux[row, col - gelu_col])),
                      // the others bf16(acc)
   kEpiF32 = 3,       // store fp32 acc
+  kEpiBf16 = 4,      // store bf16(acc)
+  kEpiGated = 5,     // a tile holds block_n / 2 columns of the gate and the same of up: store
+                     // bf16(act(gate) * up); with kept set, also gate and up themselves
+  kEpiDgated = 6,    // acc is the gradient of act(gate) * up: store bf16(act(gate) * up) (out) and
+                     // the gradients of gate and up (out1, two halves), gate and up from kept
 };
+
+// Activation of a gated feed-forward (ptb.h).
+enum GatedAct : int { kActSilu = 0, kActGelu = 1 };
 
 // Operand layouts in shared memory (bit 0: A, bit 1: B).  K-major: the
 // stored matrix is [M or N rows][K]; MN-major: it is [K rows][M or N], so the
@@ -73,6 +81,12 @@ struct GemmArgs {
   int fp8;
   const float* a_scale;
   const float* b_scale;
+  // Gated epilogues: gate and up of each row, [M, 2 ffn], gate first: bf16, or, with kept_exps
+  // set, a checkpoint's codes and exponents.
+  int act;
+  int ffn;
+  void* kept;
+  uint8_t* kept_exps;
 };
 
 // Each K piece of a split tile keeps at least this many 64-wide k-blocks.
@@ -194,6 +208,50 @@ size_t swa_packed_workspace(int batch, int64_t tokens_q, int heads, int kv_heads
 cudaError_t launch_swa_packed(const SwaPackedArgs& a, cudaStream_t stream);
 size_t swa_paged_workspace(int batch, int heads, int kv_heads, int head_dim, int sms);
 cudaError_t launch_swa_paged(const SwaPagedArgs& a, cudaStream_t stream);
+
+// -------------------------------------------- blocks with gates and norms --
+
+struct CheckpointArgs {
+  const __nv_bfloat16* x;   // pack
+  __nv_bfloat16* x_out;     // unpack
+  uint8_t *codes, *exps;
+  int64_t ld_x, ld_codes, ld_exps;
+  int64_t rows, cols;
+  int sms;
+};
+
+// y = alpha x + gate * N(o), h = N(y) (ptb_norm_residual), and its backward.
+struct NormArgs {
+  const __nv_bfloat16 *x, *o;
+  int64_t ld_x, ld_o;
+  const uint8_t* o_exps;  // backward: not null when o is a checkpoint's codes
+  int64_t ld_o_exps;
+  const __nv_bfloat16 *post_gamma, *post_beta, *pre_gamma, *pre_beta;
+  const __nv_bfloat16* gate;
+  int64_t gates;
+  float alpha, eps;
+  int rms;
+  int64_t rows;
+  int hidden;
+  __nv_bfloat16 *y, *h;  // forward
+  int64_t ld_y, ld_h;
+  float4* stats;         // (mean, 1/sd) of o and of y, per row
+  // backward
+  const __nv_bfloat16 *dy, *dh;
+  int64_t ld_dy, ld_dh;
+  __nv_bfloat16 *dx, *d_o;
+  int64_t ld_dx, ld_do;
+  float *dpost_gamma, *dpost_beta, *dgate, *dpre_gamma, *dpre_beta;
+  float* partials;
+  int sms;
+};
+
+cudaError_t launch_checkpoint_pack(const CheckpointArgs& a, cudaStream_t stream);
+cudaError_t launch_checkpoint_unpack(const CheckpointArgs& a, cudaStream_t stream);
+cudaError_t launch_norm_residual(const NormArgs& a, cudaStream_t stream);
+// Bytes of NormArgs::partials.
+size_t norm_backward_partials(int64_t rows, int64_t hidden, int64_t gates, int sms);
+cudaError_t launch_norm_residual_backward(const NormArgs& a, cudaStream_t stream);
 
 cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream);
 cudaError_t launch_layernorm(const __nv_bfloat16* x, const __nv_bfloat16* gamma,

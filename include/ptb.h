@@ -584,6 +584,141 @@ ptb_status swa_attention_paged(const ptb_bf16* q, int64_t q_sb, int64_t q_sh, co
                                size_t workspace_bytes, ptb_stream stream);
 
 /*
+ * ----------------------------------- gated feed-forward, norms, checkpoints --
+ * The parts of a block whose MLP is gated and whose norms stand on both sides
+ * of it, next to ptb_gemm_qkv_up / ptb_gemm_out_down and ptb_layernorm: they
+ * answer and they train.  Matrices have rows of contiguous elements and a row
+ * stride ld (elements, a multiple of 8, at least the row's length; the stride
+ * of a single row is not used).  Parameter vectors are contiguous.  A call with
+ * no rows writes nothing but the (zero) gradients of its parameters.  Sums run
+ * in a fixed order: the same bits on every call on one kind of device.
+ *
+ * 8-bit checkpoints hold what a backward pass reads again, in half the memory:
+ * groups of 32 neighbouring elements of a row share a power-of-two scale.
+ *   codes [rows, cols] int8, row stride a multiple of 16 bytes
+ *   exps  [rows, cols / 32] uint8, any row stride from cols / 32 on
+ * Code c of a group with exponent byte E stands for c * 2^(E - 127).  With m
+ * the group's largest magnitude, 2^(E - 127) is the smallest power of two with
+ * m < 127.5 * 2^(E - 127), at least 2^-126; c is the element divided by it,
+ * rounded to nearest, ties to even: off by at most half a step.  A group with a
+ * value that is not finite or with m >= 255 * 2^120 gets E = 255 and reads back
+ * as NaN.  Every value that a code stands for is a bf16 number, so unpacking
+ * rounds nothing.
+ *
+ * ptb_checkpoint_pack: x [rows, cols] bf16 -> codes, exps.
+ * ptb_checkpoint_unpack: codes, exps -> x.  cols a multiple of 32.
+ */
+ptb_status ptb_checkpoint_pack(const ptb_bf16* x, int64_t ld_x, int64_t rows, int64_t cols,
+                               void* codes, int64_t ld_codes, uint8_t* exps, int64_t ld_exps,
+                               ptb_stream stream);
+ptb_status ptb_checkpoint_unpack(const void* codes, int64_t ld_codes, const uint8_t* exps,
+                                 int64_t ld_exps, int64_t rows, int64_t cols, ptb_bf16* x,
+                                 int64_t ld_x, ptb_stream stream);
+
+/*
+ * ptb_gated_ffn: y = [residual +] (act(x w_gate^T) * (x w_up^T)) w_down^T.
+ *   x, y, residual [tokens, hidden] bf16, strided; residual may be NULL; y may
+ *        be x or residual itself (residual: at the same stride)
+ *   w_gate, w_up   [ffn, hidden], w_down [hidden, ffn] bf16, contiguous
+ *   activation     0: SiLU, z / (1 + e^-z); 1: tanh-GELU
+ *   kept           NULL, or what the backward pass reads: gate and up (before
+ *        the activation) side by side, [tokens, 2 * ffn] contiguous, rounded
+ *        from the fp32 accumulators to bf16 or, with kept_exps
+ *        [tokens, 2 * ffn / 32], to the codes of a checkpoint
+ *   workspace      at least ptb_gated_ffn_workspace_size() bytes (it depends on
+ *        the current device's SM count; 0 for tokens = 0 and for shapes that
+ *        are refused), 256-byte aligned; calls that may run at the same time
+ *        need one each
+ * hidden and ffn multiples of 64.  One GEMM forms both projections, the
+ * activation and the product, rounded once to bf16; a second one is the down
+ * projection.
+ */
+size_t ptb_gated_ffn_workspace_size(int64_t tokens, int64_t hidden, int64_t ffn);
+ptb_status ptb_gated_ffn(const ptb_bf16* x, int64_t ld_x, const ptb_bf16* w_gate,
+                         const ptb_bf16* w_up, const ptb_bf16* w_down, const ptb_bf16* residual,
+                         int64_t ld_residual, int64_t tokens, int64_t hidden, int64_t ffn,
+                         int32_t activation, ptb_bf16* y, int64_t ld_y, void* kept,
+                         uint8_t* kept_exps, void* workspace, size_t workspace_bytes,
+                         ptb_stream stream);
+
+/*
+ * ptb_gated_ffn_backward: gradients of the feed-forward for the upstream dy
+ * (the residual's gradient is dy itself).  With g, u the kept gate and up, as
+ * the values that they were rounded to:
+ *   a = act(g) * u,  da = dy w_down,  dg = da * u * act'(g),  du = da * act(g),
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x,
+ *   dw_down = dy^T a.
+ * a, dg and du are rounded to bf16 between the GEMMs.
+ *   x        [tokens, hidden] bf16, or with x_exps a checkpoint's codes
+ *   kept, kept_exps  as ptb_gated_ffn left them
+ *   dx       bf16; may be dy or (bf16) x itself
+ *   dw_gate, dw_up [ffn, hidden], dw_down [hidden, ffn]: grad_bits 32 fp32,
+ *            16 bf16; overwritten, not accumulated
+ *   workspace  at least ptb_gated_ffn_backward_workspace_size() bytes (x_bits
+ *            16, or 8 with x_exps), otherwise as above
+ */
+size_t ptb_gated_ffn_backward_workspace_size(int64_t tokens, int64_t hidden, int64_t ffn,
+                                             int32_t x_bits);
+ptb_status ptb_gated_ffn_backward(const ptb_bf16* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                                  const uint8_t* x_exps, int64_t ld_x_exps,
+                                  const ptb_bf16* w_gate, const ptb_bf16* w_up,
+                                  const ptb_bf16* w_down, const void* kept,
+                                  const uint8_t* kept_exps, int64_t tokens, int64_t hidden,
+                                  int64_t ffn, int32_t activation, ptb_bf16* dx, int64_t ld_dx,
+                                  void* dw_gate, void* dw_up, void* dw_down, int32_t grad_bits,
+                                  void* workspace, size_t workspace_bytes, ptb_stream stream);
+
+/*
+ * ptb_norm_residual: what stands between the output o of one block and the
+ * input h of the next on the residual stream x,
+ *   p = N(o) * post_gamma + post_beta       (post_gamma NULL: p = o)
+ *   y = alpha * x + gate * p                (gate NULL: 1)
+ *   h = N(y) * pre_gamma + pre_beta         (pre_gamma NULL: no h)
+ * N the layer norm (rms = 0; biased variance) or the rms norm (rms = 1; no
+ * betas): (v - mean) / sqrt(mean((v - mean)^2) + eps), mean = 0 for rms.  The
+ * betas may be NULL.  y is rounded to bf16 once; h is the norm of y as stored.
+ *   x, o, y, h [rows, hidden] bf16, strided.  y and h may be x or o (at the
+ *        same stride) but not each other
+ *   gate       [gates, hidden]: rows / gates rows in a row share a gate (gates
+ *        divides rows; 1: a gate per channel; the number of sequences: one for
+ *        each)
+ *   stats      NULL, or [rows, 4] fp32, 16-byte aligned: mean and
+ *        1 / sqrt(.. + eps) of o, then of y (zeros for a norm that is absent),
+ *        for the backward pass
+ * hidden a multiple of 8, at most 32768; gates at most 65533.  One kernel.
+ *
+ * ptb_norm_residual_backward: gradients for those of y (dy; NULL: zero) and of h
+ * (dh; given exactly when pre_gamma is), from y and o as they were stored and
+ * the forward pass's stats.  With d = dy + the gradient through N(y):
+ *   dx = alpha * d,   d_o = gate * d through N(o),
+ *   dgate = sum d * p (over a gate's rows),  dpost_gamma = sum gate * d * (N(o)),
+ *   dpost_beta = sum gate * d,  dpre_gamma = sum dh * N(y),  dpre_beta = sum dh.
+ *   o          bf16, or with o_exps a checkpoint's codes (hidden a multiple of
+ *        32 then)
+ *   dx, d_o    bf16; may be dy, dh, y or (bf16) o at the same stride, but not
+ *        each other
+ *   dpost_gamma .. dpre_beta  fp32, overwritten; NULL: not wanted
+ *   post_beta  is needed for dgate alone
+ *   workspace  at least ptb_norm_residual_backward_workspace_size() bytes, as
+ *        above.  Two kernels.
+ */
+ptb_status ptb_norm_residual(const ptb_bf16* x, int64_t ld_x, const ptb_bf16* o, int64_t ld_o,
+                             const ptb_bf16* post_gamma, const ptb_bf16* post_beta,
+                             const ptb_bf16* gate, int64_t gates, float alpha,
+                             const ptb_bf16* pre_gamma, const ptb_bf16* pre_beta, int32_t rms,
+                             float eps, int64_t rows, int64_t hidden, ptb_bf16* y, int64_t ld_y,
+                             ptb_bf16* h, int64_t ld_h, float* stats, ptb_stream stream);
+size_t ptb_norm_residual_backward_workspace_size(int64_t rows, int64_t hidden, int64_t gates);
+ptb_status ptb_norm_residual_backward(
+    const ptb_bf16* dy, int64_t ld_dy, const ptb_bf16* dh, int64_t ld_dh, const ptb_bf16* y,
+    int64_t ld_y, const void* o, int64_t ld_o, const uint8_t* o_exps, int64_t ld_o_exps,
+    const float* stats, const ptb_bf16* post_gamma, const ptb_bf16* post_beta,
+    const ptb_bf16* gate, int64_t gates, float alpha, const ptb_bf16* pre_gamma, int32_t rms,
+    int64_t rows, int64_t hidden, ptb_bf16* dx, int64_t ld_dx, ptb_bf16* d_o, int64_t ld_do,
+    float* dpost_gamma, float* dpost_beta, float* dgate, float* dpre_gamma, float* dpre_beta,
+    void* workspace, size_t workspace_bytes, ptb_stream stream);
+
+/*
  * ptb_last_device_error: waits for the work queued on `stream` so far
  * (cudaStreamSynchronize of that stream only; other streams keep running),
  * then returns the device status word written by the kernels and clears it
