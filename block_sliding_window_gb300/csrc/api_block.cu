@@ -50,7 +50,7 @@ ptb_status check_checkpoint(const void* codes, int64_t ld_codes, const uint8_t* 
 GemmCall call_up(int64_t t, int64_t h, int64_t f) {  // [gate | up] = x [W_gate ; W_up]^T
   GemmCall c;
   c.layout = kLayoutKK;
-  c.epilogue = kEpiGated;
+  c.epilogue = kEpiGated, c.ragged = true;
   c.M = t, c.N = 2 * f, c.K = h;
   c.lda0 = h, c.ldb0 = h;
   c.ld_out = f, c.ffn = f;
@@ -59,7 +59,7 @@ GemmCall call_up(int64_t t, int64_t h, int64_t f) {  // [gate | up] = x [W_gate 
 GemmCall call_da(int64_t t, int64_t h, int64_t f) {  // da = dy W_down
   GemmCall c;
   c.layout = kLayoutKN;
-  c.epilogue = kEpiDgated;
+  c.epilogue = kEpiDgated, c.ragged = true;
   c.M = t, c.N = f, c.K = h;
   c.lda0 = h, c.ldb0 = f;
   c.ld_out = f, c.ld_out1 = 2 * f, c.ffn = f;
@@ -68,7 +68,7 @@ GemmCall call_da(int64_t t, int64_t h, int64_t f) {  // da = dy W_down
 GemmCall call_dw_down(int64_t t, int64_t h, int64_t f, int bits) {  // dy^T a
   GemmCall c;
   c.layout = kLayoutNN;
-  c.epilogue = bits == 32 ? kEpiF32 : kEpiBf16;
+  c.epilogue = bits == 32 ? kEpiF32 : kEpiBf16, c.ragged = true;
   c.M = h, c.N = f, c.K = t;
   c.lda0 = h, c.ldb0 = f, c.ld_out = f;
   return c;
@@ -76,7 +76,7 @@ GemmCall call_dw_down(int64_t t, int64_t h, int64_t f, int bits) {  // dy^T a
 GemmCall call_dw_up(int64_t t, int64_t h, int64_t f, int bits) {  // [dg | du]^T x
   GemmCall c;
   c.layout = kLayoutNN;
-  c.epilogue = bits == 32 ? kEpiF32 : kEpiBf16;
+  c.epilogue = bits == 32 ? kEpiF32 : kEpiBf16, c.ragged = true;
   c.M = 2 * f, c.N = h, c.K = t;
   c.lda0 = 2 * f, c.ldb0 = h, c.ld_out = h, c.ld_out1 = h;
   c.out_split_row = f;
@@ -85,10 +85,16 @@ GemmCall call_dw_up(int64_t t, int64_t h, int64_t f, int bits) {  // [dg | du]^T
 GemmCall call_dx(int64_t t, int64_t h, int64_t f) {  // dg W_gate + du W_up
   GemmCall c;
   c.layout = kLayoutKN;
-  c.epilogue = kEpiBf16;
+  c.epilogue = kEpiBf16, c.ragged = true;
   c.M = t, c.N = h, c.K = 2 * f, c.k_split = f;
   c.lda0 = 2 * f, c.lda1 = 2 * f, c.ldb0 = h, c.ldb1 = h, c.ld_out = h;
   return c;
+}
+
+GemmSpec spec_down(const ptb_bf16* a, int64_t f, const ptb_bf16* w_down, int64_t h) {
+  GemmSpec g = spec_plain(a, f, f, w_down, h);
+  g.ragged = true;
+  return g;
 }
 
 struct Regions {
@@ -109,7 +115,7 @@ ForwardLayout forward_layout(int64_t t, int64_t h, int64_t f, int sms) {
   Regions r;
   const ptb_bf16* z = nullptr;
   const size_t up = call_scratch(call_up(t, h, f), sms);
-  const size_t down = spec_scratch(spec_plain(z, f, f, z, h), t, sms);
+  const size_t down = spec_scratch(spec_down(z, f, z, h), t, sms);
   l.a = r.take(static_cast<size_t>(t) * f * 2);
   l.gemm_bytes = up > down ? up : down;
   l.gemm = r.take(l.gemm_bytes);
@@ -180,6 +186,22 @@ ptb_status ptb_gated_ffn(const ptb_bf16* x, int64_t ld_x, const ptb_bf16* w_gate
   const ForwardLayout l = forward_layout(tokens, hidden, ffn, ds->sms);
   char* ws = static_cast<char*>(workspace);
   ptb_bf16* a = reinterpret_cast<ptb_bf16*>(ws + l.a);
+  if (tokens <= kThinTokens && !kept) {
+    ThinArgs n;
+    std::memset(&n, 0, sizeof(n));
+    n.x = bf(x), n.ld_x = ld_x;
+    n.w0 = bf(w_gate), n.w1 = bf(w_up);
+    n.out = bf(a), n.ld_out = ffn;
+    n.tokens = static_cast<int>(tokens), n.N = static_cast<int>(ffn), n.K = static_cast<int>(hidden);
+    n.act = activation;
+    PTB_TRY(launch_status(launch_thin(n, stream)));
+    n.x = bf(a), n.ld_x = ffn;
+    n.w0 = bf(w_down), n.w1 = nullptr;
+    n.resid = bf(residual), n.ld_resid = ld_residual;
+    n.out = bf(y), n.ld_out = ld_y;
+    n.N = static_cast<int>(hidden), n.K = static_cast<int>(ffn);
+    return launch_status(launch_thin(n, stream));
+  }
   // 1. a = act(x W_gate^T) * (x W_up^T)
   GemmCall c = call_up(tokens, hidden, ffn);
   c.a0 = x, c.lda0 = ld_x, c.b0 = w_gate, c.b1 = w_up;
@@ -188,8 +210,8 @@ ptb_status ptb_gated_ffn(const ptb_bf16* x, int64_t ld_x, const ptb_bf16* w_gate
   c.kept = kept, c.kept_exps = kept_exps;
   PTB_TRY(gemm_call(ds, c, ws + l.gemm, l.gemm_bytes, stream));
   // 2. y = [residual +] a W_down^T
-  return gemm_run(ds, spec_plain(a, ffn, ffn, w_down, hidden), tokens, y, ld_y, residual,
-                  ld_residual, hidden, ws + l.gemm, l.gemm_bytes, stream);
+  return gemm_run(ds, spec_down(a, ffn, w_down, hidden), tokens, y, ld_y, residual, ld_residual,
+                  hidden, ws + l.gemm, l.gemm_bytes, stream);
 }
 
 size_t ptb_gated_ffn_backward_workspace_size(int64_t tokens, int64_t hidden, int64_t ffn,

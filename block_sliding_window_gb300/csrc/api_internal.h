@@ -47,6 +47,7 @@ ptb_status device_state(DeviceState** out);
 int current_sms();
 ptb_status launch_status(cudaError_t e);
 int pick_block_n(int64_t a, int64_t b);
+int ragged_block_n(int64_t n);
 
 // One GEMM of the layer: C[M, N] = A[M, K] B[N, K]^T with
 //   A = [a0 | a1] split along K at k0 (k1 == 0: a0 only), and
@@ -60,10 +61,13 @@ struct GemmSpec {
   bool fp8 = false;
   const float* a_scale = nullptr;
   const float* b_scale = nullptr;
+  bool ragged = false;  // N tiles as ragged_block_n picks them
   int64_t n() const { return n0 + n1; }
   int64_t k() const { return k0 + k1; }
   int64_t kb() const { return k() / (fp8 ? 128 : 64); }
-  int block_n() const { return n1 ? pick_block_n(n0, n1) : pick_block_n(n0, n0); }
+  int block_n() const {
+    return ragged ? ragged_block_n(n0) : n1 ? pick_block_n(n0, n1) : pick_block_n(n0, n0);
+  }
 };
 
 GemmSpec spec_fp8(const void* a, int64_t lda, int64_t k, const void* b, int64_t n,
@@ -118,7 +122,9 @@ struct GemmCall {
   int64_t ffn = 0;
   void* kept = nullptr;
   uint8_t* kept_exps = nullptr;
+  bool ragged = false;  // N tiles as ragged_block_n picks them
   int block_n() const {
+    if (ragged) return ragged_block_n(N);
     return n_split ? pick_block_n(n_split, N - n_split) : pick_block_n(N, N);
   }
   int64_t kb() const { return (K + 63) / 64; }

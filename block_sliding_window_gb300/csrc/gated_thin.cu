@@ -1,0 +1,153 @@
+// The gated feed-forward of a few tokens (a decoding step): y = [resid +] (act(x Wg^T) * (x Wu^T)) Wd^T
+// for at most kThinTokens rows of x.
+//
+// The weights are read once and used for a handful of rows: a stream of 6 hidden ffn bytes, with
+// 2 flops per byte and row.  The tcgen05 kernel (128-row tiles, one CTA per SM and weight tile) left
+// a third of the SMs without a tile and reads each weight row in pieces of 128 bytes; here the rows
+// of a tile are 16, so that every SM has several blocks of warps, and a warp reads long runs of each
+// row straight into the registers that mma.sync takes them from:
+//   - a block has 16 rows of the weights (of both gate and up) and all of K, its 8 warps a slice of K
+//     each; their sums are joined in shared memory in a fixed order, then the epilogue runs;
+//   - in m16n8k16 the weights are the 16-row operand and tokens the 8 columns.  A lane loads 16
+//     bytes of a row, k = 8 t .. 8 t + 7 of 32: the fragment wants pairs of k in another order, but
+//     the order of a contraction's index does not matter as long as x is loaded in the same one.
+#include "gated_device.cuh"
+
+namespace ptb {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;  // rows of a weight matrix per block
+
+__device__ __forceinline__ uint4 load_stream(const __nv_bfloat16* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: groups of 8 tokens.  GATED: two weight matrices, act(gate) * up; else one, with the residual.
+template <int NT, bool GATED>
+__global__ void __launch_bounds__(kThreads) thin_kernel(const __grid_constant__ ThinArgs p) {
+  constexpr int NW = GATED ? 2 : 1;     // weight matrices
+  constexpr int U = GATED ? 2 : 4;      // steps of 64 k in flight
+  __shared__ float part[kWarps][NW * kRows][NT * 8 + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * kRows;
+  const int steps = p.K / 64;
+  const int first = warp * steps / kWarps, last = (warp + 1) * steps / kWarps;
+
+  const __nv_bfloat16* w[NW][2];
+#pragma unroll
+  for (int m = 0; m < NW; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[m][h] = (m ? p.w1 : p.w0) + static_cast<int64_t>(n0 + g + 8 * h) * p.K + 8 * t;
+  const __nv_bfloat16* x[NT];
+  bool live[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    live[j] = 8 * j + g < p.tokens;
+    x[j] = p.x + (live[j] ? 8 * j + g : 0) * p.ld_x + 8 * t;
+  }
+
+  float acc[NW][NT][4];
+#pragma unroll
+  for (int m = 0; m < NW; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
+
+  auto product = [&](int s, const uint4 (&wv)[NW][2][2]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        uint4 xv = make_uint4(0, 0, 0, 0);
+        if (live[j]) xv = __ldg(reinterpret_cast<const uint4*>(x[j] + s * 64 + q * 32));
+#pragma unroll
+        for (int m = 0; m < NW; ++m) {
+          const uint4 &a = wv[m][0][q], &b = wv[m][1][q];
+          mma_16x8x16(acc[m][j], a.x, b.x, a.y, b.y, xv.x, xv.y);
+          mma_16x8x16(acc[m][j], a.z, b.z, a.w, b.w, xv.z, xv.w);
+        }
+      }
+    }
+  };
+  auto load = [&](int s, uint4 (&wv)[NW][2][2]) {
+#pragma unroll
+    for (int m = 0; m < NW; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) wv[m][h][q] = load_stream(w[m][h] + s * 64 + q * 32);
+  };
+
+  int s = first;
+  for (; s + U <= last; s += U) {
+    uint4 wv[U][NW][2][2];
+#pragma unroll
+    for (int i = 0; i < U; ++i) load(s + i, wv[i]);
+#pragma unroll
+    for (int i = 0; i < U; ++i) product(s + i, wv[i]);
+  }
+  for (; s < last; ++s) {
+    uint4 wv[NW][2][2];
+    load(s, wv);
+    product(s, wv);
+  }
+
+#pragma unroll
+  for (int m = 0; m < NW; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        part[warp][m * kRows + g + 8 * (e >> 1)][8 * j + 2 * t + (e & 1)] = acc[m][j][e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kRows * p.tokens; i += kThreads) {
+    const int r = i % kRows, k = i / kRows;
+    float v[NW];
+#pragma unroll
+    for (int m = 0; m < NW; ++m) {
+      v[m] = 0.f;
+#pragma unroll
+      for (int q = 0; q < kWarps; ++q) v[m] += part[q][m * kRows + r][k];
+    }
+    float out = GATED ? gated_act(v[0], p.act) * v[NW - 1] : v[0];
+    if (!GATED && p.resid) out += __bfloat162float(p.resid[k * p.ld_resid + n0 + r]);
+    p.out[k * p.ld_out + n0 + r] = __float2bfloat16_rn(out);
+  }
+}
+
+template <bool GATED>
+cudaError_t launch(const ThinArgs& a, cudaStream_t stream) {
+  const unsigned grid = a.N / kRows;
+  const int nt = (a.tokens + 7) / 8;
+  if (nt == 1) thin_kernel<1, GATED><<<grid, kThreads, 0, stream>>>(a);
+  else if (nt == 2) thin_kernel<2, GATED><<<grid, kThreads, 0, stream>>>(a);
+  else if (nt <= 4) thin_kernel<4, GATED><<<grid, kThreads, 0, stream>>>(a);
+  else return cudaErrorInvalidValue;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_thin(const ThinArgs& a, cudaStream_t stream) {
+  return a.w1 ? launch<true>(a, stream) : launch<false>(a, stream);
+}
+
+}  // namespace ptb

@@ -381,6 +381,7 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
     float* mine = p.partials + (static_cast<int64_t>(u.slot) * ROWS + prow) * BN;
 #pragma unroll 1
     for (int c = 0; c < BN; c += 32) {
+      if (EPI != kEpiGated && n0 + c >= p.N) break;
       uint32_t r[32];
       tmem_ld_32x32b_x32(t_row + c, r);
       tmem_ld_wait();
@@ -407,7 +408,7 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
     if (finish) {
       const int group0 = u.slot < 0 ? 0 : (u.slot / p.split_s) * p.split_s;
 #pragma unroll 1
-      for (int c = 0; c < BN / 2; c += 32) {
+      for (int c = 0; c < BN / 2 && n0 / 2 + c < p.ffn; c += 32) {
         float v[2][32];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -429,7 +430,7 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
   }
   if (finish && u.slot < 0) {
 #pragma unroll 1
-    for (int c = 0; c < BN; c += 32) {
+    for (int c = 0; c < BN && n0 + c < p.N; c += 32) {
       uint32_t r[32];
       tmem_ld_32x32b_x32(t_row + c, r);
       tmem_ld_wait();
@@ -451,7 +452,7 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
     // so the result does not depend on which warp happened to finish.
     const int group0 = (u.slot / p.split_s) * p.split_s;
 #pragma unroll 1
-    for (int c = 0; c < BN; c += 32) {
+    for (int c = 0; c < BN && n0 + c < p.N; c += 32) {
       float acc[32];
       sum_pieces<BN, ROWS>(p, group0, prow, c, acc);
       if constexpr (FP8) dequantize(p, row, n0 + c, acc);
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int num_m = (p.M + BM - 1) / BM;
-  const int num_n = p.N / BN;
+  const int num_n = (p.N + BN - 1) / BN;  // columns behind N: zeros by TMA, not stored
   const int num_tiles = num_m * num_n;
   const int num_kb = (p.K + BK - 1) / BK;  // a K tail is zero-filled by TMA
 
@@ -755,7 +756,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int num_m = (p.M + 2 * BM - 1) / (2 * BM);
-  const int num_n = p.N / BN;
+  const int num_n = (p.N + BN - 1) / BN;  // columns behind N: zeros by TMA, not stored
   const int num_tiles = num_m * num_n;
   const int num_kb = (p.K + BK - 1) / BK;
 

@@ -93,6 +93,12 @@ int pick_block_n(int64_t a, int64_t b) {
   return 0;
 }
 
+// N tile of a GEMM whose last tile may reach past N.  Above 512 columns a 256-wide tile that is cut
+// wastes less than narrow ones cost: RAGGED_FIGURE
+int ragged_block_n(int64_t n) {
+  return n % 256 == 0 || n > 512 ? 256 : pick_block_n(n, n);
+}
+
 ptb_status launch_status(cudaError_t e) { return e == cudaSuccess ? PTB_OK : PTB_ERR_LAUNCH; }
 
 // SM count of the current device, or an upper bound when there is none.
@@ -128,7 +134,7 @@ bool use_pairs(const DeviceState* ds, bool shape_ok, int64_t m) {
 // Output tiles of a launch: 128-row tiles, or 256-row tiles on CTA pairs.
 int64_t gemm_tiles(int64_t m, int64_t n, int block_n, bool pair) {
   const int64_t rows = pair ? 256 : 128;
-  return (m + rows - 1) / rows * (n / block_n);
+  return (m + rows - 1) / rows * ((n + block_n - 1) / block_n);
 }
 
 // Scratch for the split last wave of an M x N x (kb k-blocks) GEMM, either
@@ -332,7 +338,7 @@ ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t s
   a.k_split = static_cast<int>(c.k_split ? c.k_split : c.K);
   a.layout = c.layout;
   a.epilogue = c.epilogue;
-  const int64_t num_m = (c.M + 127) / 128, num_n = c.N / a.block_n;
+  const int64_t num_m = (c.M + 127) / 128, num_n = (c.N + a.block_n - 1) / a.block_n;
   a.n_fastest = num_m > num_n ? 1 : 0;
   // Both operands evict_last, as in gemm_run: with the operand read once
   // per wave evict_first (the former policy) the 175B-class training step

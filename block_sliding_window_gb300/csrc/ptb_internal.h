@@ -211,6 +211,16 @@ cudaError_t launch_swa_paged(const SwaPagedArgs& a, cudaStream_t stream);
 
 // -------------------------------------------- blocks with gates and norms --
 
+// out[t, n] = act(x w0^T) * (x w1^T), or without w1 [resid +] x w0^T, for at most kThinTokens rows of
+// x; weights [N, K], K a multiple of 64, N of 16.
+constexpr int kThinTokens = 32;
+struct ThinArgs {
+  const __nv_bfloat16 *x, *w0, *w1, *resid;
+  __nv_bfloat16* out;
+  int64_t ld_x, ld_resid, ld_out;
+  int tokens, N, K, act;
+};
+
 struct CheckpointArgs {
   const __nv_bfloat16* x;   // pack
   __nv_bfloat16* x_out;     // unpack
@@ -248,6 +258,7 @@ struct NormArgs {
 
 cudaError_t launch_checkpoint_pack(const CheckpointArgs& a, cudaStream_t stream);
 cudaError_t launch_checkpoint_unpack(const CheckpointArgs& a, cudaStream_t stream);
+cudaError_t launch_thin(const ThinArgs& a, cudaStream_t stream);
 cudaError_t launch_norm_residual(const NormArgs& a, cudaStream_t stream);
 // Bytes of NormArgs::partials.
 size_t norm_backward_partials(int64_t rows, int64_t hidden, int64_t gates, int sms);
