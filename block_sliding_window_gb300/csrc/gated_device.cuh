@@ -1,46 +1,39 @@
-// The activations of the MLPs: tanh-GELU of the block's own and of the gated feed-forward, and the
-// latter's SiLU, each with its derivative.
+// The activations of a gated feed-forward, SiLU and tanh-GELU, with their derivatives.
+//
+// Both are z sigma(w) with w = z (c0 + c1 z^2): c0 = 1, c1 = 0 for SiLU, and since
+// (1 + tanh v) / 2 = sigma(2 v), c0 = 2 sqrt(2 / pi), c1 = 0.044715 c0 for the tanh-GELU.  One
+// formula without a branch keeps the epilogues' unrolled code small, and sigma keeps its relative
+// precision where 1 + tanh cancels.  The derivative is sigma + z sigma (1 - sigma) w'.
 #pragma once
 
 #include "ptb_device.cuh"
 
 namespace ptb {
 
-__device__ __forceinline__ float gelu_tanh(float z) {
-  const float k0 = 0.7978845608028654f;  // sqrt(2 / pi)
-  const float k1 = 0.044715f;
-  return 0.5f * z * (1.0f + tanhf(k0 * (z + k1 * z * z * z)));
-}
+struct GatedAct {
+  float c0, c1;
+  __device__ explicit GatedAct(int act)
+      : c0(act == kActSilu ? 1.f : 1.5957691216057308f),
+        c1(act == kActSilu ? 0.f : 0.071354816272600250f) {}
 
-// d/dz gelu_tanh(z) = 0.5 (1 + t) + 0.5 z (1 - t^2) c (1 + 3 a z^2),
-// t = tanh(c (z + a z^3)), c = sqrt(2 / pi), a = 0.044715.
-__device__ __forceinline__ float gelu_tanh_grad(float z) {
-  const float k0 = 0.7978845608028654f;
-  const float k1 = 0.044715f;
-  const float t = tanhf(k0 * (z + k1 * z * z * z));
-  return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * k0 * (1.0f + 3.0f * k1 * z * z);
-}
+  // z^2, kept finite so that c1 = 0 cannot meet an infinity.
+  static __device__ __forceinline__ float square(float z) { return fminf(z * z, 1e30f); }
 
-// 1 / (1 + e^-z).  e^-z beyond fp32 gives 0, as it should.
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
-
-__device__ __forceinline__ float gated_act(float z, int act) {
-  return act == kActSilu ? z * sigmoid(z) : gelu_tanh(z);
-}
-
-// act(z) and act'(z).
-__device__ __forceinline__ void gated_act_grad(float z, int act, float& value, float& slope) {
-  if (act == kActSilu) {
-    const float s = sigmoid(z);
-    value = z * s;
-    slope = s * (1.f + z * (1.f - s));
-  } else {
-    const float k0 = 0.7978845608028654f;
-    const float k1 = 0.044715f;
-    const float t = tanhf(k0 * (z + k1 * z * z * z));
-    value = 0.5f * z * (1.0f + t);
-    slope = 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * k0 * (1.0f + 3.0f * k1 * z * z);
+  // 1 / (1 + e^-w); e^-w beyond fp32 gives 0, as it should.
+  static __device__ __forceinline__ float sigmoid(float w) {
+    return __fdividef(1.f, 1.f + __expf(-w));
   }
-}
+
+  __device__ __forceinline__ float value(float z) const {
+    return z * sigmoid(z * fmaf(c1, square(z), c0));
+  }
+
+  __device__ __forceinline__ void value_and_slope(float z, float& v, float& slope) const {
+    const float q = square(z);
+    const float s = sigmoid(z * fmaf(c1, q, c0));
+    v = z * s;
+    slope = fmaf(v * (1.f - s), fmaf(3.f * c1, q, c0), s);
+  }
+};
 
 }  // namespace ptb

@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kThreads) thin_kernel(const __grid_constant__ 
       for (int e = 0; e < 4; ++e)
         part[warp][m * kRows + g + 8 * (e >> 1)][8 * j + 2 * t + (e & 1)] = acc[m][j][e];
   __syncthreads();
+  const GatedAct act(p.act);
   for (int i = threadIdx.x; i < kRows * p.tokens; i += kThreads) {
     const int r = i % kRows, k = i / kRows;
     float v[NW];
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) thin_kernel(const __grid_constant__ 
 #pragma unroll
       for (int q = 0; q < kWarps; ++q) v[m] += part[q][m * kRows + r][k];
     }
-    float out = GATED ? gated_act(v[0], p.act) * v[NW - 1] : v[0];
+    float out = GATED ? act.value(v[0]) * v[NW - 1] : v[0];
     if (!GATED && p.resid) out += __bfloat162float(p.resid[k * p.ld_resid + n0 + r]);
     p.out[k * p.ld_out + n0 + r] = __float2bfloat16_rn(out);
   }

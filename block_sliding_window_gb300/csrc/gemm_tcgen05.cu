@@ -19,7 +19,8 @@
 //               64-wide k-block takes ~790 cycles for 512 cycles of MMA work,
 //               matching the shared-memory traffic per k-block -- 48 KB of
 //               operand reads plus 48 KB of TMA writes at ~128 B/clk.)
-//   warps 2..5  epilogue: tcgen05.ld of the accumulator (warp w reads TMEM
+//   warps 2..5  (2..9 for the gated epilogues)
+//               epilogue: tcgen05.ld of the accumulator (warp w reads TMEM
 //               lanes 32*(w%4) .. +31, i.e. one output row per thread),
 //               GELU or residual add in fp32, bf16 stores.  The epilogue of
 //               one work unit overlaps the main loop of the next.
@@ -52,7 +53,18 @@ struct Elem {
   static constexpr int kBK = FP8 ? 128 : 64;
 };
 constexpr int kMmasPerBlock = 4;
-constexpr int kThreads = 192;
+
+// Warps of the epilogue: the gated epilogues do ten times the others' work for a value (two or three
+// outputs, an exponential, groups of 8-bit codes) and outlast the main loop on four; on eight, two
+// share the rows of a TMEM quarter and take its 32-column chunks in turn.  EPIWARPS_FIGURE
+template <int EPI>
+__host__ __device__ constexpr int epi_warps() {
+  return EPI == kEpiGated || EPI == kEpiDgated ? 8 : 4;
+}
+template <int EPI>
+__host__ __device__ constexpr int gemm_threads() {
+  return 64 + 32 * epi_warps<EPI>();
+}
 
 // The weight-gradient GEMMs (fp32 output, both operands MN-major) write
 // their large outputs through shared memory: each epilogue warp stages its
@@ -81,6 +93,12 @@ struct Cfg {
   static constexpr int kSmemBytes =
       kStages * kStageBytes + kBarBytes + (STAGE ? kF32StageBytes : 0) + 1024;
 };
+
+__device__ __forceinline__ float gelu_tanh(float z) {
+  const float k0 = 0.7978845608028654f;  // sqrt(2 / pi)
+  const float k1 = 0.044715f;
+  return 0.5f * z * (1.0f + tanhf(k0 * (z + k1 * z * z * z)));
+}
 
 // One unit of work: k-blocks [kb0, kb1) of one output tile.  slot >= 0 marks
 // a K piece of a remainder tile (its index in the partial-tile buffer).
@@ -135,6 +153,15 @@ __device__ __forceinline__ void dequantize(const GemmArgs& p, int row, int col, 
     acc[4 * v + 2] *= sa * sb.z;
     acc[4 * v + 3] *= sa * sb.w;
   }
+}
+
+// d/dz gelu_tanh(z) = 0.5 (1 + t) + 0.5 z (1 - t^2) c (1 + 3 a z^2),
+// t = tanh(c (z + a z^3)), c = sqrt(2 / pi), a = 0.044715.
+__device__ __forceinline__ float gelu_tanh_grad(float z) {
+  const float k0 = 0.7978845608028654f;
+  const float k1 = 0.044715f;
+  const float t = tanhf(k0 * (z + k1 * z * z * z));
+  return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * k0 * (1.0f + 3.0f * k1 * z * z);
 }
 
 __device__ __forceinline__ void store_bf16x32(__nv_bfloat16* dst_row, const uint32_t (&packed)[16]) {
@@ -220,6 +247,14 @@ __device__ __forceinline__ void store_chunk(const GemmArgs& p, int row, int col,
   store_bf16x32(static_cast<__nv_bfloat16*>(base) + r * ld + c, packed);
 }
 
+// 16 columns in one 32-byte store, a whole sector, for rows that begin on 32 bytes.
+__device__ __forceinline__ void store_bf16x16(__nv_bfloat16* dst, const uint32_t (&packed)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
+               "r"(packed[0]), "r"(packed[1]), "r"(packed[2]), "r"(packed[3]), "r"(packed[4]),
+               "r"(packed[5]), "r"(packed[6]), "r"(packed[7])
+               : "memory");
+}
+
 __device__ __forceinline__ void pack_row(const float (&v)[32], uint32_t (&packed)[16]) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
@@ -229,6 +264,7 @@ __device__ __forceinline__ void pack_row(const float (&v)[32], uint32_t (&packed
 // act(g) * u, rounded once; what the backward pass keeps is rounded from the accumulators, too.
 __device__ __forceinline__ void store_gated(const GemmArgs& p, int row, int col,
                                             const float (&g)[32], const float (&u)[32]) {
+  const GatedAct act(p.act);
   uint32_t packed[16];
   if (p.kept) {
     const int64_t at = static_cast<int64_t>(row) * 2 * p.ffn + col;
@@ -244,24 +280,48 @@ __device__ __forceinline__ void store_gated(const GemmArgs& p, int row, int col,
       store_bf16x32(kept + at + p.ffn, packed);
     }
   }
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + col;
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    packed[j] = pack_bf16x2(gated_act(g[2 * j], p.act) * u[2 * j],
-                            gated_act(g[2 * j + 1], p.act) * u[2 * j + 1]);
-  store_bf16x32(static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + col, packed);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t half[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = 16 * h + 2 * j;
+      half[j] = pack_bf16x2(act.value(g[e]) * u[e], act.value(g[e + 1]) * u[e + 1]);
+    }
+    store_bf16x16(out + 16 * h, half);
+  }
 }
 
-__device__ __forceinline__ void load_bf16x32(const __nv_bfloat16* src_row, float (&v)[32]) {
-  const uint4* src = reinterpret_cast<const uint4*>(src_row);
+// 16 neighbouring columns of a row, by 32-byte loads if the rows begin on 32 bytes.
+__device__ __forceinline__ void load_bf16x16(const __nv_bfloat16* src, bool wide, float (&v)[16]) {
+  uint32_t w[8];
+  if (wide) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                   "=r"(w[6]), "=r"(w[7])
+                 : "l"(src));
+  } else {
+    const uint4 p = __ldg(reinterpret_cast<const uint4*>(src));
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+    w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w, w[4] = q.x, w[5] = q.y, w[6] = q.z, w[7] = q.w;
+  }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint4 q = __ldg(src + k);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  for (int j = 0; j < 8; ++j) {
+    v[2 * j] = bf16_lo(w[j]);
+    v[2 * j + 1] = bf16_hi(w[j]);
+  }
+}
+
+__device__ __forceinline__ void load_codes16(const uint8_t* src, float scale, float (&v)[16]) {
+  const uint4 p = __ldg(reinterpret_cast<const uint4*>(src));
+  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[8 * k + 2 * j] = bf16_lo(w[j]);
-      v[8 * k + 2 * j + 1] = bf16_hi(w[j]);
-    }
+  for (int j = 0; j < 4; ++j) {
+    float f[4];
+    ckpt_unpack4(w[j], f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[4 * j + k] = f[k] * scale;
   }
 }
 
@@ -269,31 +329,43 @@ __device__ __forceinline__ void load_bf16x32(const __nv_bfloat16* src_row, float
 // act(g) * u once more for the weight gradient of the down projection, d u act'(g) and d act(g).
 __device__ __forceinline__ void store_dgated(const GemmArgs& p, int row, int col,
                                              const float (&d)[32]) {
-  float g[32], u[32];
+  const GatedAct act(p.act);
   const int64_t at = static_cast<int64_t>(row) * 2 * p.ffn + col;
+  const bool wide = (reinterpret_cast<uintptr_t>(p.kept) & 31) == 0;
+  float sg = 0.f, su = 0.f;
   if (p.kept_exps) {
-    const uint8_t* codes = static_cast<const uint8_t*>(p.kept);
-    ckpt_load_group(codes + at, p.kept_exps + at / kCkptGroup, g);
-    ckpt_load_group(codes + at + p.ffn, p.kept_exps + (at + p.ffn) / kCkptGroup, u);
-  } else {
-    const __nv_bfloat16* kept = static_cast<const __nv_bfloat16*>(p.kept);
-    load_bf16x32(kept + at, g);
-    load_bf16x32(kept + at + p.ffn, u);
+    sg = ckpt_scale(__ldg(p.kept_exps + at / kCkptGroup));
+    su = ckpt_scale(__ldg(p.kept_exps + (at + p.ffn) / kCkptGroup));
   }
-  uint32_t pa[16], pg[16], pu[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    float a0, s0, a1, s1;
-    gated_act_grad(g[2 * j], p.act, a0, s0);
-    gated_act_grad(g[2 * j + 1], p.act, a1, s1);
-    pa[j] = pack_bf16x2(a0 * u[2 * j], a1 * u[2 * j + 1]);
-    pg[j] = pack_bf16x2(d[2 * j] * u[2 * j] * s0, d[2 * j + 1] * u[2 * j + 1] * s1);
-    pu[j] = pack_bf16x2(d[2 * j] * a0, d[2 * j + 1] * a1);
-  }
-  store_bf16x32(static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + col, pa);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + col;
   __nv_bfloat16* out1 = static_cast<__nv_bfloat16*>(p.out1) + row * p.ld_out1 + col;
-  store_bf16x32(out1, pg);
-  store_bf16x32(out1 + p.ffn, pu);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float g[16], u[16];
+    if (p.kept_exps) {
+      const uint8_t* codes = static_cast<const uint8_t*>(p.kept) + at + 16 * h;
+      load_codes16(codes, sg, g);
+      load_codes16(codes + p.ffn, su, u);
+    } else {
+      const __nv_bfloat16* kept = static_cast<const __nv_bfloat16*>(p.kept) + at + 16 * h;
+      load_bf16x16(kept, wide, g);
+      load_bf16x16(kept + p.ffn, wide, u);
+    }
+    uint32_t pa[8], pg[8], pu[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float d0 = d[16 * h + 2 * j], d1 = d[16 * h + 2 * j + 1];
+      float a0, s0, a1, s1;
+      act.value_and_slope(g[2 * j], a0, s0);
+      act.value_and_slope(g[2 * j + 1], a1, s1);
+      pa[j] = pack_bf16x2(a0 * u[2 * j], a1 * u[2 * j + 1]);
+      pg[j] = pack_bf16x2(d0 * u[2 * j] * s0, d1 * u[2 * j + 1] * s1);
+      pu[j] = pack_bf16x2(d0 * a0, d1 * a1);
+    }
+    store_bf16x16(out + 16 * h, pa);
+    store_bf16x16(out1 + 16 * h, pg);
+    store_bf16x16(out1 + p.ffn + 16 * h, pu);
+  }
 }
 
 // Output tile origin of tile index t (M index fastest, or N index fastest).
@@ -346,6 +418,15 @@ __device__ __forceinline__ void store_chunk_f32_warp(const GemmArgs& p, int row,
   __syncwarp();
 }
 
+// Partial tiles: the 32 x 32 chunk of rows prow .. and columns c .. of piece `slot` is 4 KB in the
+// order in which a warp writes and reads it, 16 bytes of each lane side by side (whole lines; rows
+// of a partial would give each instruction 32 of them).
+template <int BN, int ROWS>
+__device__ __forceinline__ float4* partial_chunk(const GemmArgs& p, int slot, int prow, int c) {
+  const int64_t chunk = (static_cast<int64_t>(slot) * (ROWS / 32) + (prow >> 5)) * (BN / 32) + (c >> 5);
+  return reinterpret_cast<float4*>(p.partials) + chunk * 256 + (prow & 31);
+}
+
 // Sum of the K pieces' partials of 32 columns of a row, in piece order.
 template <int BN, int ROWS>
 __device__ __forceinline__ void sum_pieces(const GemmArgs& p, int group0, int prow, int c,
@@ -353,11 +434,10 @@ __device__ __forceinline__ void sum_pieces(const GemmArgs& p, int group0, int pr
 #pragma unroll
   for (int j = 0; j < 32; ++j) acc[j] = 0.f;
   for (int s = 0; s < p.split_s; ++s) {
-    const float4* src = reinterpret_cast<const float4*>(
-        p.partials + (static_cast<int64_t>(group0 + s) * ROWS + prow) * BN + c);
+    const float4* src = partial_chunk<BN, ROWS>(p, group0 + s, prow, c);
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
-      const float4 q = __ldcg(src + v);
+      const float4 q = __ldcg(src + 32 * v);
       acc[4 * v] += q.x;
       acc[4 * v + 1] += q.y;
       acc[4 * v + 2] += q.z;
@@ -374,27 +454,28 @@ __device__ __forceinline__ void sum_pieces(const GemmArgs& p, int group0, int pr
 template <int BN, int EPI, bool FP8, int ROWS, bool STAGE>
 __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, int row, int prow,
                                               int counter, uint32_t t_row, int n0, int lane,
-                                              float* f32_stage) {
+                                              float* f32_stage, int half) {
+  // This warp's chunks of 32 columns.
+  constexpr int stride = 32 * (epi_warps<EPI>() / 4);
+  const int first = 32 * half;
   bool finish = true;
   if (u.slot >= 0) {
     // A K piece: publish the fp32 partial, then count the arrival.
-    float* mine = p.partials + (static_cast<int64_t>(u.slot) * ROWS + prow) * BN;
 #pragma unroll 1
-    for (int c = 0; c < BN; c += 32) {
+    for (int c = first; c < BN; c += stride) {
       if (EPI != kEpiGated && n0 + c >= p.N) break;
       uint32_t r[32];
       tmem_ld_32x32b_x32(t_row + c, r);
       tmem_ld_wait();
-      float4* dst = reinterpret_cast<float4*>(mine + c);
+      float4* dst = partial_chunk<BN, ROWS>(p, u.slot, prow, c);
 #pragma unroll
       for (int v = 0; v < 8; ++v)
-        __stcg(dst + v, make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
-                                    __uint_as_float(r[4 * v + 2]),
-                                    __uint_as_float(r[4 * v + 3])));
+        __stcg(dst + 32 * v,
+               make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                           __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3])));
     }
-    // Each warp owns its 32 rows: it counts its own arrival for that
-    // quarter of the tile, and the last warp to arrive for the quarter
-    // finishes those rows.  No warp waits for another.
+    // Each warp owns its 32 rows (or its half of their chunks): it counts
+    // its own arrival for them, and the last warp to arrive finishes them.  No warp waits for another.
     __threadfence();
     __syncwarp();
     unsigned prev = 0;
@@ -408,7 +489,7 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
     if (finish) {
       const int group0 = u.slot < 0 ? 0 : (u.slot / p.split_s) * p.split_s;
 #pragma unroll 1
-      for (int c = 0; c < BN / 2 && n0 / 2 + c < p.ffn; c += 32) {
+      for (int c = first; c < BN / 2 && n0 / 2 + c < p.ffn; c += stride) {
         float v[2][32];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -430,7 +511,7 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
   }
   if (finish && u.slot < 0) {
 #pragma unroll 1
-    for (int c = 0; c < BN && n0 + c < p.N; c += 32) {
+    for (int c = first; c < BN && n0 + c < p.N; c += stride) {
       uint32_t r[32];
       tmem_ld_32x32b_x32(t_row + c, r);
       tmem_ld_wait();
@@ -452,7 +533,7 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
     // so the result does not depend on which warp happened to finish.
     const int group0 = (u.slot / p.split_s) * p.split_s;
 #pragma unroll 1
-    for (int c = 0; c < BN && n0 + c < p.N; c += 32) {
+    for (int c = first; c < BN && n0 + c < p.N; c += stride) {
       float acc[32];
       sum_pieces<BN, ROWS>(p, group0, prow, c, acc);
       if constexpr (FP8) dequantize(p, row, n0 + c, acc);
@@ -469,7 +550,7 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
 }
 
 template <int BN, int EPI, bool FP8, int LAYOUT>
-__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs p) {
+__global__ void __launch_bounds__(gemm_threads<EPI>(), 1) gemm_kernel(const __grid_constant__ GemmArgs p) {
   constexpr bool kStage = staged_f32<EPI, LAYOUT>();
   using C = Cfg<BN, kStage>;
   constexpr int BK = Elem<FP8>::kBK;
@@ -503,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull_bar[b], 1);
-      mbar_init(&tempty_bar[b], 4);
+      mbar_init(&tempty_bar[b], epi_warps<EPI>());
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -666,8 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                              static_cast<uint32_t>(acc_buf * BN);
       epilogue_unit<BN, EPI, FP8, BM, kStage>(p, u, row, row_local,
-                                              (u.slot / p.split_s) * 4 + quarter, t_row, n0,
-                                              lane, f32_stage);
+                                              (u.slot / p.split_s) * epi_warps<EPI>() + warp - 2,
+                                              t_row, n0, lane, f32_stage, (warp - 2) >> 2);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty_bar[acc_buf]);
@@ -727,7 +808,7 @@ struct PairCfg {
 };
 
 template <int EPI, int LAYOUT, bool FP8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<EPI>(), 1)
     gemm_pair_kernel(const __grid_constant__ GemmArgs p) {
   constexpr bool kStage = staged_f32<EPI, LAYOUT>();
   using C = PairCfg<kStage, pair_stages<EPI>()>;
@@ -767,7 +848,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull_bar[b], 1);
-      mbar_init(&tempty_bar[b], 8);
+      mbar_init(&tempty_bar[b], 2 * epi_warps<EPI>());
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -938,8 +1019,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                              static_cast<uint32_t>(acc_buf * BN);
       epilogue_unit<BN, EPI, FP8, 2 * BM, kStage>(
-          p, u, m0 + prow, prow, (u.slot / p.split_s) * 8 + static_cast<int>(rank) * 4 + quarter,
-          t_row, n0, lane, f32_stage);
+          p, u, m0 + prow, prow,
+          ((u.slot / p.split_s) * 2 + static_cast<int>(rank)) * epi_warps<EPI>() + warp - 2, t_row, n0,
+          lane, f32_stage, (warp - 2) >> 2);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cluster_map(&tempty_bar[acc_buf], 0));
@@ -970,7 +1052,7 @@ cudaError_t launch_pair(const GemmArgs& a, cudaStream_t stream) {
     configured_device = dev;
   }
   if (a.grid % 2) return cudaErrorInvalidValue;
-  kern<<<a.grid, kThreads, C::kSmemBytes, stream>>>(a);
+  kern<<<a.grid, gemm_threads<EPI>(), C::kSmemBytes, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -987,13 +1069,19 @@ cudaError_t launch_typed(const GemmArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  kern<<<a.grid, kThreads, C::kSmemBytes, stream>>>(a);
+  kern<<<a.grid, gemm_threads<EPI>(), C::kSmemBytes, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-GemmPlan plan_gemm(int64_t tiles, int64_t num_kb, int sms, int block_n, int rows) {
+// Arrival counters for 32 rows of a split tile.
+int gemm_counters(int epilogue) {
+  return (epilogue == kEpiGated ? epi_warps<kEpiGated>()
+          : epilogue == kEpiDgated ? epi_warps<kEpiDgated>() : 4) / 4;
+}
+
+GemmPlan plan_gemm(int64_t tiles, int64_t num_kb, int sms, int block_n, int rows, int counters) {
   GemmPlan g;
   g.grid = static_cast<int>(tiles < sms ? tiles : sms);
   g.split_r = 0;
@@ -1011,7 +1099,7 @@ GemmPlan plan_gemm(int64_t tiles, int64_t num_kb, int sms, int block_n, int rows
     }
   }
   g.partial_bytes = static_cast<size_t>(g.split_r) * g.split_s * rows * block_n * sizeof(float);
-  g.counter_bytes = static_cast<size_t>(g.split_r) * (rows / 32) * sizeof(unsigned);
+  g.counter_bytes = static_cast<size_t>(g.split_r) * (rows / 32) * counters * sizeof(unsigned);
   return g;
 }
 
@@ -1032,7 +1120,8 @@ cudaError_t launch_bn(const GemmArgs& a, cudaStream_t stream) {
 cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
   if (a.split_s >= 2 && a.split_r > 0) {
     cudaError_t e =
-        cudaMemsetAsync(a.counters, 0, a.split_r * (a.pair ? 8 : 4) * sizeof(unsigned), stream);
+        cudaMemsetAsync(a.counters, 0, a.split_r * (a.pair ? 8 : 4) * gemm_counters(a.epilogue) *
+                                           sizeof(unsigned), stream);
     if (e != cudaSuccess) return e;
   }
   if (a.pair) {  // 256-wide N tiles on CTA pairs

@@ -139,10 +139,11 @@ int64_t gemm_tiles(int64_t m, int64_t n, int block_n, bool pair) {
 
 // Scratch for the split last wave of an M x N x (kb k-blocks) GEMM, either
 // tile shape (whichever needs more).
-size_t gemm_scratch_any(int64_t m, int64_t n, int64_t kb, int block_n, int sms) {
-  const size_t a = gemm_scratch_bytes(plan_gemm(gemm_tiles(m, n, block_n, false), kb, sms, block_n));
+size_t gemm_scratch_any(int64_t m, int64_t n, int64_t kb, int block_n, int sms, int counters = 1) {
+  const size_t a = gemm_scratch_bytes(
+      plan_gemm(gemm_tiles(m, n, block_n, false), kb, sms, block_n, 128, counters));
   const size_t b = gemm_scratch_bytes(
-      plan_gemm(gemm_tiles(m, n, block_n, true), kb, sms / 2, block_n, 256));
+      plan_gemm(gemm_tiles(m, n, block_n, true), kb, sms / 2, block_n, 256, counters));
   return a > b ? a : b;
 }
 
@@ -151,7 +152,8 @@ size_t gemm_scratch_any(int64_t m, int64_t n, int64_t kb, int block_n, int sms) 
 void apply_plan(GemmArgs& a, int64_t num_kb, int sms, void* scratch, size_t scratch_bytes) {
   const int64_t tiles = gemm_tiles(a.M, a.N, a.block_n, a.pair != 0);
   const int workers = a.pair ? sms / 2 : sms;
-  GemmPlan g = plan_gemm(tiles, num_kb, workers, a.block_n, a.pair ? 256 : 128);
+  GemmPlan g = plan_gemm(tiles, num_kb, workers, a.block_n, a.pair ? 256 : 128,
+                         gemm_counters(a.epilogue));
   const int per_worker = a.pair ? 2 : 1;
   if (g.split_s >= 2 && scratch && scratch_bytes >= gemm_scratch_bytes(g)) {
     a.grid = g.grid * per_worker;
@@ -292,7 +294,7 @@ bool make_map_mn(CUtensorMap* map, const void* base, uint64_t inner, uint64_t ou
 
 size_t call_scratch(const GemmCall& c, int sms) {
   const int bn = c.block_n() ? c.block_n() : 64;
-  return gemm_scratch_any(c.M, c.N, c.kb(), bn, sms);
+  return gemm_scratch_any(c.M, c.N, c.kb(), bn, sms, gemm_counters(c.epilogue));
 }
 
 ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t scratch_bytes,

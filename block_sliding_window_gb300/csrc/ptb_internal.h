@@ -27,7 +27,7 @@ enum GemmEpilogue : int {
 };
 
 // Activation of a gated feed-forward (ptb.h).
-enum GatedAct : int { kActSilu = 0, kActGelu = 1 };
+enum GatedActivation : int { kActSilu = 0, kActGelu = 1 };
 
 // Operand layouts in shared memory (bit 0: A, bit 1: B).  K-major: the
 // stored matrix is [M or N rows][K]; MN-major: it is [K rows][M or N], so the
@@ -74,8 +74,8 @@ struct GemmArgs {
   // K split of the last, partial wave (split_s < 2: no split).
   int split_r;          // remainder tiles that are split
   int split_s;          // pieces per remainder tile
-  float* partials;      // [split_r * split_s][128][block_n] fp32
-  unsigned* counters;   // [split_r][4] arrival counters, zeroed before each launch
+  float* partials;      // [split_r * split_s] tiles of fp32
+  unsigned* counters;   // [split_r][4 (8 for pairs) x gemm_counters] arrival counters, zeroed before each launch
   // e4m3 operands (fp8 != 0): K counted in e4m3 elements, 128 per k-block;
   // a_scale [M] and b_scale [N] dequantize the fp32 accumulator.
   int fp8;
@@ -102,7 +102,10 @@ struct GemmPlan {
 // SMs the last wave would leave idle.
 // `workers` is the number of CTAs (or CTA pairs), `rows` the tile height
 // (128, or 256 for pairs).
-GemmPlan plan_gemm(int64_t tiles, int64_t num_kb, int workers, int block_n, int rows = 128);
+// `counters`: arrival counters for 32 rows (gemm_counters of the epilogue).
+GemmPlan plan_gemm(int64_t tiles, int64_t num_kb, int workers, int block_n, int rows = 128,
+                   int counters = 1);
+int gemm_counters(int epilogue);
 
 struct SwaArgs {
   const __nv_bfloat16 *q, *k, *v;
