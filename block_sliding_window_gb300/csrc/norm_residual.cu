@@ -13,18 +13,42 @@
 namespace ptb {
 namespace {
 
-__device__ __forceinline__ void unpack8(uint4 p, float (&v)[8]) {
-  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = bf16_lo(w[j]);
-    v[2 * j + 1] = bf16_hi(w[j]);
-  }
+// Eight neighbouring channels as four register pairs: with the packed arithmetic an instruction
+// serves two of them, and these kernels issue instructions rather than wait for memory (in scalar
+// form 51 a value forward and 75 backward; norm_8192's 63% of the memory rate were 70% of the issue
+// slots).
+struct V8 {
+  uint64_t p[4];
+};
+
+__device__ __forceinline__ V8 splat(float v) {
+  const uint64_t q = f2(v, v);
+  return {{q, q, q, q}};
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ V8 unpack8(uint4 q) {
+  return {{f2(bf16_lo(q.x), bf16_hi(q.x)), f2(bf16_lo(q.y), bf16_hi(q.y)),
+           f2(bf16_lo(q.z), bf16_hi(q.z)), f2(bf16_lo(q.w), bf16_hi(q.w))}};
+}
+
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+
+__device__ __forceinline__ uint4 pack8(const V8& v) {
+  return make_uint4(pack2(v.p[0]), pack2(v.p[1]), pack2(v.p[2]), pack2(v.p[3]));
+}
+
+__device__ __forceinline__ V8 load8(const __nv_bfloat16* base, int v) {
+  return unpack8(__ldg(reinterpret_cast<const uint4*>(base) + v));
+}
+
+__device__ __forceinline__ float both(uint64_t v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return lo + hi;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -63,19 +87,18 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(const __grid_constan
   const float inv_n = 1.f / static_cast<float>(a.hidden);
   int turn = 0;
 
-  float p[VPT][8];
+  V8 p[VPT];
   uint4 xv[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = lane + j * lanes;
+    uint4 ov = make_uint4(0, 0, 0, 0);
+    xv[j] = ov;
     if (v < nvec) {
-      unpack8(__ldcs(reinterpret_cast<const uint4*>(a.o + row * a.ld_o) + v), p[j]);
+      ov = __ldcs(reinterpret_cast<const uint4*>(a.o + row * a.ld_o) + v);
       xv[j] = __ldcs(reinterpret_cast<const uint4*>(a.x + row * a.ld_x) + v);
-    } else {
-      xv[j] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) p[j][e] = 0.f;
     }
+    p[j] = unpack8(ov);
   }
   float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
 
@@ -83,51 +106,63 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(const __grid_constan
   auto statistics = [&](float& mean, float& rstd) {
     mean = 0.f;
     if constexpr (!RMS) {
-      float s = 0.f;
+      uint64_t s = 0;
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += p[j][e];
-      mean = row_sum<WARP>(s, red, turn) * inv_n;
+        for (int e = 0; e < 4; ++e) s = f2_add(s, p[j].p[e]);
+      mean = row_sum<WARP>(both(s), red, turn) * inv_n;
     }
-    float s = 0.f;
+    uint64_t s = 0;
+    const uint64_t m = f2(-mean, -mean);
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
       if (lane + j * lanes < nvec)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += (p[j][e] - mean) * (p[j][e] - mean);
-    rstd = rsqrtf(row_sum<WARP>(s, red, turn) * inv_n + a.eps);
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t d = RMS ? p[j].p[e] : f2_add(p[j].p[e], m);
+          s = f2_fma(d, d, s);
+        }
+    rstd = rsqrtf(row_sum<WARP>(both(s), red, turn) * inv_n + a.eps);
+  };
+  // v -> (v - mean) / sd * gamma + beta.  (The first part as one fma with -mean / sd would leave a
+  // constant row the rounding of that quotient instead of zeros.)
+  auto normalise = [&](V8& v, int at, float mean, float rstd, const __nv_bfloat16* gamma,
+                       const __nv_bfloat16* beta) {
+    const uint64_t r = f2(rstd, rstd), c = f2(-mean, -mean);
+    const V8 g = load8(gamma, at);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v.p[e] = f2_mul(RMS ? v.p[e] : f2_add(v.p[e], c), r);
+    if (!RMS && beta) {
+      const V8 b = load8(beta, at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v.p[e] = f2_fma(v.p[e], g.p[e], b.p[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v.p[e] = f2_mul(v.p[e], g.p[e]);
+    }
   };
 
   const bool post = a.post_gamma != nullptr;
   if (post) statistics(st.x, st.y);
   const __nv_bfloat16* gate = a.gate ? a.gate + row / (a.rows / a.gates) * a.hidden : nullptr;
+  const uint64_t alpha = f2(a.alpha, a.alpha);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = lane + j * lanes;
     if (v < nvec) {
-      float f[8];
-      if (post) {
-        unpack8(__ldg(reinterpret_cast<const uint4*>(a.post_gamma) + v), f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[j][e] = (p[j][e] - st.x) * st.y * f[e];
-        if (a.post_beta) {
-          unpack8(__ldg(reinterpret_cast<const uint4*>(a.post_beta) + v), f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) p[j][e] += f[e];
-        }
-      }
+      if (post) normalise(p[j], v, st.x, st.y, a.post_gamma, a.post_beta);
       if (gate) {
-        unpack8(__ldg(reinterpret_cast<const uint4*>(gate) + v), f);
+        const V8 g = load8(gate, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[j][e] *= f[e];
+        for (int e = 0; e < 4; ++e) p[j].p[e] = f2_mul(p[j].p[e], g.p[e]);
       }
-      unpack8(xv[j], f);
+      const V8 x = unpack8(xv[j]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) p[j][e] = fmaf(a.alpha, f[e], p[j][e]);
+      for (int e = 0; e < 4; ++e) p[j].p[e] = f2_fma(alpha, x.p[e], p[j].p[e]);
       const uint4 yv = pack8(p[j]);
       reinterpret_cast<uint4*>(a.y + row * a.ld_y)[v] = yv;
-      unpack8(yv, p[j]);
+      p[j] = unpack8(yv);
     }
   }
   if (a.h) {
@@ -136,15 +171,7 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(const __grid_constan
     for (int j = 0; j < VPT; ++j) {
       const int v = lane + j * lanes;
       if (v < nvec) {
-        float f[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(a.pre_gamma) + v), f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[j][e] = (p[j][e] - st.z) * st.w * f[e];
-        if (a.pre_beta) {
-          unpack8(__ldg(reinterpret_cast<const uint4*>(a.pre_beta) + v), f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) p[j][e] += f[e];
-        }
+        normalise(p[j], v, st.z, st.w, a.pre_gamma, a.pre_beta);
         reinterpret_cast<uint4*>(a.h + row * a.ld_h)[v] = pack8(p[j]);
       }
     }
@@ -189,9 +216,9 @@ BackPlan back_plan(int64_t rows, int64_t hidden, int sms) {
   if (groups > rows) groups = rows;
   p.groups = static_cast<int>(groups < 1 ? 1 : groups);
   const size_t row = static_cast<size_t>(p.threads) * 4 * 16;
-  const size_t room = (208 * 1024) / per_sm;
+  const size_t room = (216 * 1024) / per_sm - 2560;  // less the static part and the system's
   int64_t st = static_cast<int64_t>(room / row);
-  p.stages = static_cast<int>(st > 4 ? 4 : st < 2 ? 2 : st);
+  p.stages = static_cast<int>(st > 6 ? 6 : st < 4 ? 4 : st);
   p.smem = row * p.stages;
   return p;
 }
@@ -208,43 +235,71 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Sums of a pair over the threads of a row (all blocks of the cluster), the same bits everywhere.
+// Sums of four values over the threads of a row (all blocks of the cluster), the same bits in all of
+// them.  Lanes first trade pairs of values, so that four sums take six shuffles instead of twenty.
 template <bool CLUSTER>
-__device__ __forceinline__ float2 pair_sum(float2 v, float2 (*red)[32], float2 (*peer)[8], int& turn,
+__device__ __forceinline__ float4 row_sum4(float4 v, float4 (*red)[32], float4 (*peer)[8], int& turn,
                                            int cluster, uint32_t rank) {
-  v.x = warp_sum(v.x);
-  v.y = warp_sum(v.y);
-  float2* slots = red[turn];
   const int lane = threadIdx.x & 31;
-  const int warps = blockDim.x >> 5;
-  if (lane == 0) slots[threadIdx.x >> 5] = v;
+  const bool odd1 = lane & 1, odd2 = lane & 2;
+  // after these, lane l holds value l & 3 summed over the lanes that differ in the low two bits
+  float a = odd1 ? v.y : v.x, b = odd1 ? v.w : v.z;
+  a += __shfl_xor_sync(0xffffffffu, odd1 ? v.x : v.y, 1);
+  b += __shfl_xor_sync(0xffffffffu, odd1 ? v.z : v.w, 1);
+  float t = odd2 ? b : a;
+  t += __shfl_xor_sync(0xffffffffu, odd2 ? a : b, 2);
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  float* slots = reinterpret_cast<float*>(red[turn]);
+  if (lane < 4) slots[(threadIdx.x >> 5) * 4 + lane] = t;
   __syncthreads();
-  const float2 mine = lane < warps ? slots[lane] : make_float2(0.f, 0.f);
-  v.x = warp_sum(mine.x);
-  v.y = warp_sum(mine.y);
+  const int warps = blockDim.x >> 5;
+  t = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int w = (lane >> 2) + 8 * q;
+    if (w < warps) t += slots[w * 4 + (lane & 3)];
+  }
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   if constexpr (CLUSTER) {
-    // The first lanes write this block's sums into every block of the cluster.
-    if (static_cast<int>(threadIdx.x) < cluster) {
-      const uint32_t dst = cluster_map(&peer[turn][rank], threadIdx.x);
-      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(v.x), "f"(v.y) : "memory");
+    // The first warp's lanes write this block's sums into every block of the cluster.
+    if (static_cast<int>(threadIdx.x) < 4 * cluster) {
+      const uint32_t dst = cluster_map(reinterpret_cast<float*>(&peer[turn][rank]) + (lane & 3), lane >> 2);
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(t) : "memory");
     }
     cluster_sync();
-    v = make_float2(0.f, 0.f);
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int r = 0; r < cluster; ++r) {
-      v.x += peer[turn][r].x;
-      v.y += peer[turn][r].y;
+      const float4 p = peer[turn][r];
+      v.x += p.x;
+      v.y += p.y;
+      v.z += p.z;
+      v.w += p.w;
     }
+  } else {
+    v.x = __shfl_sync(0xffffffffu, t, 0);
+    v.y = __shfl_sync(0xffffffffu, t, 1);
+    v.z = __shfl_sync(0xffffffffu, t, 2);
+    v.w = __shfl_sync(0xffffffffu, t, 3);
   }
   turn ^= 1;
   return v;
+}
+
+__device__ __forceinline__ void store_sums(float* dst, const V8& v) {
+  ulonglong2* d = reinterpret_cast<ulonglong2*>(dst);
+  d[0] = make_ulonglong2(v.p[0], v.p[1]);
+  d[1] = make_ulonglong2(v.p[2], v.p[3]);
 }
 
 template <int STAGES, bool CLUSTER, bool RMS, bool O8>
 __global__ void __launch_bounds__(kSliceMax / 8, 1)
     norm_residual_backward_kernel(const __grid_constant__ NormArgs a, int cluster, int slice, int groups) {
   extern __shared__ __align__(16) uint4 ring[];  // [STAGES][4][blockDim.x]
-  __shared__ float2 red[2][32];
-  __shared__ float2 peer[2][8];
+  __shared__ float4 red[2][32];
+  __shared__ float4 peer[2][8];
+  constexpr int AHEAD = STAGES - 2;  // rows on their way while two are worked on
   const uint32_t rank = CLUSTER ? cluster_ctarank() : 0;
   const int group = blockIdx.x / cluster;
   const int64_t lo = group * a.rows / groups, hi = (group + 1) * a.rows / groups;
@@ -255,185 +310,251 @@ __global__ void __launch_bounds__(kSliceMax / 8, 1)
   const float inv_n = 1.f / static_cast<float>(a.hidden);
   int turn = 0;
 
-  float S0[8], S1[8], S2[8], S3[8], w[8], gn[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) S0[e] = S1[e] = S2[e] = S3[e] = w[e] = gn[e] = 0.f;
-  if (in && pre) unpack8(__ldg(reinterpret_cast<const uint4*>(a.pre_gamma + col)), gn);
+  V8 S0 = splat(0.f), S1 = S0, S2 = S0, S3 = S0, w = S0, gn = S0;
+  if (in && pre) gn = load8(a.pre_gamma + col, 0);
 
-  auto slot = [&](int stage, int t) { return ring + (stage * 4 + t) * blockDim.x + threadIdx.x; };
-  auto fetch = [&](int64_t row) {
-    if (in && row < hi) {
-      const int stage = static_cast<int>((row - lo) % STAGES);
-      if (a.dy) cp_async16(slot(stage, 0), a.dy + row * a.ld_dy + col);
+  // This thread's slots: 16 bytes of each tensor, [stage][tensor][thread].
+  char* const slots = reinterpret_cast<char*>(ring + threadIdx.x);
+  const uint32_t per_tensor = blockDim.x * 16, per_stage = per_tensor * 4;
+  const uint32_t ring_bytes = per_stage * STAGES;
+  uint32_t fetch_at = 0;
+  int64_t fetch_row = lo;
+  const __nv_bfloat16* src_dy = a.dy + lo * a.ld_dy + col;
+  const __nv_bfloat16* src_dh = a.dh + lo * a.ld_dh + col;
+  const __nv_bfloat16* src_y = a.y + lo * a.ld_y + col;
+  const char* src_o = reinterpret_cast<const char*>(a.o) + (lo * a.ld_o + col) * (O8 ? 1 : 2);
+  auto fetch = [&]() {  // the next row
+    if (in && fetch_row < hi) {
+      char* dst = slots + fetch_at;
+      if (a.dy) cp_async16(dst, src_dy);
       if (O8)
-        cp_async8(slot(stage, 1), reinterpret_cast<const uint8_t*>(a.o) + row * a.ld_o + col);
+        cp_async8(dst + per_tensor, src_o);
       else
-        cp_async16(slot(stage, 1), a.o + row * a.ld_o + col);
+        cp_async16(dst + per_tensor, src_o);
       if (pre) {
-        cp_async16(slot(stage, 2), a.dh + row * a.ld_dh + col);
-        cp_async16(slot(stage, 3), a.y + row * a.ld_y + col);
+        cp_async16(dst + 2 * per_tensor, src_dh);
+        cp_async16(dst + 3 * per_tensor, src_y);
       }
+      src_dy += a.ld_dy;
+      src_dh += a.ld_dh;
+      src_y += a.ld_y;
+      src_o += a.ld_o * (O8 ? 1 : 2);
     }
+    ++fetch_row;
+    fetch_at += per_stage;
+    if (fetch_at == ring_bytes) fetch_at = 0;
     cp_async_commit();
   };
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) fetch(lo + s);
+  for (int s = 0; s < AHEAD; ++s) fetch();
+  auto value8 = [&](uint32_t at, int t) {
+    return unpack8(*reinterpret_cast<const uint4*>(slots + at + t * per_tensor));
+  };
 
-  int64_t seg = lo / rows_per_gate;
-  int64_t seg_end = 0;
-  for (int64_t row = lo; row < hi; ++row) {
+  __nv_bfloat16* out_dx = a.dx + lo * a.ld_dx + col;
+  __nv_bfloat16* out_do = a.d_o + lo * a.ld_do + col;
+  const uint64_t alpha = f2(a.alpha, a.alpha);
+  int64_t seg = 0, seg_end = lo;
+  uint32_t stage_at = 0;
+  int n;
+  for (int64_t row = lo; row < hi; row += n) {
     if (row >= seg_end) {  // the first row, or the first of another gate
       seg = row / rows_per_gate;
       seg_end = (seg + 1) * rows_per_gate;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 1.f;
+      w = splat(1.f);
       if (in) {
-        float f[8];
-        if (a.gate) unpack8(__ldg(reinterpret_cast<const uint4*>(a.gate + seg * a.hidden + col)), w);
+        if (a.gate) w = load8(a.gate + seg * a.hidden + col, 0);
         if (post) {
-          unpack8(__ldg(reinterpret_cast<const uint4*>(a.post_gamma + col)), f);
+          const V8 f = load8(a.post_gamma + col, 0);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] *= f[e];
+          for (int e = 0; e < 4; ++e) w.p[e] = f2_mul(w.p[e], f.p[e]);
         }
       }
     }
-    const float4 st = __ldg(a.stats + row);
-    float o_scale = 1.f;
-    if (O8 && in) o_scale = ckpt_scale(__ldg(a.o_exps + row * a.ld_o_exps + col / 32));
-    fetch(row + STAGES - 1);
-    cp_async_wait<STAGES - 1>();
-    const int stage = static_cast<int>((row - lo) % STAGES);
-
-    float d[8], oh[8];
+    // Two rows of one gate at a time: they share the barriers of the two rounds of sums.
+    const int64_t end = seg_end < hi ? seg_end : hi;
+    n = row + 1 < end ? 2 : 1;
+    float4 st[2];
+    float o_scale[2] = {1.f, 1.f};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) d[e] = oh[e] = 0.f;
-    if (in) {
-      if (a.dy) unpack8(*slot(stage, 0), d);
+    for (int r = 0; r < 2; ++r) {
+      st[r] = __ldg(a.stats + row + (r < n ? r : 0));
+      if (O8 && in && r < n)
+        o_scale[r] = ckpt_scale(__ldg(a.o_exps + (row + r) * a.ld_o_exps + col / 32));
+    }
+    fetch();
+    if (n == 2) fetch();
+    cp_async_wait<AHEAD>();
+    uint32_t at[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      at[r] = stage_at;
+      if (r < n) stage_at += per_stage;
+      if (stage_at == ring_bytes) stage_at = 0;
+    }
+
+    auto hat = [](V8 v, float mean, float r) {  // (v - mean) / sd
+      const uint64_t rr = f2(r, r), c = f2(-mean, -mean);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v.p[e] = f2_mul(RMS ? v.p[e] : f2_add(v.p[e], c), rr);
+      return v;
+    };
+    float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (pre) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint64_t s1 = 0, s2 = 0;
+        if (in && r < n) {
+          const V8 g = value8(at[r], 2), yh = hat(value8(at[r], 3), st[r].z, st[r].w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (!RMS) S2.p[e] = f2_add(S2.p[e], g.p[e]);
+            S3.p[e] = f2_fma(g.p[e], yh.p[e], S3.p[e]);
+            const uint64_t gg = f2_mul(g.p[e], gn.p[e]);
+            if (!RMS) s1 = f2_add(s1, gg);
+            s2 = f2_fma(gg, yh.p[e], s2);
+          }
+        }
+        if (r) m.z = both(s1), m.w = both(s2);
+        else m.x = both(s1), m.y = both(s2);
+      }
+      m = row_sum4<CLUSTER>(m, red, peer, turn, cluster, rank);
+    }
+    auto load_o = [&](int r) {
+      V8 v;
       if (O8) {
-        const uint2 c = *reinterpret_cast<const uint2*>(slot(stage, 1));
+        const uint2 c = *reinterpret_cast<const uint2*>(slots + at[r] + per_tensor);
+        const uint64_t scale = f2(o_scale[r], o_scale[r]);
         float f[4];
         ckpt_unpack4(c.x, f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) oh[e] = f[e] * o_scale;
+        v.p[0] = f2_mul(f2(f[0], f[1]), scale);
+        v.p[1] = f2_mul(f2(f[2], f[3]), scale);
         ckpt_unpack4(c.y, f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) oh[4 + e] = f[e] * o_scale;
+        v.p[2] = f2_mul(f2(f[0], f[1]), scale);
+        v.p[3] = f2_mul(f2(f[2], f[3]), scale);
       } else {
-        unpack8(*slot(stage, 1), oh);
+        v = value8(at[r], 1);
       }
-    }
-    if (pre) {
-      float yh[8], g[8];
+      return post ? hat(v, st[r].x, st[r].y) : v;
+    };
+    float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) yh[e] = g[e] = 0.f;
-      float2 m = make_float2(0.f, 0.f);
-      if (in) {
-        unpack8(*slot(stage, 2), g);
-        unpack8(*slot(stage, 3), yh);
+    for (int r = 0; r < 2; ++r) {
+      uint64_t s1 = 0, s2 = 0;
+      if (in && r < n) {
+        V8 d = a.dy ? value8(at[r], 0) : splat(0.f);
+        if (pre) {
+          const V8 g = value8(at[r], 2), yh = hat(value8(at[r], 3), st[r].z, st[r].w);
+          // d += (g gn - m1 - yh m2) / sd
+          const float m1 = (r ? m.z : m.x) * -inv_n, m2 = (r ? m.w : m.y) * -inv_n;
+          const uint64_t c1 = f2(m1, m1), c2 = f2(m2, m2), sd = f2(st[r].w, st[r].w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          yh[e] = (yh[e] - st.z) * st.w;
-          if (!RMS) S2[e] += g[e];
-          S3[e] = fmaf(g[e], yh[e], S3[e]);
-          g[e] *= gn[e];
-          if (!RMS) m.x += g[e];
-          m.y = fmaf(g[e], yh[e], m.y);
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t t = RMS ? f2_mul(yh.p[e], c2) : f2_fma(yh.p[e], c2, c1);
+            d.p[e] = f2_fma(sd, f2_fma(g.p[e], gn.p[e], t), d.p[e]);
+          }
+        }
+        V8 f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.p[e] = f2_mul(alpha, d.p[e]);
+        *reinterpret_cast<uint4*>(out_dx + r * a.ld_dx) = pack8(f);
+        const V8 oh = load_o(r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!RMS) S0.p[e] = f2_add(S0.p[e], d.p[e]);
+          S1.p[e] = f2_fma(d.p[e], oh.p[e], S1.p[e]);
+          d.p[e] = f2_mul(d.p[e], w.p[e]);
+          if (!RMS) s1 = f2_add(s1, d.p[e]);
+          s2 = f2_fma(d.p[e], oh.p[e], s2);
+        }
+        if (post) {
+          // kept for the second round in this thread's own slots, whose values are used up
+          char* mine = slots + at[r];
+          *reinterpret_cast<ulonglong2*>(mine) = make_ulonglong2(d.p[0], d.p[1]);
+          *reinterpret_cast<ulonglong2*>(mine + 2 * per_tensor) = make_ulonglong2(d.p[2], d.p[3]);
+        } else {
+          *reinterpret_cast<uint4*>(out_do + r * a.ld_do) = pack8(d);
         }
       }
-      m = pair_sum<CLUSTER>(m, red, peer, turn, cluster, rank);
-      m.x *= inv_n;
-      m.y *= inv_n;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] += st.w * (g[e] - m.x - yh[e] * m.y);
-    }
-    if (in) {
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = a.alpha * d[e];
-      *reinterpret_cast<uint4*>(a.dx + row * a.ld_dx + col) = pack8(f);
-    }
-    float2 m = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (post) oh[e] = (oh[e] - st.x) * st.y;
-      if (in) {
-        if (!RMS) S0[e] += d[e];
-        S1[e] = fmaf(d[e], oh[e], S1[e]);
-      }
-      d[e] *= w[e];
-      if (in) {
-        m.x += d[e];
-        m.y = fmaf(d[e], oh[e], m.y);
-      }
+      if (r) k.z = both(s1), k.w = both(s2);
+      else k.x = both(s1), k.y = both(s2);
     }
     if (post) {
-      m = pair_sum<CLUSTER>(m, red, peer, turn, cluster, rank);
-      m.x = RMS ? 0.f : m.x * inv_n;
-      m.y *= inv_n;
+      k = row_sum4<CLUSTER>(k, red, peer, turn, cluster, rank);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] = st.y * (d[e] - m.x - oh[e] * m.y);
+      for (int r = 0; r < 2; ++r) {
+        if (in && r < n) {
+          const float k1 = (r ? k.z : k.x) * -inv_n, k2 = (r ? k.w : k.y) * -inv_n;
+          const uint64_t c1 = f2(k1, k1), c2 = f2(k2, k2), sd = f2(st[r].y, st[r].y);
+          const V8 oh = load_o(r);
+          const char* mine = slots + at[r];
+          const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(mine);
+          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(mine + 2 * per_tensor);
+          V8 d = {{p.x, p.y, q.x, q.y}};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t t = RMS ? f2_fma(oh.p[e], c2, d.p[e]) : f2_add(f2_fma(oh.p[e], c2, c1), d.p[e]);
+            d.p[e] = f2_mul(sd, t);
+          }
+          *reinterpret_cast<uint4*>(out_do + r * a.ld_do) = pack8(d);
+        }
+      }
     }
-    if (in) *reinterpret_cast<uint4*>(a.d_o + row * a.ld_do + col) = pack8(d);
+    out_dx += n * a.ld_dx;
+    out_do += n * a.ld_do;
 
-    if (in && (row + 1 == hi || row + 1 == seg_end)) {  // this gate's rows end here
-      float4* dst = reinterpret_cast<float4*>(a.partials + (group + seg) * 2 * a.hidden + col);
-      dst[0] = make_float4(S0[0], S0[1], S0[2], S0[3]);
-      dst[1] = make_float4(S0[4], S0[5], S0[6], S0[7]);
-      dst = reinterpret_cast<float4*>(a.partials + ((group + seg) * 2 + 1) * a.hidden + col);
-      dst[0] = make_float4(S1[0], S1[1], S1[2], S1[3]);
-      dst[1] = make_float4(S1[4], S1[5], S1[6], S1[7]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) S0[e] = S1[e] = 0.f;
+    if (in && row + n == end) {  // this gate's rows of this run end here
+      float* dst = a.partials + (group + seg) * 2 * a.hidden + col;
+      store_sums(dst, S0);
+      store_sums(dst + a.hidden, S1);
+      S0 = S1 = splat(0.f);
     }
   }
   if (in && pre) {
-    float* base = a.partials + (groups + a.gates) * 2 * a.hidden + group * 2 * static_cast<int64_t>(a.hidden) + col;
-    float4* dst = reinterpret_cast<float4*>(base);
-    dst[0] = make_float4(S2[0], S2[1], S2[2], S2[3]);
-    dst[1] = make_float4(S2[4], S2[5], S2[6], S2[7]);
-    dst = reinterpret_cast<float4*>(base + a.hidden);
-    dst[0] = make_float4(S3[0], S3[1], S3[2], S3[3]);
-    dst[1] = make_float4(S3[4], S3[5], S3[6], S3[7]);
+    float* dst = a.partials + (groups + a.gates) * 2 * a.hidden + group * 2 * static_cast<int64_t>(a.hidden) + col;
+    store_sums(dst, S2);
+    store_sums(dst + a.hidden, S3);
   }
   cp_async_wait<0>();
   if constexpr (CLUSTER) cluster_sync();  // no block leaves while another may still write to it
 }
 
-// Joins the blocks' sums.  blockIdx.y = 0: dpost_gamma, dpost_beta; 1: dpre_gamma, dpre_beta;
-// 2 + g: dgate of gate g.  32 channels a block; the 8 warps take the runs of rows in turn and their
-// sums are added in order.
-__global__ void __launch_bounds__(256)
+// Joins the blocks' sums.  blockIdx.y = 0: dpost_gamma, dpost_beta and a single gate's dgate; 1:
+// dpre_gamma, dpre_beta; 2 + g: dgate of gate g of several.  32 channels a block; its warps take the
+// runs of rows in turn and their sums are added in order.
+constexpr int kJoinWarps = 16;
+
+__global__ void __launch_bounds__(kJoinWarps * 32)
     norm_backward_join_kernel(const __grid_constant__ NormArgs a, int groups) {
-  __shared__ float part[2][8][32];
+  __shared__ float part[2][kJoinWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   const bool in = col < a.hidden;
   const int64_t H = a.hidden;
+  const bool pre = blockIdx.y == 1, each = blockIdx.y > 1;
   float s0 = 0.f, s1 = 0.f;
-  if (blockIdx.y == 1) {
-    const float* src = a.partials + (groups + a.gates) * 2 * H + col;
-    if (in)
-#pragma unroll 4
-      for (int c = warp; c < groups; c += 8) {
-        s0 += __ldcg(src + (c * 2) * H);
-        s1 += __ldcg(src + (c * 2 + 1) * H);
+  const int64_t per = a.rows / a.gates;
+  const int64_t first = each ? blockIdx.y - 2 : 0;
+  const int64_t last = each || pre ? first : a.gates - 1;
+  for (int64_t g = first; g <= last; ++g) {
+    // The runs that hold rows of this gate: run c begins at row c * rows / groups.
+    int c0 = 0, c1 = groups - 1;
+    const float* src = a.partials + (groups + a.gates) * 2 * H;
+    if (!pre) {
+      c0 = static_cast<int>(((g * per + 1) * groups - 1) / a.rows);
+      c1 = static_cast<int>(((g + 1) * per * groups - 1) / a.rows);
+      src = a.partials + g * 2 * H;
+    }
+    src += col;
+    float t0 = 0.f, t1 = 0.f;
+    if (in) {
+#pragma unroll 10
+      for (int c = c0 + ((warp - c0) & (kJoinWarps - 1)); c <= c1; c += kJoinWarps) {
+        t0 += __ldcg(src + (c * 2) * H);
+        t1 += __ldcg(src + (c * 2 + 1) * H);
       }
-  } else {
-    const int64_t per = a.rows / a.gates;
-    const int64_t first = blockIdx.y ? blockIdx.y - 2 : 0;
-    const int64_t last = blockIdx.y ? first : a.gates - 1;
-    for (int64_t g = first; g <= last; ++g) {
-      // The runs that hold rows of this gate: run c begins at row c * rows / groups.
-      const int64_t c0 = ((g * per + 1) * groups - 1) / a.rows;
-      const int64_t c1 = ((g + 1) * per * groups - 1) / a.rows;
-      float t0 = 0.f, t1 = 0.f;
-      if (in)
-#pragma unroll 4
-        for (int64_t c = c0 + ((warp - c0) & 7); c <= c1; c += 8) {
-          t0 += __ldcg(a.partials + (c + g) * 2 * H + col);
-          t1 += __ldcg(a.partials + ((c + g) * 2 + 1) * H + col);
-        }
-      const float f = in && a.gate && blockIdx.y == 0 ? __bfloat162float(a.gate[g * H + col]) : 1.f;
+      const bool weigh = blockIdx.y == 0 && a.gate && a.gates > 1;
+      const float f = weigh ? __bfloat162float(a.gate[g * H + col]) : 1.f;
       s0 = fmaf(f, t0, s0);
       s1 = fmaf(f, t1, s1);
     }
@@ -444,21 +565,25 @@ __global__ void __launch_bounds__(256)
   if (warp != 0 || !in) return;
   s0 = s1 = 0.f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
+  for (int w = 0; w < kJoinWarps; ++w) {
     s0 += part[0][w][lane];
     s1 += part[1][w][lane];
   }
-  if (blockIdx.y == 0) {
-    if (a.dpost_gamma) a.dpost_gamma[col] = s1;
-    if (a.dpost_beta) a.dpost_beta[col] = s0;
-  } else if (blockIdx.y == 1) {
+  if (pre) {
     if (a.dpre_gamma) a.dpre_gamma[col] = s1;
     if (a.dpre_beta) a.dpre_beta[col] = s0;
-  } else {
+    return;
+  }
+  if (each || (a.gates == 1 && a.dgate)) {
     float v = s1;
     if (a.post_gamma) v *= __bfloat162float(a.post_gamma[col]);
     if (a.post_beta) v = fmaf(__bfloat162float(a.post_beta[col]), s0, v);
-    a.dgate[(blockIdx.y - 2) * H + col] = v;
+    a.dgate[first * H + col] = v;
+  }
+  if (!each) {
+    const float f = a.gates == 1 && a.gate ? __bfloat162float(a.gate[col]) : 1.f;
+    if (a.dpost_gamma) a.dpost_gamma[col] = f * s1;
+    if (a.dpost_beta) a.dpost_beta[col] = f * s0;
   }
 }
 
@@ -476,9 +601,7 @@ cudaError_t launch_forward(const NormArgs& a, cudaStream_t stream) {
   } else {
     const unsigned grid = static_cast<unsigned>(a.rows);
     auto threads = [&](int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; };
-    if (nvec <= 1024)
-      norm_residual_kernel<2, false, RMS><<<grid, threads(2), 0, stream>>>(a);
-    else if (nvec <= 2048)
+    if (nvec <= 2048)
       norm_residual_kernel<4, false, RMS><<<grid, threads(4), 0, stream>>>(a);
     else
       norm_residual_kernel<8, false, RMS><<<grid, threads(8), 0, stream>>>(a);
@@ -538,12 +661,13 @@ size_t norm_backward_partials(int64_t rows, int64_t hidden, int64_t gates, int s
 
 cudaError_t launch_norm_residual_backward(const NormArgs& a, cudaStream_t stream) {
   const BackPlan p = back_plan(a.rows, a.hidden, a.sms);
-  cudaError_t e = p.stages == 4   ? launch_backward_stages<4>(a, p, stream)
-                  : p.stages == 3 ? launch_backward_stages<3>(a, p, stream)
-                                  : launch_backward_stages<2>(a, p, stream);
+  cudaError_t e = p.stages == 6   ? launch_backward_stages<6>(a, p, stream)
+                  : p.stages == 5 ? launch_backward_stages<5>(a, p, stream)
+                                  : launch_backward_stages<4>(a, p, stream);
   if (e != cudaSuccess) return e;
-  const unsigned gates = a.dgate ? static_cast<unsigned>(a.gates) : 0;
-  norm_backward_join_kernel<<<dim3((a.hidden + 31) / 32, 2 + gates), 256, 0, stream>>>(a, p.groups);
+  const unsigned each = a.dgate && a.gates > 1 ? static_cast<unsigned>(a.gates) : 0;
+  norm_backward_join_kernel<<<dim3((a.hidden + 31) / 32, 2 + each), kJoinWarps * 32, 0, stream>>>(
+      a, p.groups);
   return cudaGetLastError();
 }
 
