@@ -411,6 +411,7 @@ ptb_status ptb_norm_residual_backward(
   a.dpost_gamma = dpost_gamma, a.dpost_beta = dpost_beta, a.dgate = dgate;
   a.dpre_gamma = dpre_gamma, a.dpre_beta = dpre_beta;
   a.partials = static_cast<float*>(workspace);
+  a.status = ds->status;
   a.sms = ds->sms;
   return launch_status(launch_norm_residual_backward(a, stream));
 }

@@ -53,6 +53,17 @@ __device__ __forceinline__ void ckpt_unpack4(uint32_t codes, float (&v)[4]) {
   v[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)) - 8388736.f;
 }
 
+// The same as packed pairs, times a power of two: (2^23 + 128 + c) s - (2^23 + 128) s is exact.
+__device__ __forceinline__ void ckpt_unpack4_scaled(uint32_t codes, float scale, uint64_t (&v)[2]) {
+  const uint32_t u = codes ^ 0x80808080u;
+  const uint64_t s = f2(scale, scale), off = f2(-8388736.f * scale, -8388736.f * scale);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    v[h] = f2_fma(f2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + 2 * h)),
+                     __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441 + 2 * h))),
+                  s, off);
+}
+
 // One whole group held by a thread: its 32 values to codes and an exponent byte.
 __device__ __forceinline__ void ckpt_store_group(const float (&v)[32], uint8_t* codes,
                                                  uint8_t* exponent) {

@@ -39,7 +39,7 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
 
 // NT: groups of 8 tokens.  GATED: two weight matrices, act(gate) * up; else one, with the residual.
 template <int NT, bool GATED>
-__global__ void __launch_bounds__(kThreads) thin_kernel(const __grid_constant__ ThinArgs p) {
+__global__ void __launch_bounds__(kThreads, NT > 2 ? 2 : 3) thin_kernel(const __grid_constant__ ThinArgs p) {
   constexpr int NW = GATED ? 2 : 1;     // weight matrices
   constexpr int U = GATED ? 2 : 4;      // steps of 64 k in flight
   __shared__ float part[kWarps][NW * kRows][NT * 8 + 1];

@@ -237,9 +237,20 @@ __device__ __forceinline__ void cp_async_wait() {
 
 // Sums of four values over the threads of a row (all blocks of the cluster), the same bits in all of
 // them.  Lanes first trade pairs of values, so that four sums take six shuffles instead of twenty.
+//
+// Blocks of a cluster send their sums into each other's `peer` slots, each message counting its
+// bytes on the receiver's barrier of the turn.  A block's sums of the turn after next cannot come in
+// before this block has read these: it sends its own of the next turn only after that.
+struct Exchange {
+  float4 peer[2][8];
+  uint64_t bar[2];
+  int abort;
+};
+
 template <bool CLUSTER>
-__device__ __forceinline__ float4 row_sum4(float4 v, float4 (*red)[32], float4 (*peer)[8], int& turn,
-                                           int cluster, uint32_t rank) {
+__device__ __forceinline__ float4 row_sum4(float4 v, float4 (*red)[32], Exchange* ex, unsigned& turns,
+                                           int cluster, uint32_t rank, unsigned* status) {
+  const int turn = turns & 1;
   const int lane = threadIdx.x & 31;
   const bool odd1 = lane & 1, odd2 = lane & 2;
   // after these, lane l holds value l & 3 summed over the lanes that differ in the low two bits
@@ -263,15 +274,20 @@ __device__ __forceinline__ float4 row_sum4(float4 v, float4 (*red)[32], float4 (
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   if constexpr (CLUSTER) {
-    // The first warp's lanes write this block's sums into every block of the cluster.
     if (static_cast<int>(threadIdx.x) < 4 * cluster) {
-      const uint32_t dst = cluster_map(reinterpret_cast<float*>(&peer[turn][rank]) + (lane & 3), lane >> 2);
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(t) : "memory");
+      if (threadIdx.x == 0) mbar_arrive_expect_tx(&ex->bar[turn], 16 * cluster);
+      const uint32_t to = lane >> 2;
+      const uint32_t dst = cluster_map(reinterpret_cast<float*>(&ex->peer[turn][rank]) + (lane & 3), to);
+      const uint32_t bar = cluster_map(&ex->bar[turn], to);
+      asm volatile(
+          "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst),
+          "r"(__float_as_uint(t)), "r"(bar)
+          : "memory");
     }
-    cluster_sync();
+    mbar_wait_cluster(&ex->bar[turn], (turns >> 1) & 1, &ex->abort, status);
     v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int r = 0; r < cluster; ++r) {
-      const float4 p = peer[turn][r];
+      const float4 p = ex->peer[turn][r];
       v.x += p.x;
       v.y += p.y;
       v.z += p.z;
@@ -283,14 +299,19 @@ __device__ __forceinline__ float4 row_sum4(float4 v, float4 (*red)[32], float4 (
     v.z = __shfl_sync(0xffffffffu, t, 2);
     v.w = __shfl_sync(0xffffffffu, t, 3);
   }
-  turn ^= 1;
+  ++turns;
   return v;
 }
 
-__device__ __forceinline__ void store_sums(float* dst, const V8& v) {
-  ulonglong2* d = reinterpret_cast<ulonglong2*>(dst);
-  d[0] = make_ulonglong2(v.p[0], v.p[1]);
-  d[1] = make_ulonglong2(v.p[2], v.p[3]);
+// Eight fp32 values in two pieces of 16 bytes.
+__device__ __forceinline__ void store_v8(void* lo, void* hi, const V8& v) {
+  *reinterpret_cast<ulonglong2*>(lo) = make_ulonglong2(v.p[0], v.p[1]);
+  *reinterpret_cast<ulonglong2*>(hi) = make_ulonglong2(v.p[2], v.p[3]);
+}
+__device__ __forceinline__ V8 load_v8(const void* lo, const void* hi) {
+  const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(lo);
+  const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(hi);
+  return {{p.x, p.y, q.x, q.y}};
 }
 
 template <int STAGES, bool CLUSTER, bool RMS, bool O8>
@@ -298,7 +319,7 @@ __global__ void __launch_bounds__(kSliceMax / 8, 1)
     norm_residual_backward_kernel(const __grid_constant__ NormArgs a, int cluster, int slice, int groups) {
   extern __shared__ __align__(16) uint4 ring[];  // [STAGES][4][blockDim.x]
   __shared__ float4 red[2][32];
-  __shared__ float4 peer[2][8];
+  __shared__ Exchange ex;
   constexpr int AHEAD = STAGES - 2;  // rows on their way while two are worked on
   const uint32_t rank = CLUSTER ? cluster_ctarank() : 0;
   const int group = blockIdx.x / cluster;
@@ -308,7 +329,16 @@ __global__ void __launch_bounds__(kSliceMax / 8, 1)
   const bool in = static_cast<int>(threadIdx.x) * 8 < slice && col < a.hidden;
   const bool post = a.post_gamma != nullptr, pre = a.pre_gamma != nullptr;
   const float inv_n = 1.f / static_cast<float>(a.hidden);
-  int turn = 0;
+  unsigned turns = 0;
+  if constexpr (CLUSTER) {
+    if (threadIdx.x == 0) {
+      mbar_init(&ex.bar[0], 1);
+      mbar_init(&ex.bar[1], 1);
+      ex.abort = 0;
+      mbar_fence_init();
+    }
+    cluster_sync();
+  }
 
   V8 S0 = splat(0.f), S1 = S0, S2 = S0, S3 = S0, w = S0, gn = S0;
   if (in && pre) gn = load8(a.pre_gamma + col, 0);
@@ -418,20 +448,17 @@ __global__ void __launch_bounds__(kSliceMax / 8, 1)
         if (r) m.z = both(s1), m.w = both(s2);
         else m.x = both(s1), m.y = both(s2);
       }
-      m = row_sum4<CLUSTER>(m, red, peer, turn, cluster, rank);
+      m = row_sum4<CLUSTER>(m, red, &ex, turns, cluster, rank, a.status);
     }
     auto load_o = [&](int r) {
       V8 v;
       if (O8) {
         const uint2 c = *reinterpret_cast<const uint2*>(slots + at[r] + per_tensor);
-        const uint64_t scale = f2(o_scale[r], o_scale[r]);
-        float f[4];
-        ckpt_unpack4(c.x, f);
-        v.p[0] = f2_mul(f2(f[0], f[1]), scale);
-        v.p[1] = f2_mul(f2(f[2], f[3]), scale);
-        ckpt_unpack4(c.y, f);
-        v.p[2] = f2_mul(f2(f[0], f[1]), scale);
-        v.p[3] = f2_mul(f2(f[2], f[3]), scale);
+        uint64_t f[2];
+        ckpt_unpack4_scaled(c.x, o_scale[r], f);
+        v.p[0] = f[0], v.p[1] = f[1];
+        ckpt_unpack4_scaled(c.y, o_scale[r], f);
+        v.p[2] = f[0], v.p[3] = f[1];
       } else {
         v = value8(at[r], 1);
       }
@@ -470,8 +497,8 @@ __global__ void __launch_bounds__(kSliceMax / 8, 1)
         if (post) {
           // kept for the second round in this thread's own slots, whose values are used up
           char* mine = slots + at[r];
-          *reinterpret_cast<ulonglong2*>(mine) = make_ulonglong2(d.p[0], d.p[1]);
-          *reinterpret_cast<ulonglong2*>(mine + 2 * per_tensor) = make_ulonglong2(d.p[2], d.p[3]);
+          store_v8(mine, mine + 2 * per_tensor, d);
+          store_v8(mine + per_tensor, mine + 3 * per_tensor, oh);
         } else {
           *reinterpret_cast<uint4*>(out_do + r * a.ld_do) = pack8(d);
         }
@@ -480,17 +507,15 @@ __global__ void __launch_bounds__(kSliceMax / 8, 1)
       else k.x = both(s1), k.y = both(s2);
     }
     if (post) {
-      k = row_sum4<CLUSTER>(k, red, peer, turn, cluster, rank);
+      k = row_sum4<CLUSTER>(k, red, &ex, turns, cluster, rank, a.status);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         if (in && r < n) {
           const float k1 = (r ? k.z : k.x) * -inv_n, k2 = (r ? k.w : k.y) * -inv_n;
           const uint64_t c1 = f2(k1, k1), c2 = f2(k2, k2), sd = f2(st[r].y, st[r].y);
-          const V8 oh = load_o(r);
           const char* mine = slots + at[r];
-          const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(mine);
-          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(mine + 2 * per_tensor);
-          V8 d = {{p.x, p.y, q.x, q.y}};
+          V8 d = load_v8(mine, mine + 2 * per_tensor);
+          const V8 oh = load_v8(mine + per_tensor, mine + 3 * per_tensor);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint64_t t = RMS ? f2_fma(oh.p[e], c2, d.p[e]) : f2_add(f2_fma(oh.p[e], c2, c1), d.p[e]);
@@ -505,15 +530,15 @@ __global__ void __launch_bounds__(kSliceMax / 8, 1)
 
     if (in && row + n == end) {  // this gate's rows of this run end here
       float* dst = a.partials + (group + seg) * 2 * a.hidden + col;
-      store_sums(dst, S0);
-      store_sums(dst + a.hidden, S1);
+      store_v8(dst, dst + 4, S0);
+      store_v8(dst + a.hidden, dst + a.hidden + 4, S1);
       S0 = S1 = splat(0.f);
     }
   }
   if (in && pre) {
     float* dst = a.partials + (groups + a.gates) * 2 * a.hidden + group * 2 * static_cast<int64_t>(a.hidden) + col;
-    store_sums(dst, S2);
-    store_sums(dst + a.hidden, S3);
+    store_v8(dst, dst + 4, S2);
+    store_v8(dst + a.hidden, dst + a.hidden + 4, S3);
   }
   cp_async_wait<0>();
   if constexpr (CLUSTER) cluster_sync();  // no block leaves while another may still write to it

@@ -256,6 +256,7 @@ struct NormArgs {
   int64_t ld_dx, ld_do;
   float *dpost_gamma, *dpost_beta, *dgate, *dpre_gamma, *dpre_beta;
   float* partials;
+  unsigned* status;
   int sms;
 };
 
