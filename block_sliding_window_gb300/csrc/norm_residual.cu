@@ -8,6 +8,9 @@
 // in the registers of its threads from the first load to the last store; the statistics (means,
 // then centred squares) are reduced in fp32.  Rows of up to 1024 channels are a warp's, so that
 // their reductions need no barrier; longer ones a block's.
+#include <atomic>
+#include <type_traits>
+
 #include "checkpoint_device.cuh"
 
 namespace ptb {
@@ -181,154 +184,203 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(const __grid_constan
 
 // ------------------------------------------------------------ backward --
 //
-// With d = dy + N'(dh) (the gradient of y, from the stream and through the norm before the next
-// block), oh = (o - mean) / sd and yh alike:
-//   dx = alpha d,   do = N'(gate * post_gamma * d),   N'(w) = (w - mean(w) - vh mean(w vh)) / sd,
-// and of the sums over rows four suffice: S0 = sum d, S1 = sum d oh, S2 = sum dh, S3 = sum dh yh.
+// With gg = dh * pre_gamma, w = gate * post_gamma and vh = (v - mean) / sd of y (yh) and of o (oh):
+//   d  = dy + (gg - m1 - yh m2) / sd_y,          m1 = mean(gg), m2 = mean(gg yh)
+//   dx = alpha d,   do = (w d - k1 - oh k2) / sd_o,   k1 = mean(w d), k2 = mean(w oh d)
+// (rms norms: m1 = k1 = 0).  k1 and k2 are sums over d, which needs m1 and m2 first; but with d
+// written out,
+//   k1 = mean(w dy) + (mean(w gg) - m1 mean(w) - m2 mean(w yh)) / sd_y,   k2 alike with w oh for w,
+// all ten sums (four for rms norms) come out of one look at the row and one round between the
+// threads, where d first and k after took two and kept d in shared memory in between (norm_bwd_8bit
+// 123 us, 36 of them in the two rounds).  Of the sums over rows four suffice:
+//   S0 = sum d, S1 = sum d oh, S2 = sum dh, S3 = sum dh yh   (S0, S1 for each gate's rows apart)
 //   dpost_beta = gate S0,  dpost_gamma = gate S1,  dgate = post_gamma S1 + post_beta S0,
-//   dpre_beta = S2,  dpre_gamma = S3          (S0, S1 for each gate's rows on their own).
+//   dpre_beta = S2,  dpre_gamma = S3.
 //
-// Rows are dealt to blocks in runs, a thread has 8 channels of all its block's rows and keeps their
-// sums in registers.  Each thread copies its own channels of the next rows into its own part of
-// shared memory (cp.async), so the copies run ahead of the arithmetic without any barrier.  Rows of
-// more channels than a block has threads for are split over a cluster, whose blocks exchange their
-// two pairs of sums through shared memory of each other.  The blocks' sums are joined by a second
-// kernel in a fixed order.
+// Rows are dealt to blocks in runs, a thread has VEC * 8 channels of all its block's rows and keeps
+// their sums in registers.  Each thread copies its own channels of the next rows into its own part of
+// shared memory (cp.async), so the copies run ahead of the arithmetic without any barrier; two rows
+// at a time share the round between the threads.  Rows of more channels than a block has threads for
+// are split over a cluster, whose blocks exchange their sums through each other's shared memory.
+// The blocks' sums are joined by a second kernel in a fixed order.
 
-constexpr int kSliceMax = 6144;  // channels of one block
+// Channels of one block.  Up to 5120 a thread has 8 (640 threads of 96 registers); beyond, 16 (384
+// threads of 168), or the sums of a layer norm would not fit in registers.
+constexpr int kSlice1 = 5120, kSlice2 = 6144;
+constexpr int kRing = 200 * 1024;  // shared memory for rows, per SM
 
 struct BackPlan {
-  int cluster, threads, slice, groups, stages;
+  int vec, cluster, threads, slice, groups, stages;
   size_t smem;
 };
 
 BackPlan back_plan(int64_t rows, int64_t hidden, int sms) {
   BackPlan p;
-  p.cluster = 1;
-  while (hidden > static_cast<int64_t>(kSliceMax) * p.cluster) p.cluster *= 2;
+  p.vec = hidden <= kSlice1 ? 1 : 2;
+  const int most = p.vec == 1 ? kSlice1 : kSlice2;
+  p.cluster = static_cast<int>((hidden + most - 1) / most);
   const int64_t vecs = (hidden / 8 + p.cluster - 1) / p.cluster;
   p.slice = static_cast<int>(vecs) * 8;
-  p.threads = static_cast<int>((vecs + 31) / 32) * 32;
-  int per_sm = 768 / p.threads;
+  p.threads = static_cast<int>(((vecs + p.vec - 1) / p.vec + 31) / 32) * 32;
+  int per_sm = p.vec == 1 ? kSlice1 / 8 / p.threads : 1;  // what the registers allow
   if (per_sm < 1) per_sm = 1;
-  if (per_sm > 16) per_sm = 16;
+  if (per_sm > 8) per_sm = 8;
   int64_t groups = static_cast<int64_t>(sms / p.cluster) * per_sm;
   if (groups > rows) groups = rows;
   p.groups = static_cast<int>(groups < 1 ? 1 : groups);
-  const size_t row = static_cast<size_t>(p.threads) * 4 * 16;
-  const size_t room = (216 * 1024) / per_sm - 2560;  // less the static part and the system's
-  int64_t st = static_cast<int64_t>(room / row);
+  const size_t row = static_cast<size_t>(p.threads) * p.vec * 4 * 16;
+  const int64_t st = static_cast<int64_t>(kRing / per_sm / row);
   p.stages = static_cast<int>(st > 6 ? 6 : st < 4 ? 4 : st);
   p.smem = row * p.stages;
   return p;
 }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// All but the latest `ahead` (2 to 4) groups.
+template <int AHEAD>
+__device__ __forceinline__ void wait_ahead(int ahead) {
+  if constexpr (AHEAD < 4) {
+    if (ahead != AHEAD) return wait_ahead<AHEAD + 1>(ahead);
+  }
+  cp_async_wait<AHEAD>();
+}
 
-// Sums of four values over the threads of a row (all blocks of the cluster), the same bits in all of
-// them.  Lanes first trade pairs of values, so that four sums take six shuffles instead of twenty.
-//
-// Blocks of a cluster send their sums into each other's `peer` slots, each message counting its
-// bytes on the receiver's barrier of the turn.  A block's sums of the turn after next cannot come in
-// before this block has read these: it sends its own of the next turn only after that.
+constexpr int kMostSums = 20;
+constexpr int kMostWarps = kSlice1 / 8 / 32;
+
+// What the threads of a row, and the blocks of a cluster, tell each other.  Blocks send their sums
+// into each other's `peer` slots, each message counting its bytes on the receiver's barrier of the
+// turn.  A block's sums of the turn after next cannot come in before this block has read these: it
+// sends its own of the next turn only after that.
 struct Exchange {
-  float4 peer[2][8];
+  float4 stats[6][kMostWarps];  // of the rows in the ring, a copy for each warp
+  float warp[2][kMostWarps][kMostSums];
+  float sum[kMostWarps][kMostSums];
+  float peer[2][8][kMostSums];
   uint64_t bar[2];
   int abort;
 };
 
-template <bool CLUSTER>
-__device__ __forceinline__ float4 row_sum4(float4 v, float4 (*red)[32], Exchange* ex, unsigned& turns,
-                                           int cluster, uint32_t rank, unsigned* status) {
+// Sums of V values over the threads of a row (all blocks of the cluster), the same bits in all of
+// them.  Lanes first trade pairs of values, so that four sums take six shuffles instead of twenty.
+template <int V, bool CLUSTER>
+__device__ __forceinline__ void row_sums(float (&v)[V], Exchange& ex, unsigned& turns, int cluster,
+                                         uint32_t rank, unsigned* status) {
+  static_assert(V % 4 == 0 && V <= kMostSums, "");
   const int turn = turns & 1;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const bool odd1 = lane & 1, odd2 = lane & 2;
-  // after these, lane l holds value l & 3 summed over the lanes that differ in the low two bits
-  float a = odd1 ? v.y : v.x, b = odd1 ? v.w : v.z;
-  a += __shfl_xor_sync(0xffffffffu, odd1 ? v.x : v.y, 1);
-  b += __shfl_xor_sync(0xffffffffu, odd1 ? v.z : v.w, 1);
-  float t = odd2 ? b : a;
-  t += __shfl_xor_sync(0xffffffffu, odd2 ? a : b, 2);
 #pragma unroll
-  for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  float* slots = reinterpret_cast<float*>(red[turn]);
-  if (lane < 4) slots[(threadIdx.x >> 5) * 4 + lane] = t;
+  for (int q = 0; q < V; q += 4) {
+    float a = odd1 ? v[q + 1] : v[q], b = odd1 ? v[q + 3] : v[q + 2];
+    a += __shfl_xor_sync(0xffffffffu, odd1 ? v[q] : v[q + 1], 1);
+    b += __shfl_xor_sync(0xffffffffu, odd1 ? v[q + 2] : v[q + 3], 1);
+    float t = odd2 ? b : a;
+    t += __shfl_xor_sync(0xffffffffu, odd2 ? a : b, 2);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane < 4) ex.warp[turn][warp][q + lane] = t;  // lane l has value l & 3
+  }
   __syncthreads();
-  const int warps = blockDim.x >> 5;
-  t = 0.f;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int w = (lane >> 2) + 8 * q;
-    if (w < warps) t += slots[w * 4 + (lane & 3)];
+  float t = 0.f;
+  if (lane < V) {
+#pragma unroll 4
+    for (int w = 0; w < warps; ++w) t += ex.warp[turn][w][lane];
   }
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   if constexpr (CLUSTER) {
-    if (static_cast<int>(threadIdx.x) < 4 * cluster) {
-      if (threadIdx.x == 0) mbar_arrive_expect_tx(&ex->bar[turn], 16 * cluster);
-      const uint32_t to = lane >> 2;
-      const uint32_t dst = cluster_map(reinterpret_cast<float*>(&ex->peer[turn][rank]) + (lane & 3), to);
-      const uint32_t bar = cluster_map(&ex->bar[turn], to);
-      asm volatile(
-          "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst),
-          "r"(__float_as_uint(t)), "r"(bar)
-          : "memory");
+    if (warp == 0) {
+      if (lane == 0) mbar_arrive_expect_tx(&ex.bar[turn], 4 * V * cluster);
+      __syncwarp();
+      if (lane < V)
+        for (int to = 0; to < cluster; ++to)
+          asm volatile(
+              "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                  cluster_map(&ex.peer[turn][rank][lane], to)),
+              "r"(__float_as_uint(t)), "r"(cluster_map(&ex.bar[turn], to))
+              : "memory");
+      __syncwarp();
     }
-    mbar_wait_cluster(&ex->bar[turn], (turns >> 1) & 1, &ex->abort, status);
-    v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int r = 0; r < cluster; ++r) {
-      const float4 p = ex->peer[turn][r];
-      v.x += p.x;
-      v.y += p.y;
-      v.z += p.z;
-      v.w += p.w;
-    }
-  } else {
-    v.x = __shfl_sync(0xffffffffu, t, 0);
-    v.y = __shfl_sync(0xffffffffu, t, 1);
-    v.z = __shfl_sync(0xffffffffu, t, 2);
-    v.w = __shfl_sync(0xffffffffu, t, 3);
+    mbar_wait_cluster_warp(&ex.bar[turn], (turns >> 1) & 1, &ex.abort, status);
+    t = 0.f;
+    if (lane < V)
+      for (int r = 0; r < cluster; ++r) t += ex.peer[turn][r][lane];
   }
+  // to every lane: this warp's own slots, read before the next round's barrier
+  if (lane < V) ex.sum[warp][lane] = t;
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < V; q += 4) {
+    const float4 p = *reinterpret_cast<const float4*>(&ex.sum[warp][q]);
+    v[q] = p.x, v[q + 1] = p.y, v[q + 2] = p.z, v[q + 3] = p.w;
+  }
+  __syncwarp();
   ++turns;
+}
+
+__device__ __forceinline__ void store_v8(float* dst, const V8& v) {
+  ulonglong2* d = reinterpret_cast<ulonglong2*>(dst);
+  d[0] = make_ulonglong2(v.p[0], v.p[1]);
+  d[1] = make_ulonglong2(v.p[2], v.p[3]);
+}
+
+// A load that stays where it is written: the compiler would move a plain one down to its use.
+__device__ __forceinline__ unsigned load_now(const uint8_t* p) {
+  unsigned v;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
 
-// Eight fp32 values in two pieces of 16 bytes.
-__device__ __forceinline__ void store_v8(void* lo, void* hi, const V8& v) {
-  *reinterpret_cast<ulonglong2*>(lo) = make_ulonglong2(v.p[0], v.p[1]);
-  *reinterpret_cast<ulonglong2*>(hi) = make_ulonglong2(v.p[2], v.p[3]);
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
 }
-__device__ __forceinline__ V8 load_v8(const void* lo, const void* hi) {
-  const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(lo);
-  const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(hi);
-  return {{p.x, p.y, q.x, q.y}};
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w) : "memory");
 }
 
-template <int STAGES, bool CLUSTER, bool RMS, bool O8>
-__global__ void __launch_bounds__(kSliceMax / 8, 1)
-    norm_residual_backward_kernel(const __grid_constant__ NormArgs a, int cluster, int slice, int groups) {
-  extern __shared__ __align__(16) uint4 ring[];  // [STAGES][4][blockDim.x]
-  __shared__ float4 red[2][32];
-  __shared__ Exchange ex;
-  constexpr int AHEAD = STAGES - 2;  // rows on their way while two are worked on
+// FULL: both norms and both gradients are there (the usual call); else a.dy, post_gamma or pre_gamma
+// may be absent.
+template <int VEC, bool RMS, bool O8, bool FULL>
+__global__ void __launch_bounds__(VEC == 1 ? kSlice1 / 8 : kSlice2 / 16, 1)
+    norm_residual_backward_kernel(const __grid_constant__ NormArgs a, int cluster, int slice, int groups,
+                                  int stages) {
+  constexpr bool CLUSTER = VEC == 2;
+  extern __shared__ __align__(16) uint4 ring[];  // [stages][4][VEC][blockDim.x]
+  __shared__ __align__(16) Exchange ex;
+  const int ahead = stages - 2;  // rows on their way while two are worked on
   const uint32_t rank = CLUSTER ? cluster_ctarank() : 0;
   const int group = blockIdx.x / cluster;
   const int64_t lo = group * a.rows / groups, hi = (group + 1) * a.rows / groups;
   const int64_t rows_per_gate = a.rows / a.gates;
+  // This thread's channels.  Vectors behind the row's end hold zeros, with weights of zero, and are
+  // not stored.
   const int col = static_cast<int>(rank) * slice + threadIdx.x * 8;
-  const bool in = static_cast<int>(threadIdx.x) * 8 < slice && col < a.hidden;
-  const bool post = a.post_gamma != nullptr, pre = a.pre_gamma != nullptr;
-  const float inv_n = 1.f / static_cast<float>(a.hidden);
+  const int step = blockDim.x * 8;
+  bool in[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+    in[j] = static_cast<int>(threadIdx.x) * 8 + j * step < slice && col + j * step < a.hidden;
+  const bool post = FULL || a.post_gamma != nullptr, pre = FULL || a.pre_gamma != nullptr;
+  const bool has_dy = FULL || a.dy != nullptr;
+  const float inv_n = -1.f / static_cast<float>(a.hidden);  // the means are subtracted
   unsigned turns = 0;
   if constexpr (CLUSTER) {
     if (threadIdx.x == 0) {
@@ -340,206 +392,276 @@ __global__ void __launch_bounds__(kSliceMax / 8, 1)
     cluster_sync();
   }
 
-  V8 S0 = splat(0.f), S1 = S0, S2 = S0, S3 = S0, w = S0, gn = S0;
-  if (in && pre) gn = load8(a.pre_gamma + col, 0);
+  V8 S0[VEC], S1[VEC], S2[VEC], S3[VEC], w[VEC], gn[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    S0[j] = S1[j] = S2[j] = S3[j] = gn[j] = splat(0.f);
+    if (in[j] && pre) gn[j] = load8(a.pre_gamma + col + j * step, 0);
+  }
 
-  // This thread's slots: 16 bytes of each tensor, [stage][tensor][thread].
-  char* const slots = reinterpret_cast<char*>(ring + threadIdx.x);
-  const uint32_t per_tensor = blockDim.x * 16, per_stage = per_tensor * 4;
-  const uint32_t ring_bytes = per_stage * STAGES;
-  uint32_t fetch_at = 0;
-  int64_t fetch_row = lo;
+  // This thread's slots: 16 bytes of each tensor and vector.
+  const uint32_t per_vec = blockDim.x * 16, per_tensor = per_vec * VEC, per_stage = per_tensor * 4;
+  const uint32_t mine = smem_addr(ring + threadIdx.x), ring_end = mine + per_stage * stages;
+  if (!FULL || !in[VEC - 1])  // what no copy will fill
+    for (uint32_t at = mine; at < ring_end; at += per_vec) sts16(at, make_uint4(0, 0, 0, 0));
+  uint32_t fetch_at = mine;
+  int64_t left = hi - lo;  // rows still to be fetched
+  const float4* src_stats = a.stats + lo;
+  const int warp = threadIdx.x >> 5;
+  const uint32_t stats_mine = smem_addr(&ex.stats[0][warp]);
+  uint32_t stats_fetch = stats_mine, stats_at = stats_mine;
   const __nv_bfloat16* src_dy = a.dy + lo * a.ld_dy + col;
   const __nv_bfloat16* src_dh = a.dh + lo * a.ld_dh + col;
   const __nv_bfloat16* src_y = a.y + lo * a.ld_y + col;
   const char* src_o = reinterpret_cast<const char*>(a.o) + (lo * a.ld_o + col) * (O8 ? 1 : 2);
   auto fetch = [&]() {  // the next row
-    if (in && fetch_row < hi) {
-      char* dst = slots + fetch_at;
-      if (a.dy) cp_async16(dst, src_dy);
-      if (O8)
-        cp_async8(dst + per_tensor, src_o);
-      else
-        cp_async16(dst + per_tensor, src_o);
-      if (pre) {
-        cp_async16(dst + 2 * per_tensor, src_dh);
-        cp_async16(dst + 3 * per_tensor, src_y);
+    if (left > 0) {
+      if ((threadIdx.x & 31) == 0) cp_async16(stats_fetch, src_stats);
+      ++src_stats;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        if (!in[j]) break;
+        const uint32_t at = fetch_at + j * per_vec;
+        if (has_dy) cp_async16(at, src_dy + j * step);
+        if (O8)
+          cp_async8(at + per_tensor, src_o + j * step);
+        else
+          cp_async16(at + per_tensor, src_o + j * step * 2);
+        if (pre) {
+          cp_async16(at + 2 * per_tensor, src_dh + j * step);
+          cp_async16(at + 3 * per_tensor, src_y + j * step);
+        }
       }
       src_dy += a.ld_dy;
       src_dh += a.ld_dh;
       src_y += a.ld_y;
       src_o += a.ld_o * (O8 ? 1 : 2);
+      --left;
     }
-    ++fetch_row;
     fetch_at += per_stage;
-    if (fetch_at == ring_bytes) fetch_at = 0;
+    stats_fetch += kMostWarps * 16;
+    if (fetch_at == ring_end) {
+      fetch_at = mine;
+      stats_fetch = stats_mine;
+    }
     cp_async_commit();
   };
+  for (int s = 0; s < ahead; ++s) fetch();
+
+  // Exponents are read one step ahead of their rows.
+  const uint8_t* exps[VEC];
+  int64_t exps_left = hi - lo;
 #pragma unroll
-  for (int s = 0; s < AHEAD; ++s) fetch();
-  auto value8 = [&](uint32_t at, int t) {
-    return unpack8(*reinterpret_cast<const uint4*>(slots + at + t * per_tensor));
+  for (int j = 0; j < VEC; ++j)
+    exps[j] = O8 ? a.o_exps + lo * a.ld_o_exps + (in[j] ? (col + j * step) / 32 : 0) : nullptr;
+  unsigned next_e[2][VEC];
+  auto read_ahead = [&](int n) {  // the rows n and n + 1 behind the current ones
+    if (!O8) return;
+    exps_left -= n;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      exps[j] += n * a.ld_o_exps;
+      if (exps_left > 0) next_e[0][j] = load_now(exps[j]);
+      if (exps_left > 1) next_e[1][j] = load_now(exps[j] + a.ld_o_exps);
+    }
   };
+  read_ahead(0);
 
   __nv_bfloat16* out_dx = a.dx + lo * a.ld_dx + col;
   __nv_bfloat16* out_do = a.d_o + lo * a.ld_do + col;
-  const uint64_t alpha = f2(a.alpha, a.alpha);
-  int64_t seg = 0, seg_end = lo;
-  uint32_t stage_at = 0;
-  int n;
-  for (int64_t row = lo; row < hi; row += n) {
-    if (row >= seg_end) {  // the first row, or the first of another gate
-      seg = row / rows_per_gate;
-      seg_end = (seg + 1) * rows_per_gate;
-      w = splat(1.f);
-      if (in) {
-        if (a.gate) w = load8(a.gate + seg * a.hidden + col, 0);
-        if (post) {
-          const V8 f = load8(a.post_gamma + col, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w.p[e] = f2_mul(w.p[e], f.p[e]);
-        }
-      }
-    }
-    // Two rows of one gate at a time: they share the barriers of the two rounds of sums.
-    const int64_t end = seg_end < hi ? seg_end : hi;
-    n = row + 1 < end ? 2 : 1;
-    float4 st[2];
-    float o_scale[2] = {1.f, 1.f};
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      st[r] = __ldg(a.stats + row + (r < n ? r : 0));
-      if (O8 && in && r < n)
-        o_scale[r] = ckpt_scale(__ldg(a.o_exps + (row + r) * a.ld_o_exps + col / 32));
-    }
-    fetch();
-    if (n == 2) fetch();
-    cp_async_wait<AHEAD>();
-    uint32_t at[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      at[r] = stage_at;
-      if (r < n) stage_at += per_stage;
-      if (stage_at == ring_bytes) stage_at = 0;
-    }
+  uint32_t stage_at = mine;
 
-    auto hat = [](V8 v, float mean, float r) {  // (v - mean) / sd
-      const uint64_t rr = f2(r, r), c = f2(-mean, -mean);
+  auto hat = [](V8 v, float mean, float r) {  // (v - mean) / sd
+    const uint64_t rr = f2(r, r), c = f2(-mean, -mean);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v.p[e] = f2_mul(RMS ? v.p[e] : f2_add(v.p[e], c), rr);
-      return v;
-    };
-    float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (pre) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint64_t s1 = 0, s2 = 0;
-        if (in && r < n) {
-          const V8 g = value8(at[r], 2), yh = hat(value8(at[r], 3), st[r].z, st[r].w);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (!RMS) S2.p[e] = f2_add(S2.p[e], g.p[e]);
-            S3.p[e] = f2_fma(g.p[e], yh.p[e], S3.p[e]);
-            const uint64_t gg = f2_mul(g.p[e], gn.p[e]);
-            if (!RMS) s1 = f2_add(s1, gg);
-            s2 = f2_fma(gg, yh.p[e], s2);
-          }
-        }
-        if (r) m.z = both(s1), m.w = both(s2);
-        else m.x = both(s1), m.y = both(s2);
-      }
-      m = row_sum4<CLUSTER>(m, red, &ex, turns, cluster, rank, a.status);
+    for (int e = 0; e < 4; ++e) v.p[e] = f2_mul(RMS ? v.p[e] : f2_add(v.p[e], c), rr);
+    return v;
+  };
+  auto load_oh = [&](uint32_t at, unsigned exponent, const float4& st) {
+    V8 v;
+    if (O8) {
+      const float scale = ckpt_scale(exponent);
+      const uint2 c = lds8(at + per_tensor);
+      uint64_t q[2];
+      ckpt_unpack4_scaled(c.x, scale, q);
+      v.p[0] = q[0], v.p[1] = q[1];
+      ckpt_unpack4_scaled(c.y, scale, q);
+      v.p[2] = q[0], v.p[3] = q[1];
+    } else {
+      v = unpack8(lds16(at + per_tensor));
     }
-    auto load_o = [&](int r) {
-      V8 v;
-      if (O8) {
-        const uint2 c = *reinterpret_cast<const uint2*>(slots + at[r] + per_tensor);
-        uint64_t f[2];
-        ckpt_unpack4_scaled(c.x, o_scale[r], f);
-        v.p[0] = f[0], v.p[1] = f[1];
-        ckpt_unpack4_scaled(c.y, o_scale[r], f);
-        v.p[2] = f[0], v.p[3] = f[1];
-      } else {
-        v = value8(at[r], 1);
-      }
-      return post ? hat(v, st[r].x, st[r].y) : v;
-    };
-    float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
+    return post ? hat(v, st.x, st.y) : v;
+  };
+
+  // Sums of a row: m2, B1, B2, B4, and of a layer norm m1, A1, A2, A3, A4, B3 as well.
+  constexpr int SUMS = RMS ? 4 : 10;
+  float w_sum = 0.f;  // of this thread's weights
+  // N rows of one gate.
+  auto rows = [&](auto count) {
+    constexpr int N = decltype(count)::value;
+    float4 st[N];
+    unsigned ex8[N][VEC];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      uint64_t s1 = 0, s2 = 0;
-      if (in && r < n) {
-        V8 d = a.dy ? value8(at[r], 0) : splat(0.f);
-        if (pre) {
-          const V8 g = value8(at[r], 2), yh = hat(value8(at[r], 3), st[r].z, st[r].w);
-          // d += (g gn - m1 - yh m2) / sd
-          const float m1 = (r ? m.z : m.x) * -inv_n, m2 = (r ? m.w : m.y) * -inv_n;
-          const uint64_t c1 = f2(m1, m1), c2 = f2(m2, m2), sd = f2(st[r].w, st[r].w);
+    for (int r = 0; r < N; ++r) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) ex8[r][j] = O8 ? next_e[r][j] : 0;
+    }
+    read_ahead(N);
+#pragma unroll
+    for (int r = 0; r < N; ++r) fetch();
+    wait_ahead<2>(ahead);
+    __syncwarp();  // lane 0's copies of the statistics are the whole warp's
+    uint32_t at[N];
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      at[r] = stage_at;
+      const uint4 q = lds16(stats_at);
+      st[r] = make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
+                          __uint_as_float(q.w));
+      stage_at += per_stage;
+      stats_at += kMostWarps * 16;
+      if (stage_at == ring_end) {
+        stage_at = mine;
+        stats_at = stats_mine;
+      }
+    }
+    float v[(SUMS * N + 3) / 4 * 4];
+    if (pre || post) {
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        uint64_t t[SUMS];
+#pragma unroll
+        for (int e = 0; e < SUMS; ++e) t[e] = 0;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const uint32_t p = at[r] + j * per_vec;
+          const V8 d = unpack8(lds16(p)), oh = load_oh(p, ex8[r][j], st[r]);
+          const V8 g = unpack8(lds16(p + 2 * per_tensor));
+          const V8 yh = hat(unpack8(lds16(p + 3 * per_tensor)), st[r].z, st[r].w);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint64_t t = RMS ? f2_mul(yh.p[e], c2) : f2_fma(yh.p[e], c2, c1);
-            d.p[e] = f2_fma(sd, f2_fma(g.p[e], gn.p[e], t), d.p[e]);
+            const uint64_t gg = f2_mul(g.p[e], gn[j].p[e]), wo = f2_mul(w[j].p[e], oh.p[e]);
+            t[0] = f2_fma(gg, yh.p[e], t[0]);
+            t[1] = f2_fma(wo, d.p[e], t[1]);
+            t[2] = f2_fma(wo, gg, t[2]);
+            t[3] = f2_fma(wo, yh.p[e], t[3]);
+            if constexpr (!RMS) {
+              t[4] = f2_add(t[4], gg);
+              t[5] = f2_fma(w[j].p[e], d.p[e], t[5]);
+              t[6] = f2_fma(w[j].p[e], gg, t[6]);
+              t[8] = f2_fma(w[j].p[e], yh.p[e], t[8]);
+              t[9] = f2_add(t[9], wo);
+            }
           }
         }
-        V8 f;
+#pragma unroll
+        for (int e = 0; e < SUMS; ++e) v[r * SUMS + e] = e == 7 ? w_sum : both(t[e]);
+      }
+#pragma unroll
+      for (int e = SUMS * N; e < (SUMS * N + 3) / 4 * 4; ++e) v[e] = 0.f;
+      row_sums<(SUMS * N + 3) / 4 * 4, CLUSTER>(v, ex, turns, cluster, rank, a.status);
+    }
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      float m1 = 0.f, m2 = 0.f, k1 = 0.f, k2 = 0.f;  // less the means
+      const float* q = v + r * SUMS;
+      if (pre) {
+        m2 = q[0] * inv_n;
+        if constexpr (!RMS) m1 = q[4] * inv_n;
+      }
+      if (post) {
+        float b = fmaf(m2, q[3], q[2]);
+        if constexpr (!RMS) {
+          b = fmaf(m1, q[9], b);
+          k1 = fmaf(st[r].w, fmaf(m1, q[7], fmaf(m2, q[8], q[6])), q[5]) * inv_n;
+        }
+        k2 = fmaf(st[r].w, b, q[1]) * inv_n;
+      }
+      const uint64_t c1 = f2(m1, m1), c2 = f2(m2, m2), sd = f2(st[r].w, st[r].w);
+      const uint64_t e1 = f2(k1, k1), e2 = f2(k2, k2), so = f2(st[r].y, st[r].y);
+      const uint64_t alpha = f2(a.alpha, a.alpha);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const uint32_t p = at[r] + j * per_vec;
+        V8 d = unpack8(lds16(p)), f;
+        if (pre) {
+          const V8 g = unpack8(lds16(p + 2 * per_tensor));
+          const V8 yh = hat(unpack8(lds16(p + 3 * per_tensor)), st[r].z, st[r].w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (!RMS) S2[j].p[e] = f2_add(S2[j].p[e], g.p[e]);
+            S3[j].p[e] = f2_fma(g.p[e], yh.p[e], S3[j].p[e]);
+            const uint64_t t = RMS ? f2_mul(yh.p[e], c2) : f2_fma(yh.p[e], c2, c1);
+            d.p[e] = f2_fma(sd, f2_fma(g.p[e], gn[j].p[e], t), d.p[e]);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) f.p[e] = f2_mul(alpha, d.p[e]);
-        *reinterpret_cast<uint4*>(out_dx + r * a.ld_dx) = pack8(f);
-        const V8 oh = load_o(r);
+        if (in[j]) *reinterpret_cast<uint4*>(out_dx + j * step) = pack8(f);
+        const V8 oh = load_oh(p, ex8[r][j], st[r]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (!RMS) S0.p[e] = f2_add(S0.p[e], d.p[e]);
-          S1.p[e] = f2_fma(d.p[e], oh.p[e], S1.p[e]);
-          d.p[e] = f2_mul(d.p[e], w.p[e]);
-          if (!RMS) s1 = f2_add(s1, d.p[e]);
-          s2 = f2_fma(d.p[e], oh.p[e], s2);
-        }
-        if (post) {
-          // kept for the second round in this thread's own slots, whose values are used up
-          char* mine = slots + at[r];
-          store_v8(mine, mine + 2 * per_tensor, d);
-          store_v8(mine + per_tensor, mine + 3 * per_tensor, oh);
-        } else {
-          *reinterpret_cast<uint4*>(out_do + r * a.ld_do) = pack8(d);
-        }
-      }
-      if (r) k.z = both(s1), k.w = both(s2);
-      else k.x = both(s1), k.y = both(s2);
-    }
-    if (post) {
-      k = row_sum4<CLUSTER>(k, red, &ex, turns, cluster, rank, a.status);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (in && r < n) {
-          const float k1 = (r ? k.z : k.x) * -inv_n, k2 = (r ? k.w : k.y) * -inv_n;
-          const uint64_t c1 = f2(k1, k1), c2 = f2(k2, k2), sd = f2(st[r].y, st[r].y);
-          const char* mine = slots + at[r];
-          V8 d = load_v8(mine, mine + 2 * per_tensor);
-          const V8 oh = load_v8(mine + per_tensor, mine + 3 * per_tensor);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint64_t t = RMS ? f2_fma(oh.p[e], c2, d.p[e]) : f2_add(f2_fma(oh.p[e], c2, c1), d.p[e]);
-            d.p[e] = f2_mul(sd, t);
+          if (!RMS) S0[j].p[e] = f2_add(S0[j].p[e], d.p[e]);
+          S1[j].p[e] = f2_fma(d.p[e], oh.p[e], S1[j].p[e]);
+          d.p[e] = f2_mul(d.p[e], w[j].p[e]);
+          if (post) {
+            d.p[e] = f2_fma(oh.p[e], e2, d.p[e]);
+            d.p[e] = f2_mul(so, RMS ? d.p[e] : f2_add(d.p[e], e1));
           }
-          *reinterpret_cast<uint4*>(out_do + r * a.ld_do) = pack8(d);
+        }
+        if (in[j]) *reinterpret_cast<uint4*>(out_do + j * step) = pack8(d);
+      }
+      out_dx += a.ld_dx;
+      out_do += a.ld_do;
+    }
+  };
+
+  for (int64_t row = lo; row < hi;) {  // the rows of one gate after those of another
+    const int64_t seg = row / rows_per_gate;
+    const int64_t seg_end = (seg + 1) * rows_per_gate;
+    const int64_t end = seg_end < hi ? seg_end : hi;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      w[j] = splat(in[j] ? 1.f : 0.f);
+      if (in[j]) {
+        if (a.gate) w[j] = load8(a.gate + seg * a.hidden + col + j * step, 0);
+        if (post) {
+          const V8 f = load8(a.post_gamma + col + j * step, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[j].p[e] = f2_mul(w[j].p[e], f.p[e]);
         }
       }
     }
-    out_dx += n * a.ld_dx;
-    out_do += n * a.ld_do;
-
-    if (in && row + n == end) {  // this gate's rows of this run end here
-      float* dst = a.partials + (group + seg) * 2 * a.hidden + col;
-      store_v8(dst, dst + 4, S0);
-      store_v8(dst + a.hidden, dst + a.hidden + 4, S1);
-      S0 = S1 = splat(0.f);
+    if (!RMS) {
+      uint64_t t = 0;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t = f2_add(t, w[j].p[e]);
+      w_sum = both(t);
+    }
+    int pairs = static_cast<int>((end - row) >> 1);
+    for (; pairs > 0; --pairs) rows(std::integral_constant<int, 2>());
+    if ((end - row) & 1) rows(std::integral_constant<int, 1>());
+    row = end;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      if (in[j]) {
+        float* dst = a.partials + (group + seg) * 2 * a.hidden + col + j * step;
+        store_v8(dst, S0[j]);
+        store_v8(dst + a.hidden, S1[j]);
+      }
+      S0[j] = S1[j] = splat(0.f);
     }
   }
-  if (in && pre) {
-    float* dst = a.partials + (groups + a.gates) * 2 * a.hidden + group * 2 * static_cast<int64_t>(a.hidden) + col;
-    store_v8(dst, dst + 4, S2);
-    store_v8(dst + a.hidden, dst + a.hidden + 4, S3);
-  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+    if (in[j] && pre) {
+      float* dst = a.partials + (groups + a.gates) * 2 * a.hidden +
+                   group * 2 * static_cast<int64_t>(a.hidden) + col + j * step;
+      store_v8(dst, S2[j]);
+      store_v8(dst + a.hidden, S3[j]);
+    }
   cp_async_wait<0>();
   if constexpr (CLUSTER) cluster_sync();  // no block leaves while another may still write to it
 }
@@ -634,9 +756,9 @@ cudaError_t launch_forward(const NormArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <int STAGES, bool CLUSTER, bool RMS, bool O8>
-cudaError_t launch_backward(const NormArgs& a, const BackPlan& p, cudaStream_t stream) {
-  auto kern = norm_residual_backward_kernel<STAGES, CLUSTER, RMS, O8>;
+template <int VEC, bool RMS, bool O8, bool FULL>
+cudaError_t launch_backward(const NormArgs& a, BackPlan& p, cudaStream_t stream) {
+  auto kern = norm_residual_backward_kernel<VEC, RMS, O8, FULL>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(p.smem));
   if (e != cudaSuccess) return e;
@@ -646,29 +768,33 @@ cudaError_t launch_backward(const NormArgs& a, const BackPlan& p, cudaStream_t s
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
-  if (CLUSTER) {
+  if (VEC == 2) {
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = p.cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
   }
-  return cudaLaunchKernelEx(&cfg, kern, a, p.cluster, p.slice, p.groups);
+  if (p.cluster > 2) {
+    // Larger clusters leave SMs over in each GPC: as many groups as run at once, or the last would
+    // be a wave of their own.
+    static std::atomic<int> known[9];
+    int most = known[p.cluster].load(std::memory_order_relaxed);
+    if (most == 0) {
+      e = cudaOccupancyMaxActiveClusters(&most, kern, &cfg);
+      if (e != cudaSuccess) return e;
+      known[p.cluster].store(most > 0 ? most : 1, std::memory_order_relaxed);
+    }
+    if (most > 0 && p.groups > most) p.groups = most;
+    cfg.gridDim = dim3(p.groups * p.cluster);
+  }
+  return cudaLaunchKernelEx(&cfg, kern, a, p.cluster, p.slice, p.groups, p.stages);
 }
 
-template <int STAGES>
-cudaError_t launch_backward_stages(const NormArgs& a, const BackPlan& p, cudaStream_t stream) {
-  const int key = (p.cluster > 1 ? 4 : 0) + (a.rms ? 2 : 0) + (a.o_exps ? 1 : 0);
-  switch (key) {
-    case 0: return launch_backward<STAGES, false, false, false>(a, p, stream);
-    case 1: return launch_backward<STAGES, false, false, true>(a, p, stream);
-    case 2: return launch_backward<STAGES, false, true, false>(a, p, stream);
-    case 3: return launch_backward<STAGES, false, true, true>(a, p, stream);
-    case 4: return launch_backward<STAGES, true, false, false>(a, p, stream);
-    case 5: return launch_backward<STAGES, true, false, true>(a, p, stream);
-    case 6: return launch_backward<STAGES, true, true, false>(a, p, stream);
-    default: return launch_backward<STAGES, true, true, true>(a, p, stream);
-  }
+template <int VEC, bool RMS, bool O8>
+cudaError_t launch_backward(const NormArgs& a, BackPlan& p, cudaStream_t stream) {
+  return a.dy && a.dh && a.post_gamma ? launch_backward<VEC, RMS, O8, true>(a, p, stream)
+                                      : launch_backward<VEC, RMS, O8, false>(a, p, stream);
 }
 
 }  // namespace
@@ -685,10 +811,18 @@ size_t norm_backward_partials(int64_t rows, int64_t hidden, int64_t gates, int s
 }
 
 cudaError_t launch_norm_residual_backward(const NormArgs& a, cudaStream_t stream) {
-  const BackPlan p = back_plan(a.rows, a.hidden, a.sms);
-  cudaError_t e = p.stages == 6   ? launch_backward_stages<6>(a, p, stream)
-                  : p.stages == 5 ? launch_backward_stages<5>(a, p, stream)
-                                  : launch_backward_stages<4>(a, p, stream);
+  BackPlan p = back_plan(a.rows, a.hidden, a.sms);
+  cudaError_t e;
+  switch ((p.vec > 1 ? 4 : 0) + (a.rms ? 2 : 0) + (a.o_exps ? 1 : 0)) {
+    case 0: e = launch_backward<1, false, false>(a, p, stream); break;
+    case 1: e = launch_backward<1, false, true>(a, p, stream); break;
+    case 2: e = launch_backward<1, true, false>(a, p, stream); break;
+    case 3: e = launch_backward<1, true, true>(a, p, stream); break;
+    case 4: e = launch_backward<2, false, false>(a, p, stream); break;
+    case 5: e = launch_backward<2, false, true>(a, p, stream); break;
+    case 6: e = launch_backward<2, true, false>(a, p, stream); break;
+    default: e = launch_backward<2, true, true>(a, p, stream);
+  }
   if (e != cudaSuccess) return e;
   const unsigned each = a.dgate && a.gates > 1 ? static_cast<unsigned>(a.gates) : 0;
   norm_backward_join_kernel<<<dim3((a.hidden + 31) / 32, 2 + each), kJoinWarps * 32, 0, stream>>>(
