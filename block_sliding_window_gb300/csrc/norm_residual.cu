@@ -356,6 +356,21 @@ __device__ __forceinline__ void sts16(uint32_t at, uint4 v) {
                "r"(v.w) : "memory");
 }
 
+// pre_gamma of eight channels: as fp32 pairs, or as it is stored where registers are short (a layer
+// norm has twice the sums to keep).
+template <bool WIDE>
+struct Gamma {
+  V8 v;
+  __device__ __forceinline__ void set(uint4 q) { v = unpack8(q); }
+  __device__ __forceinline__ const V8& get() const { return v; }
+};
+template <>
+struct Gamma<false> {
+  uint4 q;
+  __device__ __forceinline__ void set(uint4 p) { q = p; }
+  __device__ __forceinline__ V8 get() const { return unpack8(q); }
+};
+
 // FULL: both norms and both gradients are there (the usual call); else a.dy, post_gamma or pre_gamma
 // may be absent.
 template <int VEC, bool RMS, bool O8, bool FULL>
@@ -392,11 +407,13 @@ __global__ void __launch_bounds__(VEC == 1 ? kSlice1 / 8 : kSlice2 / 16, 1)
     cluster_sync();
   }
 
-  V8 S0[VEC], S1[VEC], S2[VEC], S3[VEC], w[VEC], gn[VEC];
+  V8 S0[VEC], S1[VEC], S2[VEC], S3[VEC], w[VEC];
+  Gamma<RMS> gn[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
-    S0[j] = S1[j] = S2[j] = S3[j] = gn[j] = splat(0.f);
-    if (in[j] && pre) gn[j] = load8(a.pre_gamma + col + j * step, 0);
+    S0[j] = S1[j] = S2[j] = S3[j] = splat(0.f);
+    gn[j].set(in[j] && pre ? __ldg(reinterpret_cast<const uint4*>(a.pre_gamma + col + j * step))
+                           : make_uint4(0, 0, 0, 0));
   }
 
   // This thread's slots: 16 bytes of each tensor and vector.
@@ -537,10 +554,10 @@ __global__ void __launch_bounds__(VEC == 1 ? kSlice1 / 8 : kSlice2 / 16, 1)
           const uint32_t p = at[r] + j * per_vec;
           const V8 d = unpack8(lds16(p)), oh = load_oh(p, ex8[r][j], st[r]);
           const V8 g = unpack8(lds16(p + 2 * per_tensor));
-          const V8 yh = hat(unpack8(lds16(p + 3 * per_tensor)), st[r].z, st[r].w);
+          const V8 yh = hat(unpack8(lds16(p + 3 * per_tensor)), st[r].z, st[r].w), gamma = gn[j].get();
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint64_t gg = f2_mul(g.p[e], gn[j].p[e]), wo = f2_mul(w[j].p[e], oh.p[e]);
+            const uint64_t gg = f2_mul(g.p[e], gamma.p[e]), wo = f2_mul(w[j].p[e], oh.p[e]);
             t[0] = f2_fma(gg, yh.p[e], t[0]);
             t[1] = f2_fma(wo, d.p[e], t[1]);
             t[2] = f2_fma(wo, gg, t[2]);
@@ -561,24 +578,28 @@ __global__ void __launch_bounds__(VEC == 1 ? kSlice1 / 8 : kSlice2 / 16, 1)
       for (int e = SUMS * N; e < (SUMS * N + 3) / 4 * 4; ++e) v[e] = 0.f;
       row_sums<(SUMS * N + 3) / 4 * 4, CLUSTER>(v, ex, turns, cluster, rank, a.status);
     }
+    float m1[N], m2[N], k1[N], k2[N];  // less the means
 #pragma unroll
     for (int r = 0; r < N; ++r) {
-      float m1 = 0.f, m2 = 0.f, k1 = 0.f, k2 = 0.f;  // less the means
+      m1[r] = m2[r] = k1[r] = k2[r] = 0.f;
       const float* q = v + r * SUMS;
       if (pre) {
-        m2 = q[0] * inv_n;
-        if constexpr (!RMS) m1 = q[4] * inv_n;
+        m2[r] = q[0] * inv_n;
+        if constexpr (!RMS) m1[r] = q[4] * inv_n;
       }
       if (post) {
-        float b = fmaf(m2, q[3], q[2]);
+        float b = fmaf(m2[r], q[3], q[2]);
         if constexpr (!RMS) {
-          b = fmaf(m1, q[9], b);
-          k1 = fmaf(st[r].w, fmaf(m1, q[7], fmaf(m2, q[8], q[6])), q[5]) * inv_n;
+          b = fmaf(m1[r], q[9], b);
+          k1[r] = fmaf(st[r].w, fmaf(m1[r], q[7], fmaf(m2[r], q[8], q[6])), q[5]) * inv_n;
         }
-        k2 = fmaf(st[r].w, b, q[1]) * inv_n;
+        k2[r] = fmaf(st[r].w, b, q[1]) * inv_n;
       }
-      const uint64_t c1 = f2(m1, m1), c2 = f2(m2, m2), sd = f2(st[r].w, st[r].w);
-      const uint64_t e1 = f2(k1, k1), e2 = f2(k2, k2), so = f2(st[r].y, st[r].y);
+    }
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      const uint64_t c1 = f2(m1[r], m1[r]), c2 = f2(m2[r], m2[r]), sd = f2(st[r].w, st[r].w);
+      const uint64_t e1 = f2(k1[r], k1[r]), e2 = f2(k2[r], k2[r]), so = f2(st[r].y, st[r].y);
       const uint64_t alpha = f2(a.alpha, a.alpha);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
@@ -586,13 +607,13 @@ __global__ void __launch_bounds__(VEC == 1 ? kSlice1 / 8 : kSlice2 / 16, 1)
         V8 d = unpack8(lds16(p)), f;
         if (pre) {
           const V8 g = unpack8(lds16(p + 2 * per_tensor));
-          const V8 yh = hat(unpack8(lds16(p + 3 * per_tensor)), st[r].z, st[r].w);
+          const V8 yh = hat(unpack8(lds16(p + 3 * per_tensor)), st[r].z, st[r].w), gamma = gn[j].get();
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (!RMS) S2[j].p[e] = f2_add(S2[j].p[e], g.p[e]);
             S3[j].p[e] = f2_fma(g.p[e], yh.p[e], S3[j].p[e]);
             const uint64_t t = RMS ? f2_mul(yh.p[e], c2) : f2_fma(yh.p[e], c2, c1);
-            d.p[e] = f2_fma(sd, f2_fma(g.p[e], gn[j].p[e], t), d.p[e]);
+            d.p[e] = f2_fma(sd, f2_fma(g.p[e], gamma.p[e], t), d.p[e]);
           }
         }
 #pragma unroll
