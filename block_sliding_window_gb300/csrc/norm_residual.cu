@@ -204,27 +204,37 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(const __grid_constan
 // are split over a cluster, whose blocks exchange their sums through each other's shared memory.
 // The blocks' sums are joined by a second kernel in a fixed order.
 
-// Channels of one block.  Up to 5120 a thread has 8 (640 threads of 96 registers); beyond, 16 (384
-// threads of 168), or the sums of a layer norm would not fit in registers.
-constexpr int kSlice1 = 5120, kSlice2 = 6144;
+// Channels of one block and of a thread.  A thread keeps the sums of its channels in registers, two
+// for a channel of an rms norm and four for one of a layer norm, and a quarter of the SM has
+// registers for whole warps only:
+//   rms norms    up to 5120 channels 640 threads of 8 (96 registers), else 384 of 16 (168) a slice;
+//   layer norms  256 threads of 16 or 24 (248).  With 168 registers the sums spill: LN_FIGURE
 constexpr int kRing = 200 * 1024;  // shared memory for rows, per SM
+
+template <int VEC, bool RMS>
+__host__ __device__ constexpr int back_threads() {
+  return RMS ? (VEC == 1 ? 640 : 384) : 256;
+}
 
 struct BackPlan {
   int vec, cluster, threads, slice, groups, stages;
   size_t smem;
 };
 
-BackPlan back_plan(int64_t rows, int64_t hidden, int sms) {
+BackPlan back_plan(int64_t rows, int64_t hidden, bool rms, int sms) {
   BackPlan p;
-  p.vec = hidden <= kSlice1 ? 1 : 2;
-  const int most = p.vec == 1 ? kSlice1 : kSlice2;
-  p.cluster = static_cast<int>((hidden + most - 1) / most);
+  const int most = !rms                                ? back_threads<3, false>()
+                   : hidden <= back_threads<1, true>() * 8 ? back_threads<1, true>()
+                                                           : back_threads<2, true>();
+  p.vec = !rms ? 3 : most == back_threads<1, true>() ? 1 : 2;
+  const int slice = most * p.vec * 8;
+  p.cluster = static_cast<int>((hidden + slice - 1) / slice);
   const int64_t vecs = (hidden / 8 + p.cluster - 1) / p.cluster;
+  if (!rms && vecs <= 2 * most) p.vec = 2;
   p.slice = static_cast<int>(vecs) * 8;
   p.threads = static_cast<int>(((vecs + p.vec - 1) / p.vec + 31) / 32) * 32;
-  int per_sm = p.vec == 1 ? kSlice1 / 8 / p.threads : 1;  // what the registers allow
-  if (per_sm < 1) per_sm = 1;
-  if (per_sm > 8) per_sm = 8;
+  int per_sm = p.cluster == 1 ? most / p.threads : 1;  // what the registers allow
+  if (per_sm > 10) per_sm = 10;
   int64_t groups = static_cast<int64_t>(sms / p.cluster) * per_sm;
   if (groups > rows) groups = rows;
   p.groups = static_cast<int>(groups < 1 ? 1 : groups);
@@ -256,7 +266,7 @@ __device__ __forceinline__ void wait_ahead(int ahead) {
 }
 
 constexpr int kMostSums = 20;
-constexpr int kMostWarps = kSlice1 / 8 / 32;
+constexpr int kMostWarps = back_threads<1, true>() / 32;
 
 // What the threads of a row, and the blocks of a cluster, tell each other.  Blocks send their sums
 // into each other's `peer` slots, each message counting its bytes on the receiver's barrier of the
@@ -373,11 +383,9 @@ struct Gamma<false> {
 
 // FULL: both norms and both gradients are there (the usual call); else a.dy, post_gamma or pre_gamma
 // may be absent.
-template <int VEC, bool RMS, bool O8, bool FULL>
-__global__ void __launch_bounds__(VEC == 1 ? kSlice1 / 8 : kSlice2 / 16, 1)
-    norm_residual_backward_kernel(const __grid_constant__ NormArgs a, int cluster, int slice, int groups,
-                                  int stages) {
-  constexpr bool CLUSTER = VEC == 2;
+template <int VEC, bool CLUSTER, bool RMS, bool O8, bool FULL>
+__device__ __forceinline__ void backward_rows(const NormArgs& a, int cluster, int slice, int groups,
+                                              int stages) {
   extern __shared__ __align__(16) uint4 ring[];  // [stages][4][VEC][blockDim.x]
   __shared__ __align__(16) Exchange ex;
   const int ahead = stages - 2;  // rows on their way while two are worked on
@@ -557,6 +565,7 @@ __global__ void __launch_bounds__(VEC == 1 ? kSlice1 / 8 : kSlice2 / 16, 1)
           const V8 yh = hat(unpack8(lds16(p + 3 * per_tensor)), st[r].z, st[r].w), gamma = gn[j].get();
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
+            if (RMS) S3[j].p[e] = f2_fma(g.p[e], yh.p[e], S3[j].p[e]);
             const uint64_t gg = f2_mul(g.p[e], gamma.p[e]), wo = f2_mul(w[j].p[e], oh.p[e]);
             t[0] = f2_fma(gg, yh.p[e], t[0]);
             t[1] = f2_fma(wo, d.p[e], t[1]);
@@ -598,7 +607,10 @@ __global__ void __launch_bounds__(VEC == 1 ? kSlice1 / 8 : kSlice2 / 16, 1)
     }
 #pragma unroll
     for (int r = 0; r < N; ++r) {
-      const uint64_t c1 = f2(m1[r], m1[r]), c2 = f2(m2[r], m2[r]), sd = f2(st[r].w, st[r].w);
+      // d = dy + gg / sd + c1 + c2 yh (c2 y for rms norms)
+      const float y2 = st[r].w * m2[r] * (RMS ? st[r].w : 1.f), y1 = st[r].w * m1[r];
+      const uint64_t c1 = f2(y1, y1), c2 = f2(y2, y2), sd = f2(st[r].w, st[r].w);
+      const uint64_t my = f2(-st[r].z, -st[r].z);
       const uint64_t e1 = f2(k1[r], k1[r]), e2 = f2(k2[r], k2[r]), so = f2(st[r].y, st[r].y);
       const uint64_t alpha = f2(a.alpha, a.alpha);
 #pragma unroll
@@ -606,14 +618,21 @@ __global__ void __launch_bounds__(VEC == 1 ? kSlice1 / 8 : kSlice2 / 16, 1)
         const uint32_t p = at[r] + j * per_vec;
         V8 d = unpack8(lds16(p)), f;
         if (pre) {
-          const V8 g = unpack8(lds16(p + 2 * per_tensor));
-          const V8 yh = hat(unpack8(lds16(p + 3 * per_tensor)), st[r].z, st[r].w), gamma = gn[j].get();
+          const V8 g = unpack8(lds16(p + 2 * per_tensor)), y = unpack8(lds16(p + 3 * per_tensor));
+          const V8 gamma = gn[j].get();
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (!RMS) S2[j].p[e] = f2_add(S2[j].p[e], g.p[e]);
-            S3[j].p[e] = f2_fma(g.p[e], yh.p[e], S3[j].p[e]);
-            const uint64_t t = RMS ? f2_mul(yh.p[e], c2) : f2_fma(yh.p[e], c2, c1);
-            d.p[e] = f2_fma(sd, f2_fma(g.p[e], gamma.p[e], t), d.p[e]);
+            uint64_t t = d.p[e];
+            if constexpr (RMS) {
+              t = f2_fma(y.p[e], c2, t);
+            } else {
+              // here and not in the first look, where the sums take the registers
+              const uint64_t yh = f2_mul(f2_add(y.p[e], my), sd);
+              S2[j].p[e] = f2_add(S2[j].p[e], g.p[e]);
+              S3[j].p[e] = f2_fma(g.p[e], yh, S3[j].p[e]);
+              t = f2_fma(yh, c2, f2_add(t, c1));
+            }
+            d.p[e] = f2_fma(sd, f2_mul(g.p[e], gamma.p[e]), t);
           }
         }
 #pragma unroll
@@ -687,71 +706,97 @@ __global__ void __launch_bounds__(VEC == 1 ? kSlice1 / 8 : kSlice2 / 16, 1)
   if constexpr (CLUSTER) cluster_sync();  // no block leaves while another may still write to it
 }
 
-// Joins the blocks' sums.  blockIdx.y = 0: dpost_gamma, dpost_beta and a single gate's dgate; 1:
-// dpre_gamma, dpre_beta; 2 + g: dgate of gate g of several.  32 channels a block; its warps take the
-// runs of rows in turn and their sums are added in order.
-constexpr int kJoinWarps = 16;
+template <int VEC, bool CLUSTER, bool O8, bool FULL>
+__global__ void __launch_bounds__(back_threads<VEC, true>(), 1)
+    norm_backward_rms_kernel(const __grid_constant__ NormArgs a, int cluster, int slice, int groups,
+                             int stages) {
+  backward_rows<VEC, CLUSTER, true, O8, FULL>(a, cluster, slice, groups, stages);
+}
 
-__global__ void __launch_bounds__(kJoinWarps * 32)
+template <int VEC, bool CLUSTER, bool O8, bool FULL>
+__global__ void __maxnreg__(248)
+    norm_backward_layer_kernel(const __grid_constant__ NormArgs a, int cluster, int slice, int groups,
+                               int stages) {
+  backward_rows<VEC, CLUSTER, false, O8, FULL>(a, cluster, slice, groups, stages);
+}
+
+// Joins the blocks' sums.  blockIdx.y = 0: dpost_gamma, dpost_beta and a single gate's dgate; 1:
+// dpre_gamma, dpre_beta; 2 + g: dgate of gate g of several.  A block has 32 channels, 8 threads of 4
+// beside one another, and deals the runs of rows to its 32 groups of 8 threads: each has a handful of
+// loads, all in flight at once.  The groups' sums are added in order.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads)
     norm_backward_join_kernel(const __grid_constant__ NormArgs a, int groups) {
-  __shared__ float part[2][kJoinWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;
+  __shared__ float4 part[2][32][8];
+  const int quad = threadIdx.x & 7, lot = threadIdx.x >> 3;
+  const int col = blockIdx.x * 32 + quad * 4;
   const bool in = col < a.hidden;
   const int64_t H = a.hidden;
   const bool pre = blockIdx.y == 1, each = blockIdx.y > 1;
-  float s0 = 0.f, s1 = 0.f;
   const int64_t per = a.rows / a.gates;
-  const int64_t first = each ? blockIdx.y - 2 : 0;
-  const int64_t last = each || pre ? first : a.gates - 1;
-  for (int64_t g = first; g <= last; ++g) {
-    // The runs that hold rows of this gate: run c begins at row c * rows / groups.
-    int c0 = 0, c1 = groups - 1;
-    const float* src = a.partials + (groups + a.gates) * 2 * H;
-    if (!pre) {
-      c0 = static_cast<int>(((g * per + 1) * groups - 1) / a.rows);
-      c1 = static_cast<int>(((g + 1) * per * groups - 1) / a.rows);
-      src = a.partials + g * 2 * H;
-    }
-    src += col;
-    float t0 = 0.f, t1 = 0.f;
-    if (in) {
-#pragma unroll 10
-      for (int c = c0 + ((warp - c0) & (kJoinWarps - 1)); c <= c1; c += kJoinWarps) {
-        t0 += __ldcg(src + (c * 2) * H);
-        t1 += __ldcg(src + (c * 2 + 1) * H);
+  float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
+  auto add = [](float4& s, float4 v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
+  auto load = [&](int64_t row) { return __ldcg(reinterpret_cast<const float4*>(a.partials + row * H + col)); };
+  if (in) {
+    if (pre || a.gates == 1) {
+      const int64_t base = pre ? (groups + a.gates) * 2 : 0;
+#pragma unroll 5
+      for (int c = lot; c < groups; c += 32) {
+        add(s0, load(base + 2 * c));
+        add(s1, load(base + 2 * c + 1));
       }
-      const bool weigh = blockIdx.y == 0 && a.gate && a.gates > 1;
-      const float f = weigh ? __bfloat162float(a.gate[g * H + col]) : 1.f;
-      s0 = fmaf(f, t0, s0);
-      s1 = fmaf(f, t1, s1);
+    } else if (each) {
+      // The runs that hold rows of this gate: run c begins at row c * rows / groups.
+      const int64_t g = blockIdx.y - 2;
+      const int c0 = static_cast<int>(((g * per + 1) * groups - 1) / a.rows);
+      const int c1 = static_cast<int>(((g + 1) * per * groups - 1) / a.rows);
+#pragma unroll 2
+      for (int c = c0 + lot; c <= c1; c += 32) {
+        add(s0, load(2 * (c + g)));
+        add(s1, load(2 * (c + g) + 1));
+      }
+    } else {
+      for (int c = lot; c < groups; c += 32) {  // a run's gates
+        const int64_t lo = static_cast<int64_t>(c) * a.rows / groups;
+        const int64_t hi = static_cast<int64_t>(c + 1) * a.rows / groups;
+        for (int64_t g = lo / per; g * per < hi; ++g) {
+          const float4 u = load(2 * (c + g)), v = load(2 * (c + g) + 1);
+          const uint2 q = __ldg(reinterpret_cast<const uint2*>(a.gate + g * H + col));
+          const float4 f = make_float4(bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y));
+          add(s0, make_float4(f.x * u.x, f.y * u.y, f.z * u.z, f.w * u.w));
+          add(s1, make_float4(f.x * v.x, f.y * v.y, f.z * v.z, f.w * v.w));
+        }
+      }
     }
   }
-  part[0][warp][lane] = s0;
-  part[1][warp][lane] = s1;
+  part[0][lot][quad] = s0;
+  part[1][lot][quad] = s1;
   __syncthreads();
-  if (warp != 0 || !in) return;
-  s0 = s1 = 0.f;
+  // One thread a channel from here.
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  if (threadIdx.x >= 32 || c >= a.hidden) return;
+  float t0 = 0.f, t1 = 0.f;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    s0 += part[0][w][lane];
-    s1 += part[1][w][lane];
+  for (int l = 0; l < 32; ++l) {
+    t0 += reinterpret_cast<const float*>(part[0][l])[threadIdx.x];
+    t1 += reinterpret_cast<const float*>(part[1][l])[threadIdx.x];
   }
   if (pre) {
-    if (a.dpre_gamma) a.dpre_gamma[col] = s1;
-    if (a.dpre_beta) a.dpre_beta[col] = s0;
+    if (a.dpre_gamma) a.dpre_gamma[c] = t1;
+    if (a.dpre_beta) a.dpre_beta[c] = t0;
     return;
   }
   if (each || (a.gates == 1 && a.dgate)) {
-    float v = s1;
-    if (a.post_gamma) v *= __bfloat162float(a.post_gamma[col]);
-    if (a.post_beta) v = fmaf(__bfloat162float(a.post_beta[col]), s0, v);
-    a.dgate[first * H + col] = v;
+    float v = t1;
+    if (a.post_gamma) v *= __bfloat162float(a.post_gamma[c]);
+    if (a.post_beta) v = fmaf(__bfloat162float(a.post_beta[c]), t0, v);
+    a.dgate[(each ? blockIdx.y - 2 : 0) * H + c] = v;
   }
   if (!each) {
-    const float f = a.gates == 1 && a.gate ? __bfloat162float(a.gate[col]) : 1.f;
-    if (a.dpost_gamma) a.dpost_gamma[col] = f * s1;
-    if (a.dpost_beta) a.dpost_beta[col] = f * s0;
+    const float f = a.gates == 1 && a.gate ? __bfloat162float(a.gate[c]) : 1.f;
+    if (a.dpost_gamma) a.dpost_gamma[c] = f * t1;
+    if (a.dpost_beta) a.dpost_beta[c] = f * t0;
   }
 }
 
@@ -777,9 +822,13 @@ cudaError_t launch_forward(const NormArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <int VEC, bool RMS, bool O8, bool FULL>
+template <int VEC, bool CLUSTER, bool RMS, bool O8, bool FULL>
 cudaError_t launch_backward(const NormArgs& a, BackPlan& p, cudaStream_t stream) {
-  auto kern = norm_residual_backward_kernel<VEC, RMS, O8, FULL>;
+  void (*kern)(NormArgs, int, int, int, int);
+  if constexpr (RMS)
+    kern = norm_backward_rms_kernel<VEC, CLUSTER, O8, FULL>;
+  else
+    kern = norm_backward_layer_kernel<VEC, CLUSTER, O8, FULL>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(p.smem));
   if (e != cudaSuccess) return e;
@@ -789,7 +838,7 @@ cudaError_t launch_backward(const NormArgs& a, BackPlan& p, cudaStream_t stream)
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
-  if (VEC == 2) {
+  if (CLUSTER) {
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = p.cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
@@ -812,10 +861,14 @@ cudaError_t launch_backward(const NormArgs& a, BackPlan& p, cudaStream_t stream)
   return cudaLaunchKernelEx(&cfg, kern, a, p.cluster, p.slice, p.groups, p.stages);
 }
 
-template <int VEC, bool RMS, bool O8>
+template <int VEC, bool CLUSTER, bool RMS>
 cudaError_t launch_backward(const NormArgs& a, BackPlan& p, cudaStream_t stream) {
-  return a.dy && a.dh && a.post_gamma ? launch_backward<VEC, RMS, O8, true>(a, p, stream)
-                                      : launch_backward<VEC, RMS, O8, false>(a, p, stream);
+  const bool full = a.dy && a.dh && a.post_gamma;
+  if (a.o_exps)
+    return full ? launch_backward<VEC, CLUSTER, RMS, true, true>(a, p, stream)
+                : launch_backward<VEC, CLUSTER, RMS, true, false>(a, p, stream);
+  return full ? launch_backward<VEC, CLUSTER, RMS, false, true>(a, p, stream)
+              : launch_backward<VEC, CLUSTER, RMS, false, false>(a, p, stream);
 }
 
 }  // namespace
@@ -827,26 +880,24 @@ cudaError_t launch_norm_residual(const NormArgs& a, cudaStream_t stream) {
 }
 
 size_t norm_backward_partials(int64_t rows, int64_t hidden, int64_t gates, int sms) {
-  const BackPlan p = back_plan(rows, hidden, sms);
-  return static_cast<size_t>(2 * p.groups + gates) * 2 * hidden * sizeof(float);
+  const int a = back_plan(rows, hidden, true, sms).groups, b = back_plan(rows, hidden, false, sms).groups;
+  return static_cast<size_t>(2 * (a > b ? a : b) + gates) * 2 * hidden * sizeof(float);
 }
 
 cudaError_t launch_norm_residual_backward(const NormArgs& a, cudaStream_t stream) {
-  BackPlan p = back_plan(a.rows, a.hidden, a.sms);
+  BackPlan p = back_plan(a.rows, a.hidden, a.rms != 0, a.sms);
+  const bool cluster = p.cluster > 1;
   cudaError_t e;
-  switch ((p.vec > 1 ? 4 : 0) + (a.rms ? 2 : 0) + (a.o_exps ? 1 : 0)) {
-    case 0: e = launch_backward<1, false, false>(a, p, stream); break;
-    case 1: e = launch_backward<1, false, true>(a, p, stream); break;
-    case 2: e = launch_backward<1, true, false>(a, p, stream); break;
-    case 3: e = launch_backward<1, true, true>(a, p, stream); break;
-    case 4: e = launch_backward<2, false, false>(a, p, stream); break;
-    case 5: e = launch_backward<2, false, true>(a, p, stream); break;
-    case 6: e = launch_backward<2, true, false>(a, p, stream); break;
-    default: e = launch_backward<2, true, true>(a, p, stream);
-  }
+  if (a.rms)  // (a slice of 16 channels a thread may be a cluster of one block)
+    e = p.vec == 1 ? launch_backward<1, false, true>(a, p, stream)
+                   : launch_backward<2, true, true>(a, p, stream);
+  else if (p.vec == 2)
+    e = cluster ? launch_backward<2, true, false>(a, p, stream) : launch_backward<2, false, false>(a, p, stream);
+  else
+    e = cluster ? launch_backward<3, true, false>(a, p, stream) : launch_backward<3, false, false>(a, p, stream);
   if (e != cudaSuccess) return e;
   const unsigned each = a.dgate && a.gates > 1 ? static_cast<unsigned>(a.gates) : 0;
-  norm_backward_join_kernel<<<dim3((a.hidden + 31) / 32, 2 + each), kJoinWarps * 32, 0, stream>>>(
+  norm_backward_join_kernel<<<dim3((a.hidden + 31) / 32, 2 + each), kJoinThreads, 0, stream>>>(
       a, p.groups);
   return cudaGetLastError();
 }
