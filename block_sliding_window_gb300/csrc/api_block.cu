@@ -91,10 +91,13 @@ GemmCall call_dx(int64_t t, int64_t h, int64_t f) {  // dg W_gate + du W_up
   return c;
 }
 
-GemmSpec spec_down(const ptb_bf16* a, int64_t f, const ptb_bf16* w_down, int64_t h) {
-  GemmSpec g = spec_plain(a, f, f, w_down, h);
-  g.ragged = true;
-  return g;
+GemmCall call_down(int64_t t, int64_t h, int64_t f) {  // a W_down^T
+  GemmCall c;
+  c.layout = kLayoutKK;
+  c.epilogue = kEpiBf16, c.ragged = true;
+  c.M = t, c.N = h, c.K = f;
+  c.lda0 = f, c.ldb0 = f, c.ld_out = h;
+  return c;
 }
 
 struct Regions {
@@ -113,9 +116,8 @@ struct ForwardLayout {
 ForwardLayout forward_layout(int64_t t, int64_t h, int64_t f, int sms) {
   ForwardLayout l;
   Regions r;
-  const ptb_bf16* z = nullptr;
   const size_t up = call_scratch(call_up(t, h, f), sms);
-  const size_t down = spec_scratch(spec_down(z, f, z, h), t, sms);
+  const size_t down = call_scratch(call_down(t, h, f), sms);
   l.a = r.take(static_cast<size_t>(t) * f * 2);
   l.gemm_bytes = up > down ? up : down;
   l.gemm = r.take(l.gemm_bytes);
@@ -210,8 +212,11 @@ ptb_status ptb_gated_ffn(const ptb_bf16* x, int64_t ld_x, const ptb_bf16* w_gate
   c.kept = kept, c.kept_exps = kept_exps;
   PTB_TRY(gemm_call(ds, c, ws + l.gemm, l.gemm_bytes, stream));
   // 2. y = [residual +] a W_down^T
-  return gemm_run(ds, spec_down(a, ffn, w_down, hidden), tokens, y, ld_y, residual, ld_residual,
-                  hidden, ws + l.gemm, l.gemm_bytes, stream);
+  c = call_down(tokens, hidden, ffn);
+  c.a0 = a, c.b0 = w_down;
+  c.out = y, c.ld_out = ld_y;
+  c.resid = residual, c.ld_resid = ld_residual;
+  return gemm_call(ds, c, ws + l.gemm, l.gemm_bytes, stream);
 }
 
 size_t ptb_gated_ffn_backward_workspace_size(int64_t tokens, int64_t hidden, int64_t ffn,

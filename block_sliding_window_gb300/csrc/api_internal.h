@@ -61,13 +61,10 @@ struct GemmSpec {
   bool fp8 = false;
   const float* a_scale = nullptr;
   const float* b_scale = nullptr;
-  bool ragged = false;  // N tiles as ragged_block_n picks them
   int64_t n() const { return n0 + n1; }
   int64_t k() const { return k0 + k1; }
   int64_t kb() const { return k() / (fp8 ? 128 : 64); }
-  int block_n() const {
-    return ragged ? ragged_block_n(n0) : n1 ? pick_block_n(n0, n1) : pick_block_n(n0, n0);
-  }
+  int block_n() const { return n1 ? pick_block_n(n0, n1) : pick_block_n(n0, n0); }
 };
 
 GemmSpec spec_fp8(const void* a, int64_t lda, int64_t k, const void* b, int64_t n,
@@ -122,6 +119,8 @@ struct GemmCall {
   int64_t ffn = 0;
   void* kept = nullptr;
   uint8_t* kept_exps = nullptr;
+  const ptb_bf16* resid = nullptr;  // kEpiBf16
+  int64_t ld_resid = 0;
   bool ragged = false;  // N tiles as ragged_block_n picks them
   int block_n() const {
     if (ragged) return ragged_block_n(N);
@@ -135,8 +134,6 @@ size_t call_scratch(const GemmCall& c, int sms);
 ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t scratch_bytes,
                      cudaStream_t stream);
 
-// Split-wave scratch of a forward GEMM.
-size_t spec_scratch(const GemmSpec& g, int64_t tokens, int sms);
 ptb_status check_gemm_shape(int64_t tokens, int64_t hidden, int64_t ffn);
 
 // Split-wave scratch of the layer's GEMMs (the largest of them).

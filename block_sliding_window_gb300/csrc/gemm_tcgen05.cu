@@ -54,12 +54,13 @@ struct Elem {
 };
 constexpr int kMmasPerBlock = 4;
 
-// Warps of the epilogue: the gated epilogues do ten times the others' work for a value (two or three
-// outputs, an exponential, groups of 8-bit codes) and outlast the main loop on four; on eight, two
-// share the rows of a TMEM quarter and take its 32-column chunks in turn.  EPIWARPS_FIGURE
+// Warps of the epilogue.  The gated epilogues do ten times the others' work for a value (two or three
+// outputs, an exponential, groups of 8-bit codes) and a weight gradient of a few hundred tokens has a
+// short main loop: both outlast it on four warps.  On eight, two share the rows of a TMEM quarter and
+// take its 32-column chunks in turn.  EPIWARPS_FIGURE
 template <int EPI>
 __host__ __device__ constexpr int epi_warps() {
-  return EPI == kEpiGated || EPI == kEpiDgated ? 8 : 4;
+  return EPI == kEpiGated || EPI == kEpiDgated || EPI == kEpiBf16 ? 8 : 4;
 }
 template <int EPI>
 __host__ __device__ constexpr int gemm_threads() {
@@ -196,10 +197,7 @@ __device__ __forceinline__ void store_chunk(const GemmArgs& p, int row, int col,
     return;
   }
   uint32_t packed[16];
-  if constexpr (EPI == kEpiBf16) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(acc[2 * j], acc[2 * j + 1]);
-  } else if constexpr (EPI == kEpiQkvGelu) {
+  if constexpr (EPI == kEpiQkvGelu) {
     if (col >= p.gelu_col) {
       if (p.aux) {  // keep the pre-activation for the backward pass
 #pragma unroll
@@ -255,6 +253,50 @@ __device__ __forceinline__ void store_bf16x16(__nv_bfloat16* dst, const uint32_t
                : "memory");
 }
 
+__device__ __forceinline__ void load16(const __nv_bfloat16* src, bool wide, uint32_t (&w)[8]) {
+  if (wide) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+          "=r"(w[7])
+        : "l"(src));
+  } else {
+    const uint4 p = __ldg(reinterpret_cast<const uint4*>(src));
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+    w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w, w[4] = q.x, w[5] = q.y, w[6] = q.z, w[7] = q.w;
+  }
+}
+
+// bf16 [resid +] acc of 32 columns of a row, rows beyond out_split_row to out1.  p.wide: every row of
+// both outputs begins on 32 bytes.
+__device__ __forceinline__ void store_bf16(const GemmArgs& p, int row, int col,
+                                           const float (&acc)[32]) {
+  const bool second = row >= p.out_split_row;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(second ? p.out1 : p.out) +
+                       (second ? (row - p.out_split_row) * p.ld_out1 : row * p.ld_out) + col;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+    if (p.resid) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.resid + row * p.ld_resid + col + 16 * h);
+      const uint4 x = src[0], y = src[1];  // the output may be the residual itself
+      const uint32_t r[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        w[j] = pack_bf16x2(acc[16 * h + 2 * j] + bf16_lo(r[j]), acc[16 * h + 2 * j + 1] + bf16_hi(r[j]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(acc[16 * h + 2 * j], acc[16 * h + 2 * j + 1]);
+    }
+    if (p.wide) {
+      store_bf16x16(dst + 16 * h, w);
+    } else {
+      uint4* d = reinterpret_cast<uint4*>(dst + 16 * h);
+      d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+
 __device__ __forceinline__ void pack_row(const float (&v)[32], uint32_t (&packed)[16]) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
@@ -293,74 +335,73 @@ __device__ __forceinline__ void store_gated(const GemmArgs& p, int row, int col,
   }
 }
 
-// 16 neighbouring columns of a row, by 32-byte loads if the rows begin on 32 bytes.
-__device__ __forceinline__ void load_bf16x16(const __nv_bfloat16* src, bool wide, float (&v)[16]) {
-  uint32_t w[8];
-  if (wide) {
-    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
-                   "=r"(w[6]), "=r"(w[7])
-                 : "l"(src));
+// What the forward pass kept of 32 columns of a row: gate and up, bf16 pairs or codes.
+struct Kept {
+  uint32_t g[16], u[16];
+  float sg, su;
+};
+
+__device__ __forceinline__ void load_kept(const GemmArgs& p, int row, int col, Kept& k) {
+  if (row >= p.M || col >= p.N) return;
+  const int64_t at = static_cast<int64_t>(row) * 2 * p.ffn + col;
+  const bool wide = (reinterpret_cast<uintptr_t>(p.kept) & 31) == 0;
+  if (p.kept_exps) {
+    const uint8_t* codes = static_cast<const uint8_t*>(p.kept) + at;
+    load16(reinterpret_cast<const __nv_bfloat16*>(codes), wide, reinterpret_cast<uint32_t(&)[8]>(k.g));
+    load16(reinterpret_cast<const __nv_bfloat16*>(codes + p.ffn), wide,
+           reinterpret_cast<uint32_t(&)[8]>(k.u));
+    k.sg = ckpt_scale(__ldg(p.kept_exps + at / kCkptGroup));
+    k.su = ckpt_scale(__ldg(p.kept_exps + (at + p.ffn) / kCkptGroup));
   } else {
-    const uint4 p = __ldg(reinterpret_cast<const uint4*>(src));
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-    w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w, w[4] = q.x, w[5] = q.y, w[6] = q.z, w[7] = q.w;
-  }
+    const __nv_bfloat16* kept = static_cast<const __nv_bfloat16*>(p.kept) + at;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[2 * j] = bf16_lo(w[j]);
-    v[2 * j + 1] = bf16_hi(w[j]);
+    for (int h = 0; h < 2; ++h) {
+      load16(kept + 16 * h, wide, reinterpret_cast<uint32_t(&)[8]>(k.g[8 * h]));
+      load16(kept + p.ffn + 16 * h, wide, reinterpret_cast<uint32_t(&)[8]>(k.u[8 * h]));
+    }
   }
 }
 
-__device__ __forceinline__ void load_codes16(const uint8_t* src, float scale, float (&v)[16]) {
-  const uint4 p = __ldg(reinterpret_cast<const uint4*>(src));
-  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+// Four neighbouring values, columns 4 q .. 4 q + 3 of the 32.
+__device__ __forceinline__ void kept4(const uint32_t (&w)[16], float scale, bool codes, int q,
+                                      float (&v)[4]) {
+  if (codes) {
+    ckpt_unpack4(w[q], v);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float f[4];
-    ckpt_unpack4(w[j], f);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[4 * j + k] = f[k] * scale;
+    for (int e = 0; e < 4; ++e) v[e] *= scale;
+  } else {
+    v[0] = bf16_lo(w[2 * q]), v[1] = bf16_hi(w[2 * q]);
+    v[2] = bf16_lo(w[2 * q + 1]), v[3] = bf16_hi(w[2 * q + 1]);
   }
 }
 
 // Backward of act(g) * u for its gradient d, 32 columns of one row, g and u as they were kept:
 // act(g) * u once more for the weight gradient of the down projection, d u act'(g) and d act(g).
 __device__ __forceinline__ void store_dgated(const GemmArgs& p, int row, int col,
-                                             const float (&d)[32]) {
+                                             const float (&d)[32], const Kept& kept) {
   const GatedAct act(p.act);
-  const int64_t at = static_cast<int64_t>(row) * 2 * p.ffn + col;
-  const bool wide = (reinterpret_cast<uintptr_t>(p.kept) & 31) == 0;
-  float sg = 0.f, su = 0.f;
-  if (p.kept_exps) {
-    sg = ckpt_scale(__ldg(p.kept_exps + at / kCkptGroup));
-    su = ckpt_scale(__ldg(p.kept_exps + (at + p.ffn) / kCkptGroup));
-  }
+  const bool codes = p.kept_exps != nullptr;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + col;
   __nv_bfloat16* out1 = static_cast<__nv_bfloat16*>(p.out1) + row * p.ld_out1 + col;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float g[16], u[16];
-    if (p.kept_exps) {
-      const uint8_t* codes = static_cast<const uint8_t*>(p.kept) + at + 16 * h;
-      load_codes16(codes, sg, g);
-      load_codes16(codes + p.ffn, su, u);
-    } else {
-      const __nv_bfloat16* kept = static_cast<const __nv_bfloat16*>(p.kept) + at + 16 * h;
-      load_bf16x16(kept, wide, g);
-      load_bf16x16(kept + p.ffn, wide, u);
-    }
     uint32_t pa[8], pg[8], pu[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float d0 = d[16 * h + 2 * j], d1 = d[16 * h + 2 * j + 1];
-      float a0, s0, a1, s1;
-      act.value_and_slope(g[2 * j], a0, s0);
-      act.value_and_slope(g[2 * j + 1], a1, s1);
-      pa[j] = pack_bf16x2(a0 * u[2 * j], a1 * u[2 * j + 1]);
-      pg[j] = pack_bf16x2(d0 * u[2 * j] * s0, d1 * u[2 * j + 1] * s1);
-      pu[j] = pack_bf16x2(d0 * a0, d1 * a1);
+    for (int q = 0; q < 4; ++q) {
+      float g[4], u[4];
+      kept4(kept.g, kept.sg, codes, 4 * h + q, g);
+      kept4(kept.u, kept.su, codes, 4 * h + q, u);
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const float d0 = d[16 * h + 4 * q + e], d1 = d[16 * h + 4 * q + e + 1];
+        float a0, s0, a1, s1;
+        act.value_and_slope(g[e], a0, s0);
+        act.value_and_slope(g[e + 1], a1, s1);
+        const int j = 2 * q + e / 2;
+        pa[j] = pack_bf16x2(a0 * u[e], a1 * u[e + 1]);
+        pg[j] = pack_bf16x2(d0 * u[e] * s0, d1 * u[e + 1] * s1);
+        pu[j] = pack_bf16x2(d0 * a0, d1 * a1);
+      }
     }
     store_bf16x16(out + 16 * h, pa);
     store_bf16x16(out1 + 16 * h, pg);
@@ -509,9 +550,16 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
     }
     return;
   }
+  // (kEpiDgated) each chunk's kept values are asked for before the chunk in front of it is worked on
+  Kept kept, next;
+  if (EPI == kEpiDgated && finish) load_kept(p, row, n0 + first, next);
   if (finish && u.slot < 0) {
 #pragma unroll 1
     for (int c = first; c < BN && n0 + c < p.N; c += stride) {
+      if constexpr (EPI == kEpiDgated) {
+        kept = next;
+        if (c + stride < BN) load_kept(p, row, n0 + c + stride, next);
+      }
       uint32_t r[32];
       tmem_ld_32x32b_x32(t_row + c, r);
       tmem_ld_wait();
@@ -523,7 +571,9 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
         store_chunk_f32_warp(p, row, n0 + c, acc, lane, f32_stage);
       else if (row < p.M) {
         if constexpr (EPI == kEpiDgated)
-          store_dgated(p, row, n0 + c, acc);
+          store_dgated(p, row, n0 + c, acc, kept);
+        else if constexpr (EPI == kEpiBf16)
+          store_bf16(p, row, n0 + c, acc);
         else
           store_chunk<EPI>(p, row, n0 + c, acc);
       }
@@ -534,6 +584,10 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
     const int group0 = (u.slot / p.split_s) * p.split_s;
 #pragma unroll 1
     for (int c = first; c < BN && n0 + c < p.N; c += stride) {
+      if constexpr (EPI == kEpiDgated) {
+        kept = next;
+        if (c + stride < BN) load_kept(p, row, n0 + c + stride, next);
+      }
       float acc[32];
       sum_pieces<BN, ROWS>(p, group0, prow, c, acc);
       if constexpr (FP8) dequantize(p, row, n0 + c, acc);
@@ -541,7 +595,9 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
         store_chunk_f32_warp(p, row, n0 + c, acc, lane, f32_stage);
       else if (row < p.M) {
         if constexpr (EPI == kEpiDgated)
-          store_dgated(p, row, n0 + c, acc);
+          store_dgated(p, row, n0 + c, acc, kept);
+        else if constexpr (EPI == kEpiBf16)
+          store_bf16(p, row, n0 + c, acc);
         else
           store_chunk<EPI>(p, row, n0 + c, acc);
       }
@@ -1077,8 +1133,10 @@ cudaError_t launch_typed(const GemmArgs& a, cudaStream_t stream) {
 
 // Arrival counters for 32 rows of a split tile.
 int gemm_counters(int epilogue) {
-  return (epilogue == kEpiGated ? epi_warps<kEpiGated>()
-          : epilogue == kEpiDgated ? epi_warps<kEpiDgated>() : 4) / 4;
+  return (epilogue == kEpiGated    ? epi_warps<kEpiGated>()
+          : epilogue == kEpiDgated ? epi_warps<kEpiDgated>()
+          : epilogue == kEpiBf16   ? epi_warps<kEpiBf16>()
+                                   : 4) / 4;
 }
 
 GemmPlan plan_gemm(int64_t tiles, int64_t num_kb, int sms, int block_n, int rows, int counters) {
@@ -1136,6 +1194,8 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
       return launch_pair<kEpiQkvGelu, kLayoutKK>(a, stream);
     if (a.layout == kLayoutKK && a.epilogue == kEpiResidual)
       return launch_pair<kEpiResidual, kLayoutKK>(a, stream);
+    if (a.layout == kLayoutKK && a.epilogue == kEpiBf16)
+      return launch_pair<kEpiBf16, kLayoutKK>(a, stream);
     if (a.layout == kLayoutKK && a.epilogue == kEpiGated)
       return launch_pair<kEpiGated, kLayoutKK>(a, stream);
     if (a.layout == kLayoutKN && a.epilogue == kEpiDgelu)
@@ -1161,6 +1221,7 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
     if (a.epilogue == kEpiResidual)
       return a.fp8 ? launch_bn<kEpiResidual, true, kLayoutKK>(a, stream)
                    : launch_bn<kEpiResidual, false, kLayoutKK>(a, stream);
+    if (a.epilogue == kEpiBf16 && !a.fp8) return launch_bn<kEpiBf16, false, kLayoutKK>(a, stream);
     if (a.epilogue == kEpiGated && !a.fp8) {
       // Half of a tile's columns are the gate's: tiles of 64 would leave 32 rows of weights a box.
       if (a.block_n == 256) return launch_typed<256, kEpiGated, false, kLayoutKK>(a, stream);

@@ -361,6 +361,9 @@ ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t s
   a.ffn = static_cast<int>(c.ffn);
   a.kept = c.kept;
   a.kept_exps = c.kept_exps;
+  a.resid = c.resid ? bf(c.resid) : nullptr;
+  a.ld_resid = c.ld_resid;
+  a.wide = aligned(a.out, 32) && aligned(a.out1, 32) && a.ld_out % 16 == 0 && a.ld_out1 % 16 == 0;
   apply_plan(a, c.kb(), ds->sms, scratch, scratch_bytes);
   a.status = ds->status;
   return launch_status(launch_gemm(a, stream));

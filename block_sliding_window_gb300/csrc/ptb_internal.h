@@ -19,7 +19,7 @@ enum GemmEpilogue : int {
   kEpiDgelu = 2,     // columns >= gelu_col store bf16(acc * gelu_tanh'(aux[row, col - gelu_col])),
                      // the others bf16(acc)
   kEpiF32 = 3,       // store fp32 acc
-  kEpiBf16 = 4,      // store bf16(acc)
+  kEpiBf16 = 4,      // store bf16(acc), with resid set bf16(acc + resid)
   kEpiGated = 5,     // a tile holds block_n / 2 columns of the gate and the same of up: store
                      // bf16(act(gate) * up); with kept set, also gate and up themselves
   kEpiDgated = 6,    // acc is the gradient of act(gate) * up: store bf16(act(gate) * up) (out) and
@@ -85,6 +85,7 @@ struct GemmArgs {
   // set, a checkpoint's codes and exponents.
   int act;
   int ffn;
+  int wide;  // kEpiBf16: every output row begins on 32 bytes
   void* kept;
   uint8_t* kept_exps;
 };
