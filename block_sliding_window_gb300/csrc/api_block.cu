@@ -195,7 +195,7 @@ ptb_status ptb_gated_ffn(const ptb_bf16* x, int64_t ld_x, const ptb_bf16* w_gate
     n.w0 = bf(w_gate), n.w1 = bf(w_up);
     n.out = bf(a), n.ld_out = ffn;
     n.tokens = static_cast<int>(tokens), n.N = static_cast<int>(ffn), n.K = static_cast<int>(hidden);
-    n.act = activation;
+    n.act = activation, n.sms = ds->sms;
     PTB_TRY(launch_status(launch_thin(n, stream)));
     n.x = bf(a), n.ld_x = ffn;
     n.w0 = bf(w_down), n.w1 = nullptr;

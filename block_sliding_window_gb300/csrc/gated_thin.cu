@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;  // rows of a weight matrix per block
+constexpr int kRows = 16;  // rows of a weight matrix per tile
 
 __device__ __forceinline__ uint4 load_stream(const __nv_bfloat16* p) {
   uint4 v;
@@ -37,24 +37,26 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT: groups of 8 tokens.  GATED: two weight matrices, act(gate) * up; else one, with the residual.
-template <int NT, bool GATED>
-__global__ void __launch_bounds__(kThreads, NT > 2 ? 2 : 3) thin_kernel(const __grid_constant__ ThinArgs p) {
-  constexpr int NW = GATED ? 2 : 1;     // weight matrices
-  constexpr int U = GATED ? 2 : 4;      // steps of 64 k in flight
-  __shared__ float part[kWarps][NW * kRows][NT * 8 + 1];
+// NT: groups of 8 tokens.  MT: tiles of 16 rows of each weight matrix per block.  GATED: two weight
+// matrices, act(gate) * up; else one, with the residual.
+template <int NT, int MT, bool GATED>
+__global__ void __launch_bounds__(kThreads, NT > 2 || MT > 1 ? 2 : 3) thin_kernel(const __grid_constant__ ThinArgs p) {
+  constexpr int NW = GATED ? 2 : 1;                  // weight matrices
+  constexpr int TILES = NW * MT;                     // 16-row tiles of a warp
+  constexpr int U = TILES >= 4 ? 1 : 4 / TILES;      // steps of 64 k in flight
+  constexpr int ROWS = TILES * kRows;
+  extern __shared__ float part[];                    // [kWarps][ROWS][NT * 8 + 1]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * kRows;
+  const int n0 = blockIdx.x * (MT * kRows);
   const int steps = p.K / 64;
   const int first = warp * steps / kWarps, last = (warp + 1) * steps / kWarps;
 
-  const __nv_bfloat16* w[NW][2];
+  const __nv_bfloat16* w[TILES];  // row g of each tile; row g + 8 is 8 K further on
 #pragma unroll
-  for (int m = 0; m < NW; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      w[m][h] = (m ? p.w1 : p.w0) + static_cast<int64_t>(n0 + g + 8 * h) * p.K + 8 * t;
+  for (int m = 0; m < TILES; ++m)
+    w[m] = (m / MT ? p.w1 : p.w0) + static_cast<int64_t>(n0 + (m % MT) * kRows + g) * p.K + 8 * t;
+  const int64_t half = 8 * static_cast<int64_t>(p.K);
   const __nv_bfloat16* x[NT];
   bool live[NT];
 #pragma unroll
@@ -63,15 +65,15 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 2 : 3) thin_kernel(const __
     x[j] = p.x + (live[j] ? 8 * j + g : 0) * p.ld_x + 8 * t;
   }
 
-  float acc[NW][NT][4];
+  float acc[TILES][NT][4];
 #pragma unroll
-  for (int m = 0; m < NW; ++m)
+  for (int m = 0; m < TILES; ++m)
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
 
-  auto product = [&](int s, const uint4 (&wv)[NW][2][2]) {
+  auto product = [&](int s, const uint4 (&wv)[TILES][2][2]) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
 #pragma unroll
@@ -79,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 2 : 3) thin_kernel(const __
         uint4 xv = make_uint4(0, 0, 0, 0);
         if (live[j]) xv = __ldg(reinterpret_cast<const uint4*>(x[j] + s * 64 + q * 32));
 #pragma unroll
-        for (int m = 0; m < NW; ++m) {
+        for (int m = 0; m < TILES; ++m) {
           const uint4 &a = wv[m][0][q], &b = wv[m][1][q];
           mma_16x8x16(acc[m][j], a.x, b.x, a.y, b.y, xv.x, xv.y);
           mma_16x8x16(acc[m][j], a.z, b.z, a.w, b.w, xv.z, xv.w);
@@ -87,46 +89,49 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 2 : 3) thin_kernel(const __
       }
     }
   };
-  auto load = [&](int s, uint4 (&wv)[NW][2][2]) {
+  auto load = [&](int s, uint4 (&wv)[TILES][2][2]) {
 #pragma unroll
-    for (int m = 0; m < NW; ++m)
+    for (int m = 0; m < TILES; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) wv[m][h][q] = load_stream(w[m][h] + s * 64 + q * 32);
+        for (int q = 0; q < 2; ++q) wv[m][h][q] = load_stream(w[m] + h * half + s * 64 + q * 32);
   };
 
   int s = first;
   for (; s + U <= last; s += U) {
-    uint4 wv[U][NW][2][2];
+    uint4 wv[U][TILES][2][2];
 #pragma unroll
     for (int i = 0; i < U; ++i) load(s + i, wv[i]);
 #pragma unroll
     for (int i = 0; i < U; ++i) product(s + i, wv[i]);
   }
-  for (; s < last; ++s) {
-    uint4 wv[NW][2][2];
-    load(s, wv);
-    product(s, wv);
+  if constexpr (U > 1) {
+    for (; s < last; ++s) {
+      uint4 wv[TILES][2][2];
+      load(s, wv);
+      product(s, wv);
+    }
   }
 
+  constexpr int PAD = NT * 8 + 1;
 #pragma unroll
-  for (int m = 0; m < NW; ++m)
+  for (int m = 0; m < TILES; ++m)
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        part[warp][m * kRows + g + 8 * (e >> 1)][8 * j + 2 * t + (e & 1)] = acc[m][j][e];
+        part[(warp * ROWS + m * kRows + g + 8 * (e >> 1)) * PAD + 8 * j + 2 * t + (e & 1)] = acc[m][j][e];
   __syncthreads();
   const GatedAct act(p.act);
-  for (int i = threadIdx.x; i < kRows * p.tokens; i += kThreads) {
-    const int r = i % kRows, k = i / kRows;
+  for (int i = threadIdx.x; i < MT * kRows * p.tokens; i += kThreads) {
+    const int r = i % (MT * kRows), k = i / (MT * kRows);
     float v[NW];
 #pragma unroll
     for (int m = 0; m < NW; ++m) {
       v[m] = 0.f;
 #pragma unroll
-      for (int q = 0; q < kWarps; ++q) v[m] += part[q][m * kRows + r][k];
+      for (int q = 0; q < kWarps; ++q) v[m] += part[(q * ROWS + m * MT * kRows + r) * PAD + k];
     }
     float out = GATED ? act.value(v[0]) * v[NW - 1] : v[0];
     if (!GATED && p.resid) out += __bfloat162float(p.resid[k * p.ld_resid + n0 + r]);
@@ -134,15 +139,31 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 2 : 3) thin_kernel(const __
   }
 }
 
+template <int NT, int MT, bool GATED>
+cudaError_t launch_one(const ThinArgs& a, cudaStream_t stream) {
+  constexpr int bytes = kWarps * (GATED ? 2 : 1) * MT * kRows * (NT * 8 + 1) * 4;
+  auto kern = thin_kernel<NT, MT, GATED>;
+  if constexpr (bytes > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<a.N / (MT * kRows), kThreads, bytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// Every block reads all of x, through L1: from 9 tokens on, two 16-row tiles a block halve that where
+// the blocks still cover the SMs (the down projection of 13824 by 5120, 24 tokens: the pair of kernels
+// 89.5 us for 96).  With both gate and up the second pair of tiles would spill (123 us).
 template <bool GATED>
 cudaError_t launch(const ThinArgs& a, cudaStream_t stream) {
-  const unsigned grid = a.N / kRows;
   const int nt = (a.tokens + 7) / 8;
-  if (nt == 1) thin_kernel<1, GATED><<<grid, kThreads, 0, stream>>>(a);
-  else if (nt == 2) thin_kernel<2, GATED><<<grid, kThreads, 0, stream>>>(a);
-  else if (nt <= 4) thin_kernel<4, GATED><<<grid, kThreads, 0, stream>>>(a);
-  else return cudaErrorInvalidValue;
-  return cudaGetLastError();
+  if (nt == 1) return launch_one<1, 1, GATED>(a, stream);
+  if (nt > 4) return cudaErrorInvalidValue;
+  if constexpr (!GATED) {
+    if (a.N / (2 * kRows) >= a.sms)
+      return nt == 2 ? launch_one<2, 2, GATED>(a, stream) : launch_one<4, 2, GATED>(a, stream);
+  }
+  return nt == 2 ? launch_one<2, 1, GATED>(a, stream) : launch_one<4, 1, GATED>(a, stream);
 }
 
 }  // namespace

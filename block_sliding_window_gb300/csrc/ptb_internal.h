@@ -222,7 +222,7 @@ struct ThinArgs {
   const __nv_bfloat16 *x, *w0, *w1, *resid;
   __nv_bfloat16* out;
   int64_t ld_x, ld_resid, ld_out;
-  int tokens, N, K, act;
+  int tokens, N, K, act, sms;
 };
 
 struct CheckpointArgs {
