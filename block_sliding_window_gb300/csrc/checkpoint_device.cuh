@@ -53,15 +53,17 @@ __device__ __forceinline__ void ckpt_unpack4(uint32_t codes, float (&v)[4]) {
   v[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)) - 8388736.f;
 }
 
-// The same as packed pairs, times a power of two: (2^23 + 128 + c) s - (2^23 + 128) s is exact.
+// The same as packed pairs, times the scale.  (As one fma, (2^23 + 128 + c) s - (2^23 + 128) s, it
+// would overflow for scales from 2^104 on.)
 __device__ __forceinline__ void ckpt_unpack4_scaled(uint32_t codes, float scale, uint64_t (&v)[2]) {
   const uint32_t u = codes ^ 0x80808080u;
-  const uint64_t s = f2(scale, scale), off = f2(-8388736.f * scale, -8388736.f * scale);
+  const uint64_t s = f2(scale, scale), off = f2(-8388736.f, -8388736.f);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    v[h] = f2_fma(f2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + 2 * h)),
-                     __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441 + 2 * h))),
-                  s, off);
+    v[h] = f2_mul(f2_add(f2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + 2 * h)),
+                            __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441 + 2 * h))),
+                         off),
+                  s);
 }
 
 // One whole group held by a thread: its 32 values to codes and an exponent byte.
