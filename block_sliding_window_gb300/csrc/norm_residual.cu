@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(const __grid_constan
 // for a channel of an rms norm and four for one of a layer norm, and a quarter of the SM has
 // registers for whole warps only:
 //   rms norms    up to 5120 channels 640 threads of 8 (96 registers), else 384 of 16 (168) a slice;
-//   layer norms  256 threads of 16 or 24 (248).  With 168 registers the sums spill: LN_FIGURE
+//   layer norms  256 threads of 16 or 24 (248).  With 168 registers the sums spill: 4096 channels
+//                162 us, with 248 100
 constexpr int kRing = 200 * 1024;  // shared memory for rows, per SM
 
 template <int VEC, bool RMS>
@@ -800,25 +801,28 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
 }
 
-template <bool WARP, bool RMS>
+// Vectors a thread: few, for rows in many blocks at once; a layer norm's four rounds of sums cost
+// less with a third one (5120 channels: 72 us for 77 with two and 78 with four; rms 56.4 with two, 58.2
+// with three; 12288: 87 with three on 512 threads, 96 with four).
+template <bool RMS>
 cudaError_t launch_forward(const NormArgs& a, cudaStream_t stream) {
   const int nvec = a.hidden / 8;
-  if constexpr (WARP) {
-    const unsigned grid = static_cast<unsigned>((a.rows + 7) / 8);
-    if (nvec <= 32)
-      norm_residual_kernel<1, true, RMS><<<grid, 256, 0, stream>>>(a);
-    else if (nvec <= 64)
-      norm_residual_kernel<2, true, RMS><<<grid, 256, 0, stream>>>(a);
-    else
-      norm_residual_kernel<4, true, RMS><<<grid, 256, 0, stream>>>(a);
-  } else {
-    const unsigned grid = static_cast<unsigned>(a.rows);
-    auto threads = [&](int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; };
-    if (nvec <= 2048)
-      norm_residual_kernel<4, false, RMS><<<grid, threads(4), 0, stream>>>(a);
-    else
-      norm_residual_kernel<8, false, RMS><<<grid, threads(8), 0, stream>>>(a);
-  }
+  const unsigned rows = static_cast<unsigned>(a.rows), warps = (rows + 7) / 8;
+  auto threads = [&](int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; };
+  if (nvec <= 32)
+    norm_residual_kernel<1, true, RMS><<<warps, 256, 0, stream>>>(a);
+  else if (nvec <= 64)
+    norm_residual_kernel<2, true, RMS><<<warps, 256, 0, stream>>>(a);
+  else if (nvec <= 128)
+    norm_residual_kernel<4, true, RMS><<<warps, 256, 0, stream>>>(a);
+  else if (nvec <= (RMS ? 1024 : 256))
+    norm_residual_kernel<2, false, RMS><<<rows, threads(2), 0, stream>>>(a);
+  else if (nvec <= 1536)
+    norm_residual_kernel<3, false, RMS><<<rows, threads(3), 0, stream>>>(a);
+  else if (nvec <= 2560)
+    norm_residual_kernel<5, false, RMS><<<rows, threads(5), 0, stream>>>(a);
+  else
+    norm_residual_kernel<8, false, RMS><<<rows, threads(8), 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -874,9 +878,7 @@ cudaError_t launch_backward(const NormArgs& a, BackPlan& p, cudaStream_t stream)
 }  // namespace
 
 cudaError_t launch_norm_residual(const NormArgs& a, cudaStream_t stream) {
-  const bool warp = a.hidden <= 1024;
-  if (a.rms) return warp ? launch_forward<true, true>(a, stream) : launch_forward<false, true>(a, stream);
-  return warp ? launch_forward<true, false>(a, stream) : launch_forward<false, false>(a, stream);
+  return a.rms ? launch_forward<true>(a, stream) : launch_forward<false>(a, stream);
 }
 
 size_t norm_backward_partials(int64_t rows, int64_t hidden, int64_t gates, int sms) {
