@@ -109,8 +109,10 @@ struct Regions {
   }
 };
 
+// The GEMMs of a call have arrival counters of their own, which one memset clears: a memset in front of
+// each was a fifth of the nodes of a small call's graph.
 struct ForwardLayout {
-  size_t a, gemm, gemm_bytes, total;
+  size_t a, gemm, gemm_bytes, counters[2], total;
 };
 
 ForwardLayout forward_layout(int64_t t, int64_t h, int64_t f, int sms) {
@@ -121,30 +123,43 @@ ForwardLayout forward_layout(int64_t t, int64_t h, int64_t f, int sms) {
   l.a = r.take(static_cast<size_t>(t) * f * 2);
   l.gemm_bytes = up > down ? up : down;
   l.gemm = r.take(l.gemm_bytes);
+  l.counters[0] = r.take(call_counters(call_up(t, h, f), sms));
+  l.counters[1] = r.take(call_counters(call_down(t, h, f), sms));
   l.total = r.off;
   return l;
 }
 
 struct BackwardLayout {
-  size_t a, dgu, x, gemm, gemm_bytes, total;
+  size_t a, dgu, x, gemm, gemm_bytes, counters[4], total;
 };
 
-BackwardLayout backward_layout(int64_t t, int64_t h, int64_t f, bool x8, int sms) {
+BackwardLayout backward_layout(int64_t t, int64_t h, int64_t f, bool x8, int bits, int sms) {
   BackwardLayout l;
   Regions r;
   l.a = r.take(static_cast<size_t>(t) * f * 2);
   l.dgu = r.take(static_cast<size_t>(t) * f * 4);
   l.x = r.take(x8 ? static_cast<size_t>(t) * h * 2 : 0);
   l.gemm_bytes = 0;
-  for (const GemmCall& c : {call_da(t, h, f), call_dw_down(t, h, f, 32), call_dw_up(t, h, f, 32),
+  for (const GemmCall& c : {call_da(t, h, f), call_dw_down(t, h, f, bits), call_dw_up(t, h, f, bits),
                             call_dx(t, h, f)}) {
     const size_t b = call_scratch(c, sms);
     l.gemm_bytes = b > l.gemm_bytes ? b : l.gemm_bytes;
   }
   l.gemm = r.take(l.gemm_bytes);
+  int k = 0;
+  for (const GemmCall& c : {call_da(t, h, f), call_dw_down(t, h, f, bits), call_dw_up(t, h, f, bits),
+                            call_dx(t, h, f)})
+    l.counters[k++] = r.take(call_counters(c, sms));
   l.total = r.off;
   return l;
 }
+
+// Clears the counters of a layout from `first` to its end; their place in it, for GEMM k.
+ptb_status clear_counters(char* ws, size_t first, size_t total, cudaStream_t stream) {
+  if (total == first) return PTB_OK;
+  return launch_status(cudaMemsetAsync(ws + first, 0, total - first, stream));
+}
+unsigned* counters_at(char* ws, size_t at) { return reinterpret_cast<unsigned*>(ws + at); }
 
 bool gated_shape_ok(int64_t tokens, int64_t hidden, int64_t ffn) {
   return tokens > 0 && check_gemm_shape(tokens, hidden, ffn) == PTB_OK && 2 * ffn <= kMaxRows;
@@ -205,7 +220,9 @@ ptb_status ptb_gated_ffn(const ptb_bf16* x, int64_t ld_x, const ptb_bf16* w_gate
     return launch_status(launch_thin(n, stream));
   }
   // 1. a = act(x W_gate^T) * (x W_up^T)
+  PTB_TRY(clear_counters(ws, l.counters[0], l.total, stream));
   GemmCall c = call_up(tokens, hidden, ffn);
+  c.counters = counters_at(ws, l.counters[0]);
   c.a0 = x, c.lda0 = ld_x, c.b0 = w_gate, c.b1 = w_up;
   c.out = a;
   c.act = activation;
@@ -213,6 +230,7 @@ ptb_status ptb_gated_ffn(const ptb_bf16* x, int64_t ld_x, const ptb_bf16* w_gate
   PTB_TRY(gemm_call(ds, c, ws + l.gemm, l.gemm_bytes, stream));
   // 2. y = [residual +] a W_down^T
   c = call_down(tokens, hidden, ffn);
+  c.counters = counters_at(ws, l.counters[1]);
   c.a0 = a, c.b0 = w_down;
   c.out = y, c.ld_out = ld_y;
   c.resid = residual, c.ld_resid = ld_residual;
@@ -222,7 +240,10 @@ ptb_status ptb_gated_ffn(const ptb_bf16* x, int64_t ld_x, const ptb_bf16* w_gate
 size_t ptb_gated_ffn_backward_workspace_size(int64_t tokens, int64_t hidden, int64_t ffn,
                                              int32_t x_bits) {
   if (!gated_shape_ok(tokens, hidden, ffn) || (x_bits != 16 && x_bits != 8)) return 0;
-  return backward_layout(tokens, hidden, ffn, x_bits == 8, current_sms()).total;
+  const int sms = current_sms();
+  const size_t a = backward_layout(tokens, hidden, ffn, x_bits == 8, 16, sms).total;
+  const size_t b = backward_layout(tokens, hidden, ffn, x_bits == 8, 32, sms).total;
+  return a > b ? a : b;
 }
 
 ptb_status ptb_gated_ffn_backward(const ptb_bf16* dy, int64_t ld_dy, const void* x, int64_t ld_x,
@@ -256,7 +277,8 @@ ptb_status ptb_gated_ffn_backward(const ptb_bf16* dy, int64_t ld_dy, const void*
       PTB_TRY(launch_status(cudaMemsetAsync(p, 0, bytes, stream)));
     return PTB_OK;
   }
-  const BackwardLayout l = backward_layout(tokens, hidden, ffn, x_exps != nullptr, ds->sms);
+  const BackwardLayout l =
+      backward_layout(tokens, hidden, ffn, x_exps != nullptr, grad_bits, ds->sms);
   char* ws = static_cast<char*>(workspace);
   ptb_bf16* a = reinterpret_cast<ptb_bf16*>(ws + l.a);
   ptb_bf16* dgu = reinterpret_cast<ptb_bf16*>(ws + l.dgu);
@@ -277,7 +299,9 @@ ptb_status ptb_gated_ffn_backward(const ptb_bf16* dy, int64_t ld_dy, const void*
     ld_x = hidden;
   }
   // 1. da = dy W_down; a, [dg | du] from it and the kept gate and up
+  PTB_TRY(clear_counters(ws, l.counters[0], l.total, stream));
   GemmCall c = call_da(tokens, hidden, ffn);
+  c.counters = counters_at(ws, l.counters[0]);
   c.a0 = dy, c.lda0 = ld_dy, c.b0 = w_down;
   c.out = a, c.out1 = dgu;
   c.act = activation;
@@ -285,16 +309,19 @@ ptb_status ptb_gated_ffn_backward(const ptb_bf16* dy, int64_t ld_dy, const void*
   PTB_TRY(gemm_call(ds, c, scratch, l.gemm_bytes, stream));
   // 2. dW_down = dy^T a
   c = call_dw_down(tokens, hidden, ffn, grad_bits);
+  c.counters = counters_at(ws, l.counters[1]);
   c.a0 = dy, c.lda0 = ld_dy, c.b0 = a;
   c.out = dw_down;
   PTB_TRY(gemm_call(ds, c, scratch, l.gemm_bytes, stream));
   // 3. [dW_gate ; dW_up] = [dg | du]^T x
   c = call_dw_up(tokens, hidden, ffn, grad_bits);
+  c.counters = counters_at(ws, l.counters[2]);
   c.a0 = dgu, c.b0 = xb, c.ldb0 = ld_x;
   c.out = dw_gate, c.out1 = dw_up;
   PTB_TRY(gemm_call(ds, c, scratch, l.gemm_bytes, stream));
   // 4. dx = dg W_gate + du W_up: the last, so that dx may be dy or x
   c = call_dx(tokens, hidden, ffn);
+  c.counters = counters_at(ws, l.counters[3]);
   c.a0 = dgu, c.a1 = dgu + ffn, c.b0 = w_gate, c.b1 = w_up;
   c.out = dx, c.ld_out = ld_dx;
   return gemm_call(ds, c, scratch, l.gemm_bytes, stream);

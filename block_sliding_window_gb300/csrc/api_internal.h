@@ -120,6 +120,7 @@ struct GemmCall {
   void* kept = nullptr;
   uint8_t* kept_exps = nullptr;
   const ptb_bf16* resid = nullptr;  // kEpiBf16
+  unsigned* counters = nullptr;  // cleared arrival counters (else in scratch, cleared by the launch)
   int64_t ld_resid = 0;
   bool ragged = false;  // N tiles as ragged_block_n picks them
   int block_n() const {
@@ -131,6 +132,8 @@ struct GemmCall {
 
 // Split-wave scratch of a backward GEMM (either tile shape), and its launch.
 size_t call_scratch(const GemmCall& c, int sms);
+// Bytes of its arrival counters alone.
+size_t call_counters(const GemmCall& c, int sms);
 ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t scratch_bytes,
                      cudaStream_t stream);
 

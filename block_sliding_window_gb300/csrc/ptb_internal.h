@@ -75,7 +75,8 @@ struct GemmArgs {
   int split_r;          // remainder tiles that are split
   int split_s;          // pieces per remainder tile
   float* partials;      // [split_r * split_s] tiles of fp32
-  unsigned* counters;   // [split_r][4 (8 for pairs) x gemm_counters] arrival counters, zeroed before each launch
+  unsigned* counters;   // [split_r][4 (8 for pairs) x gemm_counters] arrival counters
+  int counters_zero;    // 0: the launch clears them first; 1: the caller has
   // e4m3 operands (fp8 != 0): K counted in e4m3 elements, 128 per k-block;
   // a_scale [M] and b_scale [N] dequantize the fp32 accumulator.
   int fp8;
