@@ -544,6 +544,7 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, int cluster, in
       const uint4 q = lds16(stats_at);
       st[r] = make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
                           __uint_as_float(q.w));
+      if (!pre) st[r].z = st[r].w = 0.f;  // whatever is kept for a norm that is not there
       stage_at += per_stage;
       stats_at += kMostWarps * 16;
       if (stage_at == ring_end) {

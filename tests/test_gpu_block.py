@@ -167,6 +167,47 @@ def test_norm_backward_from_a_checkpoint(ptb_lib, rows, n, rms):
     assert all(torch.equal(out[k], same[k]) for k in out)
 
 
+def test_norm_backward_from_a_checkpoint_of_any_magnitude(ptb_lib):
+    # scales from 2^-126 to beyond 2^104, without a norm that would take them away
+    rows, n = 40, 320
+    o = normal(rows, n, seed=1) * torch.exp2(torch.linspace(-130, 118, rows)).unsqueeze(1).cuda()
+    o = o.to(torch.bfloat16)
+    kept = ptb_lib.checkpoint_pack(o)
+    value = ptb_lib.checkpoint_unpack(*kept)
+    gate = normal(rows, n, seed=2)
+    dy = normal(rows, n, seed=3)
+    stats = torch.zeros(rows, 4, device="cuda")
+    for rms in (False, True):
+        out = ptb_lib.norm_residual_backward(dy, None, None, kept, stats, gate=gate, rms=rms)
+        M.held_to("dgate", out["dgate"], M.d(dy) * M.values(kept), M.F * (M.d(dy) * M.values(kept)).abs())
+        same = ptb_lib.norm_residual_backward(dy, None, None, value, stats, gate=gate, rms=rms)
+        assert all(torch.equal(out[k], same[k]) for k in out)
+
+
+def test_norm_backward_without_a_norm_ignores_its_statistics(ptb_lib):
+    s = norm_inputs(9, 256, 1, 1, 0, 0, seed=11)
+    y, h, stats = ptb_lib.norm_residual_train(s["x"], s["o"], **parameters(s))
+    dy = normal(9, 256, seed=12)
+    want = ptb_lib.norm_residual_backward(dy, None, y, s["o"], stats, **parameters(s))
+    stats[:, 2:] = math.nan
+    got = ptb_lib.norm_residual_backward(dy, None, y, s["o"], stats, **parameters(s))
+    assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("n,rms", [(14400, False), (20480, False), (26000, False), (26000, True), (13312, True)])
+def test_norm_backward_of_a_cluster_captured_first(ptb_lib, n, rms):
+    # sizes that no other test calls: the launch's own set-up happens under capture
+    s = norm_inputs(64, n, 2, 1, 1, rms, seed=n)
+    y, h, stats = ptb_lib.norm_residual_train(s["x"], s["o"], rms=rms, **parameters(s))
+    dy, dh = normal(64, n, seed=1), normal(64, n, seed=2)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = ptb_lib.norm_residual_backward(dy, dh, y, s["o"], stats, rms=rms, **parameters(s))
+    g.replay()
+    torch.cuda.synchronize()
+    check_norm_backward(out, s, dy, dh, y, s["o"], 1.0, rms)
+
+
 def test_norm_without_the_streams_gradient(ptb_lib):
     s = norm_inputs(20, 256, 1, 1, 1, 0, seed=3)
     y, h, stats = ptb_lib.norm_residual_train(s["x"], s["o"], **parameters(s))
@@ -249,6 +290,10 @@ FFNS = [
     (1, 64, 64), (2, 64, 128), (3, 128, 64), (1, 1024, 2752), (7, 192, 320), (8, 256, 512), (9, 64, 192), (16, 512, 192),
     (17, 320, 128), (33, 256, 448), (64, 128, 1024), (127, 128, 192), (128, 256, 256), (129, 256, 320), (130, 192, 384),
     (200, 1088, 256), (257, 512, 640), (300, 64, 1088), (513, 256, 256), (24, 1024, 1024),
+    # the border between the kernels of few tokens and the others, and wide outputs of few tokens
+    (31, 192, 256), (32, 256, 192), (20, 5120, 64), (11, 4928, 128), (32, 4864, 64),
+    # N tiles that reach past the width, K split over the SMs
+    (260, 1088, 832), (140, 2112, 704), (700, 576, 1344),
 ]
 
 
@@ -380,6 +425,10 @@ def test_gated_ffn_rows_of_nan_stay_their_own(ptb_lib):
 def test_gated_ffn_binding_refusals(ptb_lib):
     s = ffn_inputs(4, 64, 128, seed=1)
     x, w = s["x"], weights(s)
+    with pytest.raises(ValueError):  # rows at two strides
+        ptb_lib.gated_ffn(normal(4, 6, 64, seed=1)[:, :3], *w)
+    with pytest.raises(ptb_lib.PTBError):  # rows on top of each other
+        ptb_lib.gated_ffn(x[:1].expand(3, 64), *w)
     with pytest.raises(ValueError):
         ptb_lib.gated_ffn(x, *w, activation="relu")
     with pytest.raises(ValueError):
