@@ -649,9 +649,11 @@ def swa_attention_paged(q, cache, page_table, seq_lens, kv_heads: int, page_size
 
 def _matrix(name: str, t, dev: int, cols=None, rows=None, dtype=torch.bfloat16) -> tuple:
     """[..., cols] with contiguous rows at one stride -> (pointer, row stride, rows, cols)."""
-    _tensor(name, t, dtype, dev)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(name, t, dtype)
     size = t.shape
-    if len(size) < 2:
+    dims = len(size)
+    if dims < 2:
         raise ValueError(f"{name} must have at least 2 dimensions")
     c = size[-1]
     if (cols is not None and c != cols) or c < 1:
@@ -660,9 +662,9 @@ def _matrix(name: str, t, dev: int, cols=None, rows=None, dtype=torch.bfloat16) 
     if st[-1] != 1 and c != 1:
         raise ValueError(f"{name} must have a contiguous last dimension")
     n, ld = size[-2], st[-2]
-    if len(size) > 2:
+    if dims > 2:
         # The leading dimensions have to run on at the rows' stride.
-        for d in range(len(size) - 3, -1, -1):
+        for d in range(dims - 3, -1, -1):
             if size[d] != 1:
                 if n > 1 and st[d] != n * ld:
                     raise ValueError(f"{name} must have its rows at one stride")
@@ -678,7 +680,8 @@ def _matrix(name: str, t, dev: int, cols=None, rows=None, dtype=torch.bfloat16) 
 def _vector(name: str, t, n: int, dev: int, dtype=torch.bfloat16):
     if t is None:
         return None
-    _tensor(name, t, dtype, dev)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(name, t, dtype)
     if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} entries")
     return t.data_ptr()
@@ -719,12 +722,18 @@ def checkpoint_pack(x, codes=None, exps=None, stream=None) -> tuple:
     p, ld, rows, cols = _matrix("x", x, dev)
     if cols % 32:
         raise ValueError("x must have a multiple of 32 columns")
+    size = x.shape
     if codes is None:
-        codes = _new(x, x.shape, stream, torch.int8)
+        codes = _new(x, size, stream, torch.int8)
+        cp, cld = codes.data_ptr(), cols
+    else:
+        cp, cld, _, _ = _matrix("codes", codes, dev, cols, rows, torch.int8)
     if exps is None:
-        exps = _new(x, x.shape[:-1] + (cols // 32,), stream, torch.uint8)
-    c = _checkpoint("the checkpoint", (codes, exps), dev, cols, rows)
-    st = lib.ptb_checkpoint_pack(p, ld, rows, cols, c[0], c[1], c[4], c[5], raw)
+        exps = _new(x, size[:-1] + (cols // 32,), stream, torch.uint8)
+        ep, eld = exps.data_ptr(), cols // 32
+    else:
+        ep, eld, _, _ = _matrix("exps", exps, dev, cols // 32, rows, torch.uint8)
+    st = lib.ptb_checkpoint_pack(p, ld, rows, cols, cp, cld, ep, eld, raw)
     if st:
         _check(st, "ptb_checkpoint_pack")
     return codes, exps
@@ -737,7 +746,9 @@ def checkpoint_unpack(codes, exps, x=None, stream=None) -> torch.Tensor:
     p, ld, rows, cols, ep, eld = _checkpoint("the checkpoint", (codes, exps), dev)
     if x is None:
         x = _new(codes, codes.shape, stream)
-    xp, xld, _, _ = _matrix("x", x, dev, cols, rows)
+        xp, xld = x.data_ptr(), cols
+    else:
+        xp, xld, _, _ = _matrix("x", x, dev, cols, rows)
     st = lib.ptb_checkpoint_unpack(p, ld, ep, eld, rows, cols, xp, xld, raw)
     if st:
         _check(st, "ptb_checkpoint_unpack")
@@ -792,17 +803,23 @@ def _gated_forward(x, w_gate, w_up, w_down, activation, residual, kept, bits, y,
         rp, ldr, _, _ = _matrix("residual", residual, dev, hidden, tokens)
     if y is None:
         y = _new(x, x.shape, stream)
-    yp, ldy, _, _ = _matrix("y", y, dev, hidden, tokens)
+        yp, ldy = y.data_ptr(), hidden
+    else:
+        yp, ldy, _, _ = _matrix("y", y, dev, hidden, tokens)
     kp = ke = None
     if bits == 16:
         if kept is None:
             kept = _new(x, (tokens, 2 * ffn), stream)
-        kp = _whole("kept", kept, (tokens, 2 * ffn), dev)
+            kp = kept.data_ptr()
+        else:
+            kp = _whole("kept", kept, (tokens, 2 * ffn), dev)
     elif bits == 8:
         if kept is None:
             kept = (_new(x, (tokens, 2 * ffn), stream, torch.int8),
                     _new(x, (tokens, ffn // 16), stream, torch.uint8))
-        kp, ke = _kept_pair(kept, tokens, ffn, dev)
+            kp, ke = kept[0].data_ptr(), kept[1].data_ptr()
+        else:
+            kp, ke = _kept_pair(kept, tokens, ffn, dev)
     ws, wsp, wsb = _scratch(_gated_workspace(dev, tokens, hidden, ffn), workspace, x, dev, stream)
     st = lib.ptb_gated_ffn(xp, ldx, *wp, rp, ldr, tokens, hidden, ffn, act, yp, ldy, kp, ke, wsp,
                            wsb, raw)
@@ -852,18 +869,23 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, kept, activation: str = "sil
         kp, ke = _kept_pair(kept, tokens, ffn, dev)
     else:
         kp, ke = _whole("kept", kept, (tokens, 2 * ffn), dev), None
-    if grads is None:
-        grads = dict(dx=_new(dy, dy.shape, stream), dw_gate=_new(dy, (ffn, hidden), stream, grad_dtype),
-                     dw_up=_new(dy, (ffn, hidden), stream, grad_dtype),
-                     dw_down=_new(dy, (hidden, ffn), stream, grad_dtype))
-    else:
-        grad_dtype = grads["dw_gate"].dtype
     if grad_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("weight gradients are bfloat16 or float32")
-    dxp, lddx, _, _ = _matrix("dx", grads["dx"], dev, hidden, tokens)
-    gp = (_whole("dw_gate", grads["dw_gate"], (ffn, hidden), dev, grad_dtype),
-          _whole("dw_up", grads["dw_up"], (ffn, hidden), dev, grad_dtype),
-          _whole("dw_down", grads["dw_down"], (hidden, ffn), dev, grad_dtype))
+    if grads is None:
+        dx = _new(dy, dy.shape, stream)
+        g = (_new(dy, (ffn, hidden), stream, grad_dtype), _new(dy, (ffn, hidden), stream, grad_dtype),
+             _new(dy, (hidden, ffn), stream, grad_dtype))
+        grads = dict(dx=dx, dw_gate=g[0], dw_up=g[1], dw_down=g[2])
+        dxp, lddx = dx.data_ptr(), hidden
+        gp = (g[0].data_ptr(), g[1].data_ptr(), g[2].data_ptr())
+    else:
+        grad_dtype = grads["dw_gate"].dtype
+        if grad_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("weight gradients are bfloat16 or float32")
+        dxp, lddx, _, _ = _matrix("dx", grads["dx"], dev, hidden, tokens)
+        gp = (_whole("dw_gate", grads["dw_gate"], (ffn, hidden), dev, grad_dtype),
+              _whole("dw_up", grads["dw_up"], (ffn, hidden), dev, grad_dtype),
+              _whole("dw_down", grads["dw_down"], (hidden, ffn), dev, grad_dtype))
     ws, wsp, wsb = _scratch(_gated_backward_workspace(dev, tokens, hidden, ffn, 16 if xe is None else 8),
                             workspace, dy, dev, stream)
     st = lib.ptb_gated_ffn_backward(dyp, lddy, xp, ldx, xe, ldxe, *wp, kp, ke, tokens, hidden, ffn,
@@ -906,12 +928,16 @@ def _norm_forward(x, o, post_gamma, post_beta, gate, alpha, pre_gamma, pre_beta,
     gp, gates = _gate(gate, rows, hidden, dev)
     if y is None:
         y = _new(x, x.shape, stream)
-    yp, ldy, _, _ = _matrix("y", y, dev, hidden, rows)
+        yp, ldy = y.data_ptr(), hidden
+    else:
+        yp, ldy, _, _ = _matrix("y", y, dev, hidden, rows)
     hp, ldh = None, 0
     if pre_gamma is not None:
         if h is None:
             h = _new(x, x.shape, stream)
-        hp, ldh, _, _ = _matrix("h", h, dev, hidden, rows)
+            hp, ldh = h.data_ptr(), hidden
+        else:
+            hp, ldh, _, _ = _matrix("h", h, dev, hidden, rows)
     elif h is not None:
         raise ValueError("h without pre_gamma")
     sp = None
@@ -960,8 +986,8 @@ def norm_residual_backward(dy, dh, y, o, stats, post_gamma=None, post_beta=None,
     lib = load()
     main = dh if dy is None else dy
     dev, raw = _launch_on(stream, main)
-    _, _, rows, hidden = _matrix("dy" if dy is not None else "dh", main, dev)
-    dyp, lddy = (None, 0) if dy is None else _matrix("dy", dy, dev)[:2]
+    mp, ldm, rows, hidden = _matrix("dy" if dy is not None else "dh", main, dev)
+    dyp, lddy = (None, 0) if dy is None else (mp, ldm)
     dhp = yp = None
     lddh = ldy = 0
     if pre_gamma is not None:
@@ -972,30 +998,33 @@ def norm_residual_backward(dy, dh, y, o, stats, post_gamma=None, post_beta=None,
     op, ldo, oe, ldoe, _, _ = _either("o", o, dev, hidden, rows)
     gp, gates = _gate(gate, rows, hidden, dev)
     sp = _whole("stats", stats, (rows, 4), dev, torch.float32)
-    own = grads is None
-    if own:
-        grads = dict(dx=_new(main, main.shape, stream), do=_new(main, main.shape, stream))
+    pgp = _vector("post_gamma", post_gamma, hidden, dev)
+    pbp = _vector("post_beta", post_beta, hidden, dev)
+    ngp = _vector("pre_gamma", pre_gamma, hidden, dev)
+    _vector("pre_beta", pre_beta, hidden, dev)
+    given = (("dpost_gamma", post_gamma), ("dpost_beta", post_beta), ("dgate", gate),
+             ("dpre_gamma", pre_gamma), ("dpre_beta", pre_beta))
     out = []
-    for name, t in (("post_gamma", post_gamma), ("post_beta", post_beta), ("gate", gate),
-                    ("pre_gamma", pre_gamma), ("pre_beta", pre_beta)):
-        key = "d" + name
-        if t is None:
-            out.append(None)
-            continue
-        if name != "gate":
-            _vector(name, t, hidden, dev)
-        if own:
-            grads[key] = _new(main, t.shape, stream, torch.float32)
-        g = grads.get(key)
-        out.append(None if g is None else _whole(key, g, tuple(t.shape), dev, torch.float32))
-    dxp, lddx, _, _ = _matrix("dx", grads["dx"], dev, hidden, rows)
-    dop, lddo, _, _ = _matrix("do", grads["do"], dev, hidden, rows)
+    if grads is None:
+        dx, do = _new(main, main.shape, stream), _new(main, main.shape, stream)
+        grads = dict(dx=dx, do=do)
+        dxp, lddx, dop, lddo = dx.data_ptr(), hidden, do.data_ptr(), hidden
+        for key, t in given:
+            if t is None:
+                out.append(None)
+            else:
+                grads[key] = g = _new(main, t.shape, stream, torch.float32)
+                out.append(g.data_ptr())
+    else:
+        dxp, lddx, _, _ = _matrix("dx", grads["dx"], dev, hidden, rows)
+        dop, lddo, _, _ = _matrix("do", grads["do"], dev, hidden, rows)
+        for key, t in given:
+            g = None if t is None else grads.get(key)
+            out.append(None if g is None else _whole(key, g, tuple(t.shape), dev, torch.float32))
     ws, wsp, wsb = _scratch(_norm_workspace(dev, rows, hidden, gates), workspace, main, dev, stream)
-    st = lib.ptb_norm_residual_backward(
-        dyp, lddy, dhp, lddh, yp, ldy, op, ldo, oe, ldoe, sp,
-        _vector("post_gamma", post_gamma, hidden, dev), _vector("post_beta", post_beta, hidden, dev),
-        gp, gates, alpha, _vector("pre_gamma", pre_gamma, hidden, dev), int(rms), rows, hidden, dxp,
-        lddx, dop, lddo, *out, wsp, wsb, raw)
+    st = lib.ptb_norm_residual_backward(dyp, lddy, dhp, lddh, yp, ldy, op, ldo, oe, ldoe, sp, pgp, pbp,
+                                        gp, gates, alpha, ngp, int(rms), rows, hidden, dxp, lddx, dop,
+                                        lddo, *out, wsp, wsb, raw)
     if st:
         _check(st, "ptb_norm_residual_backward")
     return grads

@@ -326,21 +326,27 @@ ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t s
   const uint32_t box_b = a.pair ? a.block_n / 2 : a.block_n;
   bool ok;
   if (amn)
-    ok = make_map_mn(&a.a0, c.a0, c.M, k0, c.lda0) && make_map_mn(&a.a1, a1, c.M, ka1, lda1);
+    ok = make_map_mn(&a.a0, c.a0, c.M, k0, c.lda0) &&
+         (!c.k_split || make_map_mn(&a.a1, a1, c.M, ka1, lda1));
   else
-    ok = make_map(&a.a0, c.a0, k0, c.M, c.lda0, 128) && make_map(&a.a1, a1, ka1, c.M, lda1, 128);
+    ok = make_map(&a.a0, c.a0, k0, c.M, c.lda0, 128) &&
+         (!c.k_split || make_map(&a.a1, a1, ka1, c.M, lda1, 128));
+  if (!c.k_split) a.a1 = a.a0;
   // B: the K extent of source i is its K part under a K split, else K; the
   // N extent is its N part under an N split, else N.
   const int64_t bk0 = c.k_split ? k0 : c.K, bk1 = c.k_split ? k1 : c.K;
   const int64_t bn0 = c.n_split ? n0 : c.N, bn1 = c.n_split ? n1 : c.N;
+  const bool two_b = c.k_split || c.n_split;
   if (c.epilogue == kEpiGated)  // half of a tile's rows from each; a pair's CTAs load one half each
     ok = ok && make_map(&a.b0, c.b0, c.K, c.N / 2, c.ldb0, a.block_n / 2) &&
          make_map(&a.b1, c.b1, c.K, c.N / 2, c.ldb0, a.block_n / 2);
   else if (bmn)
-    ok = ok && make_map_mn(&a.b0, c.b0, bn0, bk0, c.ldb0) && make_map_mn(&a.b1, b1, bn1, bk1, ldb1);
+    ok = ok && make_map_mn(&a.b0, c.b0, bn0, bk0, c.ldb0) &&
+         (!two_b || make_map_mn(&a.b1, b1, bn1, bk1, ldb1));
   else
     ok = ok && make_map(&a.b0, c.b0, bk0, bn0, c.ldb0, box_b) &&
-         make_map(&a.b1, b1, bk1, bn1, ldb1, box_b);
+         (!two_b || make_map(&a.b1, b1, bk1, bn1, ldb1, box_b));
+  if (!two_b && c.epilogue != kEpiGated) a.b1 = a.b0;
   if (!ok) return PTB_ERR_ARG;
   a.M = static_cast<int>(c.M);
   a.N = static_cast<int>(c.N);
