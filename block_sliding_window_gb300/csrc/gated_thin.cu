@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(kThreads, NT > 2 || MT > 1 ? 2 : 3) thin_kerne
   constexpr int TILES = NW * MT;                     // 16-row tiles of a warp
   constexpr int U = TILES >= 4 ? 1 : 4 / TILES;      // steps of 64 k in flight
   constexpr int ROWS = TILES * kRows;
+  constexpr int AHEAD = 8;                           // steps asked for before the wait
   extern __shared__ float part[];                    // [kWarps][ROWS][NT * 8 + 1]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -79,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, NT > 2 || MT > 1 ? 2 : 3) thin_kerne
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         uint4 xv = make_uint4(0, 0, 0, 0);
-        if (live[j]) xv = __ldg(reinterpret_cast<const uint4*>(x[j] + s * 64 + q * 32));
+        if (live[j]) xv = *reinterpret_cast<const uint4*>(x[j] + s * 64 + q * 32);
 #pragma unroll
         for (int m = 0; m < TILES; ++m) {
           const uint4 &a = wv[m][0][q], &b = wv[m][1][q];
@@ -98,6 +99,20 @@ __global__ void __launch_bounds__(kThreads, NT > 2 || MT > 1 ? 2 : 3) thin_kerne
         for (int q = 0; q < 2; ++q) wv[m][h][q] = load_stream(w[m] + h * half + s * 64 + q * 32);
   };
 
+  // The down projection's first weights are on their way to L2 while the kernel in front, whose output
+  // is its x, still runs (and writes no weights; what is in front of that one has ended, or this one
+  // could not have started).
+  if constexpr (!GATED) {
+    for (int i = 0; i < AHEAD && first + i < last; ++i)
+#pragma unroll
+      for (int m = 0; m < TILES; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (t == 0)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(w[m] + h * half + (first + i) * 64));
+  }
+  wait_for_prior();
+  dependents_may_start();
   int s = first;
   for (; s + U <= last; s += U) {
     uint4 wv[U][TILES][2][2];
@@ -147,8 +162,7 @@ cudaError_t launch_one(const ThinArgs& a, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
   }
-  kern<<<a.N / (MT * kRows), kThreads, bytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3(a.N / (MT * kRows)), dim3(kThreads), bytes, stream, a);
 }
 
 // Every block reads all of x, through L1: from 9 tokens on, two 16-row tiles a block halve that where

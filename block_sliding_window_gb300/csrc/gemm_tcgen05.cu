@@ -69,6 +69,14 @@ __host__ __device__ constexpr int gemm_threads() {
   return 64 + 32 * epi_warps<EPI>();
 }
 
+// The GEMMs of a gated feed-forward follow one another with nothing between them: each is set up
+// (barriers, tensor memory) on the SMs that the one in front has left.  A training step of 777 tokens,
+// hidden 2048, ffn 5440 takes 220 us that way and 227 without; 256 tokens of 256 by 256 12 and 14.8.
+template <int EPI>
+__host__ __device__ constexpr bool dependent() {
+  return EPI == kEpiGated || EPI == kEpiDgated || EPI == kEpiBf16;
+}
+
 // The weight-gradient GEMMs (fp32 output, both operands MN-major) write
 // their large outputs through shared memory: each epilogue warp stages its
 // 32 rows x 32 columns (rows padded to 36 floats) and then writes whole
@@ -682,6 +690,10 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1) gemm_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if constexpr (dependent<EPI>()) {
+    wait_for_prior();
+    dependents_may_start();
+  }
 
   auto stage_a = [&](int s) { return smem + s * C::kStageBytes; };
   auto stage_b = [&](int s) { return smem + s * C::kStageBytes + C::kABytes; };
@@ -947,6 +959,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<EPI>(),
   cluster_sync();  // both CTAs' barriers exist before anything crosses the pair
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if constexpr (dependent<EPI>()) {
+    wait_for_prior();
+    dependents_may_start();
+  }
 
   auto stage_a = [&](int s) { return smem + s * C::kStageBytes; };
   auto stage_b = [&](int s) { return smem + s * C::kStageBytes + C::kABytes; };
@@ -1130,6 +1146,8 @@ cudaError_t launch_pair(const GemmArgs& a, cudaStream_t stream) {
     configured_device = dev;
   }
   if (a.grid % 2) return cudaErrorInvalidValue;
+  if constexpr (dependent<EPI>())
+    return launch_dependent(kern, dim3(a.grid), dim3(gemm_threads<EPI>()), C::kSmemBytes, stream, a);
   kern<<<a.grid, gemm_threads<EPI>(), C::kSmemBytes, stream>>>(a);
   return cudaGetLastError();
 }
@@ -1147,6 +1165,8 @@ cudaError_t launch_typed(const GemmArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
+  if constexpr (dependent<EPI>())
+    return launch_dependent(kern, dim3(a.grid), dim3(gemm_threads<EPI>()), C::kSmemBytes, stream, a);
   kern<<<a.grid, gemm_threads<EPI>(), C::kSmemBytes, stream>>>(a);
   return cudaGetLastError();
 }

@@ -704,6 +704,7 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, int cluster, in
       store_v8(dst, S2[j]);
       store_v8(dst + a.hidden, S3[j]);
     }
+  dependents_may_start();
   cp_async_wait<0>();
   if constexpr (CLUSTER) cluster_sync();  // no block leaves while another may still write to it
 }
@@ -731,6 +732,7 @@ constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
     norm_backward_join_kernel(const __grid_constant__ NormArgs a, int groups) {
   __shared__ float4 part[2][32][8];
+  wait_for_prior();
   const int quad = threadIdx.x & 7, lot = threadIdx.x >> 3;
   const int col = blockIdx.x * 32 + quad * 4;
   const bool in = col < a.hidden;
@@ -900,9 +902,8 @@ cudaError_t launch_norm_residual_backward(const NormArgs& a, cudaStream_t stream
     e = cluster ? launch_backward<3, true, false>(a, p, stream) : launch_backward<3, false, false>(a, p, stream);
   if (e != cudaSuccess) return e;
   const unsigned each = a.dgate && a.gates > 1 ? static_cast<unsigned>(a.gates) : 0;
-  norm_backward_join_kernel<<<dim3((a.hidden + 31) / 32, 2 + each), kJoinThreads, 0, stream>>>(
-      a, p.groups);
-  return cudaGetLastError();
+  return launch_dependent(norm_backward_join_kernel, dim3((a.hidden + 31) / 32, 2 + each),
+                          dim3(kJoinThreads), 0, stream, a, p.groups);
 }
 
 }  // namespace ptb

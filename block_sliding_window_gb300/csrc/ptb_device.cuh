@@ -27,6 +27,20 @@ __device__ __forceinline__ void record_error(unsigned* status, unsigned code) {
   if (status) atomicCAS(status, 0u, code);
 }
 
+// ------------------------------------------------------ dependent launches --
+// A kernel launched with programmatic stream serialisation may start while the kernel in front of it
+// still runs, from the moment all of that one's blocks have called dependents_may_start() or ended.
+// wait_for_prior() returns when the kernel in front has ended and its writes can be seen; nothing of
+// its results is touched before.  Every kernel calls it before dependents_may_start(), so that when a
+// kernel starts, all but the one in front of it have ended.  Without such a launch both do nothing.
+
+__device__ __forceinline__ void dependents_may_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_prior() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ bf16 --
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
