@@ -547,6 +547,31 @@ def test_block_step_on_a_stream_and_in_two_graphs(ptb_lib):
     assert all(torch.equal(a, b) for a, b in zip(outs[0], want0))
 
 
+@pytest.mark.parametrize("t", [8, 192])
+def test_weights_that_the_call_in_front_wrote(ptb_lib, t):
+    """Kernels start while those in front of them end: none may read before what it reads is there."""
+    h = 256
+    s = ffn_inputs(h, h, h, seed=8)
+    x = normal(t, h, seed=9)
+    outs, want = [], []
+    for wait in (True, False):
+        for k in range(12):
+            first = ptb_lib.gated_ffn(s["x"] * (k + 1), *weights(s))  # [h, h]: the next call's weights
+            if wait:
+                torch.cuda.synchronize()
+            second = ptb_lib.gated_ffn(x, first, s["wu"], first)
+            if wait:
+                torch.cuda.synchronize()
+            y, kept = ptb_lib.gated_ffn_train(second, s["wg"], first, first)
+            if wait:
+                torch.cuda.synchronize()
+            g = ptb_lib.gated_ffn_backward(y, second, s["wg"], first, first, kept)
+            (want if wait else outs).append([first, second, y, kept] + list(g.values()))
+    torch.cuda.synchronize()
+    for a, b in zip(outs, want):
+        assert all(torch.equal(u.nan_to_num(), v.nan_to_num()) for u, v in zip(a, b))
+
+
 def test_two_calls_at_once(ptb_lib):
     """Two streams, each with its own workspace, interleaved."""
     s = [ffn_inputs(180, 256, 512, seed=1), ffn_inputs(33, 512, 256, seed=2)]
