@@ -194,6 +194,7 @@ ptb_status ptb_gated_ffn(const ptb_bf16* x, int64_t ld_x, const ptb_bf16* w_gate
   PTB_TRY(check_rows(x, ld_x, tokens, hidden, 8));
   PTB_TRY(check_rows(y, ld_y, tokens, hidden, 8));
   if (residual) PTB_TRY(check_rows(residual, ld_residual, tokens, hidden, 8));
+  if (tokens == 1) ld_x = ld_y = ld_residual = hidden;  // not used, but tensor maps want one
   if (y && y == residual && ld_y != ld_residual) return PTB_ERR_ARG;
   const size_t need = ptb_gated_ffn_workspace_size(tokens, hidden, ffn);
   PTB_TRY(check_workspace(workspace, workspace_bytes, need));
@@ -277,6 +278,10 @@ ptb_status ptb_gated_ffn_backward(const ptb_bf16* dy, int64_t ld_dy, const void*
       PTB_TRY(launch_status(cudaMemsetAsync(p, 0, bytes, stream)));
     return PTB_OK;
   }
+  if (tokens == 1) {  // not used, but tensor maps want one
+    ld_dy = ld_dx = hidden;
+    if (!x_exps) ld_x = hidden;
+  }
   const BackwardLayout l =
       backward_layout(tokens, hidden, ffn, x_exps != nullptr, grad_bits, ds->sms);
   char* ws = static_cast<char*>(workspace);
@@ -348,6 +353,7 @@ ptb_status ptb_norm_residual(const ptb_bf16* x, int64_t ld_x, const ptb_bf16* o,
   if (h) PTB_TRY(check_rows(h, ld_h, rows, hidden, 8));
   for (const void* p : {post_gamma, post_beta, pre_gamma, pre_beta, gate}) PTB_TRY(check_vector(p));
   PTB_TRY(check_vector(stats));
+  if (rows == 1) ld_x = ld_o = ld_y = ld_h = hidden;  // not used
   if (rows > 0 && (h == y || (y == x && ld_y != ld_x) || (y == o && ld_y != ld_o) ||
                    (h && h == x && ld_h != ld_x) || (h && h == o && ld_h != ld_o)))
     return PTB_ERR_ARG;
@@ -410,6 +416,10 @@ ptb_status ptb_norm_residual_backward(
   for (const float* p : {dpost_gamma, dpost_beta, dgate, dpre_gamma, dpre_beta})
     if (!aligned(p, 4)) return PTB_ERR_ALIGN;
   if (rows > 0 && dx == d_o) return PTB_ERR_ARG;
+  if (rows == 1) {  // not used
+    ld_dy = ld_dh = ld_y = ld_dx = ld_do = hidden;
+    if (!o_exps) ld_o = hidden;
+  }
   // In place: a row's gradients may replace what they were computed from, at the same strides.
   const struct {
     const void* p;

@@ -208,6 +208,21 @@ def test_norm_backward_of_a_cluster_captured_first(ptb_lib, n, rms):
     check_norm_backward(out, s, dy, dh, y, s["o"], 1.0, rms)
 
 
+@pytest.mark.parametrize("rms", [0, 1])
+@pytest.mark.parametrize("rows,n", [(701, 4104), (700, 5128), (701, 6144), (701, 6152), (702, 8200), (533, 12296),
+                                    (401, 16392), (300, 20488), (250, 24584), (200, 28680)])
+def test_norm_backward_of_many_wide_rows(ptb_lib, rows, n, rms):
+    # every way of cutting a row, each block with several rounds and gates that end inside its run
+    gates = 1 if rows % 2 else 2
+    s = norm_inputs(rows, n, gates, 1, 1, rms, seed=n)
+    y, h, stats = ptb_lib.norm_residual_train(s["x"], s["o"], rms=bool(rms), **parameters(s))
+    dy, dh = normal(rows, n, seed=1), normal(rows, n, seed=2)
+    out = ptb_lib.norm_residual_backward(dy, dh, y, s["o"], stats, rms=bool(rms), **parameters(s))
+    check_norm_backward(out, s, dy, dh, y, s["o"], 1.0, rms)
+    again = ptb_lib.norm_residual_backward(dy, dh, y, s["o"], stats, rms=bool(rms), **parameters(s))
+    assert all(torch.equal(out[k], again[k]) for k in out)
+
+
 def test_norm_without_the_streams_gradient(ptb_lib):
     s = norm_inputs(20, 256, 1, 1, 1, 0, seed=3)
     y, h, stats = ptb_lib.norm_residual_train(s["x"], s["o"], **parameters(s))
@@ -238,6 +253,34 @@ def test_norm_strides_and_in_place(ptb_lib, n):
     got = ptb_lib.norm_residual_backward(dy2, dh2, yy, oo, stats, grads=grads, **parameters(s))
     assert all(torch.equal(got[k], want[k]) for k in want)
     assert torch.isnan(b1[:, :8]).all() and torch.isnan(b2[:, :8]).all() and torch.isnan(b2[:, n + 8:]).all()
+
+
+@pytest.mark.parametrize("n", [192, 12288])
+def test_norm_of_one_row_uses_no_stride(ptb_lib, n):
+    lib = ptb_lib.load()
+    s = norm_inputs(1, n, 1, 1, 1, 0, seed=5)
+    y, h, stats = ptb_lib.norm_residual_train(s["x"], s["o"], **parameters(s))
+    dy, dh = normal(1, n, seed=6), normal(1, n, seed=7)
+    want = ptb_lib.norm_residual_backward(dy, dh, y, s["o"], stats, **parameters(s))
+    p = {k: s[k].data_ptr() for k in ("post_gamma", "post_beta", "gate", "pre_gamma", "pre_beta")}
+    x2, o2 = s["x"].clone(), s["o"].clone()
+    assert lib.ptb_norm_residual(x2.data_ptr(), 0, o2.data_ptr(), 8, p["post_gamma"], p["post_beta"], p["gate"], 1, 1.0,
+                                 p["pre_gamma"], p["pre_beta"], 0, 1e-5, 1, n, x2.data_ptr(), 1 << 40, o2.data_ptr(), 16,
+                                 None, None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(x2, y) and torch.equal(o2, h)
+    ws = torch.empty(ptb_lib.norm_residual_backward_workspace_size(1, n), dtype=torch.uint8, device="cuda")
+    got = {k: v.clone() for k, v in want.items() if k not in ("dx", "do")}
+    o2 = s["o"].clone()
+    assert lib.ptb_norm_residual_backward(dy.data_ptr(), 0, dh.data_ptr(), 8, y.data_ptr(), 0, o2.data_ptr(), 16, None, 0,
+                                          stats.data_ptr(), p["post_gamma"], p["post_beta"], p["gate"], 1, 1.0,
+                                          p["pre_gamma"], 0, 1, n, dy.data_ptr(), 1 << 40, o2.data_ptr(), 24,
+                                          got["dpost_gamma"].data_ptr(), got["dpost_beta"].data_ptr(),
+                                          got["dgate"].data_ptr(), got["dpre_gamma"].data_ptr(),
+                                          got["dpre_beta"].data_ptr(), ws.data_ptr(), ws.numel(), None) == 0
+    torch.cuda.synchronize()
+    got.update(dx=dy, do=o2)
+    assert all(torch.equal(got[k], want[k]) for k in want)
 
 
 def test_norm_rows_of_nan_stay_their_own(ptb_lib):
@@ -359,6 +402,32 @@ def test_gated_ffn_fp32_gradients(ptb_lib, t, h, f):
     check_ffn_backward(out, s, "silu", s["x"], kept, M.U32)
     again = ptb_lib.gated_ffn_backward(s["dy"], s["x"], *weights(s), kept, grad_dtype=torch.float32)
     assert all(torch.equal(out[k], again[k]) for k in out)
+
+
+@pytest.mark.parametrize("ld", [0, 8, 1 << 40])
+@pytest.mark.parametrize("h,f", [(128, 192), (2048, 512)])
+def test_gated_ffn_of_one_token_uses_no_stride(ptb_lib, h, f, ld):
+    lib = ptb_lib.load()
+    s = ffn_inputs(1, h, f, seed=9)
+    y, kept = ptb_lib.gated_ffn_train(s["x"], *weights(s), residual=s["resid"])
+    plain = ptb_lib.gated_ffn(s["x"], *weights(s), residual=s["resid"])
+    want = ptb_lib.gated_ffn_backward(s["dy"], s["x"], *weights(s), kept)
+    ptr = {k: v.data_ptr() for k, v in s.items()}
+    wp = ptr["wg"], ptr["wu"], ptr["wd"]
+    ws = torch.empty(max(ptb_lib.gated_ffn_workspace_size(1, h, f), ptb_lib.gated_ffn_backward_workspace_size(1, h, f)),
+                     dtype=torch.uint8, device="cuda")
+    for k, w in ((None, plain), (torch.empty_like(kept), y)):
+        got = torch.empty_like(y)
+        assert lib.ptb_gated_ffn(ptr["x"], ld, *wp, ptr["resid"], ld, 1, h, f, 0, got.data_ptr(), ld,
+                                 None if k is None else k.data_ptr(), None, ws.data_ptr(), ws.numel(), None) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(got, w) and (k is None or torch.equal(k, kept))
+    got = {k: torch.empty_like(v) for k, v in want.items()}
+    assert lib.ptb_gated_ffn_backward(ptr["dy"], ld, ptr["x"], ld, None, 0, *wp, kept.data_ptr(), None, 1, h, f, 0,
+                                      got["dx"].data_ptr(), ld, got["dw_gate"].data_ptr(), got["dw_up"].data_ptr(),
+                                      got["dw_down"].data_ptr(), 16, ws.data_ptr(), ws.numel(), None) == 0
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want)
 
 
 @pytest.mark.parametrize("t", [4, 150, 300])
