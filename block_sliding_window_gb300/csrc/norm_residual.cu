@@ -208,42 +208,15 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(const __grid_constan
 // for a channel of an rms norm and four for one of a layer norm, and a quarter of the SM has
 // registers for whole warps only:
 //   rms norms    up to 5120 channels 640 threads of 8 (96 registers), else 384 of 16 (168) a slice;
-//   layer norms  256 threads of 16 or 24 (248).  With 168 registers the sums spill: 4096 channels
-//                162 us, with 248 100
-constexpr int kRing = 200 * 1024;  // shared memory for rows, per SM
-
+//   layer norms  256 threads of 16 (248; with 168 the sums spill, 4096 channels 162 us), from 4097 to
+//                6144 channels of 24 and one row at a time (5120 channels 111 us; two rows 126, in two
+//                slices 145)
+// Rows of two to four slices are cut into twice as many, so that two blocks share an SM: one works
+// while the other waits for its cluster, and six blocks of half the size find more SMs in a GPC than
+// three (layer norms of 12288 channels on 138 SMs 148 us, on all 134; rms norms 104 and 101).
 template <int VEC, bool RMS>
 __host__ __device__ constexpr int back_threads() {
   return RMS ? (VEC == 1 ? 640 : 384) : 256;
-}
-
-struct BackPlan {
-  int vec, cluster, threads, slice, groups, stages;
-  size_t smem;
-};
-
-BackPlan back_plan(int64_t rows, int64_t hidden, bool rms, int sms) {
-  BackPlan p;
-  const int most = !rms                                ? back_threads<3, false>()
-                   : hidden <= back_threads<1, true>() * 8 ? back_threads<1, true>()
-                                                           : back_threads<2, true>();
-  p.vec = !rms ? 3 : most == back_threads<1, true>() ? 1 : 2;
-  const int slice = most * p.vec * 8;
-  p.cluster = static_cast<int>((hidden + slice - 1) / slice);
-  const int64_t vecs = (hidden / 8 + p.cluster - 1) / p.cluster;
-  if (!rms && vecs <= 2 * most) p.vec = 2;
-  p.slice = static_cast<int>(vecs) * 8;
-  p.threads = static_cast<int>(((vecs + p.vec - 1) / p.vec + 31) / 32) * 32;
-  int per_sm = p.cluster == 1 ? most / p.threads : 1;  // what the registers allow
-  if (per_sm > 10) per_sm = 10;
-  int64_t groups = static_cast<int64_t>(sms / p.cluster) * per_sm;
-  if (groups > rows) groups = rows;
-  p.groups = static_cast<int>(groups < 1 ? 1 : groups);
-  const size_t row = static_cast<size_t>(p.threads) * p.vec * 4 * 16;
-  const int64_t st = static_cast<int64_t>(kRing / per_sm / row);
-  p.stages = static_cast<int>(st > 6 ? 6 : st < 4 ? 4 : st);
-  p.smem = row * p.stages;
-  return p;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -267,26 +240,67 @@ __device__ __forceinline__ void wait_ahead(int ahead) {
 }
 
 constexpr int kMostSums = 20;
-constexpr int kMostWarps = back_threads<1, true>() / 32;
 
-// What the threads of a row, and the blocks of a cluster, tell each other.  Blocks send their sums
-// into each other's `peer` slots, each message counting its bytes on the receiver's barrier of the
-// turn.  A block's sums of the turn after next cannot come in before this block has read these: it
-// sends its own of the next turn only after that.
+// A warp's part of shared memory, behind the ring.
+struct alignas(16) WarpArea {
+  float4 stats[6];            // of the rows in the ring
+  float mine[2][kMostSums];   // its sums, for the block; two turns
+  float sum[kMostSums];       // everyone's, for its lanes
+};
+
+// What the blocks of a cluster tell each other: they send their sums into each other's `peer` slots,
+// each message counting its bytes on the receiver's barrier of the turn.  A block's sums of the turn
+// after next cannot come in before this block has read these: it sends its own of the next turn only
+// after that.
 struct Exchange {
-  float4 stats[6][kMostWarps];  // of the rows in the ring, a copy for each warp
-  float warp[2][kMostWarps][kMostSums];
-  float sum[kMostWarps][kMostSums];
   float peer[2][8][kMostSums];
   uint64_t bar[2];
   int abort;
 };
 
+constexpr size_t kShared = 226 * 1024;  // shared memory of an SM, as far as the blocks may fill it
+
+struct BackPlan {
+  int vec, cluster, threads, slice, groups, stages;
+  size_t smem;
+};
+
+BackPlan back_plan(int64_t rows, int64_t hidden, bool rms, int sms) {
+  BackPlan p;
+  const int most = !rms                                ? back_threads<2, false>()
+                   : hidden <= back_threads<1, true>() * 8 ? back_threads<1, true>()
+                                                           : back_threads<2, true>();
+  if (rms)
+    p.vec = most == back_threads<1, true>() ? 1 : 2;
+  else
+    p.vec = hidden > most * 16 && hidden <= most * 24 ? 3 : 2;
+  const int slice = most * p.vec * 8;
+  p.cluster = static_cast<int>((hidden + slice - 1) / slice);
+  if (p.cluster > 1 && p.cluster <= 4) p.cluster *= 2;  // two half blocks on an SM
+  const int64_t vecs = (hidden / 8 + p.cluster - 1) / p.cluster;
+  p.slice = static_cast<int>(vecs) * 8;
+  p.threads = static_cast<int>(((vecs + p.vec - 1) / p.vec + 31) / 32) * 32;
+  const size_t row = static_cast<size_t>(p.threads) * p.vec * 4 * 16;
+  const size_t rest = p.threads / 32 * sizeof(WarpArea);
+  // Blocks on an SM: what the registers allow and four rows a block leave room for.
+  int per_sm = most / p.threads;
+  const size_t fixed = rest + sizeof(Exchange) + 1024;
+  while (per_sm > 1 && per_sm * (4 * row + fixed) > kShared) --per_sm;
+  int64_t groups = static_cast<int64_t>(sms) * per_sm / p.cluster;
+  if (groups > rows) groups = rows;
+  p.groups = static_cast<int>(groups < 1 ? 1 : groups);
+  const int64_t st = static_cast<int64_t>((kShared / per_sm - fixed) / row);
+  p.stages = static_cast<int>(st > 6 ? 6 : st);
+  p.smem = row * p.stages + rest;
+  return p;
+}
+
 // Sums of V values over the threads of a row (all blocks of the cluster), the same bits in all of
 // them.  Lanes first trade pairs of values, so that four sums take six shuffles instead of twenty.
 template <int V, bool CLUSTER>
-__device__ __forceinline__ void row_sums(float (&v)[V], Exchange& ex, unsigned& turns, int cluster,
-                                         uint32_t rank, unsigned* status) {
+__device__ __forceinline__ void row_sums(float (&v)[V], WarpArea* areas, Exchange& ex,
+                                         unsigned& turns, int cluster, uint32_t rank,
+                                         unsigned* status) {
   static_assert(V % 4 == 0 && V <= kMostSums, "");
   const int turn = turns & 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -300,13 +314,13 @@ __device__ __forceinline__ void row_sums(float (&v)[V], Exchange& ex, unsigned& 
     t += __shfl_xor_sync(0xffffffffu, odd2 ? a : b, 2);
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (lane < 4) ex.warp[turn][warp][q + lane] = t;  // lane l has value l & 3
+    if (lane < 4) areas[warp].mine[turn][q + lane] = t;  // lane l has value l & 3
   }
   __syncthreads();
   float t = 0.f;
   if (lane < V) {
 #pragma unroll 4
-    for (int w = 0; w < warps; ++w) t += ex.warp[turn][w][lane];
+    for (int w = 0; w < warps; ++w) t += areas[w].mine[turn][lane];
   }
   if constexpr (CLUSTER) {
     if (warp == 0) {
@@ -327,11 +341,11 @@ __device__ __forceinline__ void row_sums(float (&v)[V], Exchange& ex, unsigned& 
       for (int r = 0; r < cluster; ++r) t += ex.peer[turn][r][lane];
   }
   // to every lane: this warp's own slots, read before the next round's barrier
-  if (lane < V) ex.sum[warp][lane] = t;
+  if (lane < V) areas[warp].sum[lane] = t;
   __syncwarp();
 #pragma unroll
   for (int q = 0; q < V; q += 4) {
-    const float4 p = *reinterpret_cast<const float4*>(&ex.sum[warp][q]);
+    const float4 p = *reinterpret_cast<const float4*>(&areas[warp].sum[q]);
     v[q] = p.x, v[q + 1] = p.y, v[q + 2] = p.z, v[q + 3] = p.w;
   }
   __syncwarp();
@@ -387,8 +401,8 @@ struct Gamma<false> {
 template <int VEC, bool CLUSTER, bool RMS, bool O8, bool FULL>
 __device__ __forceinline__ void backward_rows(const NormArgs& a, int cluster, int slice, int groups,
                                               int stages) {
-  extern __shared__ __align__(16) uint4 ring[];  // [stages][4][VEC][blockDim.x]
-  __shared__ __align__(16) Exchange ex;
+  extern __shared__ __align__(16) uint4 ring[];  // [stages][4][VEC][blockDim.x], then the warps' areas
+  __shared__ __align__(16) Exchange ex;          // (clusters only)
   const int ahead = stages - 2;  // rows on their way while two are worked on
   const uint32_t rank = CLUSTER ? cluster_ctarank() : 0;
   const int group = blockIdx.x / cluster;
@@ -428,13 +442,18 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, int cluster, in
   // This thread's slots: 16 bytes of each tensor and vector.
   const uint32_t per_vec = blockDim.x * 16, per_tensor = per_vec * VEC, per_stage = per_tensor * 4;
   const uint32_t mine = smem_addr(ring + threadIdx.x), ring_end = mine + per_stage * stages;
-  if (!FULL || !in[VEC - 1])  // what no copy will fill
-    for (uint32_t at = mine; at < ring_end; at += per_vec) sts16(at, make_uint4(0, 0, 0, 0));
+  for (int t = 0; t < 4; ++t)  // what no copy will fill
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (!in[j] || !(t == 0 ? has_dy : t == 1 ? true : pre))
+        for (uint32_t at = mine + t * per_tensor + j * per_vec; at < ring_end; at += per_stage)
+          sts16(at, make_uint4(0, 0, 0, 0));
   uint32_t fetch_at = mine;
   int64_t left = hi - lo;  // rows still to be fetched
   const float4* src_stats = a.stats + lo;
   const int warp = threadIdx.x >> 5;
-  const uint32_t stats_mine = smem_addr(&ex.stats[0][warp]);
+  WarpArea* const areas = reinterpret_cast<WarpArea*>(ring + stages * 4 * VEC * blockDim.x);
+  const uint32_t stats_mine = smem_addr(areas[warp].stats);
   uint32_t stats_fetch = stats_mine, stats_at = stats_mine;
   const __nv_bfloat16* src_dy = a.dy + lo * a.ld_dy + col;
   const __nv_bfloat16* src_dh = a.dh + lo * a.ld_dh + col;
@@ -465,7 +484,7 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, int cluster, in
       --left;
     }
     fetch_at += per_stage;
-    stats_fetch += kMostWarps * 16;
+    stats_fetch += 16;
     if (fetch_at == ring_end) {
       fetch_at = mine;
       stats_fetch = stats_mine;
@@ -546,7 +565,7 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, int cluster, in
                           __uint_as_float(q.w));
       if (!pre) st[r].z = st[r].w = 0.f;  // whatever is kept for a norm that is not there
       stage_at += per_stage;
-      stats_at += kMostWarps * 16;
+      stats_at += 16;
       if (stage_at == ring_end) {
         stage_at = mine;
         stats_at = stats_mine;
@@ -587,7 +606,7 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, int cluster, in
       }
 #pragma unroll
       for (int e = SUMS * N; e < (SUMS * N + 3) / 4 * 4; ++e) v[e] = 0.f;
-      row_sums<(SUMS * N + 3) / 4 * 4, CLUSTER>(v, ex, turns, cluster, rank, a.status);
+      row_sums<(SUMS * N + 3) / 4 * 4, CLUSTER>(v, areas, ex, turns, cluster, rank, a.status);
     }
     float m1[N], m2[N], k1[N], k2[N];  // less the means
 #pragma unroll
@@ -682,9 +701,12 @@ __device__ __forceinline__ void backward_rows(const NormArgs& a, int cluster, in
         for (int e = 0; e < 4; ++e) t = f2_add(t, w[j].p[e]);
       w_sum = both(t);
     }
-    int pairs = static_cast<int>((end - row) >> 1);
-    for (; pairs > 0; --pairs) rows(std::integral_constant<int, 2>());
-    if ((end - row) & 1) rows(std::integral_constant<int, 1>());
+    if constexpr (VEC == 3) {  // two rows' sums would not fit beside the channels'
+      for (int n = static_cast<int>(end - row); n > 0; --n) rows(std::integral_constant<int, 1>());
+    } else {
+      for (int n = static_cast<int>((end - row) >> 1); n > 0; --n) rows(std::integral_constant<int, 2>());
+      if ((end - row) & 1) rows(std::integral_constant<int, 1>());
+    }
     row = end;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
@@ -852,17 +874,19 @@ cudaError_t launch_backward(const NormArgs& a, BackPlan& p, cudaStream_t stream)
     cfg.attrs = at;
     cfg.numAttrs = 1;
   }
-  if (p.cluster > 2) {
-    // Larger clusters leave SMs over in each GPC: as many groups as run at once, or the last would
-    // be a wave of their own.
-    static std::atomic<int> known[9];
-    int most = known[p.cluster].load(std::memory_order_relaxed);
+  if (p.cluster > 1) {
+    // Clusters leave places over in each GPC: as many groups as run at once, or the last would be a
+    // wave of their own.  The count follows from the cluster's and the block's size.
+    static std::atomic<int> known[9][back_threads<VEC, RMS>() / 32 + 1];
+    std::atomic<int>& kept = known[p.cluster][p.threads / 32];
+    int most = kept.load(std::memory_order_relaxed);
     if (most == 0) {
       e = cudaOccupancyMaxActiveClusters(&most, kern, &cfg);
       if (e != cudaSuccess) return e;
-      known[p.cluster].store(most > 0 ? most : 1, std::memory_order_relaxed);
+      if (most < 1) most = 1;
+      kept.store(most, std::memory_order_relaxed);
     }
-    if (most > 0 && p.groups > most) p.groups = most;
+    if (p.groups > most) p.groups = most;
     cfg.gridDim = dim3(p.groups * p.cluster);
   }
   return cudaLaunchKernelEx(&cfg, kern, a, p.cluster, p.slice, p.groups, p.stages);
@@ -891,15 +915,15 @@ size_t norm_backward_partials(int64_t rows, int64_t hidden, int64_t gates, int s
 
 cudaError_t launch_norm_residual_backward(const NormArgs& a, cudaStream_t stream) {
   BackPlan p = back_plan(a.rows, a.hidden, a.rms != 0, a.sms);
-  const bool cluster = p.cluster > 1;
   cudaError_t e;
   if (a.rms)  // (a slice of 16 channels a thread may be a cluster of one block)
     e = p.vec == 1 ? launch_backward<1, false, true>(a, p, stream)
                    : launch_backward<2, true, true>(a, p, stream);
-  else if (p.vec == 2)
-    e = cluster ? launch_backward<2, true, false>(a, p, stream) : launch_backward<2, false, false>(a, p, stream);
+  else if (p.vec == 3)
+    e = launch_backward<3, false, false>(a, p, stream);
   else
-    e = cluster ? launch_backward<3, true, false>(a, p, stream) : launch_backward<3, false, false>(a, p, stream);
+    e = p.cluster > 1 ? launch_backward<2, true, false>(a, p, stream)
+                      : launch_backward<2, false, false>(a, p, stream);
   if (e != cudaSuccess) return e;
   const unsigned each = a.dgate && a.gates > 1 ? static_cast<unsigned>(a.gates) : 0;
   return launch_dependent(norm_backward_join_kernel, dim3((a.hidden + 31) / 32, 2 + each),
