@@ -478,24 +478,66 @@ __device__ __forceinline__ float4* partial_chunk(const GemmArgs& p, int slot, in
   return reinterpret_cast<float4*>(p.partials) + chunk * 256 + (prow & 31);
 }
 
-// Sum of the K pieces' partials of 32 columns of a row, in piece order.
-template <int BN, int ROWS>
-__device__ __forceinline__ void sum_pieces(const GemmArgs& p, int group0, int prow, int c,
-                                           float (&acc)[32]) {
+// Sums of the K pieces' partials, 32 columns of this thread's row at a time, in piece order.  Each
+// thread copies what it will add through its own part of the operands' ring, which no load or MMA uses
+// behind a worker's last unit: the copies of kSlots pieces are on their way at a time.
+// (Loaded into registers, a piece at a time, the join took 0.8 us more for each piece: 200 tokens by
+// 2048 by 10880 in nine pieces 36 us, 30 this way.)
+template <int BN, int EPI, int ROWS>
+struct PieceSums {
+  static constexpr int kSlots = epi_warps<EPI>() == 8 ? 5 : 8;  // of 4 KB a warp, 160 KB at most
+  static constexpr int kStride = 32 * (epi_warps<EPI>() / 4);
+  static constexpr int64_t kPiece = static_cast<int64_t>(ROWS / 32) * (BN / 32) * 256;
+  const float4* src;  // piece 0
+  uint32_t slots, at = 0;
+  int first, chunks, pieces, chunk = 0, piece = 0;
+
+  // Columns first, first + kStride .. below `end` of tile columns; of the gated epilogue each of them
+  // and then the one BN / 2 behind it.
+  __device__ __forceinline__ PieceSums(const GemmArgs& p, int slot, int prow, int first_, int end,
+                                       uint8_t* ring, int warp)
+      : slots(smem_addr(ring) + warp * kSlots * 4096 + (prow & 31) * 16), first(first_),
+        pieces(p.split_s) {
+    src = partial_chunk<BN, ROWS>(p, slot / pieces * pieces, prow, 0);
+    chunks = end > first ? (end - first + kStride - 1) / kStride : 0;
+    if (EPI == kEpiGated) chunks *= 2;
+#pragma unroll 1
+    for (int k = 0; k < kSlots; ++k) fetch();
+  }
+  __device__ __forceinline__ void fetch() {
+    if (chunk < chunks) {
+      const int c = EPI == kEpiGated ? first + (chunk >> 1) * kStride + (chunk & 1) * (BN / 2)
+                                     : first + chunk * kStride;
+      const float4* from = src + piece * kPiece + (c >> 5) * 256;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) acc[j] = 0.f;
-  for (int s = 0; s < p.split_s; ++s) {
-    const float4* src = partial_chunk<BN, ROWS>(p, group0 + s, prow, c);
+      for (int v = 0; v < 8; ++v) cp_async16(slots + at + v * 512, from + 32 * v);
+      if (++piece == pieces) {
+        piece = 0;
+        ++chunk;
+      }
+    }
+    cp_async_commit();
+    at = at == (kSlots - 1) * 4096 ? 0 : at + 4096;
+  }
+  // The next chunk.
+  __device__ __forceinline__ void sum(float (&acc)[32]) {
 #pragma unroll
-    for (int v = 0; v < 8; ++v) {
-      const float4 q = __ldcg(src + 32 * v);
-      acc[4 * v] += q.x;
-      acc[4 * v + 1] += q.y;
-      acc[4 * v + 2] += q.z;
-      acc[4 * v + 3] += q.w;
+    for (int j = 0; j < 32; ++j) acc[j] = 0.f;
+#pragma unroll 1
+    for (int s = 0; s < pieces; ++s) {
+      cp_async_wait<kSlots - 1>();
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        const uint4 q = lds16(slots + at + v * 512);
+        acc[4 * v] += __uint_as_float(q.x);
+        acc[4 * v + 1] += __uint_as_float(q.y);
+        acc[4 * v + 2] += __uint_as_float(q.z);
+        acc[4 * v + 3] += __uint_as_float(q.w);
+      }
+      fetch();
     }
   }
-}
+};
 
 // The epilogue of one unit for one thread's output row `row`: a whole tile
 // goes straight from TMEM through store_chunk; a K piece of a split tile
@@ -505,12 +547,14 @@ __device__ __forceinline__ void sum_pieces(const GemmArgs& p, int group0, int pr
 template <int BN, int EPI, bool FP8, int ROWS, bool STAGE>
 __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, int row, int prow,
                                               int counter, uint32_t t_row, int n0, int lane,
-                                              float* f32_stage, int half) {
+                                              float* f32_stage, int half, uint8_t* ring) {
   // This warp's chunks of 32 columns.
   constexpr int stride = 32 * (epi_warps<EPI>() / 4);
   const int first = 32 * half;
   bool finish = true;
+  const int warp = prow / 32 % 4 + 4 * half;  // of the epilogue
   if (u.slot >= 0) {
+    if (row - lane >= p.M) return;  // none of the warp's rows are there
     // A K piece: publish the fp32 partial, then count the arrival.
 #pragma unroll 1
     for (int c = first; c < BN; c += stride) {
@@ -537,24 +581,28 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
   }
   if constexpr (EPI == kEpiGated) {
     // Columns c and BN / 2 + c of the tile are gate and up of output column n0 / 2 + c.
-    if (finish) {
-      const int group0 = u.slot < 0 ? 0 : (u.slot / p.split_s) * p.split_s;
+    const int end = min(BN / 2, p.ffn - n0 / 2);
+    if (u.slot < 0) {
 #pragma unroll 1
-      for (int c = first; c < BN / 2 && n0 / 2 + c < p.ffn; c += stride) {
+      for (int c = first; c < end; c += stride) {
         float v[2][32];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int at = h * (BN / 2) + c;
-          if (u.slot < 0) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(t_row + at, r);
-            tmem_ld_wait();
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(t_row + h * (BN / 2) + c, r);
+          tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[h][j] = __uint_as_float(r[j]);
-          } else {
-            sum_pieces<BN, ROWS>(p, group0, prow, at, v[h]);
-          }
+          for (int j = 0; j < 32; ++j) v[h][j] = __uint_as_float(r[j]);
         }
+        if (row < p.M) store_gated(p, row, n0 / 2 + c, v[0], v[1]);
+      }
+    } else if (finish) {
+      PieceSums<BN, EPI, ROWS> pieces(p, u.slot, prow, first, end, ring, warp);
+#pragma unroll 1
+      for (int c = first; c < end; c += stride) {
+        float v[2][32];
+        pieces.sum(v[0]);
+        pieces.sum(v[1]);
         if (row < p.M) store_gated(p, row, n0 / 2 + c, v[0], v[1]);
       }
     }
@@ -611,7 +659,7 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
   } else if (finish) {
     // Sum every piece's partial (this warp's own included) in piece order,
     // so the result does not depend on which warp happened to finish.
-    const int group0 = (u.slot / p.split_s) * p.split_s;
+    PieceSums<BN, EPI, ROWS> pieces(p, u.slot, prow, first, min(BN, p.N - n0), ring, warp);
 #pragma unroll 1
     for (int c = first; c < BN && n0 + c < p.N; c += stride) {
       if constexpr (EPI == kEpiDgated) {
@@ -619,7 +667,7 @@ __device__ __forceinline__ void epilogue_unit(const GemmArgs& p, const Unit& u, 
         if (c + stride < BN) load_kept(p, row, n0 + c + stride, next);
       }
       float acc[32];
-      sum_pieces<BN, ROWS>(p, group0, prow, c, acc);
+      pieces.sum(acc);
       if constexpr (FP8) dequantize(p, row, n0 + c, acc);
       if constexpr (STAGE)
         store_chunk_f32_warp(p, row, n0 + c, acc, lane, f32_stage);
@@ -838,7 +886,7 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1) gemm_kernel(const __gr
                              static_cast<uint32_t>(acc_buf * BN);
       epilogue_unit<BN, EPI, FP8, BM, kStage>(p, u, row, row_local,
                                               (u.slot / p.split_s) * epi_warps<EPI>() + warp - 2,
-                                              t_row, n0, lane, f32_stage, (warp - 2) >> 2);
+                                              t_row, n0, lane, f32_stage, (warp - 2) >> 2, smem);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty_bar[acc_buf]);
@@ -1115,7 +1163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<EPI>(),
       epilogue_unit<BN, EPI, FP8, 2 * BM, kStage>(
           p, u, m0 + prow, prow,
           ((u.slot / p.split_s) * 2 + static_cast<int>(rank)) * epi_warps<EPI>() + warp - 2, t_row, n0,
-          lane, f32_stage, (warp - 2) >> 2);
+          lane, f32_stage, (warp - 2) >> 2, smem);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cluster_map(&tempty_bar[acc_buf], 0));
