@@ -118,13 +118,12 @@ struct ForwardLayout {
 ForwardLayout forward_layout(int64_t t, int64_t h, int64_t f, int sms) {
   ForwardLayout l;
   Regions r;
-  const size_t up = call_scratch(call_up(t, h, f), sms);
-  const size_t down = call_scratch(call_down(t, h, f), sms);
+  const CallSizes up = call_sizes(call_up(t, h, f), sms), down = call_sizes(call_down(t, h, f), sms);
   l.a = r.take(static_cast<size_t>(t) * f * 2);
-  l.gemm_bytes = up > down ? up : down;
+  l.gemm_bytes = up.scratch > down.scratch ? up.scratch : down.scratch;
   l.gemm = r.take(l.gemm_bytes);
-  l.counters[0] = r.take(call_counters(call_up(t, h, f), sms));
-  l.counters[1] = r.take(call_counters(call_down(t, h, f), sms));
+  l.counters[0] = r.take(up.counters);
+  l.counters[1] = r.take(down.counters);
   l.total = r.off;
   return l;
 }
@@ -140,16 +139,11 @@ BackwardLayout backward_layout(int64_t t, int64_t h, int64_t f, bool x8, int bit
   l.dgu = r.take(static_cast<size_t>(t) * f * 4);
   l.x = r.take(x8 ? static_cast<size_t>(t) * h * 2 : 0);
   l.gemm_bytes = 0;
-  for (const GemmCall& c : {call_da(t, h, f), call_dw_down(t, h, f, bits), call_dw_up(t, h, f, bits),
-                            call_dx(t, h, f)}) {
-    const size_t b = call_scratch(c, sms);
-    l.gemm_bytes = b > l.gemm_bytes ? b : l.gemm_bytes;
-  }
+  const CallSizes sizes[] = {call_sizes(call_da(t, h, f), sms), call_sizes(call_dw_down(t, h, f, bits), sms),
+                             call_sizes(call_dw_up(t, h, f, bits), sms), call_sizes(call_dx(t, h, f), sms)};
+  for (const CallSizes& s : sizes) l.gemm_bytes = s.scratch > l.gemm_bytes ? s.scratch : l.gemm_bytes;
   l.gemm = r.take(l.gemm_bytes);
-  int k = 0;
-  for (const GemmCall& c : {call_da(t, h, f), call_dw_down(t, h, f, bits), call_dw_up(t, h, f, bits),
-                            call_dx(t, h, f)})
-    l.counters[k++] = r.take(call_counters(c, sms));
+  for (int k = 0; k < 4; ++k) l.counters[k] = r.take(sizes[k].counters);
   l.total = r.off;
   return l;
 }

@@ -47,7 +47,6 @@ ptb_status device_state(DeviceState** out);
 int current_sms();
 ptb_status launch_status(cudaError_t e);
 int pick_block_n(int64_t a, int64_t b);
-int ragged_block_n(int64_t n);
 
 // One GEMM of the layer: C[M, N] = A[M, K] B[N, K]^T with
 //   A = [a0 | a1] split along K at k0 (k1 == 0: a0 only), and
@@ -122,18 +121,18 @@ struct GemmCall {
   const ptb_bf16* resid = nullptr;  // kEpiBf16
   unsigned* counters = nullptr;  // cleared arrival counters (else in scratch, cleared by the launch)
   int64_t ld_resid = 0;
-  bool ragged = false;  // N tiles as ragged_block_n picks them
+  bool ragged = false;  // tiles as pick_tiles picks them; the last one may reach past N
   int block_n() const {
-    if (ragged) return ragged_block_n(N);
     return n_split ? pick_block_n(n_split, N - n_split) : pick_block_n(N, N);
   }
   int64_t kb() const { return (K + 63) / 64; }
 };
 
-// Split-wave scratch of a backward GEMM (either tile shape), and its launch.
-size_t call_scratch(const GemmCall& c, int sms);
-// Bytes of its arrival counters alone.
-size_t call_counters(const GemmCall& c, int sms);
+// Split-wave scratch of a backward GEMM (either tile shape), its arrival counters alone, and its launch.
+struct CallSizes {
+  size_t scratch = 0, counters = 0;
+};
+CallSizes call_sizes(const GemmCall& c, int sms);
 ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t scratch_bytes,
                      cudaStream_t stream);
 

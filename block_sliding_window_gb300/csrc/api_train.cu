@@ -101,7 +101,7 @@ BwdLayout bwd_layout(int64_t batch, int64_t seq, int64_t hidden, int64_t ffn, in
   size_t g = 0;
   for (const GemmCall& c : {call_dgrad_out(t, hidden, ffn), call_wgrad_out(t, hidden, ffn, ldu),
                             call_dgrad_in(t, hidden, ffn, ldu), call_wgrad_in(t, hidden, ffn, ldu)}) {
-    const size_t b = call_scratch(c, sms);
+    const size_t b = call_sizes(c, sms).scratch;
     g = b > g ? b : g;
   }
   l.gemm = take(g);

@@ -1229,7 +1229,8 @@ int gemm_counters(int epilogue) {
                                    : 4) / 4;
 }
 
-GemmPlan plan_gemm(int64_t tiles, int64_t num_kb, int sms, int block_n, int rows, int counters) {
+GemmPlan plan_gemm(int64_t tiles, int64_t num_kb, int sms, int block_n, int rows, int counters,
+                   int most_s) {
   GemmPlan g;
   g.grid = static_cast<int>(tiles < sms ? tiles : sms);
   g.split_r = 0;
@@ -1240,6 +1241,7 @@ GemmPlan plan_gemm(int64_t tiles, int64_t num_kb, int sms, int block_n, int rows
     int64_t s = sms / r;
     const int64_t s_k = num_kb / kMinSplitKBlocks;  // each piece keeps >= kMinSplitKBlocks
     if (s_k < s) s = s_k;
+    if (most_s < s) s = most_s;
     if (s >= 2) {
       g.split_r = static_cast<int>(r);
       g.split_s = static_cast<int>(s);

@@ -8,6 +8,7 @@
 // and api_train.cu.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -93,14 +94,6 @@ int pick_block_n(int64_t a, int64_t b) {
   return 0;
 }
 
-// N tile of a GEMM whose last tile may reach past N.  Above 512 columns a 256-wide tile that is cut
-// wastes less than narrow ones cost: the backward pass of a gated feed-forward of 1555 tokens, hidden
-// 5120, ffn 13632 (213 tiles of 64, or 54 of 256) took 1395 us on the widest tiles that divide the
-// width and 946 on these.
-int ragged_block_n(int64_t n) {
-  return n % 256 == 0 || n > 512 ? 256 : pick_block_n(n, n);
-}
-
 ptb_status launch_status(cudaError_t e) { return e == cudaSuccess ? PTB_OK : PTB_ERR_LAUNCH; }
 
 // SM count of the current device, or an upper bound when there is none.
@@ -151,11 +144,12 @@ size_t gemm_scratch_any(int64_t m, int64_t n, int64_t kb, int block_n, int sms, 
 
 // Fills the grid / split fields of a launch (a.pair and a.block_n set).
 // Without scratch (or with too little) the GEMM runs unsplit.
-void apply_plan(GemmArgs& a, int64_t num_kb, int sms, void* scratch, size_t scratch_bytes) {
+void apply_plan(GemmArgs& a, int64_t num_kb, int sms, void* scratch, size_t scratch_bytes,
+                int most_s = 1 << 30) {
   const int64_t tiles = gemm_tiles(a.M, a.N, a.block_n, a.pair != 0);
   const int workers = a.pair ? sms / 2 : sms;
   GemmPlan g = plan_gemm(tiles, num_kb, workers, a.block_n, a.pair ? 256 : 128,
-                         gemm_counters(a.epilogue));
+                         gemm_counters(a.epilogue), most_s);
   const int per_worker = a.pair ? 2 : 1;
   if (g.split_s >= 2 && scratch && scratch_bytes >= gemm_scratch_bytes(g)) {
     a.grid = g.grid * per_worker;
@@ -294,23 +288,78 @@ bool make_map_mn(CUtensorMap* map, const void* base, uint64_t inner, uint64_t ou
   return make_map(map, base, inner, outer, ld, 64);
 }
 
-size_t call_scratch(const GemmCall& c, int sms) {
-  const int bn = c.block_n() ? c.block_n() : 64;
-  return gemm_scratch_any(c.M, c.N, c.kb(), bn, sms, gemm_counters(c.epilogue));
+// Tiles of a GEMM and the most pieces that a tile's K may be cut into.
+struct Tiles {
+  int block_n;
+  bool pair;
+  int most_s;
+};
+
+// Of a ragged call: the tiles (256 wide on pairs of CTAs, or 256, 128 or 64 on one) and the pieces of the
+// last wave's K with the least time by a model in us, of the full waves' main loops (or of the stores
+// behind them, where those take longer), the last wave's, its stores and the join of its pieces.  Wide
+// tiles and pairs do more for each byte they load; narrow ones spread few tiles, and the stores behind
+// them, over more SMs.  Fitted to 15 choices for each of 102 GEMMs (64 to 4000 tokens, hidden 512 to
+// 5120), where the tiles that it picks take 1.6% more than the best of the 15 and 16% less than pairs of
+// 256 with as many pieces as there are idle SMs.
+Tiles pick_tiles(const GemmCall& c, int sms, bool pairs) {
+  pairs = pairs && sms >= 2 && c.M > 128;
+  if (!c.ragged) return {c.block_n(), pairs && c.block_n() == 256, 1 << 30};
+  static const struct {
+    int block_n;
+    bool pair;
+    float k_block, start;
+  } kinds[] = {{256, true, 0.30f, 2.1f}, {256, false, 0.36f, 0.f}, {128, false, 0.30f, 0.f}, {64, false, 0.29f, 0.f}};
+  const float store = c.epilogue == kEpiDgated ? 10.f : c.epilogue == kEpiGated ? 2.7f : 2.6f;
+  const int kb = static_cast<int>(c.kb());
+  Tiles best{256, false, 1};
+  float best_us = 3.0e38f;
+  for (const auto& k : kinds) {
+    if (k.pair && !pairs) continue;
+    if (c.epilogue == kEpiGated && k.block_n < 128) continue;  // half of a tile is the gate's
+    const int64_t tiles = gemm_tiles(c.M, c.N, k.block_n, k.pair);
+    const int workers = k.pair ? sms / 2 : sms;
+    const int r = static_cast<int>(tiles % workers);
+    const float wide = k.block_n / 256.f, whole = kb * k.k_block, end = store * wide + 0.2f;
+    const float waves = tiles / workers * (whole > end ? whole : end) + end + k.start;
+    int most = r ? workers / r : 1;
+    if (most > kb / kMinSplitKBlocks) most = kb / kMinSplitKBlocks;
+    const float join = 1.8f * wide;
+    const int near = static_cast<int>(std::sqrt(whole / join));  // the least of whole / s + join * s
+    for (int s : {1, near < most ? near : most, near + 1 < most ? near + 1 : most}) {
+      if (s < 1) continue;
+      float us = waves;
+      if (r) us += (kb + s - 1) / s * k.k_block;
+      if (s > 1) us += 3.f + join * s;
+      if (us < best_us) {
+        best_us = us;
+        best = {k.block_n, k.pair, s};
+      }
+    }
+  }
+  return best;
 }
 
-size_t call_counters(const GemmCall& c, int sms) {
-  const int bn = c.block_n() ? c.block_n() : 64, n = gemm_counters(c.epilogue);
-  const size_t a = plan_gemm(gemm_tiles(c.M, c.N, bn, false), c.kb(), sms, bn, 128, n).counter_bytes;
-  const size_t b = plan_gemm(gemm_tiles(c.M, c.N, bn, true), c.kb(), sms / 2, bn, 256, n).counter_bytes;
-  return round_up(a > b ? a : b, kAlign);
+// (Pairs of CTAs may be switched on or off between a query and the call.)
+CallSizes call_sizes(const GemmCall& c, int sms) {
+  CallSizes most;
+  for (bool pairs : {false, true}) {
+    const Tiles t = pick_tiles(c, sms, pairs);
+    const int bn = t.block_n ? t.block_n : 64;
+    const GemmPlan g = plan_gemm(gemm_tiles(c.M, c.N, bn, t.pair), c.kb(), t.pair ? sms / 2 : sms, bn,
+                                 t.pair ? 256 : 128, gemm_counters(c.epilogue), t.most_s);
+    most.scratch = std::max(most.scratch, gemm_scratch_bytes(g));
+    most.counters = std::max(most.counters, round_up(g.counter_bytes, kAlign));
+  }
+  return most;
 }
 
 ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t scratch_bytes,
                      cudaStream_t stream) {
   GemmArgs a;
   std::memset(&a, 0, sizeof(a));
-  a.block_n = c.block_n();
+  const Tiles tiles = pick_tiles(c, ds->sms, ds->pairs != 0);
+  a.block_n = tiles.block_n;
   if (!a.block_n || c.M < 1 || c.K < 1 || c.M > (1 << 30) || c.N > (1 << 30) || c.K > (1 << 30))
     return PTB_ERR_SHAPE;
   if ((c.k_split && c.n_split) || c.k_split % 64 || c.n_split % 64) return PTB_ERR_SHAPE;
@@ -322,7 +371,7 @@ ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t s
   const ptb_bf16* b1 = (c.k_split || c.n_split) ? c.b1 : c.b0;
   const int64_t ldb1 = (c.k_split || c.n_split) ? c.ldb1 : c.ldb0;
   const int64_t ka1 = k1 ? k1 : k0;
-  a.pair = use_pairs(ds, a.block_n == 256, c.M) ? 1 : 0;
+  a.pair = tiles.pair ? 1 : 0;
   const uint32_t box_b = a.pair ? a.block_n / 2 : a.block_n;
   bool ok;
   if (amn)
@@ -379,7 +428,7 @@ ptb_status gemm_call(DeviceState* ds, const GemmCall& c, void* scratch, size_t s
   a.resid = c.resid ? bf(c.resid) : nullptr;
   a.ld_resid = c.ld_resid;
   a.wide = aligned(a.out, 32) && aligned(a.out1, 32) && a.ld_out % 16 == 0 && a.ld_out1 % 16 == 0;
-  apply_plan(a, c.kb(), ds->sms, scratch, scratch_bytes);
+  apply_plan(a, c.kb(), ds->sms, scratch, scratch_bytes, tiles.most_s);
   if (c.counters && a.counters) {
     a.counters = c.counters;
     a.counters_zero = 1;

@@ -123,8 +123,9 @@ struct GemmPlan {
 // `workers` is the number of CTAs (or CTA pairs), `rows` the tile height
 // (128, or 256 for pairs).
 // `counters`: arrival counters for 32 rows (gemm_counters of the epilogue).
+// `most_s` caps the pieces of a tile.
 GemmPlan plan_gemm(int64_t tiles, int64_t num_kb, int workers, int block_n, int rows = 128,
-                   int counters = 1);
+                   int counters = 1, int most_s = 1 << 30);
 int gemm_counters(int epilogue);
 
 struct SwaArgs {

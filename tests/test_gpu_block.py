@@ -393,6 +393,36 @@ def test_gated_ffn(ptb_lib, t, h, f, pairs, act):
         ptb_lib.set_gemm_pairs(was)
 
 
+# Every tile (256 wide on pairs of CTAs, 256, 128 and 64 on one), whole and in pieces of K, that a
+# GEMM of the call can be given.
+TILES = [
+    (32, 576, 1088), (129, 4928, 64), (37, 3712, 4928), (32, 64, 9984), (2959, 1088, 192), (644, 4864, 64),
+    (131, 5056, 3456), (551, 3968, 2240), (35, 5056, 10048), (259, 64, 9984), (2765, 192, 10816), (4040, 192, 2560),
+    (133, 2240, 11008), (129, 4928, 6976), (158, 5888, 6528), (777, 2048, 5440),
+]
+
+
+@pytest.mark.parametrize("t,h,f", TILES)
+def test_gated_ffn_of_every_tile(ptb_lib, t, h, f):
+    s = ffn_inputs(t, h, f, seed=t + h + f)
+    act, bits = ("silu", 16) if t % 2 else ("gelu", 8)
+    y, kept = ptb_lib.gated_ffn_train(s["x"], *weights(s), activation=act, bits=bits, residual=s["resid"])
+    check_ffn(s, act, y, kept, resid=s["resid"])
+    x = s["x"] if bits == 16 else ptb_lib.checkpoint_pack(s["x"])
+    out = ptb_lib.gated_ffn_backward(s["dy"], x, *weights(s), kept, activation=act)
+    check_ffn_backward(out, s, act, x, kept)
+    again = ptb_lib.gated_ffn_backward(s["dy"], x, *weights(s), kept, activation=act)
+    assert all(torch.equal(out[k], again[k]) for k in out)
+
+
+@pytest.mark.parametrize("t,h,f", [(2959, 1088, 192), (4040, 192, 2560), (2765, 192, 10816), (777, 2048, 5440)])
+def test_gated_ffn_fp32_gradients_of_every_tile(ptb_lib, t, h, f):
+    s = ffn_inputs(t, h, f, seed=2)
+    _, kept = ptb_lib.gated_ffn_train(s["x"], *weights(s))
+    out = ptb_lib.gated_ffn_backward(s["dy"], s["x"], *weights(s), kept, grad_dtype=torch.float32)
+    check_ffn_backward(out, s, "silu", s["x"], kept, M.U32)
+
+
 @pytest.mark.parametrize("t,h,f", [(5, 128, 192), (260, 256, 384), (40, 1024, 256)])
 def test_gated_ffn_fp32_gradients(ptb_lib, t, h, f):
     s = ffn_inputs(t, h, f, seed=1)
