@@ -109,6 +109,13 @@ struct Regions {
   }
 };
 
+// Few tokens go through the kernel that streams the weights.  Every block of it reads all of x, which
+// from 17 tokens on costs more than the tiles of the other kernel, unless there is little to stream: 24
+// tokens, hidden 2048, ffn 5440 26 us and 34, 4096 and 11008 63 both, 5120 and 13824 91 and 86.
+bool thin(int64_t tokens, int64_t hidden, int64_t ffn) {
+  return tokens <= kThinTokens / 2 || (tokens <= kThinTokens && hidden * ffn < 40'000'000);
+}
+
 // The GEMMs of a call have arrival counters of their own, which one memset clears: a memset in front of
 // each was a fifth of the nodes of a small call's graph.
 struct ForwardLayout {
@@ -198,7 +205,7 @@ ptb_status ptb_gated_ffn(const ptb_bf16* x, int64_t ld_x, const ptb_bf16* w_gate
   const ForwardLayout l = forward_layout(tokens, hidden, ffn, ds->sms);
   char* ws = static_cast<char*>(workspace);
   ptb_bf16* a = reinterpret_cast<ptb_bf16*>(ws + l.a);
-  if (tokens <= kThinTokens && !kept) {
+  if (thin(tokens, hidden, ffn) && !kept) {
     ThinArgs n;
     std::memset(&n, 0, sizeof(n));
     n.x = bf(x), n.ld_x = ld_x;

@@ -11,8 +11,8 @@
 //   - in m16n8k16 the weights are the 16-row operand and tokens the 8 columns.  A lane loads 16
 //     bytes of a row, k = 8 t .. 8 t + 7 of 32: the fragment wants pairs of k in another order, but
 //     the order of a contraction's index does not matter as long as x is loaded in the same one.
-// Bound by memory: hidden 5120, ffn 13824, one token 68 us (6.2 TB/s; the tcgen05 kernel 152 then, 95
-// now), 16 tokens 79, 24 tokens 90, where the reading of x by every block takes 18.  (A cluster for the
+// Bound by memory: hidden 5120, ffn 13824, one token 67 us (6.3 TB/s; the tcgen05 kernel 86), 16 tokens
+// 81, 24 tokens 91, where the reading of x by every block takes 18.  (A cluster for the
 // K of 64 rows, x in shared memory: 154 us; the rounds of copies, barriers and remote sums cost more.)
 #include "gated_device.cuh"
 

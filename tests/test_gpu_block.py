@@ -401,6 +401,9 @@ TILES = [
     (133, 2240, 11008), (129, 4928, 6976), (158, 5888, 6528), (777, 2048, 5440),
 ]
 
+# Few tokens and so many weights that the kernels of few tokens end at 16.
+MANY_WEIGHTS = [(16, 4160, 9664), (17, 4160, 9664), (32, 9664, 4160)]
+
 
 @pytest.mark.parametrize("t,h,f", TILES)
 def test_gated_ffn_of_every_tile(ptb_lib, t, h, f):
@@ -413,6 +416,13 @@ def test_gated_ffn_of_every_tile(ptb_lib, t, h, f):
     check_ffn_backward(out, s, act, x, kept)
     again = ptb_lib.gated_ffn_backward(s["dy"], x, *weights(s), kept, activation=act)
     assert all(torch.equal(out[k], again[k]) for k in out)
+
+
+@pytest.mark.parametrize("t,h,f", MANY_WEIGHTS)
+def test_gated_ffn_of_few_tokens_and_many_weights(ptb_lib, t, h, f):
+    s = ffn_inputs(t, h, f, seed=t)
+    check_ffn(s, "silu", ptb_lib.gated_ffn(s["x"], *weights(s)))
+    check_ffn(s, "silu", ptb_lib.gated_ffn(s["x"], *weights(s), residual=s["resid"]), resid=s["resid"])
 
 
 @pytest.mark.parametrize("t,h,f", [(2959, 1088, 192), (4040, 192, 2560), (2765, 192, 10816), (777, 2048, 5440)])
