@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(const __grid_constan
 //                6144 channels of 24 and one row at a time (5120 channels 111 us; two rows 126, in two
 //                slices 145)
 // Rows of two to four slices are cut into twice as many, so that two blocks share an SM: one works
-// while the other waits for its cluster (layer norms of 12288 channels 148 us in three slices, whose
-// clusters also leave 14 of 152 SMs over, 134 in six; rms norms 104 in two and 101 in four).
+// while the other waits for its cluster (layer norms of 12288 channels 148 us in three slices, 134 in
+// six, either way on 138 SMs; rms norms 104 in two and 101 in four).
 template <int VEC, bool RMS>
 __host__ __device__ constexpr int back_threads() {
   return RMS ? (VEC == 1 ? 640 : 384) : 256;
