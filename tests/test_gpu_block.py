@@ -401,6 +401,9 @@ TILES = [
     (133, 2240, 11008), (129, 4928, 6976), (158, 5888, 6528), (777, 2048, 5440),
 ]
 
+# Long and narrow: one tile of a weight gradient in dozens of pieces, rows of one tile's columns.
+LONG = [(100003, 64, 64), (20000, 128, 64), (3, 64, 39936), (65, 10240, 128)]
+
 # Few tokens and so many weights that the kernels of few tokens end at 16.
 MANY_WEIGHTS = [(16, 4160, 9664), (17, 4160, 9664), (32, 9664, 4160)]
 
@@ -416,6 +419,38 @@ def test_gated_ffn_of_every_tile(ptb_lib, t, h, f):
     check_ffn_backward(out, s, act, x, kept)
     again = ptb_lib.gated_ffn_backward(s["dy"], x, *weights(s), kept, activation=act)
     assert all(torch.equal(out[k], again[k]) for k in out)
+
+
+@pytest.mark.parametrize("t,h,f", LONG)
+def test_gated_ffn_long_and_narrow(ptb_lib, t, h, f):
+    s = ffn_inputs(t, h, f, seed=t)
+    check_ffn(s, "silu", ptb_lib.gated_ffn(s["x"], *weights(s)))
+    y, kept = ptb_lib.gated_ffn_train(s["x"], *weights(s), bits=8)
+    check_ffn(s, "silu", y, kept)
+    out = ptb_lib.gated_ffn_backward(s["dy"], s["x"], *weights(s), kept)
+    check_ffn_backward(out, s, "silu", s["x"], kept)
+    again = ptb_lib.gated_ffn_backward(s["dy"], s["x"], *weights(s), kept)
+    assert all(torch.equal(out[k], again[k]) for k in out)
+
+
+@pytest.mark.parametrize("t,h,f", [(777, 2048, 5440), (131, 5056, 3456)])
+def test_gated_ffn_without_pairs(ptb_lib, t, h, f):
+    # the workspace of a size serves either way, and a call after the switch
+    s = ffn_inputs(t, h, f, seed=3)
+    ws = torch.empty(max(ptb_lib.gated_ffn_workspace_size(t, h, f), ptb_lib.gated_ffn_backward_workspace_size(t, h, f)),
+                     dtype=torch.uint8, device="cuda")
+    was = ptb_lib.set_gemm_pairs(0)
+    try:
+        y, kept = ptb_lib.gated_ffn_train(s["x"], *weights(s), workspace=ws)
+        check_ffn(s, "silu", y, kept)
+        ptb_lib.set_gemm_pairs(1)
+        out = ptb_lib.gated_ffn_backward(s["dy"], s["x"], *weights(s), kept, workspace=ws)
+        check_ffn_backward(out, s, "silu", s["x"], kept)
+        ptb_lib.set_gemm_pairs(0)
+        out = ptb_lib.gated_ffn_backward(s["dy"], s["x"], *weights(s), kept, workspace=ws)
+        check_ffn_backward(out, s, "silu", s["x"], kept)
+    finally:
+        ptb_lib.set_gemm_pairs(was)
 
 
 @pytest.mark.parametrize("t,h,f", MANY_WEIGHTS)
