@@ -78,8 +78,8 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[32], int& turn) {
 }
 
 // VPT: 16-byte vectors of the row that a thread holds.
-template <int VPT, bool WARP, bool RMS>
-__global__ void __launch_bounds__(512) norm_residual_kernel(const __grid_constant__ NormArgs a) {
+template <int VPT, bool WARP, bool RMS, int REGS>
+__global__ void __maxnreg__(REGS) norm_residual_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float red[2][32];
   const int lanes = WARP ? 32 : blockDim.x;
   const int lane = WARP ? threadIdx.x & 31 : threadIdx.x;
@@ -812,28 +812,32 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
 }
 
-// Vectors a thread: few, for rows in many blocks at once; a layer norm's four rounds of sums cost
-// less with a third one (5120 channels: 72 us for 77 with two and 78 with four; rms 56.4 with two, 58.2
-// with three; 12288: 87 with three on 512 threads, 96 with four).
+// Vectors and registers a thread: what keeps most rows under way on an SM without spilling much, since a
+// row is a chain of loads, sums and barriers.  Layer norms have four rounds of sums, which cost less with
+// more vectors (84 MB of each tensor: 5120 channels 77 us with two, 73 with three of 60 registers, 68 with
+// four of 64; 8192 86 and 70, 16384 in 512 threads 118 with five of 128, 80; 20480 114 and 90 with five of
+// 64; 32768 121 with eight, 97).  rms norms: 56 us up to 8192, 16384 82 and 68, 32768 94 and 78.  Of a
+// warp's rows: layer norms of 256 channels 69 us with 32 registers and 76 with 46, 512 62 with 48 and 65
+// with 64, 1024 65 with 64 and 76 with 88.
 template <bool RMS>
 cudaError_t launch_forward(const NormArgs& a, cudaStream_t stream) {
   const int nvec = a.hidden / 8;
   const unsigned rows = static_cast<unsigned>(a.rows), warps = (rows + 7) / 8;
   auto threads = [&](int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; };
   if (nvec <= 32)
-    norm_residual_kernel<1, true, RMS><<<warps, 256, 0, stream>>>(a);
+    norm_residual_kernel<1, true, RMS, 32><<<warps, 256, 0, stream>>>(a);
   else if (nvec <= 64)
-    norm_residual_kernel<2, true, RMS><<<warps, 256, 0, stream>>>(a);
+    norm_residual_kernel<2, true, RMS, 48><<<warps, 256, 0, stream>>>(a);
   else if (nvec <= 128)
-    norm_residual_kernel<4, true, RMS><<<warps, 256, 0, stream>>>(a);
+    norm_residual_kernel<4, true, RMS, RMS ? 72 : 64><<<warps, 256, 0, stream>>>(a);
   else if (nvec <= (RMS ? 1024 : 256))
-    norm_residual_kernel<2, false, RMS><<<rows, threads(2), 0, stream>>>(a);
-  else if (nvec <= 1536)
-    norm_residual_kernel<3, false, RMS><<<rows, threads(3), 0, stream>>>(a);
-  else if (nvec <= 2560)
-    norm_residual_kernel<5, false, RMS><<<rows, threads(5), 0, stream>>>(a);
+    norm_residual_kernel<2, false, RMS, 40><<<rows, threads(2), 0, stream>>>(a);
+  else if (nvec > 1024 && nvec <= 1536)
+    norm_residual_kernel<3, false, RMS, 64><<<rows, threads(3), 0, stream>>>(a);
+  else if (nvec > (RMS ? 1536 : 2048) && nvec <= 2560)
+    norm_residual_kernel<5, false, RMS, 64><<<rows, threads(5), 0, stream>>>(a);
   else
-    norm_residual_kernel<8, false, RMS><<<rows, threads(8), 0, stream>>>(a);
+    norm_residual_kernel<4, false, RMS, 64><<<rows, threads(4), 0, stream>>>(a);
   return cudaGetLastError();
 }
 
