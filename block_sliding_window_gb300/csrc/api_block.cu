@@ -447,7 +447,7 @@ ptb_status ptb_norm_residual_backward(
   a.o_exps = o_exps, a.ld_o_exps = ld_o_exps;
   a.stats = reinterpret_cast<float4*>(const_cast<float*>(stats));
   a.post_gamma = bf(post_gamma), a.post_beta = bf(post_beta), a.pre_gamma = bf(pre_gamma);
-  a.gate = bf(gate), a.gates = gates;
+  a.gate = bf(gate), a.gates = gate ? gates : 1;  // without a gate there is nothing to sum by gates
   a.alpha = alpha, a.rms = rms;
   a.rows = rows, a.hidden = static_cast<int>(hidden);
   a.dx = bf(dx), a.ld_dx = ld_dx, a.d_o = bf(d_o), a.ld_do = ld_do;

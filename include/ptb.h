@@ -681,7 +681,7 @@ ptb_status ptb_gated_ffn_backward(const ptb_bf16* dy, int64_t ld_dy, const void*
  *        same stride) but not each other
  *   gate       [gates, hidden]: rows / gates rows in a row share a gate (gates
  *        divides rows; 1: a gate per channel; the number of sequences: one for
- *        each)
+ *        each; checked, but not used, without a gate)
  *   stats      NULL, or [rows, 4] fp32, 16-byte aligned: mean and
  *        1 / sqrt(.. + eps) of o, then of y (zeros for a norm that is absent),
  *        for the backward pass

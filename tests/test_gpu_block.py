@@ -283,6 +283,32 @@ def test_norm_of_one_row_uses_no_stride(ptb_lib, n):
     assert all(torch.equal(got[k], want[k]) for k in want)
 
 
+@pytest.mark.parametrize("rms", [0, 1])
+@pytest.mark.parametrize("post,pre", [(1, 1), (1, 0), (0, 1)])
+@pytest.mark.parametrize("rows,n,gates", [(4, 64, 2), (300, 320, 3), (12, 12288, 12), (700, 5120, 700)])
+def test_norm_without_a_gate_uses_no_count_of_gates(ptb_lib, rows, n, gates, post, pre, rms):
+    """A caller may pass its number of sequences whether there is a gate or not."""
+    lib = ptb_lib.load()
+    s = norm_inputs(rows, n, 0, post, pre, rms, seed=rows)
+    y, h, stats = ptb_lib.norm_residual_train(s["x"], s["o"], rms=bool(rms), **parameters(s))
+    dy, dh = normal(rows, n, seed=1), normal(rows, n, seed=2) if pre else None
+    want = ptb_lib.norm_residual_backward(dy, dh, y, s["o"], stats, rms=bool(rms), **parameters(s))
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    y2, h2 = torch.empty_like(y), torch.empty_like(y) if pre else None
+    assert lib.ptb_norm_residual(p(s["x"]), n, p(s["o"]), n, p(s["post_gamma"]), p(s["post_beta"]), None, gates, 1.0,
+                                 p(s["pre_gamma"]), p(s["pre_beta"]), rms, 1e-5, rows, n, p(y2), n, p(h2), n, None, None) == 0
+    ws = torch.empty(ptb_lib.norm_residual_backward_workspace_size(rows, n, gates), dtype=torch.uint8, device="cuda")
+    got = {k: torch.full_like(v, math.nan) for k, v in want.items()}
+    g = lambda k: p(got.get(k))  # noqa: E731
+    assert lib.ptb_norm_residual_backward(p(dy), n, p(dh), n, p(y), n, p(s["o"]), n, None, 0, p(stats), p(s["post_gamma"]),
+                                          p(s["post_beta"]), None, gates, 1.0, p(s["pre_gamma"]), rms, rows, n, g("dx"), n,
+                                          g("do"), n, g("dpost_gamma"), g("dpost_beta"), None, g("dpre_gamma"),
+                                          g("dpre_beta"), p(ws), ws.numel(), None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(y2, y) and (h is None or torch.equal(h2, h))
+    assert all(torch.equal(got[k], want[k]) for k in want)
+
+
 def test_norm_rows_of_nan_stay_their_own(ptb_lib):
     s = norm_inputs(40, 512, 1, 1, 1, 0, seed=8)
     y, h, stats = ptb_lib.norm_residual_train(s["x"], s["o"], **parameters(s))
