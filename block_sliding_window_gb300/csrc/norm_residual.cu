@@ -251,6 +251,8 @@ struct Exchange {
 };
 
 constexpr size_t kShared = 226 * 1024;  // shared memory of an SM, as far as the blocks may fill it
+// What one block may take of it beside its Exchange: back_plan's smem is at most this.
+constexpr int kMostDynamic = static_cast<int>(kShared - sizeof(Exchange) - 1024);
 
 struct BackPlan {
   int vec, cluster, threads, slice, groups, stages;
@@ -848,9 +850,19 @@ cudaError_t launch_backward(const NormArgs& a, BackPlan& p, cudaStream_t stream)
     kern = norm_backward_rms_kernel<VEC, CLUSTER, O8, FULL>;
   else
     kern = norm_backward_layer_kernel<VEC, CLUSTER, O8, FULL>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(p.smem));
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  // The limit belongs to the kernel, which serves many sizes, and not to a launch: the largest, once for
+  // each device.  (The size of each call would be another thread's limit between its set-up and its launch.)
+  static std::atomic<uint64_t> raised{0};
+  static_assert(kMaxDevices <= 64, "");
+  if (!(raised.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostDynamic);
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.groups * p.cluster);
   cfg.blockDim = dim3(p.threads);

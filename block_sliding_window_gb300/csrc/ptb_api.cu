@@ -20,8 +20,6 @@
 namespace ptb {
 namespace api {
 
-constexpr int kMaxDevices = 64;
-
 __device__ unsigned g_status_word;
 // Where take_status_kernel leaves the word it swapped out, for the host to read.
 __device__ unsigned g_status_taken;

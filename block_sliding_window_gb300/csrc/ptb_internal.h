@@ -11,6 +11,8 @@
 
 namespace ptb {
 
+constexpr int kMaxDevices = 64;  // device ordinals that the library takes: 0 .. 63
+
 // Launches `kern` so that it may start before the kernel in front of it in the stream has ended (see
 // wait_for_prior, which it has to call).
 template <typename... Args>

@@ -1,6 +1,7 @@
 """The gated feed-forward, the norms around a block and the 8-bit checkpoints on the GPU, element by
 element against the 64-bit model and the bounds of tests/block_model.py."""
 import math
+import threading
 
 import pytest
 import torch
@@ -756,3 +757,42 @@ def test_two_calls_at_once(ptb_lib):
     torch.cuda.synchronize()
     for k in (0, 1):
         assert all(torch.equal(v, want[k]) for v in got[k])
+
+
+@pytest.mark.parametrize("rms,widths", [(0, (1024, 4096)), (1, (2048, 4096)), (0, (8200, 16384))])
+def test_norm_backward_of_two_widths_from_two_threads(ptb_lib, rms, widths):
+    """Kernels of one kind serve many widths, with as much shared memory as each needs: what one thread asks
+    for is not to reach another's launch."""
+    lib = ptb_lib.load()
+    rows, calls, kept, want, got = 4, 4000, [], [], []
+    for n in widths:
+        s = norm_inputs(rows, n, 1, 1, 1, rms, seed=n)
+        y, h, stats = ptb_lib.norm_residual_train(s["x"], s["o"], rms=bool(rms), **parameters(s))
+        dy, dh = normal(rows, n, seed=1), normal(rows, n, seed=2)
+        want.append(ptb_lib.norm_residual_backward(dy, dh, y, s["o"], stats, rms=bool(rms), **parameters(s)))
+        got.append({k: torch.full_like(v, math.nan) for k, v in want[-1].items()})
+        ws = torch.empty(ptb_lib.norm_residual_backward_workspace_size(rows, n), dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.Stream()
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        g = lambda k: p(got[-1].get(k))  # noqa: E731
+        kept.append(((dy, dh, y, s, stats, ws, stream), (
+            p(dy), n, p(dh), n, p(y), n, p(s["o"]), n, None, 0, p(stats), p(s["post_gamma"]), p(s["post_beta"]),
+            p(s["gate"]), 1, 1.0, p(s["pre_gamma"]), rms, rows, n, g("dx"), n, g("do"), n, g("dpost_gamma"),
+            g("dpost_beta"), g("dgate"), g("dpre_gamma"), g("dpre_beta"), p(ws), ws.numel(), stream.cuda_stream)))
+    torch.cuda.synchronize()
+    device, start, failed = torch.cuda.current_device(), threading.Barrier(2), [-1, -1]
+
+    def work(k):
+        torch.cuda.set_device(device)
+        start.wait()
+        failed[k] = sum(lib.ptb_norm_residual_backward(*kept[k][1]) != 0 for _ in range(calls))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0, 0], f"{failed} of {calls} calls failed"
+    for k in (0, 1):
+        assert all(torch.equal(got[k][key], want[k][key]) for key in want[k])
