@@ -876,17 +876,18 @@ cudaError_t launch_backward(const NormArgs& a, BackPlan& p, cudaStream_t stream)
     cfg.attrs = at;
     cfg.numAttrs = 1;
   }
-  if (p.cluster > 1) {
+  if (CLUSTER && p.cluster > 1) {
     // Clusters leave places over in each GPC: as many groups as run at once, or the last would be a
-    // wave of their own.  The count follows from the cluster's and the block's size.
-    static std::atomic<int> known[9][back_threads<VEC, RMS>() / 32 + 1];
-    std::atomic<int>& kept = known[p.cluster][p.threads / 32];
+    // wave of their own.  The count follows from the cluster's and the block's size and from how the
+    // device's SMs lie in its GPCs, which need not be alike on two devices.
+    static std::atomic<uint16_t> known[kMaxDevices][9][back_threads<VEC, RMS>() / 32 + 1];
+    std::atomic<uint16_t>& kept = known[dev][p.cluster][p.threads / 32];
     int most = kept.load(std::memory_order_relaxed);
     if (most == 0) {
       e = cudaOccupancyMaxActiveClusters(&most, kern, &cfg);
       if (e != cudaSuccess) return e;
       if (most < 1) most = 1;
-      kept.store(most, std::memory_order_relaxed);
+      kept.store(static_cast<uint16_t>(most), std::memory_order_relaxed);
     }
     if (p.groups > most) p.groups = most;
     cfg.gridDim = dim3(p.groups * p.cluster);

@@ -591,7 +591,8 @@ ptb_status swa_attention_paged(const ptb_bf16* q, int64_t q_sb, int64_t q_sh, co
  * stride ld (elements, a multiple of 8, at least the row's length; the stride
  * of a single row is not used).  Parameter vectors are contiguous.  A call with
  * no rows writes nothing but the (zero) gradients of its parameters.  Sums run
- * in a fixed order: the same bits on every call on one kind of device.
+ * in a fixed order: the same bits on every call on one device (and with one
+ * setting of ptb_set_gemm_pairs).
  *
  * 8-bit checkpoints hold what a backward pass reads again, in half the memory:
  * groups of 32 neighbouring elements of a row share a power-of-two scale.
