@@ -92,7 +92,13 @@ int pick_block_n(int64_t a, int64_t b) {
   return 0;
 }
 
-ptb_status launch_status(cudaError_t e) { return e == cudaSuccess ? PTB_OK : PTB_ERR_LAUNCH; }
+// (The runtime keeps an error until it is asked for; a launch or copy that returned it has not asked, and
+// the next kernel's launch would report it as its own.)
+ptb_status launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return PTB_OK;
+  cudaGetLastError();
+  return PTB_ERR_LAUNCH;
+}
 
 // SM count of the current device, or an upper bound when there is none.
 int current_sms() {
@@ -807,9 +813,7 @@ ptb_status forward_host_tail(const ptb_bf16* x_dev, ptb_bf16* y_dev, ptb_bf16* y
   ptb_status st = ptb_forward(x_dev, ln_gamma, ln_beta, w_qkv, w_o, w_up, w_down, batch, seq,
                               hidden, ffn, heads, window, y_dev, layer_ws, layer_bytes, stream);
   if (st != PTB_OK) return st;
-  if (cudaMemcpyAsync(y_host, y_dev, bytes, cudaMemcpyDeviceToHost, stream) != cudaSuccess)
-    return PTB_ERR_LAUNCH;
-  return PTB_OK;
+  return launch_status(cudaMemcpyAsync(y_host, y_dev, bytes, cudaMemcpyDeviceToHost, stream));
 }
 }  // namespace
 
@@ -834,8 +838,8 @@ ptb_status ptb_forward_host(const ptb_bf16* x_host, const ptb_bf16* ln_gamma,
   DeviceState* ds = nullptr;
   ptb_status st = device_state(&ds);
   if (st != PTB_OK) return st;
-  if (cudaMemcpyAsync(x_dev, x_host, bytes, cudaMemcpyHostToDevice, stream) != cudaSuccess)
-    return PTB_ERR_LAUNCH;
+  st = launch_status(cudaMemcpyAsync(x_dev, x_host, bytes, cudaMemcpyHostToDevice, stream));
+  if (st != PTB_OK) return st;
   // The layer's kernels are persistent and take every SM.  For large layers
   // two layers in flight at once only fight over the SMs (175B-class: two
   // streams of layers 5.10 ms per layer, one stream 4.77-4.89 ms), so the
@@ -857,15 +861,15 @@ ptb_status ptb_forward_host(const ptb_bf16* x_host, const ptb_bf16* ln_gamma,
       ds->host_layer_done = nullptr;
       return PTB_ERR_DEVICE;
     }
-    if (cudaStreamWaitEvent(stream, ds->host_layer_done, 0) != cudaSuccess) return PTB_ERR_LAUNCH;
+    st = launch_status(cudaStreamWaitEvent(stream, ds->host_layer_done, 0));
+    if (st != PTB_OK) return st;
     st = ptb_forward(x_dev, ln_gamma, ln_beta, w_qkv, w_o, w_up, w_down, batch, seq, hidden, ffn,
                      heads, window, y_dev, layer_ws, layer_bytes, stream);
     if (st != PTB_OK) return st;
-    if (cudaEventRecord(ds->host_layer_done, stream) != cudaSuccess) return PTB_ERR_LAUNCH;
+    st = launch_status(cudaEventRecord(ds->host_layer_done, stream));
+    if (st != PTB_OK) return st;
   }
-  if (cudaMemcpyAsync(y_host, y_dev, bytes, cudaMemcpyDeviceToHost, stream) != cudaSuccess)
-    return PTB_ERR_LAUNCH;
-  return PTB_OK;
+  return launch_status(cudaMemcpyAsync(y_host, y_dev, bytes, cudaMemcpyDeviceToHost, stream));
 }
 
 ptb_status ptb_release_workspace(void) {

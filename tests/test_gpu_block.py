@@ -1,5 +1,6 @@
 """The gated feed-forward, the norms around a block and the 8-bit checkpoints on the GPU, element by
 element against the 64-bit model and the bounds of tests/block_model.py."""
+import ctypes
 import math
 import threading
 
@@ -796,3 +797,43 @@ def test_norm_backward_of_two_widths_from_two_threads(ptb_lib, rms, widths):
     assert failed == [0, 0], f"{failed} of {calls} calls failed"
     for k in (0, 1):
         assert all(torch.equal(got[k][key], want[k][key]) for key in want[k])
+
+
+@pytest.mark.parametrize("refused", ["few tokens", "many tokens", "norm backward", "checkpoint"])
+def test_a_failed_launch_is_not_reported_by_the_next_call(ptb_lib, refused):
+    """While a stream that waits for the legacy stream is being captured, work on the legacy stream is an error:
+    that call's, and not the next one's."""
+    lib, cu = ptb_lib.load(), ctypes.CDLL("libcuda.so.1")
+    f, s = ffn_inputs(200, 128, 192, seed=1), norm_inputs(6, 64, 1, 1, 1, 0, seed=2)
+    y, h, stats = ptb_lib.norm_residual_train(s["x"], s["o"], **parameters(s))
+    x = normal(3, 64, seed=3)
+    codes, exps = ptb_lib.checkpoint_pack(x)
+    want = [t.clone() for t in (codes, exps)]
+    ws = torch.empty(max(ptb_lib.gated_ffn_workspace_size(200, 128, 192),
+                         ptb_lib.norm_residual_backward_workspace_size(6, 64)), dtype=torch.uint8, device="cuda")
+    out = torch.empty(200, 128, dtype=torch.bfloat16, device="cuda")
+    p = lambda t: t.data_ptr()  # noqa: E731
+    pack = lambda: lib.ptb_checkpoint_pack(p(x), 64, 3, 64, p(codes), 64, p(exps), 2, None)  # noqa: E731
+    ffn = lambda t: lib.ptb_gated_ffn(p(f["x"]), 128, p(f["wg"]), p(f["wu"]), p(f["wd"]), None, 0, t, 128, 192, 0,  # noqa: E731
+                                      p(out), 128, None, None, p(ws), ws.numel(), None)
+    norm = lambda: lib.ptb_norm_residual_backward(  # noqa: E731
+        p(s["x"]), 64, p(s["x"]), 64, p(y), 64, p(s["o"]), 64, None, 0, p(stats), p(s["post_gamma"]), p(s["post_beta"]),
+        p(s["gate"]), 1, 1.0, p(s["pre_gamma"]), 0, 6, 64, p(out), 64, p(out[100:]), 64, None, None, None, None, None,
+        p(ws), ws.numel(), None)
+    call = {"few tokens": lambda: ffn(8), "many tokens": lambda: ffn(200), "norm backward": norm, "checkpoint": pack}[refused]
+    assert call() == 0
+    torch.cuda.synchronize()
+    codes.zero_(), exps.zero_()
+    torch.cuda.synchronize()
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert cu.cuStreamCreate(ctypes.byref(stream), 0) == 0
+    assert cu.cuStreamBeginCapture_v2(stream, 1) == 0  # of this thread's calls
+    st = call()
+    cu.cuStreamEndCapture(stream, ctypes.byref(graph))
+    if graph:
+        cu.cuGraphDestroy(graph)
+    assert cu.cuStreamDestroy_v2(stream) == 0
+    assert st == 5  # PTB_ERR_LAUNCH
+    assert pack() == 0
+    torch.cuda.synchronize()
+    assert torch.equal(codes, want[0]) and torch.equal(exps, want[1])
