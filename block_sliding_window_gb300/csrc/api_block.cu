@@ -19,12 +19,12 @@ constexpr int64_t kMaxRows = 1ll << 30;
     if (st_ != PTB_OK) return st_;      \
   } while (0)
 
-// A matrix of `rows` rows of `cols` elements; `unit` elements are 16 bytes.
+// A matrix of `rows` rows of `cols` elements; `unit` elements are 16 bytes.  A single row has no stride.
 ptb_status check_rows(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t unit) {
   if (rows == 0) return PTB_OK;
   if (!p) return PTB_ERR_ARG;
   if (rows > 1 && ld < cols) return PTB_ERR_ARG;
-  if (!aligned(p, 16) || ld % unit || ld < 0) return PTB_ERR_ALIGN;
+  if (!aligned(p, 16) || (rows > 1 && ld % unit)) return PTB_ERR_ALIGN;
   return PTB_OK;
 }
 
@@ -41,7 +41,7 @@ ptb_status check_workspace(const void* workspace, size_t bytes, size_t need) {
 ptb_status check_checkpoint(const void* codes, int64_t ld_codes, const uint8_t* exps,
                             int64_t ld_exps, int64_t rows, int64_t cols) {
   if (rows == 0) return PTB_OK;
-  if (!exps || (rows > 1 && ld_exps < cols / 32) || ld_exps < 0) return PTB_ERR_ARG;
+  if (!exps || (rows > 1 && ld_exps < cols / 32)) return PTB_ERR_ARG;
   return check_rows(codes, ld_codes, rows, cols, 16);
 }
 
@@ -418,8 +418,8 @@ ptb_status ptb_norm_residual_backward(
     if (!aligned(p, 4)) return PTB_ERR_ALIGN;
   if (rows > 0 && dx == d_o) return PTB_ERR_ARG;
   if (rows == 1) {  // not used
-    ld_dy = ld_dh = ld_y = ld_dx = ld_do = hidden;
-    if (!o_exps) ld_o = hidden;
+    ld_dy = ld_dh = ld_y = ld_o = ld_dx = ld_do = hidden;
+    ld_o_exps = hidden / 32;
   }
   // In place: a row's gradients may replace what they were computed from, at the same strides.
   const struct {

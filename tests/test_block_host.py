@@ -128,6 +128,25 @@ def test_checkpoints_refuse(lib, kw, code):
                                      None) == code
 
 
+ONE_ROW = [3, 4, -8, -1, 1 << 40]
+
+
+@pytest.mark.parametrize("ld", ONE_ROW)
+def test_the_stride_of_a_single_row_is_not_looked_at(lib, ld):
+    """Every call is refused, for something that is checked behind the strides."""
+    assert ffn(lib, t=1, ldx=ld, ldy=ld, r=FAKE * 4, ldr=ld, wsb=100) == WORKSPACE
+    assert ffn_bwd(lib, t=1, lddy=ld, ldx=ld, lddx=ld, wsb=64) == WORKSPACE
+    assert ffn_bwd(lib, t=1, lddy=ld, ldx=ld, xe=FAKE, ldxe=ld, lddx=ld, wsb=64) == WORKSPACE
+    assert norm(lib, rows=1, gates=1, ldx=ld, ldo=ld, ldy=ld, ldh=ld, y=FAKE * 4) == ARG  # y is h
+    assert norm(lib, rows=1, gates=1, ldx=ld, ldo=ld, ldy=ld, ldh=ld, y=FAKE * 4, stats=FAKE + 8) == ALIGN
+    one = dict(rows=1, gates=1, lddy=ld, lddh=ld, ldy=ld, ldo=ld, lddx=ld, lddo=ld, wsb=16)
+    assert norm_bwd(lib, **one) == WORKSPACE
+    assert norm_bwd(lib, oe=FAKE, ldoe=ld, **one) == WORKSPACE
+    for call in (lambda x: lib.ptb_checkpoint_pack(x, ld, 1, 64, FAKE * 2, ld, FAKE * 3, ld, None),
+                 lambda x: lib.ptb_checkpoint_unpack(FAKE * 2, ld, FAKE * 3, ld, 1, 64, x, ld, None)):
+        assert call(FAKE * 2) == ARG and call(FAKE + 4) == ALIGN  # x is the codes
+
+
 def test_calls_without_rows_pass_the_checks(lib):
     assert past_checks(ffn(lib)) and past_checks(norm(lib))
     assert past_checks(ffn(lib, x=None, y=None, ws=None, wsb=0))

@@ -311,6 +311,68 @@ def test_norm_without_a_gate_uses_no_count_of_gates(ptb_lib, rows, n, gates, pos
     assert all(torch.equal(got[k], want[k]) for k in want)
 
 
+@pytest.mark.parametrize("ld", [3, -8, 1 << 40])
+@pytest.mark.parametrize("n", [192, 12288])
+def test_one_row_of_any_stride(ptb_lib, n, ld):
+    """A single row's stride need not be one that several rows could have."""
+    lib = ptb_lib.load()
+    s = norm_inputs(1, n, 1, 1, 1, 0, seed=6)
+    p = lambda t: t.data_ptr()  # noqa: E731
+    w = [p(s[k]) for k in ("post_gamma", "post_beta", "gate", "pre_gamma", "pre_beta")]
+    y, h, stats = ptb_lib.norm_residual_train(s["x"], s["o"], **parameters(s))
+    got = [torch.full_like(t, math.nan) for t in (y, h, stats)]
+    assert lib.ptb_norm_residual(p(s["x"]), ld, p(s["o"]), ld, *w[:3], 1, 1.0, *w[3:], 0, 1e-5, 1, n, p(got[0]), ld,
+                                 p(got[1]), ld, p(got[2]), None) == 0
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, (y, h, stats)))
+    kept = ptb_lib.checkpoint_pack(s["o"])
+    codes, exps, back = torch.zeros_like(kept[0]), torch.zeros_like(kept[1]), torch.empty_like(y)
+    assert lib.ptb_checkpoint_pack(p(s["o"]), ld, 1, n, p(codes), ld, p(exps), ld, None) == 0
+    assert lib.ptb_checkpoint_unpack(p(codes), ld, p(exps), ld, 1, n, p(back), ld, None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(codes, kept[0]) and torch.equal(exps, kept[1])
+    assert torch.equal(back, ptb_lib.checkpoint_unpack(*kept))
+    dy, dh = normal(1, n, seed=1), normal(1, n, seed=2)
+    ws = torch.empty(ptb_lib.norm_residual_backward_workspace_size(1, n), dtype=torch.uint8, device="cuda")
+    for o, oe in ((s["o"], None), kept):
+        want = ptb_lib.norm_residual_backward(dy, dh, y, o if oe is None else kept, stats, **parameters(s))
+        out = {k: torch.full_like(v, math.nan) for k, v in want.items()}
+        assert lib.ptb_norm_residual_backward(
+            p(dy), ld, p(dh), ld, p(y), ld, p(o), ld, None if oe is None else p(oe), ld, p(stats), *w[:3], 1, 1.0, w[3], 0, 1,
+            n, p(out["dx"]), ld, p(out["do"]), ld, p(out["dpost_gamma"]), p(out["dpost_beta"]), p(out["dgate"]),
+            p(out["dpre_gamma"]), p(out["dpre_beta"]), p(ws), ws.numel(), None) == 0
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("ld", [3, -8])
+@pytest.mark.parametrize("h,f", [(128, 192), (2048, 512)])
+def test_gated_ffn_of_one_token_of_any_stride(ptb_lib, h, f, ld):
+    lib = ptb_lib.load()
+    s = ffn_inputs(1, h, f, seed=9)
+    y, kept = ptb_lib.gated_ffn_train(s["x"], *weights(s), residual=s["resid"])
+    plain = ptb_lib.gated_ffn(s["x"], *weights(s), residual=s["resid"])
+    x8 = ptb_lib.checkpoint_pack(s["x"])
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    wp = [p(t) for t in weights(s)]
+    ws = torch.empty(max(ptb_lib.gated_ffn_workspace_size(1, h, f), ptb_lib.gated_ffn_backward_workspace_size(1, h, f, 8)),
+                     dtype=torch.uint8, device="cuda")
+    for k, want in ((None, plain), (torch.empty_like(kept), y)):
+        got = torch.empty_like(y)
+        assert lib.ptb_gated_ffn(p(s["x"]), ld, *wp, p(s["resid"]), ld, 1, h, f, 0, p(got), ld, p(k), None, p(ws), ws.numel(),
+                                 None) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and (k is None or torch.equal(k, kept))
+    for x, xe in ((s["x"], None), x8):
+        want = ptb_lib.gated_ffn_backward(s["dy"], x if xe is None else x8, *weights(s), kept)
+        got = {k: torch.empty_like(v) for k, v in want.items()}
+        assert lib.ptb_gated_ffn_backward(p(s["dy"]), ld, p(x), ld, p(xe), ld, *wp, p(kept), None, 1, h, f, 0, p(got["dx"]), ld,
+                                          p(got["dw_gate"]), p(got["dw_up"]), p(got["dw_down"]), 16, p(ws), ws.numel(),
+                                          None) == 0
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[k], want[k]) for k in want)
+
+
 def test_norm_rows_of_nan_stay_their_own(ptb_lib):
     s = norm_inputs(40, 512, 1, 1, 1, 0, seed=8)
     y, h, stats = ptb_lib.norm_residual_train(s["x"], s["o"], **parameters(s))
