@@ -485,7 +485,8 @@ __device__ __forceinline__ float4* partial_chunk(const GemmArgs& p, int slot, in
 // 2048 by 10880 in nine pieces 36 us, 30 this way.)
 template <int BN, int EPI, int ROWS>
 struct PieceSums {
-  static constexpr int kSlots = epi_warps<EPI>() == 8 ? 5 : 8;  // of 4 KB a warp, 160 KB at most
+  static constexpr int kSlots = epi_warps<EPI>() == 8 ? 5 : 8;  // of 4 KB a warp
+  static constexpr int kRingBytes = epi_warps<EPI>() * kSlots * 4096;  // 160 KB, or 128 on four warps
   static constexpr int kStride = 32 * (epi_warps<EPI>() / 4);
   static constexpr int64_t kPiece = static_cast<int64_t>(ROWS / 32) * (BN / 32) * 256;
   const float4* src;  // piece 0
@@ -697,6 +698,8 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1) gemm_kernel(const __gr
   constexpr bool kBmn = (LAYOUT & 2) != 0;
   constexpr uint32_t kMnBlock = 64 * 128;
   static_assert(!(FP8 && LAYOUT != kLayoutKK), "e4m3 operands are K-major only");
+  static_assert(PieceSums<BN, EPI, BM>::kRingBytes <= C::kStages * C::kStageBytes,
+                "the join of K pieces would reach past the ring into the barriers");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -962,6 +965,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<EPI>(),
   constexpr bool kAmn = (LAYOUT & 1) != 0;
   constexpr bool kBmn = (LAYOUT & 2) != 0;
   constexpr uint32_t kMnBlock = 64 * 128;
+  static_assert(PieceSums<BN, EPI, 2 * BM>::kRingBytes <= NS * C::kStageBytes,
+                "the join of K pieces would reach past the ring into the barriers");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
