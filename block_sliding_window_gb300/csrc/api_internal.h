@@ -1,6 +1,7 @@
 // Internal interface shared by the translation units of the C ABI
 // (ptb_api.cu: common part and forward pass; api_swa.cu: the attention
-// operator; api_fp8.cu: the FP8 variant; api_train.cu: the training step):
+// operator; api_fp8.cu: the FP8 variant; api_train.cu: the training step;
+// api_serve.cu: the serving operators; api_block.cu: blocks with gates):
 // device state, workspace handling, argument checks and the GEMM launch
 // plumbing.  Not part of the public interface.
 #pragma once

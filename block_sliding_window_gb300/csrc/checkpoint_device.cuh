@@ -86,20 +86,4 @@ __device__ __forceinline__ void ckpt_store_group(const float (&v)[32], uint8_t* 
   *exponent = static_cast<uint8_t>(e);
 }
 
-// The values of a whole group.
-__device__ __forceinline__ void ckpt_load_group(const uint8_t* codes, const uint8_t* exponent,
-                                                float (&v)[32]) {
-  const float s = ckpt_scale(__ldg(exponent));
-  const uint4* src = reinterpret_cast<const uint4*>(codes);
-  const uint4 p = __ldg(src), q = __ldg(src + 1);
-  const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float f[4];
-    ckpt_unpack4(w[j], f);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[4 * j + k] = f[k] * s;
-  }
-}
-
 }  // namespace ptb

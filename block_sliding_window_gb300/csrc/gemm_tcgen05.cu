@@ -9,7 +9,7 @@
 // projections share one GEMM whose epilogue adds x.  GeLU is fused into the
 // first GEMM's epilogue (§2.5, Table 3, efficient-operators row).
 //
-// Kernel structure (one persistent CTA per SM, 192 threads):
+// Kernel structure (one persistent CTA per SM, 192 threads; 320 with eight epilogue warps):
 //   warp 0      TMA producer: 128 x 64 A tile and BN x 64 B tile per stage
 //               into a ring of shared-memory stages (128-byte swizzle).
 //   warp 1      owns the TMEM allocation; one thread issues tcgen05.mma
@@ -19,10 +19,10 @@
 //               64-wide k-block takes ~790 cycles for 512 cycles of MMA work,
 //               matching the shared-memory traffic per k-block -- 48 KB of
 //               operand reads plus 48 KB of TMA writes at ~128 B/clk.)
-//   warps 2..5  (2..9 for the gated epilogues)
-//               epilogue: tcgen05.ld of the accumulator (warp w reads TMEM
-//               lanes 32*(w%4) .. +31, i.e. one output row per thread),
-//               GELU or residual add in fp32, bf16 stores.  The epilogue of
+//   warps 2..5  (2..9 for the GEMMs of a gated feed-forward with bf16
+//               outputs: epi_warps) epilogue: tcgen05.ld of the accumulator
+//               (warp w reads TMEM lanes 32*(w%4) .. +31, i.e. one output row
+//               per thread), GELU or residual add in fp32, bf16 stores.  The epilogue of
 //               one work unit overlaps the main loop of the next.
 //
 // Work units.  The tiles that fill whole waves (a multiple of the grid) are
@@ -31,10 +31,11 @@
 // starts on the k-slabs the previous one left in L2.  The remaining R < grid tiles of the
 // last, partial wave are each split along K into S pieces (R*S <= grid), one
 // piece per otherwise idle CTA.  A piece writes its fp32 partial tile to the
-// workspace and bumps an arrival counter per 32-row quarter of the tile; the
-// epilogue warp that arrives last for a quarter sums the S partials of those
-// rows in piece order (so the bits do not depend on who finished) and runs
-// the epilogue for them.  Nothing ever waits on another CTA or another warp.
+// workspace, and each epilogue warp bumps an arrival counter of its 32-row
+// quarter of the tile (two warps of a quarter have one each, for their chunks
+// of columns); the warp that arrives last sums the S partials of what it
+// counts in piece order (so the bits do not depend on who finished) and runs
+// the epilogue for it.  Nothing ever waits on another CTA or another warp.
 //
 // Every mbarrier wait is bounded (see mbar_wait); on a timeout all roles
 // unwind, wait for their own copies and MMAs, free TMEM and return.
@@ -927,10 +928,11 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1) gemm_kernel(const __gr
 //   warp 1      both ranks allocate TMEM together (cta_group::2).  Rank 0
 //               issues the MMAs and commits stage and tile completion to the
 //               barriers at the same offset in both CTAs.
-//   warps 2..5  both ranks: epilogue of their 128 rows; each warp then
-//               arrives on rank 0's `tempty` barrier (8 arrivals per tile).
+//   warps 2..5  (2..9) both ranks: epilogue of their 128 rows; each warp then
+//               arrives on rank 0's `tempty` barrier (8 or 16 arrivals per
+//               tile).
 // The remainder wave is split along K per pair as in the single-CTA kernel
-// (256-row partial tiles, 8 arrival counters per tile).
+// (256-row partial tiles, 8 or 16 arrival counters per tile).
 constexpr int kPairBN = 256;
 // Stages of the ring.  Fewer stages leave more of the SM's unified L1 /
 // shared memory to L1.  With both operands loaded evict_last, 5 stages for

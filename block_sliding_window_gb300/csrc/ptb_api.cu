@@ -138,11 +138,11 @@ int64_t gemm_tiles(int64_t m, int64_t n, int block_n, bool pair) {
 
 // Scratch for the split last wave of an M x N x (kb k-blocks) GEMM, either
 // tile shape (whichever needs more).
-size_t gemm_scratch_any(int64_t m, int64_t n, int64_t kb, int block_n, int sms, int counters = 1) {
+size_t gemm_scratch_any(int64_t m, int64_t n, int64_t kb, int block_n, int sms) {
   const size_t a = gemm_scratch_bytes(
-      plan_gemm(gemm_tiles(m, n, block_n, false), kb, sms, block_n, 128, counters));
+      plan_gemm(gemm_tiles(m, n, block_n, false), kb, sms, block_n));
   const size_t b = gemm_scratch_bytes(
-      plan_gemm(gemm_tiles(m, n, block_n, true), kb, sms / 2, block_n, 256, counters));
+      plan_gemm(gemm_tiles(m, n, block_n, true), kb, sms / 2, block_n, 256));
   return a > b ? a : b;
 }
 

@@ -31,8 +31,10 @@ __device__ __forceinline__ void record_error(unsigned* status, unsigned code) {
 // A kernel launched with programmatic stream serialisation may start while the kernel in front of it
 // still runs, from the moment all of that one's blocks have called dependents_may_start() or ended.
 // wait_for_prior() returns when the kernel in front has ended and its writes can be seen; nothing of
-// its results is touched before.  Every kernel calls it before dependents_may_start(), so that when a
-// kernel starts, all but the one in front of it have ended.  Without such a launch both do nothing.
+// its results is touched before.  A kernel that is launched that way calls it before
+// dependents_may_start(); one that is launched as usual (the norm backward) starts when all in front of it
+// have ended and need not wait.  So when a kernel starts, all but the one in front of it have ended.
+// Without such a launch both do nothing.
 
 __device__ __forceinline__ void dependents_may_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
